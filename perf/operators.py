@@ -71,12 +71,8 @@ def _log_int(rng, lo, hi):
 
 
 def draw(rng):
-    limit = {c["op"]: 0 for c in listed()}
-    top = {"bytes": 0, "flops": 0}
-    for c in listed():
-        w = work(c)
-        limit[c["op"]] = max(limit[c["op"]], w["bytes"])
-        top = {k: max(top[k], w[k]) for k in top}
+    done = [work(c) for c in listed()]
+    top = {k: max(w[k] for w in done) for k in ("bytes", "flops")}
     while True:
         op = rng.choice(["dispatch", "dispatch_grad", "combine", "combine", "combine_grad",
                          "combine_grad", "route_grad", "linear_q4", "linear_q4", "ffn_q4",
