@@ -18,6 +18,9 @@
  * router matmul fused with 1), moe_forward_gate (the layer from x and the
  * gate weights), moe_forward_timed (stage events), moe_forward_launch_count,
  * moe_ffn_plan,
+ * the rows' way to expert-sorted order and back for experts of the caller's
+ * own, with gradients (moe_dispatch, moe_dispatch_backward,
+ * moe_combine_weighted, moe_combine_weighted_backward, moe_route_backward),
  * the workspace calls (moe_workspace_size, moe_workspace_init,
  * moe_workspace_regions), moe_read_status and moe_selftest_wait_timeout.
  *
@@ -358,6 +361,73 @@ moe_status moe_forward_gate(const uint16_t *x, const uint16_t *w_gate, const uin
                             int32_t *topk_indx, uint16_t *topk_vals,
                             const moe_routing_meta *meta, void *workspace,
                             size_t workspace_bytes, moe_stream stream);
+
+/* ---- Rows to expert-sorted order and back, with gradients --------------
+ * For callers that run the experts themselves (training, another precision):
+ * the layer around them as separate calls, each with its backward pass. No
+ * counterpart on the pages beyond [R2] "It is removable in plain PyTorch"
+ * (tok = order // k, x[tok], y.index_add_ of weight * expert output).
+ *
+ * row_sorted [n*k] is the metadata's dispatch index: slot f = t*k + j lies at
+ * sorted position p(f) = row_sorted[f], or is dropped where row_sorted[f] is
+ * outside [0, n*k) (an expert map writes -1). Each kept position belongs to
+ * one slot. n_kept: device pointer to the number of kept slots (the
+ * metadata's last offset, &offs[E] or &offs[n_local_experts]); the rows of
+ * positions [*n_kept, n*k) are then set to zero. NULL = no such rows.
+ *
+ * Rows are [., H] row-major of `dtype` (any H >= 1), every base aligned to
+ * its element; 16-byte aligned rows (H * size and the bases) run fastest.
+ * Sums run in fp32 in slot order and are rounded once: no atomics, the bits
+ * depend on the inputs only. No workspace. n = 0 is a no-op. An input and an
+ * output may not overlap. */
+typedef enum {
+  MOE_BF16 = 0,
+  MOE_FP16 = 1,
+  MOE_FP32 = 2
+} moe_dtype;
+
+/* x_sorted[p(t*k + j)] = x[t] for every kept slot: x [n, H], x_sorted
+ * [n*k, H]. */
+moe_status moe_dispatch(const void *x, const int32_t *row_sorted, const int32_t *n_kept, int64_t n,
+                        int32_t k, int32_t H, int32_t dtype, void *x_sorted, moe_stream stream);
+
+/* Gradient of moe_dispatch: d_x[t] = sum over the token's kept slots of
+ * d_sorted[p(t*k + j)]; zero for a token without one. */
+moe_status moe_dispatch_backward(const void *d_sorted, const int32_t *row_sorted, int64_t n,
+                                 int32_t k, int32_t H, int32_t dtype, void *d_x,
+                                 moe_stream stream);
+
+/* out[t] = sum over the token's kept slots of weights[t, j] *
+ * y_sorted[p(t*k + j)]: y_sorted [n*k, H] the experts' outputs in sorted
+ * order, weights [n, k] of weights_dtype (MOE_BF16 as moe_route's topk_vals,
+ * or MOE_FP32), out [n, H]. A dropped slot's weight is not used. */
+moe_status moe_combine_weighted(const void *y_sorted, const int32_t *row_sorted,
+                                const void *weights, int32_t weights_dtype, int64_t n, int32_t k,
+                                int32_t H, int32_t dtype, void *out, moe_stream stream);
+
+/* Gradients of moe_combine_weighted for d_out [n, H]:
+ *   d_sorted[p(t*k + j)] = weights[t, j] * d_out[t]         [n*k, H] of dtype
+ *   d_weights[t, j] = <d_out[t], y_sorted[p(t*k + j)]>, 0 for a dropped slot;
+ *                                                            [n, k] fp32 */
+moe_status moe_combine_weighted_backward(const void *d_out, const void *y_sorted,
+                                         const int32_t *row_sorted, const void *weights,
+                                         int32_t weights_dtype, const int32_t *n_kept, int64_t n,
+                                         int32_t k, int32_t H, int32_t dtype, void *d_sorted,
+                                         float *d_weights, moe_stream stream);
+
+/* Gradient of moe_route's gate weights to the logits: logits [n, E] fp32 and
+ * topk_indx [n, k] as moe_route read and wrote them, d_vals [n, k] fp32 the
+ * gradient of the weights (moe_combine_weighted_backward's d_weights),
+ * d_logits [n, E] fp32. With p the softmax of `gating` recomputed in fp32
+ * from the logits and up[e] = d_vals at a selected expert, 0 elsewhere:
+ *   d_logits[e] = p_e * (up[e] - sum_i p_i up_i)
+ * over the k selected experts (MOE_GATING_SOFTMAX_TOPK; 0 at the others) or
+ * over all E (MOE_GATING_SOFTMAX_ALL). The selection itself is piecewise
+ * constant and has no gradient. An expert id outside [0, E) counts as no
+ * selection. */
+moe_status moe_route_backward(const float *logits, const int32_t *topk_indx, const float *d_vals,
+                              int64_t n, int32_t E, int32_t k, int32_t gating, float *d_logits,
+                              moe_stream stream);
 
 /* Stage kernels of moe_forward, in launch order (indices of the events of
  * moe_forward_timed). */

@@ -22,6 +22,7 @@ ACT = {"swiglu": 0, "swiglu_oai": 1, "relu2": 2}
 LAYOUT = {"packed": 0, "interleaved": 1}
 SET_ALPHA, SET_BETA, SET_LIMIT = 1, 2, 4
 FFN_KERNEL = {"auto": 0, "tiled": 1, "swap": 2}
+DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 ABI_VERSION = 4
 
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
@@ -78,6 +79,12 @@ SIGNATURES = {
                                 _PM, _P, _SZ, _P]),
     "moe_forward_launch_count": (_I32, [_I64, _I32, _I32, _I32, _I32]),
     "moe_ffn_plan": (_I32, [_I64, _I32, _I32, _I32, _I32, _P, _P]),
+    "moe_dispatch": (_I32, [_P, _P, _P, _I64, _I32, _I32, _I32, _P, _P]),
+    "moe_dispatch_backward": (_I32, [_P, _P, _I64, _I32, _I32, _I32, _P, _P]),
+    "moe_combine_weighted": (_I32, [_P, _P, _P, _I32, _I64, _I32, _I32, _I32, _P, _P]),
+    "moe_combine_weighted_backward": (_I32, [_P, _P, _P, _P, _I32, _P, _I64, _I32, _I32, _I32, _P,
+                                             _P, _P]),
+    "moe_route_backward": (_I32, [_P, _P, _P, _I64, _I32, _I32, _I32, _P, _P]),
     "moe_read_status": (_I32, [_P, _SZ, _I32, _P]),
     "moe_selftest_wait_timeout": (_I32, [_P, _SZ, _U64, _P]),
 }
@@ -355,6 +362,156 @@ def forward_gate(x: torch.Tensor, w_gate: torch.Tensor, w13: torch.Tensor, w2: t
                                   mstruct, _ptr(ws), ws.numel(), _stream(x.device)),
            "moe_forward_gate")
     return out
+
+
+def _need_rows(t: torch.Tensor, name: str, shape=None, like: Optional[torch.Tensor] = None) -> None:
+    """A row tensor [rows, H] of one of the row types (`like`: of that
+    tensor's type and on its device)."""
+    if like is not None:
+        _need(t, name, like.dtype, shape)
+        _same_device(t, name, like)
+        return
+    if not isinstance(t, torch.Tensor) or t.dtype not in DTYPE:
+        raise ValueError(f"{name} must be a bfloat16, float16 or float32 tensor")
+    _need(t, name, t.dtype, shape)
+    if t.dim() != 2 or t.shape[1] == 0:
+        raise ValueError(f"{name} must have shape [rows, H], got {tuple(t.shape)}")
+
+
+def _same_device(t: torch.Tensor, name: str, other: torch.Tensor) -> None:
+    if t.device != other.device:
+        raise ValueError(f"{name} is on {t.device}, not on {other.device}")
+
+
+def _need_slots(meta: dict, n: int, k: int, rows: torch.Tensor) -> None:
+    """The metadata entries that the row calls read: row_sorted and offs."""
+    _need(meta["row_sorted"], "row_sorted", torch.int32, (n * k,))
+    _need(meta["offs"], "offs", torch.int32)
+    if meta["offs"].dim() != 1 or meta["offs"].numel() < 2:
+        raise ValueError("offs must have one entry per expert and one more")
+    for name in ("row_sorted", "offs"):
+        _same_device(meta[name], name, rows)
+
+
+def _kept(meta: dict) -> ctypes.c_void_p:
+    """Device address of the number of kept slots: the last offset."""
+    offs = meta["offs"]
+    return ctypes.c_void_p(offs.data_ptr() + 4 * (offs.numel() - 1))
+
+
+def _need_weights(weights: torch.Tensor, rows: torch.Tensor) -> None:
+    if not isinstance(weights, torch.Tensor) or weights.dtype not in (torch.bfloat16,
+                                                                      torch.float32):
+        raise ValueError("weights must be a bfloat16 or float32 tensor")
+    _need(weights, "weights", weights.dtype)
+    if weights.dim() != 2:
+        raise ValueError(f"weights must have shape [n, k], got {tuple(weights.shape)}")
+    _same_device(weights, "weights", rows)
+
+
+def _out_rows(out: Optional[torch.Tensor], name: str, shape, like: torch.Tensor) -> torch.Tensor:
+    if out is None:
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+    _need_rows(out, name, shape, like)
+    return out
+
+
+def dispatch(x: torch.Tensor, meta: dict, k: int,
+             out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Token rows x [n, H] (bf16, fp16 or fp32) -> expert-sorted rows [n*k, H]:
+    row row_sorted[t*k + j] is x[t]. The rows past the kept slots (an expert
+    map drops some) are zero. `meta` as from route_metadata (row_sorted and
+    offs are read)."""
+    _need_rows(x, "x")
+    n, H = x.shape
+    _need_slots(meta, n, k, x)
+    out = _out_rows(out, "out", (n * k, H), x)
+    with torch.cuda.device(x.device):
+        _check(lib().moe_dispatch(_ptr(x), _ptr(meta["row_sorted"]), _kept(meta), n, k, H,
+                                  DTYPE[x.dtype], _ptr(out), _stream(x.device)), "moe_dispatch")
+    return out
+
+
+def dispatch_backward(d_sorted: torch.Tensor, meta: dict, k: int,
+                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of dispatch: d_sorted [n*k, H] -> d_x [n, H], each token the
+    sum (fp32) of its kept slots' rows."""
+    _need_rows(d_sorted, "d_sorted")
+    N, H = d_sorted.shape
+    if k < 1 or N % k:
+        raise ValueError(f"d_sorted must have n*k rows, got {N} with k = {k}")
+    n = N // k
+    _need_slots(meta, n, k, d_sorted)
+    out = _out_rows(out, "out", (n, H), d_sorted)
+    with torch.cuda.device(d_sorted.device):
+        _check(lib().moe_dispatch_backward(_ptr(d_sorted), _ptr(meta["row_sorted"]), n, k, H,
+                                           DTYPE[d_sorted.dtype], _ptr(out),
+                                           _stream(d_sorted.device)), "moe_dispatch_backward")
+    return out
+
+
+def combine_weighted(y_sorted: torch.Tensor, meta: dict, weights: torch.Tensor,
+                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Expert-sorted rows y_sorted [n*k, H] -> [n, H]: each token the sum
+    (fp32) of its kept slots' rows times weights [n, k] (bf16 as route's
+    topk_vals, or fp32)."""
+    _need_rows(y_sorted, "y_sorted")
+    _need_weights(weights, y_sorted)
+    n, k = weights.shape
+    H = y_sorted.shape[1]
+    _need_rows(y_sorted, "y_sorted", (n * k, H))
+    _need_slots(meta, n, k, y_sorted)
+    out = _out_rows(out, "out", (n, H), y_sorted)
+    with torch.cuda.device(y_sorted.device):
+        _check(lib().moe_combine_weighted(_ptr(y_sorted), _ptr(meta["row_sorted"]), _ptr(weights),
+                                          DTYPE[weights.dtype], n, k, H, DTYPE[y_sorted.dtype],
+                                          _ptr(out), _stream(y_sorted.device)),
+               "moe_combine_weighted")
+    return out
+
+
+def combine_weighted_backward(d_out: torch.Tensor, y_sorted: torch.Tensor, meta: dict,
+                              weights: torch.Tensor):
+    """Gradients of combine_weighted -> (d_sorted [n*k, H] of the rows' type,
+    d_weights [n, k] fp32). Rows past the kept slots and the weights of
+    dropped slots get zero."""
+    _need_rows(d_out, "d_out")
+    _need_weights(weights, d_out)
+    n, k = weights.shape
+    H = d_out.shape[1]
+    _need_rows(d_out, "d_out", (n, H))
+    _need_rows(y_sorted, "y_sorted", (n * k, H), d_out)
+    _need_slots(meta, n, k, d_out)
+    d_sorted = torch.empty((n * k, H), dtype=d_out.dtype, device=d_out.device)
+    d_weights = torch.empty((n, k), dtype=torch.float32, device=d_out.device)
+    with torch.cuda.device(d_out.device):
+        _check(lib().moe_combine_weighted_backward(
+            _ptr(d_out), _ptr(y_sorted), _ptr(meta["row_sorted"]), _ptr(weights),
+            DTYPE[weights.dtype], _kept(meta), n, k, H, DTYPE[d_out.dtype], _ptr(d_sorted),
+            _ptr(d_weights), _stream(d_out.device)), "moe_combine_weighted_backward")
+    return d_sorted, d_weights
+
+
+def route_backward(logits: torch.Tensor, topk_indx: torch.Tensor, d_vals: torch.Tensor,
+                   gating: str = "softmax_topk") -> torch.Tensor:
+    """Gradient of route's gate weights: d_vals fp32 [n, k] -> d_logits fp32 [n, E]."""
+    _need(logits, "logits", torch.float32)
+    if logits.dim() != 2:
+        raise ValueError(f"logits must have shape [n, E], got {tuple(logits.shape)}")
+    n, E = logits.shape
+    _need(topk_indx, "topk_indx", torch.int32)
+    if topk_indx.dim() != 2 or topk_indx.shape[0] != n:
+        raise ValueError(f"topk_indx must have shape [n, k], got {tuple(topk_indx.shape)}")
+    k = topk_indx.shape[1]
+    _need(d_vals, "d_vals", torch.float32, (n, k))
+    for t, name in ((topk_indx, "topk_indx"), (d_vals, "d_vals")):
+        _same_device(t, name, logits)
+    d_logits = torch.empty_like(logits)
+    with torch.cuda.device(logits.device):
+        _check(lib().moe_route_backward(_ptr(logits), _ptr(topk_indx), _ptr(d_vals), n, E, k,
+                                        GATING[gating], _ptr(d_logits), _stream(logits.device)),
+               "moe_route_backward")
+    return d_logits
 
 
 STAGES = ("route", "metadata", "gather", "ffn1", "ffn2", "combine")

@@ -95,6 +95,17 @@ FfnScratch ffn_scratch(void *ws, const WorkspaceLayout &L) {
           L.x_sorted > L.sk_part ? ws_at<float>(ws, L.sk_part) : nullptr};
 }
 
+// Sizes and element types of the row calls (moe_dispatch and its kin): any H
+// up to the layer's limit.
+moe_status check_rows(int64_t n, int k, int H, int dtype) {
+  if (n < 0 || k < 1 || k > kMaxTopk || H < 1 || H > 65536) return MOE_ERR_INVALID_ARG;
+  if (n * (int64_t)k >= (int64_t)INT32_MAX) return MOE_ERR_INVALID_ARG;
+  if (dtype != MOE_BF16 && dtype != MOE_FP16 && dtype != MOE_FP32) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+inline size_t elem_align(int dtype) { return dtype == MOE_FP32 ? 4 : 2; }
+
 }  // namespace
 
 extern "C" {
@@ -438,6 +449,86 @@ moe_status moe_route_gemm(const uint16_t *x, const uint16_t *w_gate, int64_t n, 
   if (workspace_bytes < kCtrlBytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
   return from_cuda(launch_route_gemm(x, w_gate, n, E, H, k, gating, topk_indx, topk_vals, logits,
                                      ws_at<uint32_t>(workspace, 0), (cudaStream_t)stream));
+}
+
+moe_status moe_dispatch(const void *x, const int32_t *row_sorted, const int32_t *n_kept, int64_t n,
+                        int32_t k, int32_t H, int32_t dtype, void *x_sorted, moe_stream stream) {
+  moe_status st = check_rows(n, k, H, dtype);
+  if (st != MOE_OK) return st;
+  if (n == 0) return MOE_OK;
+  if (!x || !row_sorted || !x_sorted) return MOE_ERR_INVALID_ARG;
+  const size_t a = elem_align(dtype);
+  if (!aligned(x, a) || !aligned(x_sorted, a) || !aligned(row_sorted, 4) || !aligned(n_kept, 4))
+    return MOE_ERR_MISALIGNED;
+  return from_cuda(
+      launch_dispatch(x, row_sorted, n_kept, n, k, H, dtype, x_sorted, (cudaStream_t)stream));
+}
+
+moe_status moe_dispatch_backward(const void *d_sorted, const int32_t *row_sorted, int64_t n,
+                                 int32_t k, int32_t H, int32_t dtype, void *d_x,
+                                 moe_stream stream) {
+  moe_status st = check_rows(n, k, H, dtype);
+  if (st != MOE_OK) return st;
+  if (n == 0) return MOE_OK;
+  if (!d_sorted || !row_sorted || !d_x) return MOE_ERR_INVALID_ARG;
+  const size_t a = elem_align(dtype);
+  if (!aligned(d_sorted, a) || !aligned(d_x, a) || !aligned(row_sorted, 4))
+    return MOE_ERR_MISALIGNED;
+  return from_cuda(launch_combine_weighted(d_sorted, row_sorted, nullptr, MOE_FP32, n, k, H, dtype,
+                                           d_x, (cudaStream_t)stream));
+}
+
+moe_status moe_combine_weighted(const void *y_sorted, const int32_t *row_sorted,
+                                const void *weights, int32_t weights_dtype, int64_t n, int32_t k,
+                                int32_t H, int32_t dtype, void *out, moe_stream stream) {
+  moe_status st = check_rows(n, k, H, dtype);
+  if (st != MOE_OK) return st;
+  if (weights_dtype != MOE_BF16 && weights_dtype != MOE_FP32) return MOE_ERR_INVALID_ARG;
+  if (n == 0) return MOE_OK;
+  if (!y_sorted || !row_sorted || !weights || !out) return MOE_ERR_INVALID_ARG;
+  const size_t a = elem_align(dtype);
+  if (!aligned(y_sorted, a) || !aligned(out, a) || !aligned(row_sorted, 4) ||
+      !aligned(weights, elem_align(weights_dtype)))
+    return MOE_ERR_MISALIGNED;
+  return from_cuda(launch_combine_weighted(y_sorted, row_sorted, weights, weights_dtype, n, k, H,
+                                           dtype, out, (cudaStream_t)stream));
+}
+
+moe_status moe_combine_weighted_backward(const void *d_out, const void *y_sorted,
+                                         const int32_t *row_sorted, const void *weights,
+                                         int32_t weights_dtype, const int32_t *n_kept, int64_t n,
+                                         int32_t k, int32_t H, int32_t dtype, void *d_sorted,
+                                         float *d_weights, moe_stream stream) {
+  moe_status st = check_rows(n, k, H, dtype);
+  if (st != MOE_OK) return st;
+  if (weights_dtype != MOE_BF16 && weights_dtype != MOE_FP32) return MOE_ERR_INVALID_ARG;
+  if (n == 0) return MOE_OK;
+  if (!d_out || !y_sorted || !row_sorted || !weights || !d_sorted || !d_weights)
+    return MOE_ERR_INVALID_ARG;
+  const size_t a = elem_align(dtype);
+  if (!aligned(d_out, a) || !aligned(y_sorted, a) || !aligned(d_sorted, a) ||
+      !aligned(row_sorted, 4) || !aligned(n_kept, 4) || !aligned(d_weights, 4) ||
+      !aligned(weights, elem_align(weights_dtype)))
+    return MOE_ERR_MISALIGNED;
+  return from_cuda(launch_combine_backward(d_out, y_sorted, row_sorted, weights, weights_dtype,
+                                           n_kept, n, k, H, dtype, d_sorted, d_weights,
+                                           (cudaStream_t)stream));
+}
+
+moe_status moe_route_backward(const float *logits, const int32_t *topk_indx, const float *d_vals,
+                              int64_t n, int32_t E, int32_t k, int32_t gating, float *d_logits,
+                              moe_stream stream) {
+  moe_status st = check_sizes(n, E, k, 64, 64, false);
+  if (st != MOE_OK) return st;
+  if (gating != MOE_GATING_SOFTMAX_TOPK && gating != MOE_GATING_SOFTMAX_ALL)
+    return MOE_ERR_INVALID_ARG;
+  if (n == 0) return MOE_OK;
+  if (!logits || !topk_indx || !d_vals || !d_logits) return MOE_ERR_INVALID_ARG;
+  if (!aligned(logits, 4) || !aligned(topk_indx, 4) || !aligned(d_vals, 4) ||
+      !aligned(d_logits, 4))
+    return MOE_ERR_MISALIGNED;
+  return from_cuda(launch_route_backward(logits, topk_indx, d_vals, n, E, k, gating, d_logits,
+                                         (cudaStream_t)stream));
 }
 
 moe_status moe_read_status(void *workspace, size_t workspace_bytes, int32_t reset,
