@@ -21,6 +21,8 @@
  * the rows' way to expert-sorted order and back for experts of the caller's
  * own, with gradients (moe_dispatch, moe_dispatch_backward,
  * moe_combine_weighted, moe_combine_weighted_backward, moe_route_backward),
+ * products with 4-bit weights for decode (moe_linear_q4, moe_grouped_ffn_q4,
+ * the layer moe_forward_q4, moe_q4_workspace_size),
  * the workspace calls (moe_workspace_size, moe_workspace_init,
  * moe_workspace_regions), moe_read_status and moe_selftest_wait_timeout.
  *
@@ -428,6 +430,72 @@ moe_status moe_combine_weighted_backward(const void *d_out, const void *y_sorted
 moe_status moe_route_backward(const float *logits, const int32_t *topk_indx, const float *d_vals,
                               int64_t n, int32_t E, int32_t k, int32_t gating, float *d_logits,
                               moe_stream stream);
+
+/* ---- Products with 4-bit weights ----------------------------------------
+ * For decode: a handful of token rows against weights that are read once per
+ * step. Weights are E2M1 values (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives; code = sign * 8 + index), two codes per byte with the even
+ * column in the low half, one scale per group of columns of a row:
+ *   MOE_Q4_MXFP4  groups of 32, scale byte s = 2^(s - 127) (E8M0; 255 = NaN);
+ *                 the layout of gpt-oss checkpoints. Scales above 2^96 may
+ *                 overflow the fp32 sums where the result would not
+ *   MOE_Q4_NVFP4  groups of 16, scale byte an E4M3 value, times the matrix's
+ *                 matrix_scale ([R3] title: NVFP4 MoE weights)
+ * A matrix of R rows and C columns (C a multiple of 32): codes [R, C/2] and
+ * scales [R, C/group] bytes, row-major; E matrices follow one another. The
+ * products are exact in the weights, summed in fp32; activations enter as
+ * fp16 scaled by a power of two per row (what lies below 2^-28 of a row's
+ * largest magnitude loses bits, below 2^-39 it vanishes). Right for any number
+ * of rows; made for up to about 16 per matrix. */
+typedef enum {
+  MOE_Q4_MXFP4 = 0,
+  MOE_Q4_NVFP4 = 1
+} moe_q4_format;
+
+typedef struct {
+  const uint8_t *codes;       /* device, 16-byte aligned */
+  const uint8_t *scales;      /* device, 2-byte aligned */
+  const float *matrix_scale;  /* device [E] fp32, 4-byte aligned; NULL = 1 */
+  int32_t format;             /* moe_q4_format */
+} moe_q4_matrix;
+
+/* y[t, r] = sum_c W[r, c] * x[t, c]: x [n, C] and y [n, R] of `dtype`
+ * (MOE_BF16 or MOE_FP16), x 16-byte aligned, any R >= 1, one matrix. No
+ * workspace. */
+moe_status moe_linear_q4(const void *x, const moe_q4_matrix *w, int64_t n, int32_t R, int32_t C,
+                         int32_t dtype, void *y, moe_stream stream);
+
+/* Bytes of workspace for moe_grouped_ffn_q4 and moe_forward_q4 (prepared by
+ * moe_workspace_init): routing results, the fp32 intermediate h [n*k, I],
+ * the experts' outputs. 0 for invalid sizes. */
+size_t moe_q4_workspace_size(int64_t n, int32_t E, int32_t k, int32_t H, int32_t I);
+
+/* The experts of a decode step with 4-bit weights: for every kept slot, at
+ * its sorted position p (expert e, token t),
+ *   y_sorted[p] = w2_e . act(w13_e . x_t)
+ * x [n, H] of dtype (MOE_BF16 or MOE_FP16), w13 E matrices of 2I rows in
+ * params->w13_layout order (I rows for MOE_ACT_RELU2) and H columns, w2 E
+ * matrices of H rows and I columns, meta's offs and col_sorted read. y_sorted
+ * [n*k, H] of dtype; rows past the kept slots are zero. No gate weight is
+ * applied (moe_combine_weighted does). E may be less than k: a rank that
+ * holds few of the experts. h stays fp32 up to the second product,
+ * which takes it as scaled fp16. params: activation, layout and the values of
+ * `set`; gating, ffn_kernel and expert_map are not used. */
+moe_status moe_grouped_ffn_q4(const void *x, const moe_routing_meta *meta,
+                              const moe_q4_matrix *w13, const moe_q4_matrix *w2, int64_t n,
+                              int32_t E, int32_t k, int32_t H, int32_t I,
+                              const moe_params *params, int32_t dtype, void *y_sorted,
+                              void *workspace, size_t workspace_bytes, moe_stream stream);
+
+/* The layer with 4-bit experts: moe_route_metadata, moe_grouped_ffn_q4,
+ * moe_combine_weighted, with the optional outputs and the expert map of
+ * moe_forward (w13 / w2 then hold the local experts). 4 launches while the
+ * routing is one kernel. */
+moe_status moe_forward_q4(const void *x, const float *logits, const moe_q4_matrix *w13,
+                          const moe_q4_matrix *w2, int64_t n, int32_t E, int32_t k, int32_t H,
+                          int32_t I, const moe_params *params, int32_t dtype, void *out,
+                          int32_t *topk_indx, uint16_t *topk_vals, const moe_routing_meta *meta,
+                          void *workspace, size_t workspace_bytes, moe_stream stream);
 
 /* Stage kernels of moe_forward, in launch order (indices of the events of
  * moe_forward_timed). */

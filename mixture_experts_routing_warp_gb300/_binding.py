@@ -22,6 +22,8 @@ ACT = {"swiglu": 0, "swiglu_oai": 1, "relu2": 2}
 LAYOUT = {"packed": 0, "interleaved": 1}
 SET_ALPHA, SET_BETA, SET_LIMIT = 1, 2, 4
 FFN_KERNEL = {"auto": 0, "tiled": 1, "swap": 2}
+Q4_FORMAT = {"mxfp4": 0, "nvfp4": 1}
+Q4_GROUP = {"mxfp4": 32, "nvfp4": 16}
 DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 ABI_VERSION = 4
 
@@ -50,6 +52,11 @@ class RoutingMeta(ctypes.Structure):
                 ("gate_scal", ctypes.c_void_p)]
 
 
+class Q4Matrix(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("matrix_scale", ctypes.c_void_p), ("format", ctypes.c_int32)]
+
+
 _LIB = None
 
 # name -> (restype, argtypes)
@@ -57,6 +64,7 @@ _P, _I64, _I32, _SZ, _U64 = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ct
                              ctypes.c_uint64)
 _PP = ctypes.POINTER(MoeParams)
 _PM = ctypes.POINTER(RoutingMeta)
+_PQ = ctypes.POINTER(Q4Matrix)
 SIGNATURES = {
     "moe_abi_version": (_I32, []),
     "moe_status_string": (ctypes.c_char_p, [_I32]),
@@ -85,6 +93,12 @@ SIGNATURES = {
     "moe_combine_weighted_backward": (_I32, [_P, _P, _P, _P, _I32, _P, _I64, _I32, _I32, _I32, _P,
                                              _P, _P]),
     "moe_route_backward": (_I32, [_P, _P, _P, _I64, _I32, _I32, _I32, _P, _P]),
+    "moe_linear_q4": (_I32, [_P, _PQ, _I64, _I32, _I32, _I32, _P, _P]),
+    "moe_q4_workspace_size": (_SZ, [_I64, _I32, _I32, _I32, _I32]),
+    "moe_grouped_ffn_q4": (_I32, [_P, _PM, _PQ, _PQ, _I64, _I32, _I32, _I32, _I32, _PP, _I32, _P,
+                                  _P, _SZ, _P]),
+    "moe_forward_q4": (_I32, [_P, _P, _PQ, _PQ, _I64, _I32, _I32, _I32, _I32, _PP, _I32, _P, _P,
+                              _P, _PM, _P, _SZ, _P]),
     "moe_read_status": (_I32, [_P, _SZ, _I32, _P]),
     "moe_selftest_wait_timeout": (_I32, [_P, _SZ, _U64, _P]),
 }
@@ -512,6 +526,147 @@ def route_backward(logits: torch.Tensor, topk_indx: torch.Tensor, d_vals: torch.
                                         GATING[gating], _ptr(d_logits), _stream(logits.device)),
                "moe_route_backward")
     return d_logits
+
+
+class Q4Weight:
+    """4-bit weights as a checkpoint holds them: codes uint8 [R, C/2] (two E2M1
+    codes per byte, the even column low) or [E, R, C/2], scales uint8
+    [..., R, C/32] ("mxfp4": E8M0) or [..., R, C/16] ("nvfp4": E4M3, times
+    matrix_scale fp32 [E] or [1]). The tensors are used where they lie; the
+    handle keeps them alive."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, fmt: str,
+                 matrix_scale: Optional[torch.Tensor] = None):
+        if fmt not in Q4_FORMAT:
+            raise ValueError(f"fmt must be one of {sorted(Q4_FORMAT)}, got {fmt!r}")
+        _need(codes, "codes", torch.uint8)
+        if codes.dim() not in (2, 3) or codes.shape[-1] == 0 or codes.shape[-1] % 16:
+            raise ValueError("codes must have shape [R, C/2] or [E, R, C/2], C a multiple of 32")
+        self.rows, self.cols = codes.shape[-2], 2 * codes.shape[-1]
+        self.count = codes.shape[0] if codes.dim() == 3 else 1
+        _need(scales, "scales", torch.uint8,
+              (*codes.shape[:-1], self.cols // Q4_GROUP[fmt]))
+        _same_device(scales, "scales", codes)
+        if matrix_scale is not None:
+            _need(matrix_scale, "matrix_scale", torch.float32, (self.count,))
+            _same_device(matrix_scale, "matrix_scale", codes)
+        self.codes, self.scales, self.matrix_scale, self.fmt = codes, scales, matrix_scale, fmt
+        self._as_parameter_ = ctypes.byref(Q4Matrix(
+            codes.data_ptr(), scales.data_ptr(),
+            None if matrix_scale is None else matrix_scale.data_ptr(), Q4_FORMAT[fmt]))
+
+
+def _need_q4(w: Q4Weight, name: str, x: torch.Tensor) -> None:
+    if not isinstance(w, Q4Weight):
+        raise ValueError(f"{name} must be a Q4Weight")
+    _same_device(w.codes, name, x)
+
+
+def _need_q4_x(x: torch.Tensor, name: str = "x") -> None:
+    _need_rows(x, name)
+    if x.dtype == torch.float32:
+        raise ValueError(f"{name} must be bfloat16 or float16")
+
+
+def linear_q4(x: torch.Tensor, w: Q4Weight, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """x [n, C] (bf16 or fp16) times one 4-bit matrix [R, C] -> [n, R]."""
+    _need_q4_x(x)
+    _need_q4(w, "w", x)
+    n, C = x.shape
+    if w.count != 1 or w.cols != C:
+        raise ValueError(f"w must be one matrix of {C} columns, got {tuple(w.codes.shape)} codes")
+    out = _out_rows(out, "out", (n, w.rows), x)
+    with torch.cuda.device(x.device):
+        _check(lib().moe_linear_q4(_ptr(x), w, n, w.rows, C, DTYPE[x.dtype], _ptr(out),
+                                   _stream(x.device)), "moe_linear_q4")
+    return out
+
+
+def workspace_q4_size(n: int, E: int, k: int, H: int, I: int) -> int:
+    return int(lib().moe_q4_workspace_size(n, E, k, H, I))
+
+
+def workspace_q4(n: int, E: int, k: int, H: int, I: int,
+                 device: Optional[torch.device] = None) -> torch.Tensor:
+    """Allocate and initialise a workspace for grouped_ffn_q4 and forward_q4."""
+    size = workspace_q4_size(n, E, k, H, I)
+    if size == 0:
+        raise ValueError("invalid sizes for moe_q4_workspace_size")
+    ws = torch.empty(size, dtype=torch.uint8,
+                     device=torch.device("cuda") if device is None else torch.device(device))
+    with torch.cuda.device(ws.device):
+        _check(lib().moe_workspace_init(_ptr(ws), size, _stream(ws.device)), "moe_workspace_init")
+    return ws
+
+
+def _q4_experts(w13: Q4Weight, w2: Q4Weight, E: int, H: int, x: torch.Tensor,
+                params: MoeParams) -> int:
+    """Checks the experts' matrices against each other; returns I."""
+    _need_q4(w13, "w13", x)
+    _need_q4(w2, "w2", x)
+    I = w2.cols
+    rows = I if params.activation == ACT["relu2"] else 2 * I
+    if (w13.count, w13.rows, w13.cols) != (E, rows, H):
+        raise ValueError(f"w13 must be {E} matrices of {rows} x {H}, got "
+                         f"{(w13.count, w13.rows, w13.cols)}")
+    if (w2.count, w2.rows) != (E, H):
+        raise ValueError(f"w2 must be {E} matrices of {H} rows, got {(w2.count, w2.rows)}")
+    return I
+
+
+def grouped_ffn_q4(x: torch.Tensor, meta: dict, w13: Q4Weight, w2: Q4Weight, k: int,
+                   ws: torch.Tensor, params: MoeParams,
+                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The experts of a decode step with 4-bit weights: x [n, H] (bf16 or
+    fp16) -> their outputs in expert-sorted order [n*k, H], without gate
+    weights (combine_weighted applies them); rows past the kept slots are
+    zero. `ws` from workspace_q4."""
+    _need_q4_x(x)
+    n, H = x.shape
+    E = w13.count if isinstance(w13, Q4Weight) else 0
+    I = _q4_experts(w13, w2, E, H, x, params)
+    _need(meta["offs"], "offs", torch.int32, (E + 1,))
+    _need(meta["col_sorted"], "col_sorted", torch.int32, (n * k,))
+    for name in ("offs", "col_sorted"):
+        _same_device(meta[name], name, x)
+    _need(ws, "ws", torch.uint8)
+    _same_device(ws, "ws", x)
+    out = _out_rows(out, "out", (n * k, H), x)
+    m = RoutingMeta(None, meta["offs"].data_ptr(), meta["col_sorted"].data_ptr(), None, None)
+    with torch.cuda.device(x.device):
+        _check(lib().moe_grouped_ffn_q4(_ptr(x), ctypes.byref(m), w13, w2, n, E, k, H, I,
+                                        ctypes.byref(params), DTYPE[x.dtype], _ptr(out),
+                                        _ptr(ws), ws.numel(), _stream(x.device)),
+               "moe_grouped_ffn_q4")
+    return out
+
+
+def forward_q4(x: torch.Tensor, logits: torch.Tensor, w13: Q4Weight, w2: Q4Weight, k: int,
+               params: MoeParams, ws: torch.Tensor, out: Optional[torch.Tensor] = None,
+               topk: Optional[tuple] = None, meta: Optional[dict] = None) -> torch.Tensor:
+    """forward() with 4-bit experts: route_metadata, grouped_ffn_q4 and
+    combine_weighted in one library call. x and out bf16 or fp16, `ws` from
+    workspace_q4."""
+    _need_q4_x(x)
+    n, H = x.shape
+    _need(logits, "logits", torch.float32)
+    if logits.dim() != 2 or logits.shape[0] != n:
+        raise ValueError(f"logits must have shape [{n}, E], got {tuple(logits.shape)}")
+    _same_device(logits, "logits", x)
+    E = logits.shape[1]
+    E_w = params.n_local_experts if params.expert_map else E  # experts held in w13 / w2
+    I = _q4_experts(w13, w2, E_w, H, x, params)
+    _need(ws, "ws", torch.uint8)
+    _same_device(ws, "ws", x)
+    out = _out_rows(out, "out", (n, H), x)
+    indx, vals = topk if topk is not None else (None, None)
+    mstruct = ctypes.byref(_meta_struct(meta)) if meta is not None else None
+    with torch.cuda.device(x.device):
+        _check(lib().moe_forward_q4(_ptr(x), _ptr(logits), w13, w2, n, E, k, H, I,
+                                    ctypes.byref(params), DTYPE[x.dtype], _ptr(out), _ptr(indx),
+                                    _ptr(vals), mstruct, _ptr(ws), ws.numel(),
+                                    _stream(x.device)), "moe_forward_q4")
+    return out
 
 
 STAGES = ("route", "metadata", "gather", "ffn1", "ffn2", "combine")

@@ -104,6 +104,41 @@ moe_status check_rows(int64_t n, int k, int H, int dtype) {
   return MOE_OK;
 }
 
+// What moe_forward_q4 keeps: the routing part of the layer's workspace (up to
+// its sync words), then h and the sorted outputs.
+struct Q4Layout {
+  WorkspaceLayout L;
+  size_t h, y, total;
+};
+Q4Layout q4_layout(int64_t n, int E, int k, int H, int I) {
+  Q4Layout q;
+  q.L = workspace_layout(n, E, k, H, I);
+  const size_t N = (size_t)n * (size_t)k;
+  q.h = q.L.sync;
+  q.y = align_up(q.h + N * (size_t)I * 4, kAlign);
+  q.total = align_up(q.y + N * (size_t)H * 2, kAlign);
+  return q;
+}
+
+// Sizes of the 4-bit experts: the layer's, but a rank may hold fewer experts
+// than a token selects (k > E).
+moe_status check_q4_sizes(int64_t n, int E, int k, int H, int I) {
+  if (E < 1 || E > kMaxExperts) return MOE_ERR_INVALID_ARG;
+  return check_sizes(n, kMaxExperts, k, H, I, true);
+}
+
+moe_status check_q4(const moe_q4_matrix *w) {
+  if (!w || !w->codes || !w->scales) return MOE_ERR_INVALID_ARG;
+  if (w->format != MOE_Q4_MXFP4 && w->format != MOE_Q4_NVFP4) return MOE_ERR_INVALID_ARG;
+  if (!aligned(w->codes, 16) || !aligned(w->scales, 2) || !aligned(w->matrix_scale, 4))
+    return MOE_ERR_MISALIGNED;
+  return MOE_OK;
+}
+
+moe_status check_q4_dtype(int dtype) {
+  return dtype == MOE_BF16 || dtype == MOE_FP16 ? MOE_OK : MOE_ERR_INVALID_ARG;
+}
+
 inline size_t elem_align(int dtype) { return dtype == MOE_FP32 ? 4 : 2; }
 
 }  // namespace
@@ -529,6 +564,102 @@ moe_status moe_route_backward(const float *logits, const int32_t *topk_indx, con
     return MOE_ERR_MISALIGNED;
   return from_cuda(launch_route_backward(logits, topk_indx, d_vals, n, E, k, gating, d_logits,
                                          (cudaStream_t)stream));
+}
+
+moe_status moe_linear_q4(const void *x, const moe_q4_matrix *w, int64_t n, int32_t R, int32_t C,
+                         int32_t dtype, void *y, moe_stream stream) {
+  if (n < 0 || n >= (int64_t)INT32_MAX || R < 1 || R > (1 << 30) || C < 32 || C % 32 != 0 ||
+      C > (1 << 24))
+    return MOE_ERR_INVALID_ARG;
+  moe_status st = check_q4_dtype(dtype);
+  if (st != MOE_OK) return st;
+  if ((st = check_q4(w)) != MOE_OK) return st;
+  if (n == 0) return MOE_OK;
+  if (!x || !y) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(y, 2)) return MOE_ERR_MISALIGNED;
+  return from_cuda(launch_linear_q4(x, *w, n, R, C, dtype, y, (cudaStream_t)stream));
+}
+
+size_t moe_q4_workspace_size(int64_t n, int32_t E, int32_t k, int32_t H, int32_t I) {
+  if (check_q4_sizes(n, E, k, H, I) != MOE_OK) return 0;
+  return q4_layout(n, E, k, H, I).total;
+}
+
+moe_status moe_grouped_ffn_q4(const void *x, const moe_routing_meta *meta,
+                              const moe_q4_matrix *w13, const moe_q4_matrix *w2, int64_t n,
+                              int32_t E, int32_t k, int32_t H, int32_t I,
+                              const moe_params *params, int32_t dtype, void *y_sorted,
+                              void *workspace, size_t workspace_bytes, moe_stream stream) {
+  moe_status st = check_q4_sizes(n, E, k, H, I);
+  if (st != MOE_OK) return st;
+  ActParams act;
+  if ((st = resolve_params(params, act, nullptr)) != MOE_OK) return st;
+  if ((st = check_q4_dtype(dtype)) != MOE_OK) return st;
+  if ((st = check_q4(w13)) != MOE_OK || (st = check_q4(w2)) != MOE_OK) return st;
+  if (!meta || !meta->offs || (n > 0 && !meta->col_sorted)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(meta->offs, 4) || !aligned(meta->col_sorted, 4)) return MOE_ERR_MISALIGNED;
+  if (n == 0) return MOE_OK;
+  if (!x || !y_sorted || !workspace) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(y_sorted, 16) || !aligned(workspace, kAlign))
+    return MOE_ERR_MISALIGNED;
+  const Q4Layout q = q4_layout(n, E, k, H, I);
+  if (workspace_bytes < q.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  return from_cuda(launch_ffn_q4(x, *meta, *w13, *w2, n * k, E, k, H, I, act, dtype,
+                                 ws_at<float>(workspace, q.h), y_sorted, (cudaStream_t)stream));
+}
+
+moe_status moe_forward_q4(const void *x, const float *logits, const moe_q4_matrix *w13,
+                          const moe_q4_matrix *w2, int64_t n, int32_t E, int32_t k, int32_t H,
+                          int32_t I, const moe_params *params, int32_t dtype, void *out,
+                          int32_t *topk_indx, uint16_t *topk_vals, const moe_routing_meta *meta,
+                          void *workspace, size_t workspace_bytes, moe_stream stream) {
+  moe_status st = check_sizes(n, E, k, H, I, true);
+  if (st != MOE_OK) return st;
+  ActParams act;
+  int gating = 0;
+  if ((st = resolve_params(params, act, &gating)) != MOE_OK) return st;
+  if ((st = check_q4_dtype(dtype)) != MOE_OK) return st;
+  if ((st = check_q4(w13)) != MOE_OK || (st = check_q4(w2)) != MOE_OK) return st;
+  if (meta && (st = check_meta(meta, n)) != MOE_OK) return st;
+  if ((topk_indx == nullptr) != (topk_vals == nullptr)) return MOE_ERR_INVALID_ARG;
+  const int32_t *emap = params->expert_map;
+  const int32_t E_loc = emap ? params->n_local_experts : E;
+  if (E_loc < 1 || E_loc > E) return MOE_ERR_INVALID_ARG;
+  if (!aligned(emap, 4)) return MOE_ERR_MISALIGNED;
+  if (n == 0) return MOE_OK;
+  if (!x || !logits || !out || !workspace) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(out, 16) || !aligned(logits, 4) ||
+      !aligned(workspace, kAlign) || !aligned(topk_indx, 4) || !aligned(topk_vals, 2))
+    return MOE_ERR_MISALIGNED;
+  const Q4Layout q = q4_layout(n, E, k, H, I);
+  if (workspace_bytes < q.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const WorkspaceLayout &L = q.L;
+  cudaStream_t s = (cudaStream_t)stream;
+  int32_t *indx = topk_indx ? topk_indx : ws_at<int32_t>(workspace, L.topk_indx);
+  uint16_t *vals = topk_vals ? topk_vals : ws_at<uint16_t>(workspace, L.topk_vals);
+  const moe_routing_meta m =
+      meta ? *meta
+           : moe_routing_meta{ws_at<int32_t>(workspace, L.col_sum),
+                              ws_at<int32_t>(workspace, L.offs),
+                              ws_at<int32_t>(workspace, L.col_sorted),
+                              ws_at<int32_t>(workspace, L.row_sorted),
+                              ws_at<uint16_t>(workspace, L.gate_scal)};
+  uint32_t *ctrl = ws_at<uint32_t>(workspace, L.ctrl);
+  if (route_metadata_fits(n, k)) {
+    if (launch_route_metadata(logits, n, E, k, gating, indx, vals, m, ctrl, s, nullptr, emap,
+                              E_loc) != cudaSuccess)
+      return MOE_ERR_CUDA;
+  } else if (launch_route(logits, n, E, k, gating, indx, vals, ctrl, s) != cudaSuccess ||
+             launch_metadata(indx, vals, n, E, k, m, ws_at<int32_t>(workspace, L.hist), ctrl, s,
+                             nullptr, emap, E_loc) != cudaSuccess) {
+    return MOE_ERR_CUDA;
+  }
+  void *y = ws_at<uint16_t>(workspace, q.y);
+  if (launch_ffn_q4(x, m, *w13, *w2, n * k, E_loc, k, H, I, act, dtype,
+                    ws_at<float>(workspace, q.h), y, s) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  return from_cuda(
+      launch_combine_weighted(y, m.row_sorted, vals, MOE_BF16, n, k, H, dtype, out, s));
 }
 
 moe_status moe_read_status(void *workspace, size_t workspace_bytes, int32_t reset,

@@ -554,6 +554,14 @@ cudaError_t launch_route_backward(const float *logits, const int32_t *topk_indx,
                                   const float *d_vals, int64_t n, int E, int k, int gating,
                                   float *d_logits, cudaStream_t s);
 
+// Products with 4-bit weights (q4_matvec.cu). h: fp32 [N, I] scratch.
+cudaError_t launch_linear_q4(const void *x, const moe_q4_matrix &w, int64_t n, int R, int C,
+                             int dtype, void *y, cudaStream_t s);
+cudaError_t launch_ffn_q4(const void *x, const moe_routing_meta &m, const moe_q4_matrix &w13,
+                          const moe_q4_matrix &w2, int64_t N, int E, int k, int H, int I,
+                          const ActParams &act, int dtype, float *h, void *y_sorted,
+                          cudaStream_t s);
+
 cudaError_t launch_wait_selftest(uint32_t *ctrl, unsigned long long timeout_ns, cudaStream_t s);
 
 }  // namespace moe
