@@ -454,7 +454,7 @@ typedef enum {
 
 typedef struct {
   const uint8_t *codes;       /* device, 16-byte aligned */
-  const uint8_t *scales;      /* device, 2-byte aligned */
+  const uint8_t *scales;      /* device, 4-byte aligned */
   const float *matrix_scale;  /* device [E] fp32, 4-byte aligned; NULL = 1 */
   int32_t format;             /* moe_q4_format */
 } moe_q4_matrix;

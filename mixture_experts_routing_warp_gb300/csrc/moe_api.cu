@@ -130,7 +130,7 @@ moe_status check_q4_sizes(int64_t n, int E, int k, int H, int I) {
 moe_status check_q4(const moe_q4_matrix *w) {
   if (!w || !w->codes || !w->scales) return MOE_ERR_INVALID_ARG;
   if (w->format != MOE_Q4_MXFP4 && w->format != MOE_Q4_NVFP4) return MOE_ERR_INVALID_ARG;
-  if (!aligned(w->codes, 16) || !aligned(w->scales, 2) || !aligned(w->matrix_scale, 4))
+  if (!aligned(w->codes, 16) || !aligned(w->scales, 4) || !aligned(w->matrix_scale, 4))
     return MOE_ERR_MISALIGNED;
   return MOE_OK;
 }
@@ -605,7 +605,8 @@ moe_status moe_grouped_ffn_q4(const void *x, const moe_routing_meta *meta,
   const Q4Layout q = q4_layout(n, E, k, H, I);
   if (workspace_bytes < q.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
   return from_cuda(launch_ffn_q4(x, *meta, *w13, *w2, n * k, E, k, H, I, act, dtype,
-                                 ws_at<float>(workspace, q.h), y_sorted, (cudaStream_t)stream));
+                                 ws_at<float>(workspace, q.h), y_sorted,
+                                 ws_at<uint32_t>(workspace, q.L.ctrl), (cudaStream_t)stream));
 }
 
 moe_status moe_forward_q4(const void *x, const float *logits, const moe_q4_matrix *w13,
@@ -656,7 +657,7 @@ moe_status moe_forward_q4(const void *x, const float *logits, const moe_q4_matri
   }
   void *y = ws_at<uint16_t>(workspace, q.y);
   if (launch_ffn_q4(x, m, *w13, *w2, n * k, E_loc, k, H, I, act, dtype,
-                    ws_at<float>(workspace, q.h), y, s) != cudaSuccess)
+                    ws_at<float>(workspace, q.h), y, ctrl, s) != cudaSuccess)
     return MOE_ERR_CUDA;
   return from_cuda(
       launch_combine_weighted(y, m.row_sorted, vals, MOE_BF16, n, k, H, dtype, out, s));

@@ -560,7 +560,7 @@ cudaError_t launch_linear_q4(const void *x, const moe_q4_matrix &w, int64_t n, i
 cudaError_t launch_ffn_q4(const void *x, const moe_routing_meta &m, const moe_q4_matrix &w13,
                           const moe_q4_matrix &w2, int64_t N, int E, int k, int H, int I,
                           const ActParams &act, int dtype, float *h, void *y_sorted,
-                          cudaStream_t s);
+                          uint32_t *ctrl, cudaStream_t s);
 
 cudaError_t launch_wait_selftest(uint32_t *ctrl, unsigned long long timeout_ns, cudaStream_t s);
 

@@ -27,9 +27,9 @@
 //    fp16's 11) significant bits stay exact down to 2^-28 of the row's
 //    maximum (fp32 h: 11 bits, half an fp16 step), values below 2^-39 of it
 //    vanish. The sum is scaled back in fp32.
-#include "moe_internal.cuh"
-
 #include <cuda_fp16.h>
+
+#include "tc_ptx.cuh"
 
 namespace moe {
 namespace {
@@ -37,9 +37,15 @@ namespace {
 constexpr int kQ4Threads = 512;  // one CTA per SM
 constexpr int kQ4Warps = kQ4Threads / 32;
 constexpr int kSlab = 128;         // columns per warp step: 32 per lane of a quad
-constexpr int kRing = 4;           // steps of weights in flight per warp
 constexpr int kSlabXBytes = 2048;  // fp16 fragments of 8 tokens x 128 columns
-constexpr int kMaxSlabsX = 96;     // slabs x 8-token blocks of activations resident at once
+constexpr int kSmemMax = 226 * 1024;  // dynamic and static shared memory of a CTA
+
+// Shared memory of one step: the lanes' codes of two rows each, 16 bytes a
+// lane and row, then the 16 rows' scales as whole 4-byte words.
+__host__ __device__ constexpr int scale_words(int fmt) { return fmt == MOE_Q4_MXFP4 ? 2 : 3; }
+__host__ __device__ constexpr int step_bytes(int fmt) { return 1024 + 64 * scale_words(fmt); }
+// Units whose partial sums may be on their way to the warps that join them.
+__host__ __device__ constexpr int red_slots(int nb) { return nb == 1 ? 3 : 2; }
 
 // Which row of x a slot reads, and where its result goes.
 enum Q4Mode {
@@ -62,6 +68,8 @@ struct Q4Args {
   int act;                    // Q4_W13: moe_activation, layout in `ap`
   int slabs;                  // slabs of a row
   int chunk, chunks;          // slabs whose activations are resident at once; how many such
+  int64_t scale_bytes;        // of all matrices
+  uint32_t *ctrl;             // control block for the status of the bounded waits, or null
   ActParams ap;
 };
 
@@ -97,13 +105,32 @@ __device__ __forceinline__ void mma16816(float *d, const uint32_t *a, uint32_t b
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Weights are read once: keep them out of L1.
-__device__ __forceinline__ uint4 ld_stream(const void *p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+// Asynchronous copies to shared memory of which `bytes` are read and the rest
+// filled with zeros; one group per warp step.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Wait for a phase of an mbarrier, at most kWaitTimeoutNs; a wait that gives
+// up is recorded and the kernel goes on to its end (its result is void).
+__device__ __forceinline__ void wait_phase(uint32_t bar, uint32_t parity, uint32_t *ctrl) {
+  if (tc::mbar_try_wait(bar, parity)) return;
+  const long long deadline = wait_deadline(kWaitTimeoutNs);
+  while (!tc::mbar_try_wait(bar, parity))
+    if (clock64() > deadline) {
+      record_status(ctrl, MOE_ERR_TIMEOUT);
+      return;
+    }
 }
 
 // Eight consecutive activations (16-byte aligned) as floats.
@@ -136,38 +163,42 @@ __device__ __forceinline__ float exp2i(int e) {
   return e == -127 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-// A unit: a group of row tiles of one expert against one block of its tokens.
-struct Q4Unit {
-  int e, tb, tg;  // expert, token block, tile group
-};
-
 template <int NB>
 struct Q4Shared {
-  alignas(16) float red[2][kQ4Warps][NB][32][4];  // partial sums, read and written as float4
+  unsigned long long full[red_slots(NB)], empty[red_slots(NB)];  // mbarriers
+  int4 info[red_slots(NB)];  // unit in a slot: expert, first token slot, tokens, tile group
+  int part[red_slots(NB)];   // and its part of amax
   int cnt[kMaxExperts + 1];  // first slot of each expert (offs)
   int blk[kMaxExperts + 1];  // exclusive prefix of the experts' token blocks
   int warp_sum[kQ4Warps];
   int row[8 * NB];           // the block's rows of x
-  uint32_t amax[8 * NB];     // largest magnitude of each (bits)
-  float inv[8 * NB];         // what undoes their scaling
+  uint32_t amax[4][8 * NB];  // largest magnitude of each token's row (bits), by block
 };
 
-// A warp step's share of a lane: 32 codes of two rows and their scales.
-struct Q4Step {
-  uint4 w0, w1;
-  uint32_t s0, s1;
-};
+// Scale exponent of a row: its largest magnitude comes into [2^14, 2^15); a
+// row of zeros, or one that is not finite, keeps its values.
+__device__ __forceinline__ int row_exponent(uint32_t amax) {
+  const int ex = (int)(amax >> 23);
+  return amax == 0u || ex == 255 ? 0 : min(14 + 127 - ex, 126);
+}
 
-// FMT: moe_q4_format; NB: blocks of 8 tokens per unit.
-template <int FMT, int NB>
+// FMT: moe_q4_format; NB: blocks of 8 tokens per unit; RING: steps of weights
+// in flight per warp, in shared memory.
+template <int FMT, int NB, int RING>
 __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
   constexpr int TB = 8 * NB;                        // tokens per unit
   constexpr int G = FMT == MOE_Q4_MXFP4 ? 32 : 16;  // columns per scale
-  extern __shared__ __align__(16) unsigned char smem_x[];
+  constexpr int SW = scale_words(FMT), RS = red_slots(NB), STEP = step_bytes(FMT);
+  extern __shared__ __align__(16) unsigned char smem[];
   __shared__ Q4Shared<NB> sh;
   const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
+  float4 *red = reinterpret_cast<float4 *>(smem);  // [RS][kQ4Warps][NB][32]
+  unsigned char *ring = smem + RS * kQ4Warps * NB * 512 + wid * (RING * STEP);
+  uint4 *xs = reinterpret_cast<uint4 *>(smem + RS * kQ4Warps * NB * 512 + kQ4Warps * RING * STEP);
+  const uint32_t full_at = tc::smem_u32(sh.full), empty_at = tc::smem_u32(sh.empty);
 
+  if (tid < 4 * TB) (&sh.amax[0][0])[tid] = 0u;
   // offs may come from the kernel before this one (Q4_W13); before Q4_W2 lies
   // the Q4_W13 launch, which passed its own wait before triggering this one,
   // so what offs holds is complete and the weights can be fetched ahead.
@@ -206,99 +237,135 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
     __syncthreads();
   }
 
-  // Warps along a row (kw): one needs no join, but a unit is then 16 row
-  // tiles, and units are dealt out whole. The fewest that leave a CTA 12
-  // units or more, so that the last round idles little; at most 8, and no
-  // more than the row has slabs.
-  const int blocks = sh.blk[a.E], tiles = (a.R + 15) / 16;
-  int kw = 1, tile_groups = (tiles + kQ4Warps - 1) / kQ4Warps;
-  while (kw < 8 && kw * 2 <= min(a.slabs, a.chunk) &&
-         (int64_t)blocks * tile_groups < 12 * (int64_t)gridDim.x) {
+  // Warps along a row (kw): a unit is kQ4Warps / kw row tiles, dealt out
+  // whole, and costs its warps about two steps besides its own. The fewest
+  // that leave a CTA 8 units or more, so that the last ones idle little; at
+  // most 8, and no more than the row has slabs.
+  const int blocks = sh.blk[a.E], tiles = (a.R + 15) / 16, in_row = min(a.slabs, a.chunk);
+  int kw = 1;
+  while (kw < 8 && kw * 2 <= in_row &&
+         (int64_t)blocks * tiles * kw < 8 * kQ4Warps * (int64_t)gridDim.x)
     kw *= 2;
-    tile_groups = (tiles * kw + kQ4Warps - 1) / kQ4Warps;
+  const int rws = kQ4Warps / kw, kpart = wid & (kw - 1), rw = wid / kw;
+  const int tile_groups = (tiles + rws - 1) / rws;
+  const int items = rws * NB;  // joins per unit
+  if (tid == 0) {
+    for (int i = 0; i < RS; ++i) {
+      tc::mbar_init(full_at + 8 * i, kQ4Warps);
+      tc::mbar_init(empty_at + 8 * i, items);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  const int rws = kQ4Warps / kw, kpart = wid % kw, rw = wid / kw;
-  const int share = (min(a.slabs, a.chunk) + kw - 1) / kw;  // slabs per warp and chunk
-  const int rounds = (share + kRing - 1) / kRing;
 
+  // this CTA's units (a unit stores 128 values or more: the count fits an int)
   const int64_t units = (int64_t)blocks * tile_groups;
   const int64_t first = units * blockIdx.x / gridDim.x;
-  int64_t left = units * (blockIdx.x + 1) / gridDim.x - first;  // units this CTA still has
-
-  Q4Unit cur;
-  {
-    const int b = (int)(first / tile_groups);
-    cur.tg = (int)(first - (int64_t)b * tile_groups);
-    int lo = 0, hi = a.E;  // the last expert whose prefix is <= b: it has a block there
+  const int count = (int)(units * (blockIdx.x + 1) / gridDim.x - first);
+  // unit u of the CTA: token block b, tile group tg; block b is the tb-th of
+  // expert e, the last one whose prefix is <= b
+  int cur_b = (int)(first / tile_groups), cur_tg = (int)(first - (int64_t)cur_b * tile_groups);
+  auto where = [&](int b, int &e, int &tb) {
+    int lo = 0, hi = a.E;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (sh.blk[mid] <= b) lo = mid; else hi = mid;
     }
-    cur.e = lo;
-    cur.tb = b - sh.blk[lo];
-  }
+    e = lo;
+    tb = b - sh.blk[lo];
+  };
+  // this warp's slabs of a chunk: n of them from lo
+  auto slabs_of = [&](int ch, int &lo, int &n) {
+    const int m = min(a.chunk, a.slabs - ch * a.chunk), at = m * kpart / kw;
+    lo = ch * a.chunk + at;
+    n = m * (kpart + 1) / kw - at;
+  };
 
-  // ---- the ring of weights: `rem` columns are left from this lane's next
-  // step on (none when <= 0), its pointers stand there.
+  // ---- weights on their way: step after step, RING steps ahead of the
+  // products, by an iterator over (unit, chunk, slab)
   const bool gated = a.mode == Q4_W13 && a.act != MOE_ACT_RELU2;
-  const uint8_t *pw0, *pw1, *ps0, *ps1;
-  int rem;
-  // the lane's two weight rows of a unit: gate and up of one h column for a
-  // gated w13, rows g and g + 8 of the tile otherwise. Rows past the end read
-  // the last row; their results are dropped.
-  auto point = [&](const Q4Unit &q, int ch) {
-    const int tile = q.tg * rws + rw;
-    int r0, r1;
-    if (!gated) {
-      r0 = tile * 16 + g;
-      r1 = r0 + 8;
-    } else if (a.ap.layout == MOE_W13_INTERLEAVED) {
-      r0 = tile * 16 + 2 * g;
-      r1 = r0 + 1;
-    } else {
-      r0 = tile * 8 + g;
-      r1 = (a.R >> 1) + r0;
-    }
-    const int col = (ch * a.chunk + kpart * share) * kSlab + 32 * c;
-    const int end = min(min((kpart + 1) * share, a.chunk) + ch * a.chunk, a.slabs) * kSlab;
-    rem = min(end, a.C) - col;
-    const int64_t at = (int64_t)q.e * a.R;
-    const int64_t b0 = at + min(r0, a.R - 1), b1 = at + min(r1, a.R - 1);
-    pw0 = a.codes + b0 * (a.C / 2) + col / 2;
-    pw1 = a.codes + b1 * (a.C / 2) + col / 2;
-    ps0 = a.scales + b0 * (a.C / G) + col / G;
-    ps1 = a.scales + b1 * (a.C / G) + col / G;
+  const bool split = gated && a.ap.layout == MOE_W13_PACKED;  // up rows I below the gate rows
+  // Row r (0..15) of a tile. Fragment rows g and g + 8 are gate and up of one
+  // column of h for a gated w13. Rows past the end read the last row; their
+  // results are dropped.
+  auto tile_row = [&](int tile, int r) {
+    const int row = !split ? tile * 16 + r
+                           : tile * 8 + (r & 7) + (r & 8 ? a.R >> 1 : 0);
+    return min(row, a.R - 1);
   };
-  auto fetch = [&](Q4Step &st, int d) {
-    if (rem > d * kSlab) {
-      st.w0 = ld_stream(pw0 + d * (kSlab / 2));
-      st.w1 = ld_stream(pw1 + d * (kSlab / 2));
-      if (FMT == MOE_Q4_MXFP4) {
-        st.s0 = __ldg(ps0 + d * (kSlab / G));
-        st.s1 = __ldg(ps1 + d * (kSlab / G));
-      } else {
-        st.s0 = __ldg(reinterpret_cast<const uint16_t *>(ps0 + d * (kSlab / G)));
-        st.s1 = __ldg(reinterpret_cast<const uint16_t *>(ps1 + d * (kSlab / G)));
+  const int frag0 = gated && !split ? 2 * g : g, frag1 = gated && !split ? 2 * g + 1 : g + 8;
+  int p_units = count, p_b = cur_b, p_tg = cur_tg, p_ch = 0;
+  int p_n = 0, p_left = 0;               // steps to issue; columns left from the lane's next one
+  const uint8_t *pw0, *pw1, *ps;         // the lane's two code rows and scale words there
+  const uint32_t ring_at = tc::smem_u32(ring);
+  uint32_t p_at = ring_at;
+  auto point = [&]() {
+    int e, tb, lo;
+    where(p_b, e, tb);
+    slabs_of(p_ch, lo, p_n);
+    const int tile = p_tg * rws + rw;
+    const int64_t at = (int64_t)e * a.R;
+    const int64_t col = (int64_t)lo * (kSlab / 2) + 16 * c;
+    pw0 = a.codes + (at + tile_row(tile, frag0)) * (a.C / 2) + col;
+    pw1 = a.codes + (at + tile_row(tile, frag1)) * (a.C / 2) + col;
+    p_left = a.C - lo * kSlab - 32 * c;
+    // whole words around the row's bytes of the slab, two lanes per row
+    ps = a.scales + ((at + tile_row(tile, lane >> 1)) * (a.C / G) & ~(int64_t)3) +
+         lo * (kSlab / G) + 4 * (lane & 1);
+  };
+  // a word at the array's end: unread ones move inside, a last part is cut off
+  const uint8_t *const last_word = a.scales + a.scale_bytes - 4;
+  auto copy_word = [&](uint32_t dst, const uint8_t *src) {
+    if ((a.scale_bytes & 3) == 0) {
+      copy4(dst, src < last_word ? src : last_word, 4);
+    } else {
+      const int64_t left = last_word + 4 - src;
+      copy4(dst, left > 0 ? src : a.scales, left >= 4 ? 4 : left > 0 ? (int)left : 0);
+    }
+  };
+  auto fetch = [&]() {
+    while (p_n == 0 && p_units > 0) {  // on to the next chunk, the next unit
+      if (++p_ch == a.chunks) {
+        p_ch = 0;
+        --p_units;
+        if (++p_tg == tile_groups) {
+          p_tg = 0;
+          ++p_b;
+        }
       }
-    } else {
-      st.w0 = st.w1 = make_uint4(0u, 0u, 0u, 0u);
-      st.s0 = st.s1 = FMT == MOE_Q4_MXFP4 ? 127u : 0u;
+      if (p_units > 0) point();
     }
+    if (p_n > 0) {
+      const bool in = p_left > 0;
+      copy16(p_at + lane * 16, in ? pw0 : a.codes, in ? 16 : 0);
+      copy16(p_at + 512 + lane * 16, in ? pw1 : a.codes, in ? 16 : 0);
+      copy_word(p_at + 1024 + (lane >> 1) * (4 * SW) + (lane & 1) * 4, ps);
+      if (SW == 3 && a.C % 64 != 0 && lane < 16) {
+        // 8 bytes that may start inside a word: a third one
+        int e, tb, lo, n;
+        where(p_b, e, tb);
+        slabs_of(p_ch, lo, n);
+        const int64_t r = (int64_t)e * a.R + tile_row(p_tg * rws + rw, lane);
+        copy_word(p_at + 1024 + lane * (4 * SW) + 8, a.scales + (r * (a.C / G) & ~(int64_t)3) + 8 +
+                                                         (lo + n - p_n) * (kSlab / G));
+      }
+      pw0 += kSlab / 2;
+      pw1 += kSlab / 2;
+      ps += kSlab / G;
+      p_left -= kSlab;
+      --p_n;
+      p_at = p_at == ring_at + (RING - 1) * STEP ? ring_at : p_at + STEP;
+    }
+    copies_commit();  // a group per step, also past the end: the waits count groups
   };
-  auto advance = [&]() {
-    rem -= kRing * kSlab;
-    pw0 += kRing * (kSlab / 2);
-    pw1 += kRing * (kSlab / 2);
-    ps0 += kRing * (kSlab / G);
-    ps1 += kRing * (kSlab / G);
-  };
-  Q4Step ring[kRing];
-  if (left > 0) {
-    point(cur, 0);
-#pragma unroll
-    for (int d = 0; d < kRing; ++d) fetch(ring[d], d);
-    advance();
-  }
+  if (count > 0) point();
+#pragma unroll 1
+  for (int d = 0; d < RING; ++d) fetch();
+  // where the lane's scales lie in a step: fixed, as tiles are 8 or 16 rows
+  // apart and several matrices have a multiple of 64 rows
+  const int s_at0 =
+      1024 + frag0 * (4 * SW) + ((uint32_t)tile_row(rw, frag0) * (a.C / G) & 3) + c * (32 / G);
+  const int s_at1 =
+      1024 + frag1 * (4 * SW) + ((uint32_t)tile_row(rw, frag1) * (a.C / G) & 3) + c * (32 / G);
 
   if (a.mode == Q4_W2) {
     pdl_wait();
@@ -307,50 +374,50 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
 
   // ---- activations of a token block as fp16 B fragments: for slab s, quarter
   // q and token block b, lane (g, c) finds columns 128 s + 32 c + 8 q .. + 7 of
-  // token 8 b + g in its 16 bytes.
-  int nt = 0;
-  auto load_x = [&](const Q4Unit &q, int ch, bool fresh) {
-    const int p0 = sh.cnt[q.e] + q.tb * TB;
-    nt = max(min(TB, sh.cnt[q.e + 1] - p0), 0);
-    __syncthreads();  // the previous block's fragments and scales are no longer read
+  // token 8 b + g in its 16 bytes. What lies there for tokens past the block's
+  // end reaches only sums that are dropped.
+  int nt = 0, part = 3, cur_e = 0, cur_p0 = 0;  // tokens of the block; its part of sh.amax
+  auto load_x = [&](int ch, bool fresh) {
     if (fresh) {
-      if (tid < TB) {
-        sh.amax[tid] = 0u;
-        if (tid < nt)  // a row in range whatever col_sorted holds
-          sh.row[tid] = a.mode != Q4_W13
-                            ? p0 + tid
-                            : min(max(__ldg(a.col_sorted + p0 + tid), 0), (int)a.N - 1) / a.k;
-      }
-      __syncthreads();
-      const int segs = (a.C / 8 + 31) / 32;  // a warp takes 32 x 8 columns of one token
+      int tb;
+      where(cur_b, cur_e, tb);
+      cur_p0 = sh.cnt[cur_e] + tb * TB;
+      nt = max(min(TB, sh.cnt[cur_e + 1] - cur_p0), 0);
+      part = (part + 1) & 3;
+      if (tid < nt)  // a row in range whatever col_sorted holds
+        sh.row[tid] = a.mode != Q4_W13
+                          ? cur_p0 + tid
+                          : min(max(__ldg(a.col_sorted + cur_p0 + tid), 0), (int)a.N - 1) / a.k;
+    }
+    __syncthreads();  // the previous fragments are no longer read
+    if (fresh) {
+      const int segs = (a.C + 255) / 256;  // a warp takes 256 columns of one token
       for (int i = wid; i < nt * segs; i += kQ4Warps) {
-        const int t = i / segs, at = (i - t * segs) * 256 + lane * 8;
+        const int t = i / segs, col = (i - t * segs) * 256 + lane * 8;
         uint32_t m = 0u;
-        if (at < a.C) {
+        if (col < a.C) {
           float v[8];
-          load_x8(a.x, a.x_dtype, (int64_t)sh.row[t] * a.C + at, v);
+          load_x8(a.x, a.x_dtype, (int64_t)sh.row[t] * a.C + col, v);
 #pragma unroll
           for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
         }
         m = __reduce_max_sync(0xffffffffu, m);
-        if (lane == 0) atomicMax(&sh.amax[t], m);
+        if (lane == 0) atomicMax(&sh.amax[part][t], m);
       }
       __syncthreads();
+      // the block before the last has been stored by every warp: its part of
+      // amax is free for the block after the next, past another barrier
+      if (tid < TB) sh.amax[(part + 2) & 3][tid] = 0u;
     }
     const int c_lo = ch * a.chunk * kSlab;
-    const int per = (min(a.slabs, (ch + 1) * a.chunk) * kSlab - c_lo) / 8;
+    const int per = min(a.chunk, a.slabs - ch * a.chunk) * (kSlab / 8);
     for (int i = tid; i < nt * per; i += kQ4Threads) {
       const int t = i / per, at = i - t * per, col = c_lo + at * 8;
-      // scale exponent: the row's largest magnitude into [2^14, 2^15); a row
-      // of zeros, or one that is not finite, keeps its values
-      const uint32_t m = sh.amax[t];
-      const int ex = (int)(m >> 23);
-      const int sc = m == 0u || ex == 255 ? 0 : min(14 + 127 - ex, 126);
-      const float f = exp2i(sc);
-      if (at == 0) sh.inv[t] = exp2i(-sc);
+      const uint32_t m = sh.amax[part][t];
+      const float f = exp2i(row_exponent(m));
       float x[8] = {};
       if (col < a.C) load_x8(a.x, a.x_dtype, (int64_t)sh.row[t] * a.C + col, x);
-      if (ex == 255) {  // finite values of a row that holds an infinity stay finite
+      if ((m >> 23) == 255u) {  // finite values beside an infinity stay finite
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           if (fabsf(x[j]) < INFINITY) x[j] = fminf(fmaxf(x[j], -65504.f), 65504.f);
@@ -361,8 +428,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
       uint4 v;
       memcpy(&v, h, 16);
       // at = 16 s + 4 c + q
-      reinterpret_cast<uint4 *>(
-          smem_x)[(((at >> 4) * 4 + (at & 3)) * NB + (t >> 3)) * 32 + (t & 7) * 4 + ((at >> 2) & 3)] = v;
+      xs[(((at >> 4) * 4 + (at & 3)) * NB + (t >> 3)) * 32 + (t & 7) * 4 + ((at >> 2) & 3)] = v;
     }
     __syncthreads();
   };
@@ -375,10 +441,10 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
 
   // one step's products into d: the lane's codes times m0 / m1 (a half-pair
   // each for columns 0..15 and 16..31 of its 32)
-  auto products = [&](float (*d)[4], const Q4Step &st, const uint4 *frag, const uint32_t *m0,
-                      const uint32_t *m1) {
-    const uint32_t w0[4] = {st.w0.x, st.w0.y, st.w0.z, st.w0.w};
-    const uint32_t w1[4] = {st.w1.x, st.w1.y, st.w1.z, st.w1.w};
+  auto products = [&](float (*d)[4], const uint4 &c0, const uint4 &c1, const uint4 *x,
+                      const uint32_t *m0, const uint32_t *m1) {
+    const uint32_t w0[4] = {c0.x, c0.y, c0.z, c0.w};
+    const uint32_t w1[4] = {c1.x, c1.y, c1.z, c1.w};
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       uint32_t v0[4], v1[4], A[2][4];
@@ -393,63 +459,81 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
         }
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (b * 8 + g < nt) x = frag[(q * NB + b) * 32];
-        mma16816(d[b], A[0], x.x, x.y);
-        mma16816(d[NB == 1 ? 1 : b], A[1], x.z, x.w);
+        const uint4 f = x[(q * NB + b) * 32];
+        mma16816(d[b], A[0], f.x, f.y);
+        mma16816(d[NB == 1 ? 1 : b], A[1], f.z, f.w);
       }
     }
   };
-  auto compute = [&](const Q4Step &st, const uint4 *frag) {
+  // a step: slab `left` columns before the row's end for this lane
+  auto compute = [&](const unsigned char *st, const uint4 *x, bool fresh, int left) {
+    const uint4 c0 = *reinterpret_cast<const uint4 *>(st + lane * 16);
+    const uint4 c1 = *reinterpret_cast<const uint4 *>(st + 512 + lane * 16);
+    // columns past the row's end have zero codes, and no scale of theirs
+    const bool in = left > 0;
     if (FMT == MOE_Q4_NVFP4) {
-      const uint32_t h0 = e4m3x2_to_half2(st.s0), h1 = e4m3x2_to_half2(st.s1);
+      const uint32_t h0 =
+          e4m3x2_to_half2(in ? *reinterpret_cast<const uint16_t *>(st + s_at0) : 0u);
+      const uint32_t h1 =
+          e4m3x2_to_half2(in ? *reinterpret_cast<const uint16_t *>(st + s_at1) : 0u);
+      __syncwarp();  // read by all: the slot takes the step RING ahead
+      fetch();
       const uint32_t m0[2] = {__byte_perm(h0, h0, 0x1010), __byte_perm(h0, h0, 0x3232)};
       const uint32_t m1[2] = {__byte_perm(h1, h1, 0x1010), __byte_perm(h1, h1, 0x3232)};
-      products(acc, st, frag, m0, m1);
-      return;
-    }
-    const int d0 = (int)st.s0 - (int)ref0, d1 = (int)st.s1 - (int)ref1;
-    const bool far = (uint32_t)(d0 + 14) > 26u || (uint32_t)(d1 + 14) > 26u || st.s0 == 255u ||
-                     st.s1 == 255u;
-    uint32_t e0 = (uint32_t)(d0 + 15) * 0x04000400u, e1 = (uint32_t)(d1 + 15) * 0x04000400u;
-    if (!__any_sync(0xffffffffu, far)) {
-      const uint32_t m0[2] = {e0, e0}, m1[2] = {e1, e1};
-      products(acc, st, frag, m0, m1);
-      return;
-    }
+      products(acc, c0, c1, x, m0, m1);
+    } else {
+      uint32_t s0 = st[s_at0], s1 = st[s_at1];
+      __syncwarp();
+      fetch();
+      if (fresh) {  // the unit's first step: each row's reference, where 2^(s - ref) has room
+        ref0 = min(max(__shfl_sync(0xffffffffu, s0, lane & ~3), 96u), 158u);
+        ref1 = min(max(__shfl_sync(0xffffffffu, s1, lane & ~3), 96u), 158u);
+      }
+      if (!in) {
+        s0 = ref0;
+        s1 = ref1;
+      }
+      const int d0 = (int)s0 - (int)ref0, d1 = (int)s1 - (int)ref1;
+      const bool far = (uint32_t)(d0 + 14) > 26u || (uint32_t)(d1 + 14) > 26u;
+      const uint32_t e0 = (uint32_t)(d0 + 15) * 0x04000400u, e1 = (uint32_t)(d1 + 15) * 0x04000400u;
+      if (!__any_sync(0xffffffffu, far)) {
+        const uint32_t m0[2] = {e0, e0}, m1[2] = {e1, e1};
+        products(acc, c0, c1, x, m0, m1);
+      } else {
 #pragma unroll 1
-    for (int j = 0; j < 4; ++j) {  // the lanes c = j of every row: one group per row
-      const uint32_t t0 = __shfl_sync(0xffffffffu, st.s0, (lane & ~3) + j);
-      const uint32_t t1 = __shfl_sync(0xffffffffu, st.s1, (lane & ~3) + j);
-      const uint32_t one = c == j ? 0x3c003c00u : 0u;
-      const uint32_t m[2] = {one, one};
-      float d[NS][4] = {};
-      products(d, st, frag, m, m);
-      // 2^(t - ref) in two factors, each in range
-      const int h0 = ((int)t0 - (int)ref0) / 2, h1 = ((int)t1 - (int)ref1) / 2;
-      const float a0 = t0 == 255u ? NAN : exp2i(h0), b0 = exp2i((int)t0 - (int)ref0 - h0);
-      const float a1 = t1 == 255u ? NAN : exp2i(h1), b1 = exp2i((int)t1 - (int)ref1 - h1);
+        for (int j = 0; j < 4; ++j) {  // the lanes c = j of every row: one group per row
+          const uint32_t t0 = __shfl_sync(0xffffffffu, s0, (lane & ~3) + j);
+          const uint32_t t1 = __shfl_sync(0xffffffffu, s1, (lane & ~3) + j);
+          const uint32_t one = c == j ? 0x3c003c00u : 0u;
+          const uint32_t m[2] = {one, one};
+          float d[NS][4] = {};
+          products(d, c0, c1, x, m, m);
+          // 2^(t - ref) in two factors, each in range
+          const int h0 = ((int)t0 - (int)ref0) / 2, h1 = ((int)t1 - (int)ref1) / 2;
+          const float a0 = t0 == 255u ? NAN : exp2i(h0), b0 = exp2i((int)t0 - (int)ref0 - h0);
+          const float a1 = t1 == 255u ? NAN : exp2i(h1), b1 = exp2i((int)t1 - (int)ref1 - h1);
 #pragma unroll
-      for (int b = 0; b < NS; ++b) {
-        acc[b][0] = fmaf(d[b][0] * a0, b0, acc[b][0]);
-        acc[b][1] = fmaf(d[b][1] * a0, b0, acc[b][1]);
-        acc[b][2] = fmaf(d[b][2] * a1, b1, acc[b][2]);
-        acc[b][3] = fmaf(d[b][3] * a1, b1, acc[b][3]);
+          for (int b = 0; b < NS; ++b) {
+            acc[b][0] = fmaf(d[b][0] * a0, b0, acc[b][0]);
+            acc[b][1] = fmaf(d[b][1] * a0, b0, acc[b][1]);
+            acc[b][2] = fmaf(d[b][2] * a1, b1, acc[b][2]);
+            acc[b][3] = fmaf(d[b][3] * a1, b1, acc[b][3]);
+          }
+        }
       }
     }
   };
-  // the finished sums v of one row tile and token block: rows g, g + 8 (or
-  // gate, up) of tokens 2 c and 2 c + 1
-  auto store = [&](const float *v, int tile, int b) {
-    const float ms = a.mscale ? __ldg(a.mscale + cur.e) : 1.f;
-    const int64_t p0 = sh.cnt[cur.e] + cur.tb * TB;
+  // The finished sums v of one row tile and token block: fragment rows g and
+  // g + 8 of tokens 2 c and 2 c + 1.
+  auto store = [&](const float *v, int e, int p0, int q_nt, int q_part, int tile, int b) {
+    const float ms = a.mscale ? __ldg(a.mscale + e) : 1.f;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int t = b * 8 + c * 2 + j;
-      if (t >= nt) continue;
-      const float s = sh.inv[t];
+      if (t >= q_nt) continue;
+      const float s = exp2i(-row_exponent(sh.amax[q_part][t]));
       const float lo = v[j] * ms * s, hi = v[2 + j] * ms * s;
-      const int64_t p = p0 + t;
+      const int64_t p = (int64_t)p0 + t;
       const int row = tile * 16 + g;
       if (a.mode == Q4_W13) {
         float *h = static_cast<float *>(a.out);
@@ -470,57 +554,47 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
       }
     }
   };
-
-  bool new_block = true;
-  int turn = 0, ch = 0, round = 0, x_chunk = -1;
-  while (left > 0) {
-    if (new_block || ch != x_chunk) {
-      load_x(cur, ch, new_block);
-      x_chunk = ch;
-      new_block = false;
-    }
-    if (FMT == MOE_Q4_MXFP4 && round == 0 && ch == 0) {
-      // each row's first scale, kept where 2^(s - ref) of any s has room
-      ref0 = __shfl_sync(0xffffffffu, ring[0].s0, lane & ~3);
-      ref1 = __shfl_sync(0xffffffffu, ring[0].s1, lane & ~3);
-      ref0 = min(max(ref0, 96u), 158u);
-      ref1 = min(max(ref1, 96u), 158u);
-    }
-    // what the ring takes up next: the next round, chunk or unit
-    Q4Unit nxt = cur;
-    bool next_block = false, more = true;
-    const bool round_last = round + 1 == rounds, unit_last = round_last && ch + 1 == a.chunks;
-    if (unit_last) {
-      more = left > 1;
-      if (++nxt.tg == tile_groups) {
-        nxt.tg = 0;
-        ++nxt.tb;
-        next_block = true;
-        while (nxt.e < a.E - 1 && sh.blk[nxt.e] + nxt.tb >= sh.blk[nxt.e + 1]) {
-          ++nxt.e;
-          nxt.tb = 0;
-        }
+  // Joins a unit's partial sums along the row; other warps take it each unit.
+  auto join = [&](int u, int rs, uint32_t phase) {
+    for (int i = (wid - u * items) & (kQ4Warps - 1); i < items; i += kQ4Warps) {
+      const int b = i % NB, r = i / NB;
+      wait_phase(full_at + 8 * rs, phase, a.ctrl);
+      const int4 q = sh.info[rs];
+      const int q_part = sh.part[rs];
+      float v[4] = {};
+      for (int w = 0; w < kw; ++w) {
+        const float4 t = red[((rs * kQ4Warps + r * kw + w) * NB + b) * 32 + lane];
+        v[0] += t.x;
+        v[1] += t.y;
+        v[2] += t.z;
+        v[3] += t.w;
       }
-      if (more) point(nxt, 0);
-    } else if (round_last) {
-      point(cur, ch + 1);
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(empty_at + 8 * rs);
+      store(v, q.x, q.y, q.z, q_part, q.w * rws + r, b);
     }
-    // this round's slabs inside the chunk: s0 .. s0 + steps - 1
-    const int s0 = kpart * share + round * kRing;
-    const int steps = min(min((kpart + 1) * share, a.chunk), a.slabs - ch * a.chunk) - s0;
-    const uint4 *frag = reinterpret_cast<const uint4 *>(smem_x) + s0 * (4 * NB * 32) + lane;
-#pragma unroll
-    for (int d = 0; d < kRing; ++d) {
-      if (d < steps) compute(ring[d], frag + d * (4 * NB * 32));
-      if (more) fetch(ring[d], d);
+  };
+
+  int rs = 0, slot = 0;
+  uint32_t rs_phase = 0;  // the slot of red; how often it came round, modulo 2
+  for (int u = 0; u < count; ++u) {
+    const bool new_block = u == 0 || cur_tg == 0;
+    for (int ch = 0; ch < a.chunks; ++ch) {
+      if (new_block || a.chunks > 1) load_x(ch, new_block && ch == 0);
+      int lo, n;
+      slabs_of(ch, lo, n);
+      const uint4 *x = xs + (lo - ch * a.chunk) * (4 * NB * 32) + lane;
+      int left = a.C - lo * kSlab - 32 * c;
+#pragma unroll 1
+      for (int d = 0; d < n; ++d) {
+        copies_wait<RING - 1>();
+        __syncwarp();  // the lanes' copies are in, for all lanes
+        compute(ring + slot, x, ch == 0 && d == 0, left);
+        slot = slot == (RING - 1) * STEP ? 0 : slot + STEP;
+        x += 4 * NB * 32;
+        left -= kSlab;
+      }
     }
-    if (more) advance();
-    if (!unit_last) {
-      if (round_last) ++ch;
-      round = round_last ? 0 : round + 1;
-      continue;
-    }
-    // ---- the unit's end
     if (NB == 1) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[0][i] += acc[NS - 1][i];
@@ -537,38 +611,38 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
     }
     if (kw == 1) {
 #pragma unroll
-      for (int b = 0; b < NB; ++b) store(acc[b], cur.tg * rws + rw, b);
+      for (int b = 0; b < NB; ++b) store(acc[b], cur_e, cur_p0, nt, part, cur_tg * rws + rw, b);
     } else {
-      // join the warps along the row; another warp finishes a tile each unit
-      const int buf = turn & 1;
+      wait_phase(empty_at + 8 * rs, rs_phase ^ 1u, a.ctrl);
 #pragma unroll
       for (int b = 0; b < NB; ++b)
-        *reinterpret_cast<float4 *>(sh.red[buf][wid][b][lane]) =
+        red[((rs * kQ4Warps + wid) * NB + b) * 32 + lane] =
             make_float4(acc[b][0], acc[b][1], acc[b][2], acc[b][3]);
-      __syncthreads();  // the other buffer's readers passed this barrier a unit ago
-      for (int i = (wid + turn * rws * NB) & (kQ4Warps - 1); i < rws * NB; i += kQ4Warps) {
-        const int b = i % NB, r = i / NB;
-        float v[4] = {};
-        for (int w = 0; w < kw; ++w) {
-          const float4 t = *reinterpret_cast<const float4 *>(sh.red[buf][r * kw + w][b][lane]);
-          v[0] += t.x;
-          v[1] += t.y;
-          v[2] += t.z;
-          v[3] += t.w;
-        }
-        store(v, cur.tg * rws + r, b);
+      if (tid == 0) {
+        sh.info[rs] = make_int4(cur_e, cur_p0, nt, cur_tg);
+        sh.part[rs] = part;
       }
-      ++turn;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(full_at + 8 * rs);
+      // one unit late, so that the other warps' sums are there
+      if (u > 0) join(u - 1, rs == 0 ? RS - 1 : rs - 1, rs == 0 ? rs_phase ^ 1u : rs_phase);
+      if (++rs == RS) {
+        rs = 0;
+        rs_phase ^= 1u;
+      }
     }
 #pragma unroll
     for (int b = 0; b < NS; ++b)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[b][i] = 0.f;
-    cur = nxt;
-    new_block = next_block;
-    --left;
-    ch = round = 0;
+    if (++cur_tg == tile_groups) {
+      cur_tg = 0;
+      ++cur_b;
+    }
   }
+  if (kw > 1 && count > 0)
+    join(count - 1, rs == 0 ? RS - 1 : rs - 1, rs == 0 ? rs_phase ^ 1u : rs_phase);
+  copies_wait<0>();
 
   if (a.mode == Q4_W2) {  // rows of no kept slot
     const int64_t words = (a.N - sh.cnt[a.E]) * a.R / 2;  // R is even: 4-byte words
@@ -580,29 +654,50 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
   }
 }
 
-template <int FMT, int NB>
+// Slabs whose activations fit beside the ring and the partial sums.
+template <int FMT, int NB, int RING>
+constexpr int slabs_that_fit() {
+  return (kSmemMax - (int)sizeof(Q4Shared<NB>) -
+          kQ4Warps * (RING * step_bytes(FMT) + red_slots(NB) * NB * 512)) /
+         (NB * kSlabXBytes);
+}
+
+template <int FMT, int NB, int RING>
 cudaError_t launch(Q4Args &a, cudaStream_t s) {
-  a.slabs = (a.C + kSlab - 1) / kSlab;
-  a.chunk = a.slabs < kMaxSlabsX / NB ? a.slabs : kMaxSlabsX / NB;
+  constexpr int fit = slabs_that_fit<FMT, NB, RING>();
+  constexpr int fixed = kQ4Warps * (RING * step_bytes(FMT) + red_slots(NB) * NB * 512);
+  a.chunk = a.slabs < fit ? a.slabs : fit;
   a.chunks = (a.slabs + a.chunk - 1) / a.chunk;
+  a.scale_bytes = (int64_t)a.E * a.R * (a.C / (FMT == MOE_Q4_MXFP4 ? 32 : 16));
   static PerDeviceOnce configured;
   cudaError_t err = configured.run([] {
-    cudaError_t e = uniform_carveout(q4_kernel<FMT, NB>);
+    cudaError_t e = uniform_carveout(q4_kernel<FMT, NB, RING>);
     if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(q4_kernel<FMT, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kMaxSlabsX * kSlabXBytes);
+    return cudaFuncSetAttribute(q4_kernel<FMT, NB, RING>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                fixed + fit * NB * kSlabXBytes);
   });
   if (err != cudaSuccess) return err;
-  err = launch_dependent(q4_kernel<FMT, NB>, dim3((unsigned)device_sm_count()), dim3(kQ4Threads),
-                         (size_t)a.chunk * NB * kSlabXBytes, s, a);
+  err = launch_dependent(q4_kernel<FMT, NB, RING>, dim3((unsigned)device_sm_count()),
+                         dim3(kQ4Threads), (size_t)(fixed + a.chunk * NB * kSlabXBytes), s, a);
   return err == cudaSuccess ? cudaGetLastError() : err;
 }
 
-cudaError_t launch_format(Q4Args &a, int format, cudaStream_t s) {
+// Two token blocks per unit where experts have more than 8 tokens on average
+// or nearly so, if a row's activations then stay resident; a short ring where
+// only that leaves room for them.
+template <int FMT>
+cudaError_t launch_sized(Q4Args &a, cudaStream_t s) {
+  a.slabs = (a.C + kSlab - 1) / kSlab;
   const bool two = a.N > 8 * (int64_t)(a.offs ? a.E / 2 : 1);
-  if (format == MOE_Q4_MXFP4)
-    return two ? launch<MOE_Q4_MXFP4, 2>(a, s) : launch<MOE_Q4_MXFP4, 1>(a, s);
-  return two ? launch<MOE_Q4_NVFP4, 2>(a, s) : launch<MOE_Q4_NVFP4, 1>(a, s);
+  if (two && a.slabs <= slabs_that_fit<FMT, 2, 4>()) return launch<FMT, 2, 4>(a, s);
+  if (a.slabs <= slabs_that_fit<FMT, 1, 8>()) return launch<FMT, 1, 8>(a, s);
+  return launch<FMT, 1, 4>(a, s);
+}
+
+cudaError_t launch_format(Q4Args &a, int format, cudaStream_t s) {
+  return format == MOE_Q4_MXFP4 ? launch_sized<MOE_Q4_MXFP4>(a, s)
+                                : launch_sized<MOE_Q4_NVFP4>(a, s);
 }
 
 }  // namespace
@@ -628,8 +723,9 @@ cudaError_t launch_linear_q4(const void *x, const moe_q4_matrix &w, int64_t n, i
 cudaError_t launch_ffn_q4(const void *x, const moe_routing_meta &m, const moe_q4_matrix &w13,
                           const moe_q4_matrix &w2, int64_t N, int E, int k, int H, int I,
                           const ActParams &act, int dtype, float *h, void *y_sorted,
-                          cudaStream_t s) {
+                          uint32_t *ctrl, cudaStream_t s) {
   Q4Args a = {};
+  a.ctrl = ctrl;
   a.codes = w13.codes;
   a.scales = w13.scales;
   a.mscale = w13.matrix_scale;

@@ -68,7 +68,7 @@ def test_matrix_arguments(L, call):
     name = "w" if call is linear else "w2"
     for bad in (q4(codes=0), q4(scales=0), q4(fmt=2), q4(fmt=-1)):
         assert call(L, **{name: bad}) == INVALID
-    for bad in (q4(codes=BASE + 8), q4(scales=BASE + 1), q4(whole=BASE + 2)):
+    for bad in (q4(codes=BASE + 8), q4(scales=BASE + 2), q4(whole=BASE + 2)):
         assert call(L, **{name: bad}) == MISALIGNED
 
 
