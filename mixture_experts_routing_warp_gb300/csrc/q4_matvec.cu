@@ -105,11 +105,10 @@ __device__ __forceinline__ void mma16816(float *d, const uint32_t *a, uint32_t b
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Asynchronous copies to shared memory of which `bytes` are read and the rest
-// filled with zeros; one group per warp step.
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
+// Asynchronous copies to shared memory (of a word, `bytes` are read and the
+// rest filled with zeros); one group per warp step.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy4(uint32_t dst, const void *src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
@@ -166,7 +165,8 @@ __device__ __forceinline__ float exp2i(int e) {
 template <int NB>
 struct Q4Shared {
   unsigned long long full[red_slots(NB)], empty[red_slots(NB)];  // mbarriers
-  int4 info[red_slots(NB)];  // unit in a slot: expert, first token slot, tokens, tile group
+  int4 info[red_slots(NB)];  // unit in a slot: expert, first token slot, tokens, first tile
+  int tile_end[red_slots(NB)];  // tiles from here on are not the unit's
   int part[red_slots(NB)];   // and its part of amax
   int cnt[kMaxExperts + 1];  // first slot of each expert (offs)
   int blk[kMaxExperts + 1];  // exclusive prefix of the experts' token blocks
@@ -237,17 +237,26 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
     __syncthreads();
   }
 
-  // Warps along a row (kw): a unit is kQ4Warps / kw row tiles, dealt out
-  // whole, and costs its warps about two steps besides its own. The fewest
-  // that leave a CTA 8 units or more, so that the last ones idle little; at
-  // most 8, and no more than the row has slabs.
+  // Row tiles (16 rows) of all token blocks are dealt out evenly, in order, to
+  // the CTAs. A unit is what a CTA works on at a time: kQ4Warps / kw tiles of
+  // one block, kw warps along each row. More warps along a row leave fewer
+  // idle at the end of the CTA's tiles, but cost a join and, for each unit,
+  // about the time of two steps.
   const int blocks = sh.blk[a.E], tiles = (a.R + 15) / 16, in_row = min(a.slabs, a.chunk);
   int kw = 1;
-  while (kw < 8 && kw * 2 <= in_row &&
-         (int64_t)blocks * tiles * kw < 8 * kQ4Warps * (int64_t)gridDim.x)
-    kw *= 2;
+  {
+    const int64_t per_cta = ((int64_t)blocks * tiles + gridDim.x - 1) / gridDim.x;
+    int64_t best = INT64_MAX;
+    for (int w = 1; w <= 8 && w <= in_row; w *= 2) {
+      const int64_t n = (per_cta * w + kQ4Warps - 1) / kQ4Warps;
+      const int64_t cost = n * ((in_row + w - 1) / w + 2);
+      if (cost < best) {
+        best = cost;
+        kw = w;
+      }
+    }
+  }
   const int rws = kQ4Warps / kw, kpart = wid & (kw - 1), rw = wid / kw;
-  const int tile_groups = (tiles + rws - 1) / rws;
   const int items = rws * NB;  // joins per unit
   if (tid == 0) {
     for (int i = 0; i < RS; ++i) {
@@ -256,14 +265,16 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-
-  // this CTA's units (a unit stores 128 values or more: the count fits an int)
-  const int64_t units = (int64_t)blocks * tile_groups;
-  const int64_t first = units * blockIdx.x / gridDim.x;
-  const int count = (int)(units * (blockIdx.x + 1) / gridDim.x - first);
-  // unit u of the CTA: token block b, tile group tg; block b is the tb-th of
-  // expert e, the last one whose prefix is <= b
-  int cur_b = (int)(first / tile_groups), cur_tg = (int)(first - (int64_t)cur_b * tile_groups);
+  const int64_t all = (int64_t)blocks * tiles;
+  const int64_t t0 = all * blockIdx.x / gridDim.x, t1 = all * (blockIdx.x + 1) / gridDim.x;
+  // the CTA's tiles [lo, hi) of a block
+  auto tiles_of = [&](int b, int &lo, int &hi) {
+    const int64_t at = (int64_t)b * tiles;
+    lo = (int)max(t0 - at, (int64_t)0);
+    hi = (int)min(t1 - at, (int64_t)tiles);
+  };
+  const int b0 = (int)(t0 / tiles), b1 = t1 > t0 ? (int)((t1 - 1) / tiles) : b0 - 1;
+  // block b is the tb-th of expert e, the last one whose prefix is <= b
   auto where = [&](int b, int &e, int &tb) {
     int lo = 0, hi = a.E;
     while (hi - lo > 1) {
@@ -279,9 +290,11 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
     lo = ch * a.chunk + at;
     n = m * (kpart + 1) / kw - at;
   };
+  int s_lo, s_n;  // with a single chunk, for good
+  slabs_of(0, s_lo, s_n);
 
   // ---- weights on their way: step after step, RING steps ahead of the
-  // products, by an iterator over (unit, chunk, slab)
+  // products, by an iterator over (block, tile, chunk, slab)
   const bool gated = a.mode == Q4_W13 && a.act != MOE_ACT_RELU2;
   const bool split = gated && a.ap.layout == MOE_W13_PACKED;  // up rows I below the gate rows
   // Row r (0..15) of a tile. Fragment rows g and g + 8 are gate and up of one
@@ -293,73 +306,86 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
     return min(row, a.R - 1);
   };
   const int frag0 = gated && !split ? 2 * g : g, frag1 = gated && !split ? 2 * g + 1 : g + 8;
-  int p_units = count, p_b = cur_b, p_tg = cur_tg, p_ch = 0;
-  int p_n = 0, p_left = 0;               // steps to issue; columns left from the lane's next one
-  const uint8_t *pw0, *pw1, *ps;         // the lane's two code rows and scale words there
-  const uint32_t ring_at = tc::smem_u32(ring);
-  uint32_t p_at = ring_at;
+  int p_b = b0, p_tile = 0, p_end = 0, p_ch = 0;
+  int p_n = 0, p_left = 0;        // steps to issue; columns left from the lane's next one
+  const uint8_t *pw0, *pw1, *ps;  // the lane's two code rows and scale words there
+  int64_t p_rows = 0;             // rows of the matrices before the block's
+  bool p_edge = false;            // a scale word may lie past the array's end
+  const uint8_t *const s_end = a.scales + a.scale_bytes;
   auto point = [&]() {
-    int e, tb, lo;
-    where(p_b, e, tb);
-    slabs_of(p_ch, lo, p_n);
-    const int tile = p_tg * rws + rw;
-    const int64_t at = (int64_t)e * a.R;
+    int lo = s_lo;
+    p_n = s_n;
+    if (a.chunks > 1) slabs_of(p_ch, lo, p_n);
     const int64_t col = (int64_t)lo * (kSlab / 2) + 16 * c;
-    pw0 = a.codes + (at + tile_row(tile, frag0)) * (a.C / 2) + col;
-    pw1 = a.codes + (at + tile_row(tile, frag1)) * (a.C / 2) + col;
+    pw0 = a.codes + (p_rows + tile_row(p_tile, frag0)) * (a.C / 2) + col;
+    pw1 = a.codes + (p_rows + tile_row(p_tile, frag1)) * (a.C / 2) + col;
     p_left = a.C - lo * kSlab - 32 * c;
     // whole words around the row's bytes of the slab, two lanes per row
-    ps = a.scales + ((at + tile_row(tile, lane >> 1)) * (a.C / G) & ~(int64_t)3) +
+    ps = a.scales + ((p_rows + tile_row(p_tile, lane >> 1)) * (a.C / G) & ~(int64_t)3) +
          lo * (kSlab / G) + 4 * (lane & 1);
+    p_edge = __any_sync(0xffffffffu, s_end - ps < (p_n - 1) * (kSlab / G) + 4);
   };
-  // a word at the array's end: unread ones move inside, a last part is cut off
-  const uint8_t *const last_word = a.scales + a.scale_bytes - 4;
-  auto copy_word = [&](uint32_t dst, const uint8_t *src) {
-    if ((a.scale_bytes & 3) == 0) {
-      copy4(dst, src < last_word ? src : last_word, 4);
-    } else {
-      const int64_t left = last_word + 4 - src;
-      copy4(dst, left > 0 ? src : a.scales, left >= 4 ? 4 : left > 0 ? (int)left : 0);
-    }
+  auto enter = [&]() {  // the first tile of block p_b for this warp
+    int e, tb, lo;
+    where(p_b, e, tb);
+    p_rows = (int64_t)e * a.R;
+    tiles_of(p_b, lo, p_end);
+    p_tile = lo + rw;
   };
-  auto fetch = [&]() {
-    while (p_n == 0 && p_units > 0) {  // on to the next chunk, the next unit
-      if (++p_ch == a.chunks) {
-        p_ch = 0;
-        --p_units;
-        if (++p_tg == tile_groups) {
-          p_tg = 0;
-          ++p_b;
+  // bytes before the array's end of a word that may pass it
+  auto copy_edge = [&](uint32_t dst, const uint8_t *src) {
+    const int64_t left = s_end - src;
+    copy4(dst, left > 0 ? src : a.scales, left >= 4 ? 4 : left > 0 ? (int)left : 0);
+  };
+  auto fetch = [&](uint32_t dst) {
+    if (p_n == 0 && p_b <= b1) {  // on to the next chunk, the next tile, the next block
+      do {
+        if (p_tile >= p_end || ++p_ch == a.chunks) {
+          p_ch = 0;
+          if (p_tile < p_end) p_tile += rws;
+          if (p_tile >= p_end) {
+            if (++p_b > b1) break;
+            enter();
+            if (p_tile >= p_end) continue;
+          }
         }
-      }
-      if (p_units > 0) point();
+        point();
+      } while (p_n == 0);
     }
     if (p_n > 0) {
-      const bool in = p_left > 0;
-      copy16(p_at + lane * 16, in ? pw0 : a.codes, in ? 16 : 0);
-      copy16(p_at + 512 + lane * 16, in ? pw1 : a.codes, in ? 16 : 0);
-      copy_word(p_at + 1024 + (lane >> 1) * (4 * SW) + (lane & 1) * 4, ps);
+      // (a slot that is not filled keeps older codes: finite, against zero activations)
+      if (p_left > 0) {
+        copy16(dst + lane * 16, pw0);
+        copy16(dst + 512 + lane * 16, pw1);
+      }
+      const uint32_t sdst = dst + 1024 + (lane >> 1) * (4 * SW) + (lane & 1) * 4;
+      if (!p_edge)
+        copy4(sdst, ps, 4);
+      else
+        copy_edge(sdst, ps);
       if (SW == 3 && a.C % 64 != 0 && lane < 16) {
         // 8 bytes that may start inside a word: a third one
-        int e, tb, lo, n;
-        where(p_b, e, tb);
-        slabs_of(p_ch, lo, n);
-        const int64_t r = (int64_t)e * a.R + tile_row(p_tg * rws + rw, lane);
-        copy_word(p_at + 1024 + lane * (4 * SW) + 8, a.scales + (r * (a.C / G) & ~(int64_t)3) + 8 +
-                                                         (lo + n - p_n) * (kSlab / G));
+        int lo = s_lo, n = s_n;
+        if (a.chunks > 1) slabs_of(p_ch, lo, n);
+        const int64_t r = p_rows + tile_row(p_tile, lane);
+        copy_edge(dst + 1024 + lane * (4 * SW) + 8, a.scales + (r * (a.C / G) & ~(int64_t)3) + 8 +
+                                                        (int64_t)(lo + n - p_n) * (kSlab / G));
       }
       pw0 += kSlab / 2;
       pw1 += kSlab / 2;
       ps += kSlab / G;
       p_left -= kSlab;
       --p_n;
-      p_at = p_at == ring_at + (RING - 1) * STEP ? ring_at : p_at + STEP;
     }
     copies_commit();  // a group per step, also past the end: the waits count groups
   };
-  if (count > 0) point();
+  const uint32_t ring_at = tc::smem_u32(ring);
+  if (b0 <= b1) {
+    enter();
+    if (p_tile < p_end) point();
+  }
 #pragma unroll 1
-  for (int d = 0; d < RING; ++d) fetch();
+  for (int d = 0; d < RING; ++d) fetch(ring_at + d * STEP);
   // where the lane's scales lie in a step: fixed, as tiles are 8 or 16 rows
   // apart and several matrices have a multiple of 64 rows
   const int s_at0 =
@@ -377,6 +403,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
   // token 8 b + g in its 16 bytes. What lies there for tokens past the block's
   // end reaches only sums that are dropped.
   int nt = 0, part = 3, cur_e = 0, cur_p0 = 0;  // tokens of the block; its part of sh.amax
+  int cur_b = b0;
   auto load_x = [&](int ch, bool fresh) {
     if (fresh) {
       int tb;
@@ -390,45 +417,72 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
                           : min(max(__ldg(a.col_sorted + cur_p0 + tid), 0), (int)a.N - 1) / a.k;
     }
     __syncthreads();  // the previous fragments are no longer read
+    // a warp takes 256 columns of one token at a time, 4 such loads in flight
+    const int c_lo = ch * a.chunk * kSlab;
+    const int c_hi = min(a.C, c_lo + a.chunk * kSlab);
     if (fresh) {
-      const int segs = (a.C + 255) / 256;  // a warp takes 256 columns of one token
-      for (int i = wid; i < nt * segs; i += kQ4Warps) {
-        const int t = i / segs, col = (i - t * segs) * 256 + lane * 8;
-        uint32_t m = 0u;
-        if (col < a.C) {
-          float v[8];
-          load_x8(a.x, a.x_dtype, (int64_t)sh.row[t] * a.C + col, v);
+      const int segs = (a.C + 255) / 256;
+      for (int i0 = wid; i0 < nt * segs; i0 += 4 * kQ4Warps) {
+        float v[4][8];
+        int t[4];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+        for (int k = 0; k < 4; ++k) {
+          const int i = i0 + k * kQ4Warps;
+          t[k] = i / segs;
+          const int col = (i - t[k] * segs) * 256 + lane * 8;
+          const bool in = i < nt * segs && col < a.C;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[k][j] = 0.f;
+          if (in) load_x8(a.x, a.x_dtype, (int64_t)sh.row[t[k]] * a.C + col, v[k]);
         }
-        m = __reduce_max_sync(0xffffffffu, m);
-        if (lane == 0) atomicMax(&sh.amax[part][t], m);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t m = 0u;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[k][j]) & 0x7fffffffu);
+          m = __reduce_max_sync(0xffffffffu, m);
+          if (lane == 0 && m != 0u) atomicMax(&sh.amax[part][t[k]], m);
+        }
       }
       __syncthreads();
       // the block before the last has been stored by every warp: its part of
       // amax is free for the block after the next, past another barrier
       if (tid < TB) sh.amax[(part + 2) & 3][tid] = 0u;
     }
-    const int c_lo = ch * a.chunk * kSlab;
-    const int per = min(a.chunk, a.slabs - ch * a.chunk) * (kSlab / 8);
-    for (int i = tid; i < nt * per; i += kQ4Threads) {
-      const int t = i / per, at = i - t * per, col = c_lo + at * 8;
-      const uint32_t m = sh.amax[part][t];
-      const float f = exp2i(row_exponent(m));
-      float x[8] = {};
-      if (col < a.C) load_x8(a.x, a.x_dtype, (int64_t)sh.row[t] * a.C + col, x);
-      if ((m >> 23) == 255u) {  // finite values beside an infinity stay finite
+    const int segs = (min(a.chunk, a.slabs - ch * a.chunk) + 1) / 2;  // 256 columns: two slabs
+    const int last = min(a.chunk, a.slabs - ch * a.chunk);
+    for (int i0 = wid; i0 < nt * segs; i0 += 4 * kQ4Warps) {
+      float x[4][8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (fabsf(x[j]) < INFINITY) x[j] = fminf(fmaxf(x[j], -65504.f), 65504.f);
+      for (int k = 0; k < 4; ++k) {
+        const int i = i0 + k * kQ4Warps, t = i / segs;
+        const int col = c_lo + (i - t * segs) * 256 + lane * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[k][j] = 0.f;
+        if (i < nt * segs && col < c_hi)
+          load_x8(a.x, a.x_dtype, (int64_t)sh.row[t] * a.C + col, x[k]);
       }
-      __half2 h[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) h[j] = __floats2half2_rn(x[2 * j] * f, x[2 * j + 1] * f);
-      uint4 v;
-      memcpy(&v, h, 16);
-      // at = 16 s + 4 c + q
-      xs[(((at >> 4) * 4 + (at & 3)) * NB + (t >> 3)) * 32 + (t & 7) * 4 + ((at >> 2) & 3)] = v;
+      for (int k = 0; k < 4; ++k) {
+        const int i = i0 + k * kQ4Warps, t = i / segs, seg = i - t * segs;
+        const int sl = 2 * seg + (lane >> 4);  // slab of the chunk
+        if (i >= nt * segs || sl >= last) continue;
+        const uint32_t m = sh.amax[part][t];
+        const float f = exp2i(row_exponent(m));
+        if ((m >> 23) == 255u) {  // finite values beside an infinity stay finite
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (fabsf(x[k][j]) < INFINITY) x[k][j] = fminf(fmaxf(x[k][j], -65504.f), 65504.f);
+        }
+        __half2 h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          h[j] = __floats2half2_rn(x[k][2 * j] * f, x[k][2 * j + 1] * f);
+        uint4 v;
+        memcpy(&v, h, 16);
+        // the lane's 8 columns: 16 to a slab, quarter lane % 4 of fragment lane c
+        xs[((sl * 4 + (lane & 3)) * NB + (t >> 3)) * 32 + (t & 7) * 4 + ((lane >> 2) & 3)] = v;
+      }
     }
     __syncthreads();
   };
@@ -466,7 +520,8 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
     }
   };
   // a step: slab `left` columns before the row's end for this lane
-  auto compute = [&](const unsigned char *st, const uint4 *x, bool fresh, int left) {
+  auto compute = [&](int slot, const uint4 *x, bool fresh, int left) {
+    const unsigned char *st = ring + slot;
     const uint4 c0 = *reinterpret_cast<const uint4 *>(st + lane * 16);
     const uint4 c1 = *reinterpret_cast<const uint4 *>(st + 512 + lane * 16);
     // columns past the row's end have zero codes, and no scale of theirs
@@ -477,14 +532,14 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
       const uint32_t h1 =
           e4m3x2_to_half2(in ? *reinterpret_cast<const uint16_t *>(st + s_at1) : 0u);
       __syncwarp();  // read by all: the slot takes the step RING ahead
-      fetch();
+      fetch(ring_at + slot);
       const uint32_t m0[2] = {__byte_perm(h0, h0, 0x1010), __byte_perm(h0, h0, 0x3232)};
       const uint32_t m1[2] = {__byte_perm(h1, h1, 0x1010), __byte_perm(h1, h1, 0x3232)};
       products(acc, c0, c1, x, m0, m1);
     } else {
       uint32_t s0 = st[s_at0], s1 = st[s_at1];
       __syncwarp();
-      fetch();
+      fetch(ring_at + slot);
       if (fresh) {  // the unit's first step: each row's reference, where 2^(s - ref) has room
         ref0 = min(max(__shfl_sync(0xffffffffu, s0, lane & ~3), 96u), 158u);
         ref1 = min(max(__shfl_sync(0xffffffffu, s1, lane & ~3), 96u), 158u);
@@ -560,88 +615,97 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
       const int b = i % NB, r = i / NB;
       wait_phase(full_at + 8 * rs, phase, a.ctrl);
       const int4 q = sh.info[rs];
-      const int q_part = sh.part[rs];
+      const int q_part = sh.part[rs], tile = q.w + r;
+      const bool real = tile < sh.tile_end[rs];
       float v[4] = {};
-      for (int w = 0; w < kw; ++w) {
-        const float4 t = red[((rs * kQ4Warps + r * kw + w) * NB + b) * 32 + lane];
-        v[0] += t.x;
-        v[1] += t.y;
-        v[2] += t.z;
-        v[3] += t.w;
-      }
+      if (real)
+        for (int w = 0; w < kw; ++w) {
+          const float4 t = red[((rs * kQ4Warps + r * kw + w) * NB + b) * 32 + lane];
+          v[0] += t.x;
+          v[1] += t.y;
+          v[2] += t.z;
+          v[3] += t.w;
+        }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(empty_at + 8 * rs);
-      store(v, q.x, q.y, q.z, q_part, q.w * rws + r, b);
+      if (real) store(v, q.x, q.y, q.z, q_part, tile, b);
     }
   };
 
-  int rs = 0, slot = 0;
+  int rs = 0, slot = 0, u = 0;
   uint32_t rs_phase = 0;  // the slot of red; how often it came round, modulo 2
-  for (int u = 0; u < count; ++u) {
-    const bool new_block = u == 0 || cur_tg == 0;
-    for (int ch = 0; ch < a.chunks; ++ch) {
-      if (new_block || a.chunks > 1) load_x(ch, new_block && ch == 0);
-      int lo, n;
-      slabs_of(ch, lo, n);
-      const uint4 *x = xs + (lo - ch * a.chunk) * (4 * NB * 32) + lane;
-      int left = a.C - lo * kSlab - 32 * c;
+  for (; cur_b <= b1; ++cur_b) {
+    int t_lo, t_hi;
+    tiles_of(cur_b, t_lo, t_hi);
+    load_x(0, true);
+    for (int tile0 = t_lo; tile0 < t_hi; tile0 += rws) {
+      const bool busy = tile0 + rw < t_hi;
+      for (int ch = 0; ch < a.chunks; ++ch) {
+        int lo = s_lo, n = s_n;
+        if (a.chunks > 1) {
+          if (ch > 0 || tile0 > t_lo) load_x(ch, false);
+          slabs_of(ch, lo, n);
+        }
+        if (!busy) n = 0;
+        const uint4 *x = xs + (lo - ch * a.chunk) * (4 * NB * 32) + lane;
+        int left = a.C - lo * kSlab - 32 * c;
 #pragma unroll 1
-      for (int d = 0; d < n; ++d) {
-        copies_wait<RING - 1>();
-        __syncwarp();  // the lanes' copies are in, for all lanes
-        compute(ring + slot, x, ch == 0 && d == 0, left);
-        slot = slot == (RING - 1) * STEP ? 0 : slot + STEP;
-        x += 4 * NB * 32;
-        left -= kSlab;
+        for (int d = 0; d < n; ++d) {
+          copies_wait<RING - 1>();
+          __syncwarp();  // the lanes' copies are in, for all lanes
+          compute(slot, x, ch == 0 && d == 0, left);
+          slot = slot == (RING - 1) * STEP ? 0 : slot + STEP;
+          x += 4 * NB * 32;
+          left -= kSlab;
+        }
       }
-    }
-    if (NB == 1) {
+      if (NB == 1) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[0][i] += acc[NS - 1][i];
-    }
-    if (FMT == MOE_Q4_MXFP4) {
-      const float f0 = exp2i((int)ref0 - 127), f1 = exp2i((int)ref1 - 127);
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        acc[b][0] *= f0;
-        acc[b][1] *= f0;
-        acc[b][2] *= f1;
-        acc[b][3] *= f1;
+        for (int i = 0; i < 4; ++i) acc[0][i] += acc[NS - 1][i];
       }
-    }
-    if (kw == 1) {
+      if (FMT == MOE_Q4_MXFP4) {
+        const float f0 = exp2i((int)ref0 - 127), f1 = exp2i((int)ref1 - 127);
 #pragma unroll
-      for (int b = 0; b < NB; ++b) store(acc[b], cur_e, cur_p0, nt, part, cur_tg * rws + rw, b);
-    } else {
-      wait_phase(empty_at + 8 * rs, rs_phase ^ 1u, a.ctrl);
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-        red[((rs * kQ4Warps + wid) * NB + b) * 32 + lane] =
-            make_float4(acc[b][0], acc[b][1], acc[b][2], acc[b][3]);
-      if (tid == 0) {
-        sh.info[rs] = make_int4(cur_e, cur_p0, nt, cur_tg);
-        sh.part[rs] = part;
+        for (int b = 0; b < NB; ++b) {
+          acc[b][0] *= f0;
+          acc[b][1] *= f0;
+          acc[b][2] *= f1;
+          acc[b][3] *= f1;
+        }
       }
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(full_at + 8 * rs);
-      // one unit late, so that the other warps' sums are there
-      if (u > 0) join(u - 1, rs == 0 ? RS - 1 : rs - 1, rs == 0 ? rs_phase ^ 1u : rs_phase);
-      if (++rs == RS) {
-        rs = 0;
-        rs_phase ^= 1u;
+      if (kw == 1) {
+        if (busy)
+#pragma unroll
+          for (int b = 0; b < NB; ++b) store(acc[b], cur_e, cur_p0, nt, part, tile0 + rw, b);
+      } else {
+        wait_phase(empty_at + 8 * rs, rs_phase ^ 1u, a.ctrl);
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          red[((rs * kQ4Warps + wid) * NB + b) * 32 + lane] =
+              make_float4(acc[b][0], acc[b][1], acc[b][2], acc[b][3]);
+        if (tid == 0) {
+          sh.info[rs] = make_int4(cur_e, cur_p0, nt, tile0);
+          sh.tile_end[rs] = t_hi;
+          sh.part[rs] = part;
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(full_at + 8 * rs);
+        // one unit late, so that the other warps' sums are there
+        if (u > 0) join(u - 1, rs == 0 ? RS - 1 : rs - 1, rs == 0 ? rs_phase ^ 1u : rs_phase);
+        if (++rs == RS) {
+          rs = 0;
+          rs_phase ^= 1u;
+        }
       }
-    }
 #pragma unroll
-    for (int b = 0; b < NS; ++b)
+      for (int b = 0; b < NS; ++b)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[b][i] = 0.f;
-    if (++cur_tg == tile_groups) {
-      cur_tg = 0;
-      ++cur_b;
+        for (int i = 0; i < 4; ++i) acc[b][i] = 0.f;
+      ++u;
     }
   }
-  if (kw > 1 && count > 0)
-    join(count - 1, rs == 0 ? RS - 1 : rs - 1, rs == 0 ? rs_phase ^ 1u : rs_phase);
+  if (kw > 1 && u > 0)
+    join(u - 1, rs == 0 ? RS - 1 : rs - 1, rs == 0 ? rs_phase ^ 1u : rs_phase);
   copies_wait<0>();
 
   if (a.mode == Q4_W2) {  // rows of no kept slot
