@@ -120,10 +120,14 @@ Q4Layout q4_layout(int64_t n, int E, int k, int H, int I) {
   return q;
 }
 
+// Codes of one 4-bit matrix at most: the kernel's offsets in one fit 32 bits.
+constexpr int64_t kMaxQ4Codes = (int64_t)1 << 36;
+
 // Sizes of the 4-bit experts: the layer's, but a rank may hold fewer experts
 // than a token selects (k > E).
 moe_status check_q4_sizes(int64_t n, int E, int k, int H, int I) {
   if (E < 1 || E > kMaxExperts) return MOE_ERR_INVALID_ARG;
+  if ((int64_t)H * I > kMaxQ4Codes / 2) return MOE_ERR_INVALID_ARG;
   return check_sizes(n, kMaxExperts, k, H, I, true);
 }
 
@@ -569,7 +573,7 @@ moe_status moe_route_backward(const float *logits, const int32_t *topk_indx, con
 moe_status moe_linear_q4(const void *x, const moe_q4_matrix *w, int64_t n, int32_t R, int32_t C,
                          int32_t dtype, void *y, moe_stream stream) {
   if (n < 0 || n >= (int64_t)INT32_MAX || R < 1 || R > (1 << 30) || C < 32 || C % 32 != 0 ||
-      C > (1 << 24))
+      C > (1 << 24) || (int64_t)R * C > kMaxQ4Codes)
     return MOE_ERR_INVALID_ARG;
   moe_status st = check_q4_dtype(dtype);
   if (st != MOE_OK) return st;

@@ -221,18 +221,19 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
       if (tid == a.E - 1) sh.cnt[a.E] = hi;
     }
     int inc = nb;
+    if (a.E > 1) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      if (lane == 31) sh.warp_sum[wid] = inc;
+      __syncthreads();
+      for (int w = 0; w < wid && w < kMaxExperts / 32; ++w) inc += sh.warp_sum[w];
     }
-    if (lane == 31) sh.warp_sum[wid] = inc;
-    __syncthreads();
-    int base = 0;
-    for (int w = 0; w < wid; ++w) base += sh.warp_sum[w];
     if (tid < a.E) {
-      sh.blk[tid] = base + inc - nb;
-      if (tid == a.E - 1) sh.blk[a.E] = base + inc;
+      sh.blk[tid] = inc - nb;
+      if (tid == a.E - 1) sh.blk[a.E] = inc;
     }
     __syncthreads();
   }
@@ -244,15 +245,17 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
   // about the time of two steps.
   const int blocks = sh.blk[a.E], tiles = (a.R + 15) / 16, in_row = min(a.slabs, a.chunk);
   int kw = 1;
+  const int64_t all = (int64_t)blocks * tiles;
+  const int64_t share = all >> 32 ? all / gridDim.x : (uint32_t)all / gridDim.x;
+  const int rest = (int)(all - share * gridDim.x);  // CTAs with one tile more
   {
-    const int64_t per_cta = ((int64_t)blocks * tiles + gridDim.x - 1) / gridDim.x;
     int64_t best = INT64_MAX;
-    for (int w = 1; w <= 8 && w <= in_row; w *= 2) {
-      const int64_t n = (per_cta * w + kQ4Warps - 1) / kQ4Warps;
-      const int64_t cost = n * ((in_row + w - 1) / w + 2);
+    for (int w = 0; w <= 3 && 1 << w <= in_row; ++w) {
+      const int64_t n = (((share + 1) << w) + kQ4Warps - 1) / kQ4Warps;
+      const int64_t cost = n * (((in_row + (1 << w) - 1) >> w) + 2);
       if (cost < best) {
         best = cost;
-        kw = w;
+        kw = 1 << w;
       }
     }
   }
@@ -265,15 +268,17 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  const int64_t all = (int64_t)blocks * tiles;
-  const int64_t t0 = all * blockIdx.x / gridDim.x, t1 = all * (blockIdx.x + 1) / gridDim.x;
+  const int64_t t0 = share * blockIdx.x + min((int)blockIdx.x, rest);
+  const int64_t t1 = t0 + share + ((int)blockIdx.x < rest ? 1 : 0);
   // the CTA's tiles [lo, hi) of a block
   auto tiles_of = [&](int b, int &lo, int &hi) {
     const int64_t at = (int64_t)b * tiles;
     lo = (int)max(t0 - at, (int64_t)0);
     hi = (int)min(t1 - at, (int64_t)tiles);
   };
-  const int b0 = (int)(t0 / tiles), b1 = t1 > t0 ? (int)((t1 - 1) / tiles) : b0 - 1;
+  const int b0 = (int)(t0 >> 32 ? t0 / tiles : (uint32_t)t0 / (uint32_t)tiles);
+  const int b1 = t1 == t0 ? b0 - 1
+                          : b0 + (int)((uint32_t)(t1 - 1 - (int64_t)b0 * tiles) / (uint32_t)tiles);
   // block b is the tb-th of expert e, the last one whose prefix is <= b
   auto where = [&](int b, int &e, int &tb) {
     int lo = 0, hi = a.E;
@@ -308,33 +313,36 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
   const int frag0 = gated && !split ? 2 * g : g, frag1 = gated && !split ? 2 * g + 1 : g + 8;
   int p_b = b0, p_tile = 0, p_end = 0, p_ch = 0;
   int p_n = 0, p_left = 0;        // steps to issue; columns left from the lane's next one
-  const uint8_t *pw0, *pw1, *ps;  // the lane's two code rows and scale words there
-  int64_t p_rows = 0;             // rows of the matrices before the block's
-  bool p_edge = false;            // a scale word may lie past the array's end
-  const uint8_t *const s_end = a.scales + a.scale_bytes;
+  // the block's matrix, and in it the lane's two code rows (in 16 bytes; a
+  // matrix has 2^36 codes at most) and its scale words (in bytes)
+  const uint8_t *p_codes = a.codes, *p_scales = a.scales;
+  uint32_t pw0 = 0, pw1 = 0, ps = 0;
+  uint32_t p_safe = 0;  // scale words from here on may pass the array's end
   auto point = [&]() {
     int lo = s_lo;
     p_n = s_n;
     if (a.chunks > 1) slabs_of(p_ch, lo, p_n);
-    const int64_t col = (int64_t)lo * (kSlab / 2) + 16 * c;
-    pw0 = a.codes + (p_rows + tile_row(p_tile, frag0)) * (a.C / 2) + col;
-    pw1 = a.codes + (p_rows + tile_row(p_tile, frag1)) * (a.C / 2) + col;
+    const uint32_t row16 = (uint32_t)a.C / 32, col16 = (uint32_t)lo * 4 + c;
+    pw0 = (uint32_t)tile_row(p_tile, frag0) * row16 + col16;
+    pw1 = (uint32_t)tile_row(p_tile, frag1) * row16 + col16;
     p_left = a.C - lo * kSlab - 32 * c;
     // whole words around the row's bytes of the slab, two lanes per row
-    ps = a.scales + ((p_rows + tile_row(p_tile, lane >> 1)) * (a.C / G) & ~(int64_t)3) +
-         lo * (kSlab / G) + 4 * (lane & 1);
-    p_edge = __any_sync(0xffffffffu, s_end - ps < (p_n - 1) * (kSlab / G) + 4);
+    ps = ((uint32_t)tile_row(p_tile, lane >> 1) * (uint32_t)(a.C / G) & ~3u) + lo * (kSlab / G) +
+         4 * (lane & 1);
   };
   auto enter = [&]() {  // the first tile of block p_b for this warp
     int e, tb, lo;
     where(p_b, e, tb);
-    p_rows = (int64_t)e * a.R;
     tiles_of(p_b, lo, p_end);
     p_tile = lo + rw;
+    p_codes = a.codes + (int64_t)e * a.R * (a.C / 2);
+    const int64_t at = (int64_t)e * a.R * (a.C / G);  // a multiple of 4 where e > 0
+    p_scales = a.scales + at;
+    p_safe = (uint32_t)min(max(a.scale_bytes - at - 3, (int64_t)0), (int64_t)UINT32_MAX);
   };
   // bytes before the array's end of a word that may pass it
   auto copy_edge = [&](uint32_t dst, const uint8_t *src) {
-    const int64_t left = s_end - src;
+    const int64_t left = a.scales + a.scale_bytes - src;
     copy4(dst, left > 0 ? src : a.scales, left >= 4 ? 4 : left > 0 ? (int)left : 0);
   };
   auto fetch = [&](uint32_t dst) {
@@ -355,24 +363,24 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
     if (p_n > 0) {
       // (a slot that is not filled keeps older codes: finite, against zero activations)
       if (p_left > 0) {
-        copy16(dst + lane * 16, pw0);
-        copy16(dst + 512 + lane * 16, pw1);
+        copy16(dst + lane * 16, p_codes + (uint64_t)pw0 * 16);
+        copy16(dst + 512 + lane * 16, p_codes + (uint64_t)pw1 * 16);
       }
       const uint32_t sdst = dst + 1024 + (lane >> 1) * (4 * SW) + (lane & 1) * 4;
-      if (!p_edge)
-        copy4(sdst, ps, 4);
+      if (ps < p_safe)
+        copy4(sdst, p_scales + ps, 4);
       else
-        copy_edge(sdst, ps);
+        copy_edge(sdst, p_scales + ps);
       if (SW == 3 && a.C % 64 != 0 && lane < 16) {
         // 8 bytes that may start inside a word: a third one
         int lo = s_lo, n = s_n;
         if (a.chunks > 1) slabs_of(p_ch, lo, n);
-        const int64_t r = p_rows + tile_row(p_tile, lane);
-        copy_edge(dst + 1024 + lane * (4 * SW) + 8, a.scales + (r * (a.C / G) & ~(int64_t)3) + 8 +
-                                                        (int64_t)(lo + n - p_n) * (kSlab / G));
+        const uint32_t at = ((uint32_t)tile_row(p_tile, lane) * (uint32_t)(a.C / G) & ~3u) + 8 +
+                            (lo + n - p_n) * (kSlab / G);
+        copy_edge(dst + 1024 + lane * (4 * SW) + 8, p_scales + at);
       }
-      pw0 += kSlab / 2;
-      pw1 += kSlab / 2;
+      pw0 += kSlab / 32;
+      pw1 += kSlab / 32;
       ps += kSlab / G;
       p_left -= kSlab;
       --p_n;
@@ -417,74 +425,70 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
                           : min(max(__ldg(a.col_sorted + cur_p0 + tid), 0), (int)a.N - 1) / a.k;
     }
     __syncthreads();  // the previous fragments are no longer read
-    // a warp takes 256 columns of one token at a time, 4 such loads in flight
+    // Four warps take a token's row together, kBatch times 8 columns per lane
+    // in flight; a row of one batch is read once, its values held until the
+    // row's largest magnitude is known.
+    constexpr int kBatch = 3, kPer = kBatch * 128;  // 8-column pieces of a batch
     const int c_lo = ch * a.chunk * kSlab;
-    const int c_hi = min(a.C, c_lo + a.chunk * kSlab);
-    if (fresh) {
-      const int segs = (a.C + 255) / 256;
-      for (int i0 = wid; i0 < nt * segs; i0 += 4 * kQ4Warps) {
-        float v[4][8];
-        int t[4];
+    const int pieces = min(a.chunk, a.slabs - ch * a.chunk) * (kSlab / 8);
+    const bool once = fresh && a.chunks == 1 && pieces <= kPer;
+#pragma unroll 1
+    for (int t4 = 0; t4 < nt; t4 += 4) {
+      const int t = t4 + (wid >> 2), q0 = (wid & 3) * 32 + lane;
+      const int64_t row = t < nt ? (int64_t)sh.row[t] * a.C : 0;
+      float x[kBatch][8];
+      auto load = [&](int col0, int from) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int i = i0 + k * kQ4Warps;
-          t[k] = i / segs;
-          const int col = (i - t[k] * segs) * 256 + lane * 8;
-          const bool in = i < nt * segs && col < a.C;
+        for (int k = 0; k < kBatch; ++k) {
+          const int col = col0 + (from + k * 128 + q0) * 8;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[k][j] = 0.f;
-          if (in) load_x8(a.x, a.x_dtype, (int64_t)sh.row[t[k]] * a.C + col, v[k]);
+          for (int j = 0; j < 8; ++j) x[k][j] = 0.f;
+          if (t < nt && col < a.C) load_x8(a.x, a.x_dtype, row + col, x[k]);
         }
+      };
+      if (fresh) {
+        uint32_t m = 0u;
+#pragma unroll 1
+        for (int from = 0; from < a.slabs * (kSlab / 8); from += kPer) {
+          load(0, from);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t m = 0u;
+          for (int k = 0; k < kBatch; ++k)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[k][j]) & 0x7fffffffu);
-          m = __reduce_max_sync(0xffffffffu, m);
-          if (lane == 0 && m != 0u) atomicMax(&sh.amax[part][t[k]], m);
+            for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(x[k][j]) & 0x7fffffffu);
         }
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == 0 && t < nt) atomicMax(&sh.amax[part][t], m);
+        __syncthreads();
       }
-      __syncthreads();
-      // the block before the last has been stored by every warp: its part of
-      // amax is free for the block after the next, past another barrier
-      if (tid < TB) sh.amax[(part + 2) & 3][tid] = 0u;
-    }
-    const int segs = (min(a.chunk, a.slabs - ch * a.chunk) + 1) / 2;  // 256 columns: two slabs
-    const int last = min(a.chunk, a.slabs - ch * a.chunk);
-    for (int i0 = wid; i0 < nt * segs; i0 += 4 * kQ4Warps) {
-      float x[4][8];
+      const uint32_t m = t < nt ? sh.amax[part][t] : 0u;
+      const float f = exp2i(row_exponent(m));
+#pragma unroll 1
+      for (int from = 0; from < pieces; from += kPer) {
+        if (!once) load(c_lo, from);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int i = i0 + k * kQ4Warps, t = i / segs;
-        const int col = c_lo + (i - t * segs) * 256 + lane * 8;
+        for (int k = 0; k < kBatch; ++k) {
+          const int at = from + k * 128 + q0;
+          if (t >= nt || at >= pieces) continue;
+          if ((m >> 23) == 255u) {  // finite values beside an infinity stay finite
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[k][j] = 0.f;
-        if (i < nt * segs && col < c_hi)
-          load_x8(a.x, a.x_dtype, (int64_t)sh.row[t] * a.C + col, x[k]);
-      }
+            for (int j = 0; j < 8; ++j)
+              if (fabsf(x[k][j]) < INFINITY) x[k][j] = fminf(fmaxf(x[k][j], -65504.f), 65504.f);
+          }
+          __half2 h[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int i = i0 + k * kQ4Warps, t = i / segs, seg = i - t * segs;
-        const int sl = 2 * seg + (lane >> 4);  // slab of the chunk
-        if (i >= nt * segs || sl >= last) continue;
-        const uint32_t m = sh.amax[part][t];
-        const float f = exp2i(row_exponent(m));
-        if ((m >> 23) == 255u) {  // finite values beside an infinity stay finite
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (fabsf(x[k][j]) < INFINITY) x[k][j] = fminf(fmaxf(x[k][j], -65504.f), 65504.f);
+          for (int j = 0; j < 4; ++j)
+            h[j] = __floats2half2_rn(x[k][2 * j] * f, x[k][2 * j + 1] * f);
+          uint4 v;
+          memcpy(&v, h, 16);
+          // at = 16 slab + 4 c + quarter
+          xs[(((at >> 4) * 4 + (at & 3)) * NB + (t >> 3)) * 32 + (t & 7) * 4 + ((at >> 2) & 3)] = v;
         }
-        __half2 h[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          h[j] = __floats2half2_rn(x[k][2 * j] * f, x[k][2 * j + 1] * f);
-        uint4 v;
-        memcpy(&v, h, 16);
-        // the lane's 8 columns: 16 to a slab, quarter lane % 4 of fragment lane c
-        xs[((sl * 4 + (lane & 3)) * NB + (t >> 3)) * 32 + (t & 7) * 4 + ((lane >> 2) & 3)] = v;
       }
     }
     __syncthreads();
+    // the block before the last has been stored by every warp: its part of
+    // amax is free for the block after the next, past another barrier
+    if (fresh && tid < TB) sh.amax[(part + 2) & 3][tid] = 0u;
   };
 
   // Sums of the unit. With one token block the two products of a quarter go
