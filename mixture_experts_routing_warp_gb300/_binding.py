@@ -378,56 +378,67 @@ def forward_gate(x: torch.Tensor, w_gate: torch.Tensor, w13: torch.Tensor, w2: t
     return out
 
 
-def _need_rows(t: torch.Tensor, name: str, shape=None, like: Optional[torch.Tensor] = None) -> None:
-    """A row tensor [rows, H] of one of the row types (`like`: of that
-    tensor's type and on its device)."""
-    if like is not None:
-        _need(t, name, like.dtype, shape)
-        _same_device(t, name, like)
-        return
+def _need_on(t: torch.Tensor, name: str, dtype: torch.dtype, device: int, shape=None) -> None:
+    """_need, and on the CUDA device of that index (a few hundred ns when all is well)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device >= 0
+            and t.is_contiguous() and (shape is None or t.shape == shape)):
+        _need(t, name, dtype, shape)
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
+
+
+def _need_rows(t: torch.Tensor, name: str) -> int:
+    """A row tensor [rows, H] of one of the row types; its device's index."""
     if not isinstance(t, torch.Tensor) or t.dtype not in DTYPE:
         raise ValueError(f"{name} must be a bfloat16, float16 or float32 tensor")
-    _need(t, name, t.dtype, shape)
+    device = t.get_device()
+    _need_on(t, name, t.dtype, device)
     if t.dim() != 2 or t.shape[1] == 0:
         raise ValueError(f"{name} must have shape [rows, H], got {tuple(t.shape)}")
+    return device
 
 
-def _same_device(t: torch.Tensor, name: str, other: torch.Tensor) -> None:
-    if t.device != other.device:
-        raise ValueError(f"{name} is on {t.device}, not on {other.device}")
-
-
-def _need_slots(meta: dict, n: int, k: int, rows: torch.Tensor) -> None:
+def _need_slots(meta: dict, slots: int, device: int) -> None:
     """The metadata entries that the row calls read: row_sorted and offs."""
-    _need(meta["row_sorted"], "row_sorted", torch.int32, (n * k,))
-    _need(meta["offs"], "offs", torch.int32)
-    if meta["offs"].dim() != 1 or meta["offs"].numel() < 2:
+    _need_on(meta["row_sorted"], "row_sorted", torch.int32, device, (slots,))
+    offs = meta["offs"]
+    _need_on(offs, "offs", torch.int32, device)
+    if offs.dim() != 1 or offs.shape[0] < 2:
         raise ValueError("offs must have one entry per expert and one more")
-    for name in ("row_sorted", "offs"):
-        _same_device(meta[name], name, rows)
 
 
-def _kept(meta: dict) -> ctypes.c_void_p:
+def _kept(meta: dict) -> int:
     """Device address of the number of kept slots: the last offset."""
     offs = meta["offs"]
-    return ctypes.c_void_p(offs.data_ptr() + 4 * (offs.numel() - 1))
+    return offs.data_ptr() + 4 * (offs.shape[0] - 1)
 
 
-def _need_weights(weights: torch.Tensor, rows: torch.Tensor) -> None:
+def _need_weights(weights: torch.Tensor, device: int) -> None:
     if not isinstance(weights, torch.Tensor) or weights.dtype not in (torch.bfloat16,
                                                                       torch.float32):
         raise ValueError("weights must be a bfloat16 or float32 tensor")
-    _need(weights, "weights", weights.dtype)
+    _need_on(weights, "weights", weights.dtype, device)
     if weights.dim() != 2:
         raise ValueError(f"weights must have shape [n, k], got {tuple(weights.shape)}")
-    _same_device(weights, "weights", rows)
 
 
 def _out_rows(out: Optional[torch.Tensor], name: str, shape, like: torch.Tensor) -> torch.Tensor:
     if out is None:
         return torch.empty(shape, dtype=like.dtype, device=like.device)
-    _need_rows(out, name, shape, like)
+    _need_on(out, name, like.dtype, like.get_device(), shape)
     return out
+
+
+def _run(name: str, device: int, *args) -> None:
+    """The library call `name`(*args, stream) on the device's current stream,
+    with that device current."""
+    fn = getattr(_LIB or lib(), name)
+    if device == torch.cuda.current_device():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+    if status != 0:
+        raise MoEError(status, name)
 
 
 def dispatch(x: torch.Tensor, meta: dict, k: int,
@@ -436,13 +447,12 @@ def dispatch(x: torch.Tensor, meta: dict, k: int,
     row row_sorted[t*k + j] is x[t]. The rows past the kept slots (an expert
     map drops some) are zero. `meta` as from route_metadata (row_sorted and
     offs are read)."""
-    _need_rows(x, "x")
+    device = _need_rows(x, "x")
     n, H = x.shape
-    _need_slots(meta, n, k, x)
+    _need_slots(meta, n * k, device)
     out = _out_rows(out, "out", (n * k, H), x)
-    with torch.cuda.device(x.device):
-        _check(lib().moe_dispatch(_ptr(x), _ptr(meta["row_sorted"]), _kept(meta), n, k, H,
-                                  DTYPE[x.dtype], _ptr(out), _stream(x.device)), "moe_dispatch")
+    _run("moe_dispatch", device, x.data_ptr(), meta["row_sorted"].data_ptr(), _kept(meta), n, k,
+         H, DTYPE[x.dtype], out.data_ptr())
     return out
 
 
@@ -450,17 +460,15 @@ def dispatch_backward(d_sorted: torch.Tensor, meta: dict, k: int,
                       out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Gradient of dispatch: d_sorted [n*k, H] -> d_x [n, H], each token the
     sum (fp32) of its kept slots' rows."""
-    _need_rows(d_sorted, "d_sorted")
+    device = _need_rows(d_sorted, "d_sorted")
     N, H = d_sorted.shape
     if k < 1 or N % k:
         raise ValueError(f"d_sorted must have n*k rows, got {N} with k = {k}")
     n = N // k
-    _need_slots(meta, n, k, d_sorted)
+    _need_slots(meta, N, device)
     out = _out_rows(out, "out", (n, H), d_sorted)
-    with torch.cuda.device(d_sorted.device):
-        _check(lib().moe_dispatch_backward(_ptr(d_sorted), _ptr(meta["row_sorted"]), n, k, H,
-                                           DTYPE[d_sorted.dtype], _ptr(out),
-                                           _stream(d_sorted.device)), "moe_dispatch_backward")
+    _run("moe_dispatch_backward", device, d_sorted.data_ptr(), meta["row_sorted"].data_ptr(), n,
+         k, H, DTYPE[d_sorted.dtype], out.data_ptr())
     return out
 
 
@@ -469,18 +477,17 @@ def combine_weighted(y_sorted: torch.Tensor, meta: dict, weights: torch.Tensor,
     """Expert-sorted rows y_sorted [n*k, H] -> [n, H]: each token the sum
     (fp32) of its kept slots' rows times weights [n, k] (bf16 as route's
     topk_vals, or fp32)."""
-    _need_rows(y_sorted, "y_sorted")
-    _need_weights(weights, y_sorted)
+    device = _need_rows(y_sorted, "y_sorted")
+    _need_weights(weights, device)
     n, k = weights.shape
-    H = y_sorted.shape[1]
-    _need_rows(y_sorted, "y_sorted", (n * k, H))
-    _need_slots(meta, n, k, y_sorted)
+    N, H = y_sorted.shape
+    if N != n * k:
+        raise ValueError(f"y_sorted must have {n * k} rows, got {N}")
+    _need_slots(meta, N, device)
     out = _out_rows(out, "out", (n, H), y_sorted)
-    with torch.cuda.device(y_sorted.device):
-        _check(lib().moe_combine_weighted(_ptr(y_sorted), _ptr(meta["row_sorted"]), _ptr(weights),
-                                          DTYPE[weights.dtype], n, k, H, DTYPE[y_sorted.dtype],
-                                          _ptr(out), _stream(y_sorted.device)),
-               "moe_combine_weighted")
+    _run("moe_combine_weighted", device, y_sorted.data_ptr(), meta["row_sorted"].data_ptr(),
+         weights.data_ptr(), DTYPE[weights.dtype], n, k, H, DTYPE[y_sorted.dtype],
+         out.data_ptr())
     return out
 
 
@@ -489,20 +496,19 @@ def combine_weighted_backward(d_out: torch.Tensor, y_sorted: torch.Tensor, meta:
     """Gradients of combine_weighted -> (d_sorted [n*k, H] of the rows' type,
     d_weights [n, k] fp32). Rows past the kept slots and the weights of
     dropped slots get zero."""
-    _need_rows(d_out, "d_out")
-    _need_weights(weights, d_out)
+    device = _need_rows(d_out, "d_out")
+    _need_weights(weights, device)
     n, k = weights.shape
     H = d_out.shape[1]
-    _need_rows(d_out, "d_out", (n, H))
-    _need_rows(y_sorted, "y_sorted", (n * k, H), d_out)
-    _need_slots(meta, n, k, d_out)
+    if d_out.shape[0] != n:
+        raise ValueError(f"d_out must have {n} rows, got {d_out.shape[0]}")
+    _need_on(y_sorted, "y_sorted", d_out.dtype, device, (n * k, H))
+    _need_slots(meta, n * k, device)
     d_sorted = torch.empty((n * k, H), dtype=d_out.dtype, device=d_out.device)
     d_weights = torch.empty((n, k), dtype=torch.float32, device=d_out.device)
-    with torch.cuda.device(d_out.device):
-        _check(lib().moe_combine_weighted_backward(
-            _ptr(d_out), _ptr(y_sorted), _ptr(meta["row_sorted"]), _ptr(weights),
-            DTYPE[weights.dtype], _kept(meta), n, k, H, DTYPE[d_out.dtype], _ptr(d_sorted),
-            _ptr(d_weights), _stream(d_out.device)), "moe_combine_weighted_backward")
+    _run("moe_combine_weighted_backward", device, d_out.data_ptr(), y_sorted.data_ptr(),
+         meta["row_sorted"].data_ptr(), weights.data_ptr(), DTYPE[weights.dtype], _kept(meta), n,
+         k, H, DTYPE[d_out.dtype], d_sorted.data_ptr(), d_weights.data_ptr())
     return d_sorted, d_weights
 
 
@@ -512,19 +518,16 @@ def route_backward(logits: torch.Tensor, topk_indx: torch.Tensor, d_vals: torch.
     _need(logits, "logits", torch.float32)
     if logits.dim() != 2:
         raise ValueError(f"logits must have shape [n, E], got {tuple(logits.shape)}")
+    device = logits.get_device()
     n, E = logits.shape
-    _need(topk_indx, "topk_indx", torch.int32)
+    _need_on(topk_indx, "topk_indx", torch.int32, device)
     if topk_indx.dim() != 2 or topk_indx.shape[0] != n:
         raise ValueError(f"topk_indx must have shape [n, k], got {tuple(topk_indx.shape)}")
     k = topk_indx.shape[1]
-    _need(d_vals, "d_vals", torch.float32, (n, k))
-    for t, name in ((topk_indx, "topk_indx"), (d_vals, "d_vals")):
-        _same_device(t, name, logits)
-    d_logits = torch.empty_like(logits)
-    with torch.cuda.device(logits.device):
-        _check(lib().moe_route_backward(_ptr(logits), _ptr(topk_indx), _ptr(d_vals), n, E, k,
-                                        GATING[gating], _ptr(d_logits), _stream(logits.device)),
-               "moe_route_backward")
+    _need_on(d_vals, "d_vals", torch.float32, device, (n, k))
+    d_logits = torch.empty((n, E), dtype=torch.float32, device=logits.device)
+    _run("moe_route_backward", device, logits.data_ptr(), topk_indx.data_ptr(),
+         d_vals.data_ptr(), n, E, k, GATING[gating], d_logits.data_ptr())
     return d_logits
 
 
@@ -546,39 +549,40 @@ class Q4Weight:
         self.count = codes.shape[0] if codes.dim() == 3 else 1
         _need(scales, "scales", torch.uint8,
               (*codes.shape[:-1], self.cols // Q4_GROUP[fmt]))
-        _same_device(scales, "scales", codes)
+        self.device = codes.get_device()
+        _need_on(scales, "scales", torch.uint8, self.device,
+                 (*codes.shape[:-1], self.cols // Q4_GROUP[fmt]))
         if matrix_scale is not None:
-            _need(matrix_scale, "matrix_scale", torch.float32, (self.count,))
-            _same_device(matrix_scale, "matrix_scale", codes)
+            _need_on(matrix_scale, "matrix_scale", torch.float32, self.device, (self.count,))
         self.codes, self.scales, self.matrix_scale, self.fmt = codes, scales, matrix_scale, fmt
         self._as_parameter_ = ctypes.byref(Q4Matrix(
             codes.data_ptr(), scales.data_ptr(),
             None if matrix_scale is None else matrix_scale.data_ptr(), Q4_FORMAT[fmt]))
 
 
-def _need_q4(w: Q4Weight, name: str, x: torch.Tensor) -> None:
+def _need_q4(w: Q4Weight, name: str, device: int) -> None:
     if not isinstance(w, Q4Weight):
         raise ValueError(f"{name} must be a Q4Weight")
-    _same_device(w.codes, name, x)
+    if w.device != device:
+        raise ValueError(f"{name} is on cuda:{w.device}, not on cuda:{device}")
 
 
-def _need_q4_x(x: torch.Tensor, name: str = "x") -> None:
-    _need_rows(x, name)
-    if x.dtype == torch.float32:
-        raise ValueError(f"{name} must be bfloat16 or float16")
+def _need_q4_x(x: torch.Tensor) -> int:
+    device = _need_rows(x, "x")
+    if x.dtype is torch.float32:
+        raise ValueError("x must be bfloat16 or float16")
+    return device
 
 
 def linear_q4(x: torch.Tensor, w: Q4Weight, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """x [n, C] (bf16 or fp16) times one 4-bit matrix [R, C] -> [n, R]."""
-    _need_q4_x(x)
-    _need_q4(w, "w", x)
+    device = _need_q4_x(x)
+    _need_q4(w, "w", device)
     n, C = x.shape
     if w.count != 1 or w.cols != C:
         raise ValueError(f"w must be one matrix of {C} columns, got {tuple(w.codes.shape)} codes")
     out = _out_rows(out, "out", (n, w.rows), x)
-    with torch.cuda.device(x.device):
-        _check(lib().moe_linear_q4(_ptr(x), w, n, w.rows, C, DTYPE[x.dtype], _ptr(out),
-                                   _stream(x.device)), "moe_linear_q4")
+    _run("moe_linear_q4", device, x.data_ptr(), w, n, w.rows, C, DTYPE[x.dtype], out.data_ptr())
     return out
 
 
@@ -599,11 +603,11 @@ def workspace_q4(n: int, E: int, k: int, H: int, I: int,
     return ws
 
 
-def _q4_experts(w13: Q4Weight, w2: Q4Weight, E: int, H: int, x: torch.Tensor,
+def _q4_experts(w13: Q4Weight, w2: Q4Weight, E: int, H: int, device: int,
                 params: MoeParams) -> int:
     """Checks the experts' matrices against each other; returns I."""
-    _need_q4(w13, "w13", x)
-    _need_q4(w2, "w2", x)
+    _need_q4(w13, "w13", device)
+    _need_q4(w2, "w2", device)
     I = w2.cols
     rows = I if params.activation == ACT["relu2"] else 2 * I
     if (w13.count, w13.rows, w13.cols) != (E, rows, H):
@@ -621,23 +625,18 @@ def grouped_ffn_q4(x: torch.Tensor, meta: dict, w13: Q4Weight, w2: Q4Weight, k: 
     fp16) -> their outputs in expert-sorted order [n*k, H], without gate
     weights (combine_weighted applies them); rows past the kept slots are
     zero. `ws` from workspace_q4."""
-    _need_q4_x(x)
+    device = _need_q4_x(x)
     n, H = x.shape
     E = w13.count if isinstance(w13, Q4Weight) else 0
-    I = _q4_experts(w13, w2, E, H, x, params)
-    _need(meta["offs"], "offs", torch.int32, (E + 1,))
-    _need(meta["col_sorted"], "col_sorted", torch.int32, (n * k,))
-    for name in ("offs", "col_sorted"):
-        _same_device(meta[name], name, x)
-    _need(ws, "ws", torch.uint8)
-    _same_device(ws, "ws", x)
+    I = _q4_experts(w13, w2, E, H, device, params)
+    offs, col_sorted = meta["offs"], meta["col_sorted"]
+    _need_on(offs, "offs", torch.int32, device, (E + 1,))
+    _need_on(col_sorted, "col_sorted", torch.int32, device, (n * k,))
+    _need_on(ws, "ws", torch.uint8, device)
     out = _out_rows(out, "out", (n * k, H), x)
-    m = RoutingMeta(None, meta["offs"].data_ptr(), meta["col_sorted"].data_ptr(), None, None)
-    with torch.cuda.device(x.device):
-        _check(lib().moe_grouped_ffn_q4(_ptr(x), ctypes.byref(m), w13, w2, n, E, k, H, I,
-                                        ctypes.byref(params), DTYPE[x.dtype], _ptr(out),
-                                        _ptr(ws), ws.numel(), _stream(x.device)),
-               "moe_grouped_ffn_q4")
+    m = RoutingMeta(None, offs.data_ptr(), col_sorted.data_ptr(), None, None)
+    _run("moe_grouped_ffn_q4", device, x.data_ptr(), ctypes.byref(m), w13, w2, n, E, k, H, I,
+         ctypes.byref(params), DTYPE[x.dtype], out.data_ptr(), ws.data_ptr(), ws.numel())
     return out
 
 
@@ -647,25 +646,32 @@ def forward_q4(x: torch.Tensor, logits: torch.Tensor, w13: Q4Weight, w2: Q4Weigh
     """forward() with 4-bit experts: route_metadata, grouped_ffn_q4 and
     combine_weighted in one library call. x and out bf16 or fp16, `ws` from
     workspace_q4."""
-    _need_q4_x(x)
+    device = _need_q4_x(x)
     n, H = x.shape
-    _need(logits, "logits", torch.float32)
+    _need_on(logits, "logits", torch.float32, device)
     if logits.dim() != 2 or logits.shape[0] != n:
         raise ValueError(f"logits must have shape [{n}, E], got {tuple(logits.shape)}")
-    _same_device(logits, "logits", x)
     E = logits.shape[1]
     E_w = params.n_local_experts if params.expert_map else E  # experts held in w13 / w2
-    I = _q4_experts(w13, w2, E_w, H, x, params)
-    _need(ws, "ws", torch.uint8)
-    _same_device(ws, "ws", x)
+    I = _q4_experts(w13, w2, E_w, H, device, params)
+    _need_on(ws, "ws", torch.uint8, device)
     out = _out_rows(out, "out", (n, H), x)
-    indx, vals = topk if topk is not None else (None, None)
-    mstruct = ctypes.byref(_meta_struct(meta)) if meta is not None else None
-    with torch.cuda.device(x.device):
-        _check(lib().moe_forward_q4(_ptr(x), _ptr(logits), w13, w2, n, E, k, H, I,
-                                    ctypes.byref(params), DTYPE[x.dtype], _ptr(out), _ptr(indx),
-                                    _ptr(vals), mstruct, _ptr(ws), ws.numel(),
-                                    _stream(x.device)), "moe_forward_q4")
+    indx = vals = None
+    if topk is not None:
+        indx, vals = topk
+        _need_on(indx, "topk_indx", torch.int32, device, (n, k))
+        _need_on(vals, "topk_vals", torch.bfloat16, device, (n, k))
+    mstruct = None
+    if meta is not None:
+        for name, dtype, size in (("col_sum", torch.int32, E_w), ("offs", torch.int32, E_w + 1),
+                                  ("col_sorted", torch.int32, n * k),
+                                  ("row_sorted", torch.int32, n * k),
+                                  ("gate_scal", torch.bfloat16, n * k)):
+            _need_on(meta[name], name, dtype, device, (size,))
+        mstruct = ctypes.byref(_meta_struct(meta))
+    _run("moe_forward_q4", device, x.data_ptr(), logits.data_ptr(), w13, w2, n, E, k, H, I,
+         ctypes.byref(params), DTYPE[x.dtype], out.data_ptr(), _ptr(indx), _ptr(vals), mstruct,
+         ws.data_ptr(), ws.numel())
     return out
 
 

@@ -17,11 +17,14 @@
 
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 namespace moe {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMaxThreads = 256;
+constexpr int kMaxRowThreads = 512;
 
 template <int B>
 struct Vec;
@@ -40,295 +43,331 @@ __device__ __forceinline__ typename Vec<B>::type vec_zero() {
 }
 
 // The B / sizeof(T) elements of a vector as floats, and back (rounded once,
-// to nearest even).
+// to nearest even); 16-bit types by pairs, one conversion instruction each.
 template <typename T, int B>
 __device__ __forceinline__ void unpack(typename Vec<B>::type v, float *f) {
-  T e[B / sizeof(T)];
-  memcpy(e, &v, B);
+  if constexpr (sizeof(T) == 4) {
+    memcpy(f, &v, B);
+  } else if constexpr (B == 2) {
+    T e;
+    memcpy(&e, &v, 2);
+    f[0] = (float)e;
+  } else {
+    uint32_t w[B / 4];
+    memcpy(w, &v, B);
 #pragma unroll
-  for (int i = 0; i < (int)(B / sizeof(T)); ++i) f[i] = (float)e[i];
+    for (int i = 0; i < B / 4; ++i) {
+      if constexpr (std::is_same_v<T, __half>) {
+        __half2 h;
+        memcpy(&h, &w[i], 4);
+        const float2 d = __half22float2(h);
+        f[2 * i] = d.x;
+        f[2 * i + 1] = d.y;
+      } else {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    }
+  }
 }
 
 template <typename T, int B>
 __device__ __forceinline__ typename Vec<B>::type pack(const float *f) {
-  T e[B / sizeof(T)];
-#pragma unroll
-  for (int i = 0; i < (int)(B / sizeof(T)); ++i) e[i] = (T)f[i];
   typename Vec<B>::type v;
-  memcpy(&v, e, B);
+  if constexpr (sizeof(T) == 4) {
+    memcpy(&v, f, B);
+  } else if constexpr (B == 2) {
+    const T e = (T)f[0];
+    memcpy(&v, &e, 2);
+  } else {
+    uint32_t w[B / 4];
+#pragma unroll
+    for (int i = 0; i < B / 4; ++i) {
+      if constexpr (std::is_same_v<T, __half>) {
+        const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+        memcpy(&w[i], &h, 4);
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        memcpy(&w[i], &h, 4);
+      }
+    }
+    memcpy(&v, w, B);
+  }
   return v;
 }
 
-__device__ __forceinline__ float load_weight(const void *w, int w_dtype, int64_t f) {
-  return w_dtype == MOE_FP32 ? __ldg(static_cast<const float *>(w) + f)
-                             : bf16_bits_to_float(__ldg(static_cast<const uint16_t *>(w) + f));
+// Positions (-1: dropped) and weights (1 where w is null) of the slots f ..
+// f + 3 as far as `left` of them exist: all loads before their first use, so
+// that the rows' loads wait for one latency and not for four.
+__device__ __forceinline__ void load_slots(const int32_t *row_sorted, const void *w, int w_dtype,
+                                           int64_t f, int left, int64_t N, int64_t *p, float *wj) {
+  int32_t at[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) at[j] = j < left ? __ldg(row_sorted + f + j) : -1;
+  if (!w) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) wj[j] = 1.f;
+  } else if (w_dtype == MOE_FP32) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      wj[j] = j < left ? __ldg(static_cast<const float *>(w) + f + j) : 0.f;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      wj[j] = j < left ? bf16_bits_to_float(__ldg(static_cast<const uint16_t *>(w) + f + j)) : 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) p[j] = at[j] >= 0 && at[j] < N ? at[j] : -1;
 }
 
-// Zeros for the rows of no kept slot, [*n_kept, N): warp `warp` of `warps`
-// takes every warps-th row, `vecs` vectors from `c0`, 32 lanes apart.
+// How a kernel's CTA covers rows: `lanes` threads (a power of two) per token's
+// row, U vectors each at a time. The whole row is in flight at once where
+// 3 * 256 vectors hold it: one row's bytes, contiguous in HBM, are then read
+// and written together (the dispatch of 8192 tokens, H 2880, k 4: 41.8 us with
+// rows in pieces of 64 vectors by different CTAs, 37.0 us so).
+struct RowMap {
+  int lanes, per_cta, vpr;  // threads per row, rows per CTA, vectors per row
+};
+
+// Zeros for the rows of no kept slot, [*n_kept, N), dealt out like tokens.
 template <int B>
-__device__ __forceinline__ void zero_tail(void *dst, const int32_t *n_kept, int64_t N, int vpr,
-                                          int c0, int c1, int64_t warp, int64_t warps) {
+__device__ __forceinline__ void zero_tail(void *dst, const int32_t *n_kept, int64_t N,
+                                          const RowMap &m, int64_t first, int lane) {
   if (!n_kept) return;
   using V = typename Vec<B>::type;
   const int64_t kept = max(__ldg(n_kept), 0);
-  for (int64_t r = kept + warp; r < N; r += warps)
-    for (int c = c0; c < c1; c += 32) static_cast<V *>(dst)[r * vpr + c] = vec_zero<B>();
+  for (int64_t r = kept + first; r < N; r += (int64_t)gridDim.x * m.per_cta)
+    for (int c = lane; c < m.vpr; c += m.lanes) static_cast<V *>(dst)[r * m.vpr + c] = vec_zero<B>();
 }
 
-// A warp copies 32 * CPL vectors (column block blockIdx.y) of one token's
-// row to the token's k sorted rows.
-template <int B, int CPL>
-__global__ void __launch_bounds__(kThreads)
+template <int B, int U>
+__global__ void __launch_bounds__(kMaxThreads)
 dispatch_kernel(const void *x, const int32_t *row_sorted, const int32_t *n_kept, int64_t n, int k,
-                int vpr, void *x_sorted) {
+                RowMap m, void *x_sorted) {
   using V = typename Vec<B>::type;
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t warps = (int64_t)gridDim.x * kWarps, N = n * k;
-  const int64_t warp = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int c0 = blockIdx.y * 32 * CPL + (threadIdx.x & 31);
-  for (int64_t t = warp; t < n; t += warps) {
-    V v[CPL];
+  const int lane = threadIdx.x & (m.lanes - 1);
+  const int64_t N = n * k, t = (int64_t)blockIdx.x * m.per_cta + threadIdx.x / m.lanes;
+  if (t < n)
+    for (int c0 = lane; c0 < m.vpr; c0 += U * m.lanes) {
+      V v[U];
 #pragma unroll
-    for (int q = 0; q < CPL; ++q)
-      if (c0 + 32 * q < vpr) v[q] = static_cast<const V *>(x)[t * vpr + c0 + 32 * q];
-    for (int j = 0; j < k; ++j) {
-      const int64_t p = __ldg(row_sorted + t * k + j);
-      if (p < 0 || p >= N) continue;
+      for (int u = 0; u < U; ++u)
+        if (c0 + u * m.lanes < m.vpr) v[u] = static_cast<const V *>(x)[t * m.vpr + c0 + u * m.lanes];
+      for (int j0 = 0; j0 < k; j0 += 4) {
+        int64_t p[4];
+        float one[4];
+        load_slots(row_sorted, nullptr, MOE_FP32, t * k + j0, k - j0, N, p, one);
 #pragma unroll
-      for (int q = 0; q < CPL; ++q)
-        if (c0 + 32 * q < vpr) static_cast<V *>(x_sorted)[p * vpr + c0 + 32 * q] = v[q];
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (p[j] >= 0 && c0 + u * m.lanes < m.vpr)
+              static_cast<V *>(x_sorted)[p[j] * m.vpr + c0 + u * m.lanes] = v[u];
+      }
     }
-  }
-  zero_tail<B>(x_sorted, n_kept, N, vpr, c0, min(vpr, (int)(blockIdx.y + 1) * 32 * CPL), warp,
-               warps);
+  zero_tail<B>(x_sorted, n_kept, N, m, t, lane);
 }
 
-// A warp sums 32 * CPL vectors of one token's k sorted rows. Four rows are in
-// flight at a time; `w` null: all weights 1 (the dispatch's backward pass).
-template <typename T, int B, int CPL>
-__global__ void __launch_bounds__(kThreads)
+// One vector per thread and row, four rows in flight; blockDim.x threads along
+// the row, blockDim.y tokens. `w` null: all weights 1 (the dispatch's backward
+// pass). One vector a thread keeps the kernel at 40 registers and the SM full:
+// three vectors a thread measured 98 us where this takes 70 (16384 tokens,
+// H 2880, k 4). The sums leave by streaming stores (74 us without).
+template <typename T, int B>
+__global__ void __launch_bounds__(kMaxRowThreads, 3)
 combine_weighted_kernel(const void *y_sorted, const int32_t *row_sorted, const void *w,
                         int w_dtype, int64_t n, int k, int vpr, void *out) {
   using V = typename Vec<B>::type;
   constexpr int EPV = B / sizeof(T);
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t warps = (int64_t)gridDim.x * kWarps, N = n * k;
-  const int64_t warp = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int c0 = blockIdx.y * 32 * CPL + (threadIdx.x & 31);
-  for (int64_t t = warp; t < n; t += warps) {
-    float acc[CPL][EPV] = {};
+  const int64_t N = n * k, t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  if (t >= n) return;
+  for (int c = threadIdx.x; c < vpr; c += blockDim.x) {
+    float acc[EPV] = {};
     for (int j0 = 0; j0 < k; j0 += 4) {
-      V v[4][CPL];
+      V v[4];
+      int64_t p[4];
       float wj[4];
-      bool live[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t f = t * k + j0 + j;
-        const int64_t p = j0 + j < k ? __ldg(row_sorted + f) : -1;
-        live[j] = p >= 0 && p < N;
-        wj[j] = live[j] && w ? load_weight(w, w_dtype, f) : 1.f;
-#pragma unroll
-        for (int q = 0; q < CPL; ++q)
-          v[j][q] = live[j] && c0 + 32 * q < vpr
-                        ? __ldcs(static_cast<const V *>(y_sorted) + p * vpr + c0 + 32 * q)
-                        : vec_zero<B>();
-      }
+      load_slots(row_sorted, w, w_dtype, t * k + j0, k - j0, N, p, wj);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (live[j])
+        v[j] = p[j] >= 0 ? __ldcs(static_cast<const V *>(y_sorted) + p[j] * vpr + c)
+                         : vec_zero<B>();
 #pragma unroll
-          for (int q = 0; q < CPL; ++q) {
-            float f[EPV];
-            unpack<T, B>(v[j][q], f);
+      for (int j = 0; j < 4; ++j)
+        if (p[j] >= 0) {
+          float f[EPV];
+          unpack<T, B>(v[j], f);
 #pragma unroll
-            for (int i = 0; i < EPV; ++i) acc[q][i] = fmaf(wj[j], f[i], acc[q][i]);
-          }
+          for (int i = 0; i < EPV; ++i) acc[i] = fmaf(wj[j], f[i], acc[i]);
+        }
     }
-#pragma unroll
-    for (int q = 0; q < CPL; ++q)
-      if (c0 + 32 * q < vpr)
-        static_cast<V *>(out)[t * vpr + c0 + 32 * q] = pack<T, B>(acc[q]);
+    __stcs(static_cast<V *>(out) + t * vpr + c, pack<T, B>(acc));
   }
 }
 
-// WPT warps hold one token: each reads its share of d_out[t] once, writes the
-// k scaled copies and adds up the k dot products with the sorted rows; the
-// dot products are joined over lanes, then over the WPT warps.
-template <typename T, int B, int WPT>
-__global__ void __launch_bounds__(kThreads)
+// A row's threads read their share of d_out[t] once, write the k scaled
+// copies and add up the k dot products with the sorted rows; those are joined
+// over lanes, then over the row's warps. K: 4, or 8 where k > 4.
+template <typename T, int B, int U, int K>
+__global__ void __launch_bounds__(kMaxThreads, U == 3 ? 2 : 3)
 combine_backward_kernel(const void *d_out, const void *y_sorted, const int32_t *row_sorted,
                         const void *w, int w_dtype, const int32_t *n_kept, int64_t n, int k,
-                        int vpr, void *d_sorted, float *d_weights) {
+                        RowMap m, void *d_sorted, float *d_weights) {
   using V = typename Vec<B>::type;
-  constexpr int EPV = B / sizeof(T), TPB = kWarps / WPT;
-  __shared__ float s_dot[TPB][WPT][kMaxTopk];
+  constexpr int EPV = B / sizeof(T);
+  __shared__ float s_dot[kMaxThreads / 32][K];
   pdl_wait();
   pdl_launch_dependents();
-  const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int slot = wid / WPT, part = wid % WPT;
-  const int64_t N = n * k;
-  // every warp of a block makes the same number of rounds (__syncthreads)
-  for (int64_t t0 = (int64_t)blockIdx.x * TPB; t0 < n; t0 += (int64_t)gridDim.x * TPB) {
-    const int64_t t = t0 + slot;
-    float dot[kMaxTopk] = {};
-    if (t < n) {
-      int64_t p[kMaxTopk];
-      float wj[kMaxTopk];
+  const int lane = threadIdx.x & (m.lanes - 1), wid = threadIdx.x >> 5;
+  const int64_t N = n * k, t = (int64_t)blockIdx.x * m.per_cta + threadIdx.x / m.lanes;
+  float dot[K] = {};
+  if (t < n) {
+#pragma unroll 1
+    for (int c0 = lane; c0 < m.vpr; c0 += U * m.lanes) {
+      V g[U];
 #pragma unroll
-      for (int j = 0; j < kMaxTopk; ++j) {
-        p[j] = j < k ? __ldg(row_sorted + t * k + j) : -1;
-        if (p[j] >= N) p[j] = -1;
-        wj[j] = p[j] >= 0 ? load_weight(w, w_dtype, t * k + j) : 0.f;
-      }
-      for (int c = part * 32 + lane; c < vpr; c += WPT * 32) {
-        float d[EPV];
-        unpack<T, B>(static_cast<const V *>(d_out)[t * vpr + c], d);
+      for (int u = 0; u < U; ++u)
+        g[u] = c0 + u * m.lanes < m.vpr
+                   ? __ldcs(static_cast<const V *>(d_out) + t * m.vpr + c0 + u * m.lanes)
+                   : vec_zero<B>();
 #pragma unroll
-        for (int j0 = 0; j0 < kMaxTopk; j0 += 4) {
-          if (j0 >= k) break;
-          V v[4];
+      for (int j0 = 0; j0 < K; j0 += 4) {
+        if (j0 >= k) break;
+        V v[4][U];
+        int64_t p[4];
+        float wj[4];
+        load_slots(row_sorted, w, w_dtype, t * k + j0, k - j0, N, p, wj);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            v[j] = p[j0 + j] >= 0
-                       ? __ldcs(static_cast<const V *>(y_sorted) + p[j0 + j] * vpr + c)
-                       : vec_zero<B>();
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (p[j0 + j] >= 0) {
-              float f[EPV], g[EPV];
-              unpack<T, B>(v[j], f);
+          for (int u = 0; u < U; ++u)
+            v[j][u] = p[j] >= 0 && c0 + u * m.lanes < m.vpr
+                          ? __ldcs(static_cast<const V *>(y_sorted) + p[j] * m.vpr + c0 +
+                                   u * m.lanes)
+                          : vec_zero<B>();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (p[j] >= 0)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              if (c0 + u * m.lanes >= m.vpr) continue;
+              float d[EPV], f[EPV], o[EPV];
+              unpack<T, B>(g[u], d);
+              unpack<T, B>(v[j][u], f);
 #pragma unroll
               for (int i = 0; i < EPV; ++i) {
                 dot[j0 + j] = fmaf(d[i], f[i], dot[j0 + j]);
-                g[i] = wj[j0 + j] * d[i];
+                o[i] = wj[j] * d[i];
               }
-              static_cast<V *>(d_sorted)[p[j0 + j] * vpr + c] = pack<T, B>(g);
+              static_cast<V *>(d_sorted)[p[j] * m.vpr + c0 + u * m.lanes] = pack<T, B>(o);
             }
-        }
       }
-    }
-#pragma unroll
-    for (int j = 0; j < kMaxTopk; ++j)
-      if (j < k)
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
-    if (WPT == 1) {
-#pragma unroll
-      for (int j = 0; j < kMaxTopk; ++j)
-        if (t < n && j < k && lane == j) d_weights[t * k + j] = dot[j];
-    } else {
-#pragma unroll
-      for (int j = 0; j < kMaxTopk; ++j)
-        if (lane == 0 && j < k) s_dot[slot][part][j] = dot[j];
-      __syncthreads();
-      if (part == 0 && lane < k && t < n) {
-        float sum = 0.f;
-#pragma unroll
-        for (int q = 0; q < WPT; ++q) sum += s_dot[slot][q][lane];
-        d_weights[t * k + lane] = sum;
-      }
-      __syncthreads();
     }
   }
-  const int64_t warps = (int64_t)gridDim.x * kWarps;
-  zero_tail<B>(d_sorted, n_kept, N, vpr, lane, vpr, (int64_t)blockIdx.x * kWarps + wid, warps);
+#pragma unroll
+  for (int j = 0; j < K; ++j)
+    if (j < k) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
+      if ((threadIdx.x & 31) == 0) s_dot[wid][j] = dot[j];
+    }
+  __syncthreads();
+  if (t < n && lane < k) {
+    float sum = 0.f;
+    for (int q = 0; q < m.lanes / 32; ++q) sum += s_dot[wid + q][lane];
+    d_weights[t * k + lane] = sum;
+  }
+  zero_tail<B>(d_sorted, n_kept, N, m, t, lane);
 }
 
 // dz = p * (up - <p, up>) over the softmax's support (the k selected experts
-// or all E), up = d_vals at the selected experts and 0 elsewhere. G lanes
-// hold one token's E logits, V of them per load, NQ loads per lane.
-template <int V, int NQ>
+// or all E), up = d_vals at the selected experts and 0 elsewhere. G lanes hold
+// one token's E logits, V of them per load, NQ loads per lane; every lane
+// looks through the k selected ids for its own experts, so that no load waits
+// for another, and the two sums of the softmax are joined over the lanes
+// together. One group per token: a chain of one load, some 100 instructions
+// and two joins, so tokens are best all in flight at once. K: 4, or 8 where k > 4.
+template <int V, int NQ, int K>
 __global__ void __launch_bounds__(kThreads)
 route_backward_kernel(const float *logits, const int32_t *topk_indx, const float *d_vals,
                       int64_t n, int E, int k, int gating, int G, float *d_logits) {
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, g = lane & (G - 1);
-  const int64_t groups = (int64_t)gridDim.x * (kThreads / G);
+  const int g = threadIdx.x & (G - 1);
   const bool all = gating == MOE_GATING_SOFTMAX_ALL;
-  // every lane of a warp makes the same number of rounds (full-warp shuffles)
-  for (int64_t t0 = ((int64_t)blockIdx.x * kThreads + (threadIdx.x & ~31)) / G; t0 < n;
-       t0 += groups) {
-    const int64_t t = t0 + lane / G;
-    const bool on = t < n;
-    float z[NQ][V];
-    float top = -INFINITY;
-    if (all) {
+  const int64_t t = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / G;
+  const bool on = t < n;
+  float z[NQ][V], up[NQ][V];
 #pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        const int e = (q * G + g) * V;
+  for (int q = 0; q < NQ; ++q) {
+    const int e = (q * G + g) * V;
 #pragma unroll
-        for (int i = 0; i < V; ++i) z[q][i] = -INFINITY;
-        if (on && e < E) {
-          if (V == 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(logits + t * E + e);
-            z[q][0] = v.x, z[q][V > 1 ? 1 : 0] = v.y, z[q][V > 2 ? 2 : 0] = v.z;
-            z[q][V > 3 ? 3 : 0] = v.w;
-          } else {
-            z[q][0] = logits[t * E + e];
-          }
+    for (int i = 0; i < V; ++i) {
+      z[q][i] = -INFINITY;
+      up[q][i] = 0.f;
+    }
+    if (on && e < E) {
+      if constexpr (V == 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(logits + t * E + e);
+        z[q][0] = v.x, z[q][1] = v.y, z[q][2] = v.z, z[q][3] = v.w;
+      } else {
+        z[q][0] = logits[t * E + e];
+      }
+    }
+  }
+  int idx[K];
+  float d[K];
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    idx[j] = on && j < k ? __ldg(topk_indx + t * k + j) : -1;
+    d[j] = on && j < k ? __ldg(d_vals + t * k + j) : 0.f;
+  }
+  float top = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < NQ; ++q)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = (q * G + g) * V + i;
+      bool chosen = false;
+#pragma unroll
+      for (int j = 0; j < K; ++j)
+        if (j < k && idx[j] == e) {
+          up[q][i] = d[j];
+          chosen = true;
         }
-#pragma unroll
-        for (int i = 0; i < V; ++i) top = fmaxf(top, z[q][i]);
-      }
+      if (!all && !chosen) z[q][i] = -INFINITY;
+      top = fmaxf(top, z[q][i]);
     }
-    // the k selected: every lane of the group holds all of them
-    int idx[kMaxTopk];
-    float up[kMaxTopk], zs[kMaxTopk];
+  for (int o = G >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float den = 0.f, dot = 0.f;
 #pragma unroll
-    for (int j = 0; j < kMaxTopk; ++j) {
-      idx[j] = on && j < k ? __ldg(topk_indx + t * k + j) : -1;
-      if (idx[j] >= E) idx[j] = -1;
-      up[j] = idx[j] >= 0 ? __ldg(d_vals + t * k + j) : 0.f;
-      zs[j] = idx[j] >= 0 ? __ldg(logits + t * E + idx[j]) : -INFINITY;
-      top = fmaxf(top, zs[j]);
+  for (int q = 0; q < NQ; ++q)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      z[q][i] = z[q][i] == -INFINITY ? 0.f : expf(z[q][i] - top);
+      den += z[q][i];
+      dot = fmaf(z[q][i], up[q][i], dot);
     }
-    if (all)
-      for (int o = G >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float den = 0.f, mean = 0.f, p[kMaxTopk];
-    if (all) {
+  for (int o = G >> 1; o > 0; o >>= 1) {
+    den += __shfl_xor_sync(0xffffffffu, den, o);
+    dot += __shfl_xor_sync(0xffffffffu, dot, o);
+  }
+  const float scale = den > 0.f ? 1.f / den : 0.f, mean = dot * scale;
 #pragma unroll
-      for (int q = 0; q < NQ; ++q)
+  for (int q = 0; q < NQ; ++q) {
+    const int e = (q * G + g) * V;
+    if (!on || e >= E) continue;
+    float o[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          z[q][i] = z[q][i] == -INFINITY ? 0.f : expf(z[q][i] - top);
-          den += z[q][i];
-        }
-      for (int o = G >> 1; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-    }
-#pragma unroll
-    for (int j = 0; j < kMaxTopk; ++j) {
-      p[j] = idx[j] >= 0 ? expf(zs[j] - top) : 0.f;
-      if (!all) den += p[j];
-    }
-#pragma unroll
-    for (int j = 0; j < kMaxTopk; ++j)
-      if (idx[j] >= 0) {
-        p[j] /= den;
-        mean = fmaf(p[j], up[j], mean);
-      }
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-      const int e = (q * G + g) * V;
-      float o[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        o[i] = all ? -(z[q][i] / den) * mean : 0.f;
-#pragma unroll
-        for (int j = 0; j < kMaxTopk; ++j)
-          if (idx[j] == e + i) o[i] = p[j] * (up[j] - mean);
-      }
-      if (on && e < E) {
-        if (V == 4)
-          *reinterpret_cast<float4 *>(d_logits + t * E + e) =
-              make_float4(o[0], o[V > 1 ? 1 : 0], o[V > 2 ? 2 : 0], o[V > 3 ? 3 : 0]);
-        else
-          d_logits[t * E + e] = o[0];
-      }
-    }
+    for (int i = 0; i < V; ++i) o[i] = z[q][i] * scale * (up[q][i] - mean);
+    if constexpr (V == 4)
+      *reinterpret_cast<float4 *>(d_logits + t * E + e) = make_float4(o[0], o[1], o[2], o[3]);
+    else
+      d_logits[t * E + e] = o[0];
   }
 }
 
@@ -341,39 +380,59 @@ inline int vec_bytes(size_t row_bytes, const void *a, const void *b) {
   return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
 }
 
-// Column blocks of 32 * cpl vectors on y, enough CTAs on x for one warp per
-// token, at most 16 per SM in all.
-inline dim3 row_grid(int64_t n, int vpr, int cpl) {
-  const int64_t gy = (vpr + 32 * cpl - 1) / (32 * cpl);
-  int64_t gx = (n + kWarps - 1) / kWarps;
-  const int64_t cap = ((int64_t)device_sm_count() * 16 + gy - 1) / gy;
-  if (gx > cap) gx = cap;
-  return dim3((unsigned)gx, (unsigned)gy);
+// The fewest threads per row (32, 64, 128 or 256) with at most 3 vectors each;
+// rows beyond 768 vectors go round.
+inline RowMap row_map(int vpr) {
+  int lanes = 32;
+  while (lanes < kMaxThreads && vpr > 3 * lanes) lanes *= 2;
+  const int cta = lanes < kThreads ? kThreads : lanes;
+  return {lanes, cta / lanes, vpr};
 }
 
+// These kernels keep the default split of L1 and shared memory: with the
+// library's usual one (all shared) L1 is too small for the rows in flight, and
+// the combine above takes 96 us in place of 70.
 template <auto Kern, typename... Args>
-cudaError_t go(dim3 grid, cudaStream_t s, Args... args) {
-  static PerDeviceOnce configured;
-  cudaError_t err = configured.run([] { return uniform_carveout(Kern); });
-  if (err != cudaSuccess) return err;
-  err = launch_dependent(Kern, grid, dim3(kThreads), 0, s, args...);
+cudaError_t go(dim3 grid, dim3 block, cudaStream_t s, Args... args) {
+  const cudaError_t err = launch_dependent(Kern, grid, block, 0, s, args...);
   return err == cudaSuccess ? cudaGetLastError() : err;
 }
+
+// One CTA per per_cta tokens; F<U>::kern is the kernel for U vectors a thread.
+template <template <int> class F, typename... Args>
+cudaError_t go_rows(int64_t n, const RowMap &m, cudaStream_t s, Args... args) {
+  const dim3 grid((unsigned)((n + m.per_cta - 1) / m.per_cta));
+  const dim3 threads(m.lanes * m.per_cta);
+  if (m.vpr <= m.lanes) return go<F<1>::kern>(grid, threads, s, args...);
+  if (m.vpr <= 2 * m.lanes) return go<F<2>::kern>(grid, threads, s, args...);
+  return go<F<3>::kern>(grid, threads, s, args...);
+}
+template <int B>
+struct Dispatch {
+  template <int U>
+  struct F {
+    static constexpr auto kern = dispatch_kernel<B, U>;
+  };
+};
+template <typename T, int B, int K>
+struct Backward {
+  template <int U>
+  struct F {
+    static constexpr auto kern = combine_backward_kernel<T, B, U, K>;
+  };
+};
 
 }  // namespace
 
 cudaError_t launch_dispatch(const void *x, const int32_t *row_sorted, const int32_t *n_kept,
                             int64_t n, int k, int H, int dtype, void *x_sorted, cudaStream_t s) {
   const size_t rb = (size_t)H * elem_bytes(dtype);
-  const int vb = vec_bytes(rb, x, x_sorted), vpr = (int)(rb / vb);
+  const int vb = vec_bytes(rb, x, x_sorted);
+  const RowMap m = row_map((int)(rb / vb));
   if (vb == 16)
-    return go<dispatch_kernel<16, 2>>(row_grid(n, vpr, 2), s, x, row_sorted, n_kept, n, k, vpr,
-              x_sorted);
-  if (vb == 4)
-    return go<dispatch_kernel<4, 4>>(row_grid(n, vpr, 4), s, x, row_sorted, n_kept, n, k, vpr,
-              x_sorted);
-  return go<dispatch_kernel<2, 4>>(row_grid(n, vpr, 4), s, x, row_sorted, n_kept, n, k, vpr,
-            x_sorted);
+    return go_rows<Dispatch<16>::F>(n, m, s, x, row_sorted, n_kept, n, k, m, x_sorted);
+  if (vb == 4) return go_rows<Dispatch<4>::F>(n, m, s, x, row_sorted, n_kept, n, k, m, x_sorted);
+  return go_rows<Dispatch<2>::F>(n, m, s, x, row_sorted, n_kept, n, k, m, x_sorted);
 }
 
 template <typename T>
@@ -381,15 +440,17 @@ static cudaError_t combine_typed(const void *y, const int32_t *row_sorted, const
                                  int64_t n, int k, int H, void *out, cudaStream_t s) {
   const size_t rb = (size_t)H * sizeof(T);
   const int vb = vec_bytes(rb, y, out), vpr = (int)(rb / vb);
+  // a thread per vector of the row, rows of up to 128 vectors several to a CTA
+  int lanes = (vpr + 31) / 32 * 32;
+  if (lanes > kMaxRowThreads) lanes = kMaxRowThreads;
+  const int per_cta = lanes < 256 ? 256 / lanes : 1;
+  const dim3 grid((unsigned)((n + per_cta - 1) / per_cta)), block(lanes, per_cta);
   if (vb == 16)
-    return go<combine_weighted_kernel<T, 16, 2>>(row_grid(n, vpr, 2), s, y, row_sorted, w, wd, n,
-              k, vpr, out);
+    return go<combine_weighted_kernel<T, 16>>(grid, block, s, y, row_sorted, w, wd, n, k, vpr, out);
   if (vb == 4)
-    return go<combine_weighted_kernel<T, 4, 4>>(row_grid(n, vpr, 4), s, y, row_sorted, w, wd, n,
-              k, vpr, out);
+    return go<combine_weighted_kernel<T, 4>>(grid, block, s, y, row_sorted, w, wd, n, k, vpr, out);
   if constexpr (sizeof(T) == 2)
-    return go<combine_weighted_kernel<T, 2, 4>>(row_grid(n, vpr, 4), s, y, row_sorted, w, wd, n,
-              k, vpr, out);
+    return go<combine_weighted_kernel<T, 2>>(grid, block, s, y, row_sorted, w, wd, n, k, vpr, out);
   return cudaErrorInvalidValue;
 }
 
@@ -403,38 +464,24 @@ cudaError_t launch_combine_weighted(const void *y_sorted, const int32_t *row_sor
   return combine_typed<__nv_bfloat16>(y_sorted, row_sorted, weights, w_dtype, n, k, H, out, s);
 }
 
-template <typename T, int B>
-static cudaError_t backward_vec(const void *d_out, const void *y, const int32_t *row_sorted,
-                                const void *w, int wd, const int32_t *n_kept, int64_t n, int k,
-                                int vpr, void *d_sorted, float *dw, cudaStream_t s) {
-  // Rows beyond a couple of vectors per lane are shared by the block's four warps.
-  const bool wide = vpr > 64;
-  int64_t blocks = wide ? n : (n + kWarps - 1) / kWarps;
-  const int64_t cap = (int64_t)device_sm_count() * 16;
-  if (blocks > cap) blocks = cap;
-  const dim3 grid((unsigned)blocks);
-  if (wide)
-    return go<combine_backward_kernel<T, B, kWarps>>(grid, s, d_out, y, row_sorted, w, wd, n_kept,
-              n, k, vpr, d_sorted, dw);
-  return go<combine_backward_kernel<T, B, 1>>(grid, s, d_out, y, row_sorted, w, wd, n_kept, n, k,
-            vpr, d_sorted, dw);
-}
-
 template <typename T>
 static cudaError_t backward_typed(const void *d_out, const void *y, const int32_t *row_sorted,
                                   const void *w, int wd, const int32_t *n_kept, int64_t n, int k,
                                   int H, void *d_sorted, float *dw, cudaStream_t s) {
   const size_t rb = (size_t)H * sizeof(T);
-  int vb = vec_bytes(rb, d_out, y);
-  if (vec_bytes(rb, d_sorted, d_sorted) < vb) vb = vec_bytes(rb, d_sorted, d_sorted);
-  const int vpr = (int)(rb / vb);
-  if (vb == 16)
-    return backward_vec<T, 16>(d_out, y, row_sorted, w, wd, n_kept, n, k, vpr, d_sorted, dw, s);
-  if (vb == 4)
-    return backward_vec<T, 4>(d_out, y, row_sorted, w, wd, n_kept, n, k, vpr, d_sorted, dw, s);
-  if constexpr (sizeof(T) == 2)
-    return backward_vec<T, 2>(d_out, y, row_sorted, w, wd, n_kept, n, k, vpr, d_sorted, dw, s);
+  const int va = vec_bytes(rb, d_out, y), vd = vec_bytes(rb, d_sorted, d_sorted);
+  const int vb = va < vd ? va : vd;
+  const RowMap m = row_map((int)(rb / vb));
+#define MOE_BACKWARD(B_)                                                                       \
+  return k <= 4 ? go_rows<Backward<T, B_, 4>::template F>(n, m, s, d_out, y, row_sorted, w, wd, \
+                                                          n_kept, n, k, m, d_sorted, dw)       \
+                : go_rows<Backward<T, B_, 8>::template F>(n, m, s, d_out, y, row_sorted, w, wd, \
+                                                          n_kept, n, k, m, d_sorted, dw)
+  if (vb == 16) MOE_BACKWARD(16);
+  if (vb == 4) MOE_BACKWARD(4);
+  if constexpr (sizeof(T) == 2) MOE_BACKWARD(2);
   return cudaErrorInvalidValue;
+#undef MOE_BACKWARD
 }
 
 cudaError_t launch_combine_backward(const void *d_out, const void *y_sorted,
@@ -459,13 +506,14 @@ cudaError_t launch_route_backward(const float *logits, const int32_t *topk_indx,
   int G = 1;
   while (G < 32 && G < per) G *= 2;
   const int nq = (per + G - 1) / G;
-  int64_t blocks = (n * G + kThreads - 1) / kThreads;
-  const int64_t cap = (int64_t)device_sm_count() * 16;
-  if (blocks > cap) blocks = cap;
-  const dim3 grid((unsigned)blocks);
-#define MOE_ROUTE_BACKWARD(V_, NQ_)                                                            \
-  return go<route_backward_kernel<V_, NQ_>>(grid, s, logits, topk_indx, d_vals, n, E, k, gating, \
-            G, d_logits)
+  const dim3 grid((unsigned)((n * G + kThreads - 1) / kThreads));
+#define MOE_ROUTE_BACKWARD(V_, NQ_)                                                          \
+  return k <= 4 ? go<route_backward_kernel<V_, NQ_, 4>>(grid, dim3(kThreads), s, logits,     \
+                                                        topk_indx, d_vals, n, E, k, gating, \
+                                                        G, d_logits)                         \
+                : go<route_backward_kernel<V_, NQ_, 8>>(grid, dim3(kThreads), s, logits,     \
+                                                        topk_indx, d_vals, n, E, k, gating, \
+                                                        G, d_logits)
   if (vec) {
     if (nq == 1) MOE_ROUTE_BACKWARD(4, 1);
     MOE_ROUTE_BACKWARD(4, 2);
