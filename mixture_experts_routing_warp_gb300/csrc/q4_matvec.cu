@@ -29,6 +29,8 @@
 //    vanish. The sum is scaled back in fp32.
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "tc_ptx.cuh"
 
 namespace moe {
@@ -40,10 +42,11 @@ constexpr int kSlab = 128;         // columns per warp step: 32 per lane of a qu
 constexpr int kSlabXBytes = 2048;  // fp16 fragments of 8 tokens x 128 columns
 constexpr int kSmemMax = 226 * 1024;  // dynamic and static shared memory of a CTA
 
-// Shared memory of one step: the lanes' codes of two rows each, 16 bytes a
-// lane and row, then the 16 rows' scales as whole 4-byte words.
-__host__ __device__ constexpr int scale_words(int fmt) { return fmt == MOE_Q4_MXFP4 ? 2 : 3; }
-__host__ __device__ constexpr int step_bytes(int fmt) { return 1024 + 64 * scale_words(fmt); }
+// Shared memory of one step (two slabs): the lanes' codes of two rows each,
+// 16 bytes a lane, row and slab, then the 16 rows' scales as whole 4-byte
+// words, one word more than they fill where they start inside one.
+__host__ __device__ constexpr int scale_words(int fmt) { return fmt == MOE_Q4_MXFP4 ? 3 : 5; }
+__host__ __device__ constexpr int step_bytes(int fmt) { return 2048 + 64 * scale_words(fmt); }
 // Units whose partial sums may be on their way to the warps that join them.
 __host__ __device__ constexpr int red_slots(int nb) { return nb == 1 ? 3 : 2; }
 
@@ -105,10 +108,20 @@ __device__ __forceinline__ void mma16816(float *d, const uint32_t *a, uint32_t b
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Asynchronous copies to shared memory (of a word, `bytes` are read and the
-// rest filled with zeros); one group per warp step.
+// Asynchronous copies to shared memory, AT and FROM bytes past the addresses
+// (of a word, `bytes` are read and the rest filled with zeros); one group per
+// warp step.
+template <int AT, int FROM>
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src), "n"(AT),
+               "n"(FROM)
+               : "memory");
+}
+template <int AT, int FROM>
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0 + %2], [%1 + %3], 4;" ::"r"(dst), "l"(src), "n"(AT),
+               "n"(FROM)
+               : "memory");
 }
 __device__ __forceinline__ void copy4(uint32_t dst, const void *src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
@@ -130,31 +143,6 @@ __device__ __forceinline__ void wait_phase(uint32_t bar, uint32_t parity, uint32
       record_status(ctrl, MOE_ERR_TIMEOUT);
       return;
     }
-}
-
-// Eight consecutive activations (16-byte aligned) as floats.
-__device__ __forceinline__ void load_x8(const void *x, int dtype, int64_t i, float *f) {
-  if (dtype == MOE_FP32) {
-    const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(x) + i);
-    const float4 u = p[0], v = p[1];
-    f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w;
-    f[4] = v.x, f[5] = v.y, f[6] = v.z, f[7] = v.w;
-    return;
-  }
-  const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(x) + i);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (dtype == MOE_FP16) {
-      __half2 h;
-      memcpy(&h, &w[j], 4);
-      f[2 * j] = __low2float(h);
-      f[2 * j + 1] = __high2float(h);
-    } else {
-      f[2 * j] = __uint_as_float(w[j] << 16);
-      f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-    }
-  }
 }
 
 // 2^e as a float, e in [-127, 127].
@@ -180,6 +168,72 @@ struct Q4Shared {
 __device__ __forceinline__ int row_exponent(uint32_t amax) {
   const int ex = (int)(amax >> 23);
   return amax == 0u || ex == 255 ? 0 : min(14 + 127 - ex, 126);
+}
+
+// Sums of a unit. With one token block the two products of a quarter go to
+// sums of their own, which halves the chain of dependent instructions.
+template <int NB>
+struct Q4Sums {
+  static constexpr int N = NB == 1 ? 2 : NB;
+  float v[N][4];
+};
+
+// One slab's products into d: the lane's codes of two rows times m0 / m1 (a
+// half-pair each for columns 0..15 and 16..31 of its 32).
+template <int NB>
+__device__ __forceinline__ void products(Q4Sums<NB> &d, const uint4 &c0, const uint4 &c1,
+                                         const uint4 *x, const uint32_t *m0, const uint32_t *m1) {
+  const uint32_t w0[4] = {c0.x, c0.y, c0.z, c0.w};
+  const uint32_t w1[4] = {c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t v0[4], v1[4], A[2][4];
+    e2m1x8_to_half2(w0[q], v0);
+    e2m1x8_to_half2(w1[q], v1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        A[i][2 * h] = hmul2(v0[2 * i + h], m0[q >> 1]);
+        A[i][2 * h + 1] = hmul2(v1[2 * i + h], m1[q >> 1]);
+      }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const uint4 f = x[(q * NB + b) * 32];
+      mma16816(d.v[b], A[0], f.x, f.y);
+      mma16816(d.v[NB == 1 ? 1 : b], A[1], f.z, f.w);
+    }
+  }
+}
+
+// An MXFP4 slab whose scales do not fit one reference: one group per row at a
+// time, the lanes c = j. A call, so that its registers are its own.
+template <int NB>
+__device__ __noinline__ Q4Sums<NB> products_far(Q4Sums<NB> acc, uint4 c0, uint4 c1,
+                                                const uint4 *x, uint32_t s0, uint32_t s1,
+                                                uint32_t ref0, uint32_t ref1) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t t0 = __shfl_sync(0xffffffffu, s0, (lane & ~3) + j);
+    const uint32_t t1 = __shfl_sync(0xffffffffu, s1, (lane & ~3) + j);
+    const uint32_t one = (lane & 3) == j ? 0x3c003c00u : 0u;
+    const uint32_t m[2] = {one, one};
+    Q4Sums<NB> d = {};
+    products<NB>(d, c0, c1, x, m, m);
+    // 2^(t - ref) in two factors, each in range
+    const int h0 = ((int)t0 - (int)ref0) / 2, h1 = ((int)t1 - (int)ref1) / 2;
+    const float a0 = t0 == 255u ? NAN : exp2i(h0), b0 = exp2i((int)t0 - (int)ref0 - h0);
+    const float a1 = t1 == 255u ? NAN : exp2i(h1), b1 = exp2i((int)t1 - (int)ref1 - h1);
+#pragma unroll
+    for (int b = 0; b < Q4Sums<NB>::N; ++b) {
+      acc.v[b][0] = fmaf(d.v[b][0] * a0, b0, acc.v[b][0]);
+      acc.v[b][1] = fmaf(d.v[b][1] * a0, b0, acc.v[b][1]);
+      acc.v[b][2] = fmaf(d.v[b][2] * a1, b1, acc.v[b][2]);
+      acc.v[b][3] = fmaf(d.v[b][3] * a1, b1, acc.v[b][3]);
+    }
+  }
+  return acc;
 }
 
 // FMT: moe_q4_format; NB: blocks of 8 tokens per unit; RING: steps of weights
@@ -312,7 +366,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
   };
   const int frag0 = gated && !split ? 2 * g : g, frag1 = gated && !split ? 2 * g + 1 : g + 8;
   int p_b = b0, p_tile = 0, p_end = 0, p_ch = 0;
-  int p_n = 0, p_left = 0;        // steps to issue; columns left from the lane's next one
+  int p_n = 0, p_left = 0;  // slabs to issue; columns left from the lane's next one
   // the block's matrix, and in it the lane's two code rows (in 16 bytes; a
   // matrix has 2^36 codes at most) and its scale words (in bytes)
   const uint8_t *p_codes = a.codes, *p_scales = a.scales;
@@ -338,15 +392,20 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
     p_codes = a.codes + (int64_t)e * a.R * (a.C / 2);
     const int64_t at = (int64_t)e * a.R * (a.C / G);  // a multiple of 4 where e > 0
     p_scales = a.scales + at;
-    p_safe = (uint32_t)min(max(a.scale_bytes - at - 3, (int64_t)0), (int64_t)UINT32_MAX);
+    p_safe = (uint32_t)min(max(a.scale_bytes - at - (4 * SW - 1), (int64_t)0),
+                           (int64_t)UINT32_MAX);
   };
   // bytes before the array's end of a word that may pass it
+  const uint32_t lane_at = tc::smem_u32(ring) + lane * 16;
+  const uint32_t scales_at =
+      tc::smem_u32(ring) + 2048 + (lane >> 1) * (4 * SW) + (lane & 1) * 4;
   auto copy_edge = [&](uint32_t dst, const uint8_t *src) {
     const int64_t left = a.scales + a.scale_bytes - src;
     copy4(dst, left > 0 ? src : a.scales, left >= 4 ? 4 : left > 0 ? (int)left : 0);
   };
-  auto fetch = [&](uint32_t dst) {
-    if (p_n == 0 && p_b <= b1) {  // on to the next chunk, the next tile, the next block
+  const bool words_fit = a.C % (SW == 3 ? 128 : 64) == 0;  // every row starts on a word
+  auto fetch = [&](uint32_t slot) {
+    if (p_n <= 0 && p_b <= b1) {  // on to the next chunk, the next tile, the next block
       do {
         if (p_tile >= p_end || ++p_ch == a.chunks) {
           p_ch = 0;
@@ -358,53 +417,45 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
           }
         }
         point();
-      } while (p_n == 0);
+      } while (p_n <= 0);
     }
     if (p_n > 0) {
-      // (a slot that is not filled keeps older codes: finite, against zero activations)
+      // (places that are not filled keep older codes: finite, against zero activations)
+      const uint32_t dst = lane_at + slot;
+      const uint8_t *w0 = p_codes + (uint64_t)pw0 * 16, *w1 = p_codes + (uint64_t)pw1 * 16;
       if (p_left > 0) {
-        copy16(dst + lane * 16, p_codes + (uint64_t)pw0 * 16);
-        copy16(dst + 512 + lane * 16, p_codes + (uint64_t)pw1 * 16);
+        copy16<0, 0>(dst, w0);
+        copy16<512, 0>(dst, w1);
       }
-      const uint32_t sdst = dst + 1024 + (lane >> 1) * (4 * SW) + (lane & 1) * 4;
-      if (ps < p_safe)
-        copy4(sdst, p_scales + ps, 4);
-      else
-        copy_edge(sdst, p_scales + ps);
-      if (SW == 3 && a.C % 64 != 0 && lane < 16) {
-        // 8 bytes that may start inside a word: a third one
-        int lo = s_lo, n = s_n;
-        if (a.chunks > 1) slabs_of(p_ch, lo, n);
-        const uint32_t at = ((uint32_t)tile_row(p_tile, lane) * (uint32_t)(a.C / G) & ~3u) + 8 +
-                            (lo + n - p_n) * (kSlab / G);
-        copy_edge(dst + 1024 + lane * (4 * SW) + 8, p_scales + at);
+      if (p_n > 1 && p_left > kSlab) {
+        copy16<1024, kSlab / 2>(dst, w0);
+        copy16<1536, kSlab / 2>(dst, w1);
       }
-      pw0 += kSlab / 32;
-      pw1 += kSlab / 32;
-      ps += kSlab / G;
-      p_left -= kSlab;
-      --p_n;
+      const uint32_t sdst = scales_at + slot;
+      const uint8_t *src = p_scales + ps;
+      if (ps < p_safe) {
+        copy4<0, 0>(sdst, src);
+        if (SW == 5) copy4<8, 8>(sdst, src);
+        if (!words_fit && (lane & 1) == 0) copy4<4 * (SW - 1), 4 * (SW - 1)>(sdst, src);
+      } else {
+        copy_edge(sdst, src);
+        if (SW == 5) copy_edge(sdst + 8, src + 8);
+        if (!words_fit && (lane & 1) == 0) copy_edge(sdst + 4 * (SW - 1), src + 4 * (SW - 1));
+      }
+      pw0 += 2 * kSlab / 32;
+      pw1 += 2 * kSlab / 32;
+      ps += 2 * kSlab / G;
+      p_left -= 2 * kSlab;
+      p_n -= 2;
     }
     copies_commit();  // a group per step, also past the end: the waits count groups
   };
-  const uint32_t ring_at = tc::smem_u32(ring);
-  if (b0 <= b1) {
-    enter();
-    if (p_tile < p_end) point();
-  }
-#pragma unroll 1
-  for (int d = 0; d < RING; ++d) fetch(ring_at + d * STEP);
   // where the lane's scales lie in a step: fixed, as tiles are 8 or 16 rows
   // apart and several matrices have a multiple of 64 rows
   const int s_at0 =
-      1024 + frag0 * (4 * SW) + ((uint32_t)tile_row(rw, frag0) * (a.C / G) & 3) + c * (32 / G);
+      2048 + frag0 * (4 * SW) + ((uint32_t)tile_row(rw, frag0) * (a.C / G) & 3) + c * (32 / G);
   const int s_at1 =
-      1024 + frag1 * (4 * SW) + ((uint32_t)tile_row(rw, frag1) * (a.C / G) & 3) + c * (32 / G);
-
-  if (a.mode == Q4_W2) {
-    pdl_wait();
-    pdl_launch_dependents();
-  }
+      2048 + frag1 * (4 * SW) + ((uint32_t)tile_row(rw, frag1) * (a.C / G) & 3) + c * (32 / G);
 
   // ---- activations of a token block as fp16 B fragments: for slab s, quarter
   // q and token block b, lane (g, c) finds columns 128 s + 32 c + 8 q .. + 7 of
@@ -412,6 +463,100 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
   // end reaches only sums that are dropped.
   int nt = 0, part = 3, cur_e = 0, cur_p0 = 0;  // tokens of the block; its part of sh.amax
   int cur_b = b0;
+  // BYTES of an activation: 4 warps (fp32; 2 for 16 bits) take a token's row
+  // together, 3 (6) times 8 columns per lane in flight. A row that fits is
+  // read once, its values held until the row's largest magnitude is known.
+  auto load_rows = [&](auto bytes, int ch, bool fresh) {
+    constexpr int WPT = decltype(bytes)::value, BATCH = 12 / WPT, PER = BATCH * 32 * WPT;
+    constexpr int RAW = WPT / 2;  // 16-byte words of 8 columns
+    const int c_lo = ch * a.chunk * kSlab;
+    const int pieces = min(a.chunk, a.slabs - ch * a.chunk) * (kSlab / 8);
+    const bool once = fresh && a.chunks == 1 && pieces <= PER;
+#pragma unroll 1
+    for (int t0 = 0; t0 < nt; t0 += kQ4Warps / WPT) {
+      const int t = t0 + wid / WPT, q0 = wid % WPT * 32 + lane;
+      const uint4 *row = reinterpret_cast<const uint4 *>(
+          static_cast<const char *>(a.x) + (t < nt ? (int64_t)sh.row[t] * a.C * WPT : 0));
+      uint4 raw[BATCH][RAW];
+      auto load = [&](int col0, int from) {
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+          const int at = from + k * 32 * WPT + q0;
+#pragma unroll
+          for (int i = 0; i < RAW; ++i) {
+            raw[k][i] = make_uint4(0u, 0u, 0u, 0u);
+            if (t < nt && col0 + at * 8 < a.C) raw[k][i] = row[(col0 / 8 + at) * RAW + i];
+          }
+        }
+      };
+      auto floats = [&](const uint4 *r, float *f) {
+        const uint32_t w[4] = {r[0].x, r[0].y, r[0].z, r[0].w};
+        if constexpr (WPT == 4) {
+          const uint32_t v[4] = {r[RAW - 1].x, r[RAW - 1].y, r[RAW - 1].z, r[RAW - 1].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            f[j] = __uint_as_float(w[j]);
+            f[4 + j] = __uint_as_float(v[j]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (a.x_dtype == MOE_FP16) {
+              __half2 h;
+              memcpy(&h, &w[j], 4);
+              f[2 * j] = __low2float(h);
+              f[2 * j + 1] = __high2float(h);
+            } else {
+              f[2 * j] = __uint_as_float(w[j] << 16);
+              f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+            }
+          }
+        }
+      };
+      if (fresh) {
+        uint32_t m = 0u;
+#pragma unroll 1
+        for (int from = 0; from < a.slabs * (kSlab / 8); from += PER) {
+          load(0, from);
+#pragma unroll
+          for (int k = 0; k < BATCH; ++k) {
+            float v[8];
+            floats(raw[k], v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+          }
+        }
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == 0 && t < nt) atomicMax(&sh.amax[part][t], m);
+        __syncthreads();
+      }
+      const uint32_t m = t < nt ? sh.amax[part][t] : 0u;
+      const float f = exp2i(row_exponent(m));
+#pragma unroll 1
+      for (int from = 0; from < pieces; from += PER) {
+        if (!once) load(c_lo, from);
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+          const int at = from + k * 32 * WPT + q0;
+          if (t >= nt || at >= pieces) continue;
+          float x[8];
+          floats(raw[k], x);
+          if ((m >> 23) == 255u) {  // finite values beside an infinity stay finite
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (fabsf(x[j]) < INFINITY) x[j] = fminf(fmaxf(x[j], -65504.f), 65504.f);
+          }
+          __half2 h[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) h[j] = __floats2half2_rn(x[2 * j] * f, x[2 * j + 1] * f);
+          uint4 v;
+          memcpy(&v, h, 16);
+          // at = 16 slab + 4 c + quarter
+          xs[(((at >> 4) * 4 + (at & 3)) * NB + (t >> 3)) * 32 + (t & 7) * 4 + ((at >> 2) & 3)] = v;
+        }
+      }
+    }
+  };
   auto load_x = [&](int ch, bool fresh) {
     if (fresh) {
       int tb;
@@ -425,130 +570,62 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
                           : min(max(__ldg(a.col_sorted + cur_p0 + tid), 0), (int)a.N - 1) / a.k;
     }
     __syncthreads();  // the previous fragments are no longer read
-    // Four warps take a token's row together, kBatch times 8 columns per lane
-    // in flight; a row of one batch is read once, its values held until the
-    // row's largest magnitude is known.
-    constexpr int kBatch = 3, kPer = kBatch * 128;  // 8-column pieces of a batch
-    const int c_lo = ch * a.chunk * kSlab;
-    const int pieces = min(a.chunk, a.slabs - ch * a.chunk) * (kSlab / 8);
-    const bool once = fresh && a.chunks == 1 && pieces <= kPer;
-#pragma unroll 1
-    for (int t4 = 0; t4 < nt; t4 += 4) {
-      const int t = t4 + (wid >> 2), q0 = (wid & 3) * 32 + lane;
-      const int64_t row = t < nt ? (int64_t)sh.row[t] * a.C : 0;
-      float x[kBatch][8];
-      auto load = [&](int col0, int from) {
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int col = col0 + (from + k * 128 + q0) * 8;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[k][j] = 0.f;
-          if (t < nt && col < a.C) load_x8(a.x, a.x_dtype, row + col, x[k]);
-        }
-      };
-      if (fresh) {
-        uint32_t m = 0u;
-#pragma unroll 1
-        for (int from = 0; from < a.slabs * (kSlab / 8); from += kPer) {
-          load(0, from);
-#pragma unroll
-          for (int k = 0; k < kBatch; ++k)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(x[k][j]) & 0x7fffffffu);
-        }
-        m = __reduce_max_sync(0xffffffffu, m);
-        if (lane == 0 && t < nt) atomicMax(&sh.amax[part][t], m);
-        __syncthreads();
-      }
-      const uint32_t m = t < nt ? sh.amax[part][t] : 0u;
-      const float f = exp2i(row_exponent(m));
-#pragma unroll 1
-      for (int from = 0; from < pieces; from += kPer) {
-        if (!once) load(c_lo, from);
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int at = from + k * 128 + q0;
-          if (t >= nt || at >= pieces) continue;
-          if ((m >> 23) == 255u) {  // finite values beside an infinity stay finite
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (fabsf(x[k][j]) < INFINITY) x[k][j] = fminf(fmaxf(x[k][j], -65504.f), 65504.f);
-          }
-          __half2 h[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            h[j] = __floats2half2_rn(x[k][2 * j] * f, x[k][2 * j + 1] * f);
-          uint4 v;
-          memcpy(&v, h, 16);
-          // at = 16 slab + 4 c + quarter
-          xs[(((at >> 4) * 4 + (at & 3)) * NB + (t >> 3)) * 32 + (t & 7) * 4 + ((at >> 2) & 3)] = v;
-        }
-      }
-    }
+    if (a.x_dtype == MOE_FP32)
+      load_rows(std::integral_constant<int, 4>{}, ch, fresh);
+    else
+      load_rows(std::integral_constant<int, 2>{}, ch, fresh);
     __syncthreads();
     // the block before the last has been stored by every warp: its part of
     // amax is free for the block after the next, past another barrier
     if (fresh && tid < TB) sh.amax[(part + 2) & 3][tid] = 0u;
   };
 
-  // Sums of the unit. With one token block the two products of a quarter go
-  // to sums of their own, which halves the chain of dependent instructions.
-  constexpr int NS = NB == 1 ? 2 : NB;
-  float acc[NS][4] = {};
+  // The first block's activations come before the weights, whose copies would
+  // keep them waiting; but the Q4_W2 launch may only fetch weights until the
+  // one before it is done.
+  if (b0 <= b1) {
+    if (a.mode != Q4_W2) load_x(0, true);
+    enter();
+    if (p_tile < p_end) point();
+  }
+#pragma unroll 1
+  for (int d = 0; d < RING; ++d) fetch(d * STEP);
+  if (a.mode == Q4_W2) {
+    pdl_wait();
+    pdl_launch_dependents();
+    if (b0 <= b1) load_x(0, true);
+  }
+
+  constexpr int NS = Q4Sums<NB>::N;
+  Q4Sums<NB> acc = {};
   uint32_t ref0 = 127u, ref1 = 127u;  // MXFP4: the rows' reference scales
 
-  // one step's products into d: the lane's codes times m0 / m1 (a half-pair
-  // each for columns 0..15 and 16..31 of its 32)
-  auto products = [&](float (*d)[4], const uint4 &c0, const uint4 &c1, const uint4 *x,
-                      const uint32_t *m0, const uint32_t *m1) {
-    const uint32_t w0[4] = {c0.x, c0.y, c0.z, c0.w};
-    const uint32_t w1[4] = {c1.x, c1.y, c1.z, c1.w};
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t v0[4], v1[4], A[2][4];
-      e2m1x8_to_half2(w0[q], v0);
-      e2m1x8_to_half2(w1[q], v1);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          A[i][2 * h] = hmul2(v0[2 * i + h], m0[q >> 1]);
-          A[i][2 * h + 1] = hmul2(v1[2 * i + h], m1[q >> 1]);
-        }
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const uint4 f = x[(q * NB + b) * 32];
-        mma16816(d[b], A[0], f.x, f.y);
-        mma16816(d[NB == 1 ? 1 : b], A[1], f.z, f.w);
-      }
-    }
-  };
-  // a step: slab `left` columns before the row's end for this lane
-  auto compute = [&](int slot, const uint4 *x, bool fresh, int left) {
-    const unsigned char *st = ring + slot;
-    const uint4 c0 = *reinterpret_cast<const uint4 *>(st + lane * 16);
-    const uint4 c1 = *reinterpret_cast<const uint4 *>(st + 512 + lane * 16);
-    // columns past the row's end have zero codes, and no scale of theirs
-    const bool in = left > 0;
+  // A slab of a step: H 0 or 1, `left` columns before the row's end for this
+  // lane (columns past it have no codes and scales of their own, and
+  // activations of zero: any finite weight will do). `then` runs when the
+  // slab's codes and scales are read.
+  auto slab = [&](auto which, const unsigned char *st, const uint4 *x, bool fresh, int left,
+                  auto then) {
+    constexpr int H = decltype(which)::value;
+    const uint4 c0 = *reinterpret_cast<const uint4 *>(st + H * 1024 + lane * 16);
+    const uint4 c1 = *reinterpret_cast<const uint4 *>(st + H * 1024 + 512 + lane * 16);
     if (FMT == MOE_Q4_NVFP4) {
-      const uint32_t h0 =
-          e4m3x2_to_half2(in ? *reinterpret_cast<const uint16_t *>(st + s_at0) : 0u);
-      const uint32_t h1 =
-          e4m3x2_to_half2(in ? *reinterpret_cast<const uint16_t *>(st + s_at1) : 0u);
-      __syncwarp();  // read by all: the slot takes the step RING ahead
-      fetch(ring_at + slot);
+      uint32_t s0 = *reinterpret_cast<const uint16_t *>(st + s_at0 + H * 8);
+      uint32_t s1 = *reinterpret_cast<const uint16_t *>(st + s_at1 + H * 8);
+      then();
+      if (left <= 0) s0 = s1 = 0u;
+      const uint32_t h0 = e4m3x2_to_half2(s0), h1 = e4m3x2_to_half2(s1);
       const uint32_t m0[2] = {__byte_perm(h0, h0, 0x1010), __byte_perm(h0, h0, 0x3232)};
       const uint32_t m1[2] = {__byte_perm(h1, h1, 0x1010), __byte_perm(h1, h1, 0x3232)};
-      products(acc, c0, c1, x, m0, m1);
+      products<NB>(acc, c0, c1, x, m0, m1);
     } else {
-      uint32_t s0 = st[s_at0], s1 = st[s_at1];
-      __syncwarp();
-      fetch(ring_at + slot);
+      uint32_t s0 = st[s_at0 + H * 4], s1 = st[s_at1 + H * 4];
+      then();
       if (fresh) {  // the unit's first step: each row's reference, where 2^(s - ref) has room
         ref0 = min(max(__shfl_sync(0xffffffffu, s0, lane & ~3), 96u), 158u);
         ref1 = min(max(__shfl_sync(0xffffffffu, s1, lane & ~3), 96u), 158u);
       }
-      if (!in) {
+      if (left <= 0) {
         s0 = ref0;
         s1 = ref1;
       }
@@ -557,29 +634,25 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
       const uint32_t e0 = (uint32_t)(d0 + 15) * 0x04000400u, e1 = (uint32_t)(d1 + 15) * 0x04000400u;
       if (!__any_sync(0xffffffffu, far)) {
         const uint32_t m0[2] = {e0, e0}, m1[2] = {e1, e1};
-        products(acc, c0, c1, x, m0, m1);
+        products<NB>(acc, c0, c1, x, m0, m1);
       } else {
-#pragma unroll 1
-        for (int j = 0; j < 4; ++j) {  // the lanes c = j of every row: one group per row
-          const uint32_t t0 = __shfl_sync(0xffffffffu, s0, (lane & ~3) + j);
-          const uint32_t t1 = __shfl_sync(0xffffffffu, s1, (lane & ~3) + j);
-          const uint32_t one = c == j ? 0x3c003c00u : 0u;
-          const uint32_t m[2] = {one, one};
-          float d[NS][4] = {};
-          products(d, c0, c1, x, m, m);
-          // 2^(t - ref) in two factors, each in range
-          const int h0 = ((int)t0 - (int)ref0) / 2, h1 = ((int)t1 - (int)ref1) / 2;
-          const float a0 = t0 == 255u ? NAN : exp2i(h0), b0 = exp2i((int)t0 - (int)ref0 - h0);
-          const float a1 = t1 == 255u ? NAN : exp2i(h1), b1 = exp2i((int)t1 - (int)ref1 - h1);
-#pragma unroll
-          for (int b = 0; b < NS; ++b) {
-            acc[b][0] = fmaf(d[b][0] * a0, b0, acc[b][0]);
-            acc[b][1] = fmaf(d[b][1] * a0, b0, acc[b][1]);
-            acc[b][2] = fmaf(d[b][2] * a1, b1, acc[b][2]);
-            acc[b][3] = fmaf(d[b][3] * a1, b1, acc[b][3]);
-          }
-        }
+        acc = products_far<NB>(acc, c0, c1, x, s0, s1, ref0, ref1);
       }
+    }
+  };
+  // a step of two slabs, or one at a row's end; its place takes the step RING
+  // ahead as soon as it is read by all lanes
+  auto compute = [&](int slot, const uint4 *x, bool fresh, int left, bool two) {
+    const unsigned char *st = ring + slot;
+    auto refill = [&] {
+      __syncwarp();
+      fetch(slot);
+    };
+    if (two) {
+      slab(std::integral_constant<int, 0>{}, st, x, fresh, left, [] {});
+      slab(std::integral_constant<int, 1>{}, st, x + 4 * NB * 32, false, left - kSlab, refill);
+    } else {
+      slab(std::integral_constant<int, 0>{}, st, x, fresh, left, refill);
     }
   };
   // The finished sums v of one row tile and token block: fragment rows g and
@@ -641,7 +714,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
   for (; cur_b <= b1; ++cur_b) {
     int t_lo, t_hi;
     tiles_of(cur_b, t_lo, t_hi);
-    load_x(0, true);
+    if (cur_b > b0) load_x(0, true);
     for (int tile0 = t_lo; tile0 < t_hi; tile0 += rws) {
       const bool busy = tile0 + rw < t_hi;
       for (int ch = 0; ch < a.chunks; ++ch) {
@@ -654,39 +727,39 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
         const uint4 *x = xs + (lo - ch * a.chunk) * (4 * NB * 32) + lane;
         int left = a.C - lo * kSlab - 32 * c;
 #pragma unroll 1
-        for (int d = 0; d < n; ++d) {
+        for (int d = 0; d < n; d += 2) {
           copies_wait<RING - 1>();
           __syncwarp();  // the lanes' copies are in, for all lanes
-          compute(slot, x, ch == 0 && d == 0, left);
+          compute(slot, x, ch == 0 && d == 0, left, d + 1 < n);
           slot = slot == (RING - 1) * STEP ? 0 : slot + STEP;
-          x += 4 * NB * 32;
-          left -= kSlab;
+          x += 2 * 4 * NB * 32;
+          left -= 2 * kSlab;
         }
       }
       if (NB == 1) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[0][i] += acc[NS - 1][i];
+        for (int i = 0; i < 4; ++i) acc.v[0][i] += acc.v[NS - 1][i];
       }
       if (FMT == MOE_Q4_MXFP4) {
         const float f0 = exp2i((int)ref0 - 127), f1 = exp2i((int)ref1 - 127);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          acc[b][0] *= f0;
-          acc[b][1] *= f0;
-          acc[b][2] *= f1;
-          acc[b][3] *= f1;
+          acc.v[b][0] *= f0;
+          acc.v[b][1] *= f0;
+          acc.v[b][2] *= f1;
+          acc.v[b][3] *= f1;
         }
       }
       if (kw == 1) {
         if (busy)
 #pragma unroll
-          for (int b = 0; b < NB; ++b) store(acc[b], cur_e, cur_p0, nt, part, tile0 + rw, b);
+          for (int b = 0; b < NB; ++b) store(acc.v[b], cur_e, cur_p0, nt, part, tile0 + rw, b);
       } else {
         wait_phase(empty_at + 8 * rs, rs_phase ^ 1u, a.ctrl);
 #pragma unroll
         for (int b = 0; b < NB; ++b)
           red[((rs * kQ4Warps + wid) * NB + b) * 32 + lane] =
-              make_float4(acc[b][0], acc[b][1], acc[b][2], acc[b][3]);
+              make_float4(acc.v[b][0], acc.v[b][1], acc.v[b][2], acc.v[b][3]);
         if (tid == 0) {
           sh.info[rs] = make_int4(cur_e, cur_p0, nt, tile0);
           sh.tile_end[rs] = t_hi;
@@ -704,7 +777,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
 #pragma unroll
       for (int b = 0; b < NS; ++b)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[b][i] = 0.f;
+        for (int i = 0; i < 4; ++i) acc.v[b][i] = 0.f;
       ++u;
     }
   }
@@ -758,9 +831,9 @@ template <int FMT>
 cudaError_t launch_sized(Q4Args &a, cudaStream_t s) {
   a.slabs = (a.C + kSlab - 1) / kSlab;
   const bool two = a.N > 8 * (int64_t)(a.offs ? a.E / 2 : 1);
-  if (two && a.slabs <= slabs_that_fit<FMT, 2, 4>()) return launch<FMT, 2, 4>(a, s);
-  if (a.slabs <= slabs_that_fit<FMT, 1, 8>()) return launch<FMT, 1, 8>(a, s);
-  return launch<FMT, 1, 4>(a, s);
+  if (two && a.slabs <= slabs_that_fit<FMT, 2, 2>()) return launch<FMT, 2, 2>(a, s);
+  if (a.slabs <= slabs_that_fit<FMT, 1, 4>()) return launch<FMT, 1, 4>(a, s);
+  return launch<FMT, 1, 2>(a, s);
 }
 
 cudaError_t launch_format(Q4Args &a, int format, cudaStream_t s) {
