@@ -42,11 +42,17 @@ constexpr int kSlab = 128;         // columns per warp step: 32 per lane of a qu
 constexpr int kSlabXBytes = 2048;  // fp16 fragments of 8 tokens x 128 columns
 constexpr int kSmemMax = 226 * 1024;  // dynamic and static shared memory of a CTA
 
-// Shared memory of one step (two slabs): the lanes' codes of two rows each,
-// 16 bytes a lane, row and slab, then the 16 rows' scales as whole 4-byte
+// Slabs per step. Two halve the waits and the ring's bookkeeping: NVFP4, 64
+// tokens of the GPT-OSS experts, 170 -> 154 us. MXFP4 needs more registers for
+// its scales and spills with two: 154 -> 199 us, so it takes one.
+__host__ __device__ constexpr int step_slabs(int fmt) { return fmt == MOE_Q4_MXFP4 ? 1 : 2; }
+// Shared memory of one step: the lanes' codes of two rows each, 16 bytes a
+// lane, row and slab, then the 16 rows' scales (4 bytes; 16) as whole 4-byte
 // words, one word more than they fill where they start inside one.
-__host__ __device__ constexpr int scale_words(int fmt) { return fmt == MOE_Q4_MXFP4 ? 3 : 5; }
-__host__ __device__ constexpr int step_bytes(int fmt) { return 2048 + 64 * scale_words(fmt); }
+__host__ __device__ constexpr int scale_words(int fmt) { return fmt == MOE_Q4_MXFP4 ? 2 : 5; }
+__host__ __device__ constexpr int step_bytes(int fmt) {
+  return 1024 * step_slabs(fmt) + 64 * scale_words(fmt);
+}
 // Units whose partial sums may be on their way to the warps that join them.
 __host__ __device__ constexpr int red_slots(int nb) { return nb == 1 ? 3 : 2; }
 
@@ -159,6 +165,7 @@ struct Q4Shared {
   int cnt[kMaxExperts + 1];  // first slot of each expert (offs)
   int blk[kMaxExperts + 1];  // exclusive prefix of the experts' token blocks
   int warp_sum[kQ4Warps];
+  int64_t t0, t1;            // the CTA's row tiles
   int row[8 * NB];           // the block's rows of x
   uint32_t amax[4][8 * NB];  // largest magnitude of each token's row (bits), by block
 };
@@ -207,33 +214,52 @@ __device__ __forceinline__ void products(Q4Sums<NB> &d, const uint4 &c0, const u
 }
 
 // An MXFP4 slab whose scales do not fit one reference: one group per row at a
-// time, the lanes c = j. A call, so that its registers are its own.
+// time, the lanes c = j. Rare (no quantiser spreads a row's scales over 2^26),
+// so it is kept small: a quarter at a time, codes read where they are used.
 template <int NB>
-__device__ __noinline__ Q4Sums<NB> products_far(Q4Sums<NB> acc, uint4 c0, uint4 c1,
-                                                const uint4 *x, uint32_t s0, uint32_t s1,
-                                                uint32_t ref0, uint32_t ref1) {
+__device__ __forceinline__ void products_far(Q4Sums<NB> &acc, const unsigned char *codes,
+                                             const uint4 *x, uint32_t s0, uint32_t s1,
+                                             uint32_t ref0, uint32_t ref1) {
   const int lane = threadIdx.x & 31;
 #pragma unroll 1
   for (int j = 0; j < 4; ++j) {
+    const uint32_t one = (lane & 3) == j ? 0x3c003c00u : 0u;
+    float d[NB][4] = {};
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+      uint32_t v0[4], v1[4];
+      e2m1x8_to_half2(*reinterpret_cast<const uint32_t *>(codes + 4 * q), v0);
+      e2m1x8_to_half2(*reinterpret_cast<const uint32_t *>(codes + 512 + 4 * q), v1);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t A[4] = {hmul2(v0[2 * i], one), hmul2(v1[2 * i], one),
+                               hmul2(v0[2 * i + 1], one), hmul2(v1[2 * i + 1], one)};
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const uint4 f = x[(q * NB + b) * 32];
+          mma16816(d[b], A, i ? f.z : f.x, i ? f.w : f.y);
+        }
+      }
+    }
+    // 2^(t - ref) in two factors, each in range
     const uint32_t t0 = __shfl_sync(0xffffffffu, s0, (lane & ~3) + j);
     const uint32_t t1 = __shfl_sync(0xffffffffu, s1, (lane & ~3) + j);
-    const uint32_t one = (lane & 3) == j ? 0x3c003c00u : 0u;
-    const uint32_t m[2] = {one, one};
-    Q4Sums<NB> d = {};
-    products<NB>(d, c0, c1, x, m, m);
-    // 2^(t - ref) in two factors, each in range
     const int h0 = ((int)t0 - (int)ref0) / 2, h1 = ((int)t1 - (int)ref1) / 2;
     const float a0 = t0 == 255u ? NAN : exp2i(h0), b0 = exp2i((int)t0 - (int)ref0 - h0);
     const float a1 = t1 == 255u ? NAN : exp2i(h1), b1 = exp2i((int)t1 - (int)ref1 - h1);
 #pragma unroll
-    for (int b = 0; b < Q4Sums<NB>::N; ++b) {
-      acc.v[b][0] = fmaf(d.v[b][0] * a0, b0, acc.v[b][0]);
-      acc.v[b][1] = fmaf(d.v[b][1] * a0, b0, acc.v[b][1]);
-      acc.v[b][2] = fmaf(d.v[b][2] * a1, b1, acc.v[b][2]);
-      acc.v[b][3] = fmaf(d.v[b][3] * a1, b1, acc.v[b][3]);
+    for (int b = 0; b < NB; ++b) {
+      acc.v[b][0] = fmaf(d[b][0] * a0, b0, acc.v[b][0]);
+      acc.v[b][1] = fmaf(d[b][1] * a0, b0, acc.v[b][1]);
+      acc.v[b][2] = fmaf(d[b][2] * a1, b1, acc.v[b][2]);
+      acc.v[b][3] = fmaf(d[b][3] * a1, b1, acc.v[b][3]);
     }
   }
-  return acc;
+}
+
+// Only this variant's launches may have rows too long to be resident.
+constexpr bool in_chunks(int fmt, int nb, int ring) {
+  return nb == 1 && ring * step_slabs(fmt) == 4;
 }
 
 // FMT: moe_q4_format; NB: blocks of 8 tokens per unit; RING: steps of weights
@@ -243,6 +269,9 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
   constexpr int TB = 8 * NB;                        // tokens per unit
   constexpr int G = FMT == MOE_Q4_MXFP4 ? 32 : 16;  // columns per scale
   constexpr int SW = scale_words(FMT), RS = red_slots(NB), STEP = step_bytes(FMT);
+  constexpr int SL = step_slabs(FMT);
+  constexpr bool CHUNKS = in_chunks(FMT, NB, RING);
+  const int chunks = CHUNKS ? a.chunks : 1;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ Q4Shared<NB> sh;
   const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
@@ -325,10 +354,15 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
   const int64_t t0 = share * blockIdx.x + min((int)blockIdx.x, rest);
   const int64_t t1 = t0 + share + ((int)blockIdx.x < rest ? 1 : 0);
   // the CTA's tiles [lo, hi) of a block
+  if (tid == 0) {
+    sh.t0 = t0;
+    sh.t1 = t1;
+  }
+  __syncthreads();
   auto tiles_of = [&](int b, int &lo, int &hi) {
     const int64_t at = (int64_t)b * tiles;
-    lo = (int)max(t0 - at, (int64_t)0);
-    hi = (int)min(t1 - at, (int64_t)tiles);
+    lo = (int)max(sh.t0 - at, (int64_t)0);
+    hi = (int)min(sh.t1 - at, (int64_t)tiles);
   };
   const int b0 = (int)(t0 >> 32 ? t0 / tiles : (uint32_t)t0 / (uint32_t)tiles);
   const int b1 = t1 == t0 ? b0 - 1
@@ -375,7 +409,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
   auto point = [&]() {
     int lo = s_lo;
     p_n = s_n;
-    if (a.chunks > 1) slabs_of(p_ch, lo, p_n);
+    if (chunks > 1) slabs_of(p_ch, lo, p_n);
     const uint32_t row16 = (uint32_t)a.C / 32, col16 = (uint32_t)lo * 4 + c;
     pw0 = (uint32_t)tile_row(p_tile, frag0) * row16 + col16;
     pw1 = (uint32_t)tile_row(p_tile, frag1) * row16 + col16;
@@ -398,16 +432,16 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
   // bytes before the array's end of a word that may pass it
   const uint32_t lane_at = tc::smem_u32(ring) + lane * 16;
   const uint32_t scales_at =
-      tc::smem_u32(ring) + 2048 + (lane >> 1) * (4 * SW) + (lane & 1) * 4;
+      tc::smem_u32(ring) + 1024 * SL + (lane >> 1) * (4 * SW) + (lane & 1) * 4;
   auto copy_edge = [&](uint32_t dst, const uint8_t *src) {
     const int64_t left = a.scales + a.scale_bytes - src;
     copy4(dst, left > 0 ? src : a.scales, left >= 4 ? 4 : left > 0 ? (int)left : 0);
   };
-  const bool words_fit = a.C % (SW == 3 ? 128 : 64) == 0;  // every row starts on a word
+  const bool words_fit = FMT == MOE_Q4_MXFP4 || a.C % 64 == 0;  // in SW - 1 words, or in two
   auto fetch = [&](uint32_t slot) {
     if (p_n <= 0 && p_b <= b1) {  // on to the next chunk, the next tile, the next block
       do {
-        if (p_tile >= p_end || ++p_ch == a.chunks) {
+        if (p_tile >= p_end || ++p_ch == chunks) {
           p_ch = 0;
           if (p_tile < p_end) p_tile += rws;
           if (p_tile >= p_end) {
@@ -427,7 +461,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
         copy16<0, 0>(dst, w0);
         copy16<512, 0>(dst, w1);
       }
-      if (p_n > 1 && p_left > kSlab) {
+      if (SL == 2 && p_n > 1 && p_left > kSlab) {
         copy16<1024, kSlab / 2>(dst, w0);
         copy16<1536, kSlab / 2>(dst, w1);
       }
@@ -442,20 +476,20 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
         if (SW == 5) copy_edge(sdst + 8, src + 8);
         if (!words_fit && (lane & 1) == 0) copy_edge(sdst + 4 * (SW - 1), src + 4 * (SW - 1));
       }
-      pw0 += 2 * kSlab / 32;
-      pw1 += 2 * kSlab / 32;
-      ps += 2 * kSlab / G;
-      p_left -= 2 * kSlab;
-      p_n -= 2;
+      pw0 += SL * kSlab / 32;
+      pw1 += SL * kSlab / 32;
+      ps += SL * kSlab / G;
+      p_left -= SL * kSlab;
+      p_n -= SL;
     }
     copies_commit();  // a group per step, also past the end: the waits count groups
   };
   // where the lane's scales lie in a step: fixed, as tiles are 8 or 16 rows
   // apart and several matrices have a multiple of 64 rows
   const int s_at0 =
-      2048 + frag0 * (4 * SW) + ((uint32_t)tile_row(rw, frag0) * (a.C / G) & 3) + c * (32 / G);
+      1024 * SL + frag0 * (4 * SW) + ((uint32_t)tile_row(rw, frag0) * (a.C / G) & 3) + c * (32 / G);
   const int s_at1 =
-      2048 + frag1 * (4 * SW) + ((uint32_t)tile_row(rw, frag1) * (a.C / G) & 3) + c * (32 / G);
+      1024 * SL + frag1 * (4 * SW) + ((uint32_t)tile_row(rw, frag1) * (a.C / G) & 3) + c * (32 / G);
 
   // ---- activations of a token block as fp16 B fragments: for slab s, quarter
   // q and token block b, lane (g, c) finds columns 128 s + 32 c + 8 q .. + 7 of
@@ -471,7 +505,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
     constexpr int RAW = WPT / 2;  // 16-byte words of 8 columns
     const int c_lo = ch * a.chunk * kSlab;
     const int pieces = min(a.chunk, a.slabs - ch * a.chunk) * (kSlab / 8);
-    const bool once = fresh && a.chunks == 1 && pieces <= PER;
+    const bool once = fresh && chunks == 1 && pieces <= PER;
 #pragma unroll 1
     for (int t0 = 0; t0 < nt; t0 += kQ4Warps / WPT) {
       const int t = t0 + wid / WPT, q0 = wid % WPT * 32 + lane;
@@ -600,27 +634,39 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
   Q4Sums<NB> acc = {};
   uint32_t ref0 = 127u, ref1 = 127u;  // MXFP4: the rows' reference scales
 
-  // A slab of a step: H 0 or 1, `left` columns before the row's end for this
-  // lane (columns past it have no codes and scales of their own, and
-  // activations of zero: any finite weight will do). `then` runs when the
-  // slab's codes and scales are read.
-  auto slab = [&](auto which, const unsigned char *st, const uint4 *x, bool fresh, int left,
-                  auto then) {
-    constexpr int H = decltype(which)::value;
-    const uint4 c0 = *reinterpret_cast<const uint4 *>(st + H * 1024 + lane * 16);
-    const uint4 c1 = *reinterpret_cast<const uint4 *>(st + H * 1024 + 512 + lane * 16);
-    if (FMT == MOE_Q4_NVFP4) {
-      uint32_t s0 = *reinterpret_cast<const uint16_t *>(st + s_at0 + H * 8);
-      uint32_t s1 = *reinterpret_cast<const uint16_t *>(st + s_at1 + H * 8);
-      then();
-      if (left <= 0) s0 = s1 = 0u;
-      const uint32_t h0 = e4m3x2_to_half2(s0), h1 = e4m3x2_to_half2(s1);
-      const uint32_t m0[2] = {__byte_perm(h0, h0, 0x1010), __byte_perm(h0, h0, 0x3232)};
-      const uint32_t m1[2] = {__byte_perm(h1, h1, 0x1010), __byte_perm(h1, h1, 0x3232)};
-      products<NB>(acc, c0, c1, x, m0, m1);
+  // A step, `left` columns before the row's end for this lane (columns past it
+  // have no codes and scales of their own, and activations of zero: any finite
+  // weight will do); `two`: its second slab is not past the warp's share. Its
+  // place takes the step RING ahead as soon as it is read by all lanes.
+  auto compute = [&](int slot, const uint4 *x, bool fresh, int left, bool two) {
+    const unsigned char *st = ring + slot, *codes = st + lane * 16;
+    auto code = [&](int h, int row) {
+      return *reinterpret_cast<const uint4 *>(codes + h * 1024 + row * 512);
+    };
+    auto refill = [&] {
+      __syncwarp();
+      fetch(slot);
+    };
+    if constexpr (FMT == MOE_Q4_NVFP4) {
+      auto slab = [&](int h, auto then) {
+        uint32_t s0 = *reinterpret_cast<const uint16_t *>(st + s_at0 + h * 8);
+        uint32_t s1 = *reinterpret_cast<const uint16_t *>(st + s_at1 + h * 8);
+        if (left <= h * kSlab) s0 = s1 = 0u;
+        const uint32_t h0 = e4m3x2_to_half2(s0), h1 = e4m3x2_to_half2(s1);
+        const uint32_t m0[2] = {__byte_perm(h0, h0, 0x1010), __byte_perm(h0, h0, 0x3232)};
+        const uint32_t m1[2] = {__byte_perm(h1, h1, 0x1010), __byte_perm(h1, h1, 0x3232)};
+        const uint4 c0 = code(h, 0), c1 = code(h, 1);
+        then();
+        products<NB>(acc, c0, c1, x + h * (4 * NB * 32), m0, m1);
+      };
+      if (two) {
+        slab(0, [] {});
+        slab(1, refill);
+      } else {
+        slab(0, refill);
+      }
     } else {
-      uint32_t s0 = st[s_at0 + H * 4], s1 = st[s_at1 + H * 4];
-      then();
+      uint32_t s0 = st[s_at0], s1 = st[s_at1];
       if (fresh) {  // the unit's first step: each row's reference, where 2^(s - ref) has room
         ref0 = min(max(__shfl_sync(0xffffffffu, s0, lane & ~3), 96u), 158u);
         ref1 = min(max(__shfl_sync(0xffffffffu, s1, lane & ~3), 96u), 158u);
@@ -629,30 +675,16 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
         s0 = ref0;
         s1 = ref1;
       }
-      const int d0 = (int)s0 - (int)ref0, d1 = (int)s1 - (int)ref1;
-      const bool far = (uint32_t)(d0 + 14) > 26u || (uint32_t)(d1 + 14) > 26u;
-      const uint32_t e0 = (uint32_t)(d0 + 15) * 0x04000400u, e1 = (uint32_t)(d1 + 15) * 0x04000400u;
-      if (!__any_sync(0xffffffffu, far)) {
-        const uint32_t m0[2] = {e0, e0}, m1[2] = {e1, e1};
-        products<NB>(acc, c0, c1, x, m0, m1);
-      } else {
-        acc = products_far<NB>(acc, c0, c1, x, s0, s1, ref0, ref1);
+      const uint32_t d0 = s0 - ref0 + 14u, d1 = s1 - ref1 + 14u;
+      uint32_t e0 = d0 * 0x04000400u + 0x04000400u, e1 = d1 * 0x04000400u + 0x04000400u;
+      if (__any_sync(0xffffffffu, d0 > 26u || d1 > 26u)) {
+        products_far<NB>(acc, codes, x, s0, s1, ref0, ref1);
+        e0 = e1 = 0u;  // what follows adds zeros
       }
-    }
-  };
-  // a step of two slabs, or one at a row's end; its place takes the step RING
-  // ahead as soon as it is read by all lanes
-  auto compute = [&](int slot, const uint4 *x, bool fresh, int left, bool two) {
-    const unsigned char *st = ring + slot;
-    auto refill = [&] {
-      __syncwarp();
-      fetch(slot);
-    };
-    if (two) {
-      slab(std::integral_constant<int, 0>{}, st, x, fresh, left, [] {});
-      slab(std::integral_constant<int, 1>{}, st, x + 4 * NB * 32, false, left - kSlab, refill);
-    } else {
-      slab(std::integral_constant<int, 0>{}, st, x, fresh, left, refill);
+      const uint32_t m0[2] = {e0, e0}, m1[2] = {e1, e1};
+      const uint4 c0 = code(0, 0), c1 = code(0, 1);
+      refill();
+      products<NB>(acc, c0, c1, x, m0, m1);
     }
   };
   // The finished sums v of one row tile and token block: fragment rows g and
@@ -717,9 +749,9 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
     if (cur_b > b0) load_x(0, true);
     for (int tile0 = t_lo; tile0 < t_hi; tile0 += rws) {
       const bool busy = tile0 + rw < t_hi;
-      for (int ch = 0; ch < a.chunks; ++ch) {
+      for (int ch = 0; ch < chunks; ++ch) {
         int lo = s_lo, n = s_n;
-        if (a.chunks > 1) {
+        if (chunks > 1) {
           if (ch > 0 || tile0 > t_lo) load_x(ch, false);
           slabs_of(ch, lo, n);
         }
@@ -727,13 +759,13 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
         const uint4 *x = xs + (lo - ch * a.chunk) * (4 * NB * 32) + lane;
         int left = a.C - lo * kSlab - 32 * c;
 #pragma unroll 1
-        for (int d = 0; d < n; d += 2) {
+        for (int d = 0; d < n; d += SL) {
           copies_wait<RING - 1>();
           __syncwarp();  // the lanes' copies are in, for all lanes
-          compute(slot, x, ch == 0 && d == 0, left, d + 1 < n);
+          compute(slot, x, ch == 0 && d == 0, left, SL == 2 && d + 1 < n);
           slot = slot == (RING - 1) * STEP ? 0 : slot + STEP;
-          x += 2 * 4 * NB * 32;
-          left -= 2 * kSlab;
+          x += SL * 4 * NB * 32;
+          left -= SL * kSlab;
         }
       }
       if (NB == 1) {
@@ -808,7 +840,7 @@ cudaError_t launch(Q4Args &a, cudaStream_t s) {
   constexpr int fit = slabs_that_fit<FMT, NB, RING>();
   constexpr int fixed = kQ4Warps * (RING * step_bytes(FMT) + red_slots(NB) * NB * 512);
   a.chunk = a.slabs < fit ? a.slabs : fit;
-  a.chunks = (a.slabs + a.chunk - 1) / a.chunk;
+  a.chunks = (a.slabs + a.chunk - 1) / a.chunk;  // 1 unless in_chunks(FMT, NB, RING)
   a.scale_bytes = (int64_t)a.E * a.R * (a.C / (FMT == MOE_Q4_MXFP4 ? 32 : 16));
   static PerDeviceOnce configured;
   cudaError_t err = configured.run([] {
@@ -825,15 +857,16 @@ cudaError_t launch(Q4Args &a, cudaStream_t s) {
 }
 
 // Two token blocks per unit where experts have more than 8 tokens on average
-// or nearly so, if a row's activations then stay resident; a short ring where
-// only that leaves room for them.
+// or nearly so, if a row's activations then stay resident; a short ring (4
+// slabs in place of 8) where only that leaves room for them.
 template <int FMT>
 cudaError_t launch_sized(Q4Args &a, cudaStream_t s) {
+  constexpr int LONG = 8 / step_slabs(FMT), SHORT = 4 / step_slabs(FMT);
   a.slabs = (a.C + kSlab - 1) / kSlab;
   const bool two = a.N > 8 * (int64_t)(a.offs ? a.E / 2 : 1);
-  if (two && a.slabs <= slabs_that_fit<FMT, 2, 2>()) return launch<FMT, 2, 2>(a, s);
-  if (a.slabs <= slabs_that_fit<FMT, 1, 4>()) return launch<FMT, 1, 4>(a, s);
-  return launch<FMT, 1, 2>(a, s);
+  if (two && a.slabs <= slabs_that_fit<FMT, 2, SHORT>()) return launch<FMT, 2, SHORT>(a, s);
+  if (a.slabs <= slabs_that_fit<FMT, 1, LONG>()) return launch<FMT, 1, LONG>(a, s);
+  return launch<FMT, 1, SHORT>(a, s);
 }
 
 cudaError_t launch_format(Q4Args &a, int format, cudaStream_t s) {
