@@ -53,6 +53,10 @@ __host__ __device__ constexpr int scale_words(int fmt) { return fmt == MOE_Q4_MX
 __host__ __device__ constexpr int step_bytes(int fmt) {
   return 1024 * step_slabs(fmt) + 64 * scale_words(fmt);
 }
+// Steps of weights on their way per warp: four slabs, 70 KB per SM in all. More
+// only make the first copies wait for one another: eight took the experts of
+// one token (GPT-OSS, MXFP4) from 30.3 us to 31.5.
+__host__ __device__ constexpr int ring_steps(int fmt) { return 4 / step_slabs(fmt); }
 // Units whose partial sums may be on their way to the warps that join them.
 __host__ __device__ constexpr int red_slots(int nb) { return nb == 1 ? 3 : 2; }
 
@@ -257,20 +261,14 @@ __device__ __forceinline__ void products_far(Q4Sums<NB> &acc, const unsigned cha
   }
 }
 
-// Only this variant's launches may have rows too long to be resident.
-constexpr bool in_chunks(int fmt, int nb, int ring) {
-  return nb == 1 && ring * step_slabs(fmt) == 4;
-}
-
-// FMT: moe_q4_format; NB: blocks of 8 tokens per unit; RING: steps of weights
-// in flight per warp, in shared memory.
-template <int FMT, int NB, int RING>
+// FMT: moe_q4_format; NB: blocks of 8 tokens per unit; CHUNKS: rows may be too
+// long for all their activations to be resident.
+template <int FMT, int NB, bool CHUNKS>
 __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
   constexpr int TB = 8 * NB;                        // tokens per unit
   constexpr int G = FMT == MOE_Q4_MXFP4 ? 32 : 16;  // columns per scale
   constexpr int SW = scale_words(FMT), RS = red_slots(NB), STEP = step_bytes(FMT);
-  constexpr int SL = step_slabs(FMT);
-  constexpr bool CHUNKS = in_chunks(FMT, NB, RING);
+  constexpr int SL = step_slabs(FMT), RING = ring_steps(FMT);
   const int chunks = CHUNKS ? a.chunks : 1;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ Q4Shared<NB> sh;
@@ -828,45 +826,43 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
 }
 
 // Slabs whose activations fit beside the ring and the partial sums.
-template <int FMT, int NB, int RING>
+template <int FMT, int NB>
 constexpr int slabs_that_fit() {
   return (kSmemMax - (int)sizeof(Q4Shared<NB>) -
-          kQ4Warps * (RING * step_bytes(FMT) + red_slots(NB) * NB * 512)) /
+          kQ4Warps * (ring_steps(FMT) * step_bytes(FMT) + red_slots(NB) * NB * 512)) /
          (NB * kSlabXBytes);
 }
 
-template <int FMT, int NB, int RING>
+template <int FMT, int NB, bool CHUNKS>
 cudaError_t launch(Q4Args &a, cudaStream_t s) {
-  constexpr int fit = slabs_that_fit<FMT, NB, RING>();
-  constexpr int fixed = kQ4Warps * (RING * step_bytes(FMT) + red_slots(NB) * NB * 512);
+  constexpr int fit = slabs_that_fit<FMT, NB>();
+  constexpr int fixed = kQ4Warps * (ring_steps(FMT) * step_bytes(FMT) + red_slots(NB) * NB * 512);
   a.chunk = a.slabs < fit ? a.slabs : fit;
-  a.chunks = (a.slabs + a.chunk - 1) / a.chunk;  // 1 unless in_chunks(FMT, NB, RING)
+  a.chunks = (a.slabs + a.chunk - 1) / a.chunk;  // 1 unless CHUNKS
   a.scale_bytes = (int64_t)a.E * a.R * (a.C / (FMT == MOE_Q4_MXFP4 ? 32 : 16));
   static PerDeviceOnce configured;
   cudaError_t err = configured.run([] {
-    cudaError_t e = uniform_carveout(q4_kernel<FMT, NB, RING>);
+    cudaError_t e = uniform_carveout(q4_kernel<FMT, NB, CHUNKS>);
     if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(q4_kernel<FMT, NB, RING>,
+    return cudaFuncSetAttribute(q4_kernel<FMT, NB, CHUNKS>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 fixed + fit * NB * kSlabXBytes);
   });
   if (err != cudaSuccess) return err;
-  err = launch_dependent(q4_kernel<FMT, NB, RING>, dim3((unsigned)device_sm_count()),
+  err = launch_dependent(q4_kernel<FMT, NB, CHUNKS>, dim3((unsigned)device_sm_count()),
                          dim3(kQ4Threads), (size_t)(fixed + a.chunk * NB * kSlabXBytes), s, a);
   return err == cudaSuccess ? cudaGetLastError() : err;
 }
 
 // Two token blocks per unit where experts have more than 8 tokens on average
-// or nearly so, if a row's activations then stay resident; a short ring (4
-// slabs in place of 8) where only that leaves room for them.
+// or nearly so, if a row's activations then stay resident.
 template <int FMT>
 cudaError_t launch_sized(Q4Args &a, cudaStream_t s) {
-  constexpr int LONG = 8 / step_slabs(FMT), SHORT = 4 / step_slabs(FMT);
   a.slabs = (a.C + kSlab - 1) / kSlab;
   const bool two = a.N > 8 * (int64_t)(a.offs ? a.E / 2 : 1);
-  if (two && a.slabs <= slabs_that_fit<FMT, 2, SHORT>()) return launch<FMT, 2, SHORT>(a, s);
-  if (a.slabs <= slabs_that_fit<FMT, 1, LONG>()) return launch<FMT, 1, LONG>(a, s);
-  return launch<FMT, 1, SHORT>(a, s);
+  if (two && a.slabs <= slabs_that_fit<FMT, 2>()) return launch<FMT, 2, false>(a, s);
+  if (a.slabs <= slabs_that_fit<FMT, 1>()) return launch<FMT, 1, false>(a, s);
+  return launch<FMT, 1, true>(a, s);
 }
 
 cudaError_t launch_format(Q4Args &a, int format, cudaStream_t s) {
