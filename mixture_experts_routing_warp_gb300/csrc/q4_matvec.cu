@@ -77,7 +77,6 @@ struct Q4Args {
   int64_t N;                  // slots at most (rows of out)
   int E, k, R, C;             // matrices of R rows, C columns
   int x_dtype, out_dtype;     // moe_dtype
-  int mode;
   int act;                    // Q4_W13: moe_activation, layout in `ap`
   int slabs;                  // slabs of a row
   int chunk, chunks;          // slabs whose activations are resident at once; how many such
@@ -162,7 +161,7 @@ __device__ __forceinline__ float exp2i(int e) {
 
 template <int NB>
 struct Q4Shared {
-  unsigned long long full[red_slots(NB)], empty[red_slots(NB)];  // mbarriers
+  unsigned long long full[2][red_slots(NB)], empty[2][red_slots(NB)];  // mbarriers, by product
   int4 info[red_slots(NB)];  // unit in a slot: expert, first token slot, tokens, first tile
   int tile_end[red_slots(NB)];  // tiles from here on are not the unit's
   int part[red_slots(NB)];   // and its part of amax
@@ -261,34 +260,36 @@ __device__ __forceinline__ void products_far(Q4Sums<NB> &acc, const unsigned cha
   }
 }
 
-// FMT: moe_q4_format; NB: blocks of 8 tokens per unit; CHUNKS: rows may be too
-// long for all their activations to be resident.
-template <int FMT, int NB, bool CHUNKS>
-__global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
+// One product. FMT: moe_q4_format; NB: blocks of 8 tokens per unit; CHUNKS:
+// rows may be too long for all their activations to be resident; SECOND: after
+// a Q4_W13 in the same launch, whose h is complete when the grid barrier that
+// this CTA arrived at (`arrived`) opens.
+template <int FMT, int NB, bool CHUNKS, int MODE, bool SECOND>
+__device__ __forceinline__ void q4_run(const Q4Args &a, Q4Shared<NB> &sh, uint32_t arrived) {
   constexpr int TB = 8 * NB;                        // tokens per unit
   constexpr int G = FMT == MOE_Q4_MXFP4 ? 32 : 16;  // columns per scale
   constexpr int SW = scale_words(FMT), RS = red_slots(NB), STEP = step_bytes(FMT);
   constexpr int SL = step_slabs(FMT), RING = ring_steps(FMT);
   const int chunks = CHUNKS ? a.chunks : 1;
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ Q4Shared<NB> sh;
   const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
   float4 *red = reinterpret_cast<float4 *>(smem);  // [RS][kQ4Warps][NB][32]
   unsigned char *ring = smem + RS * kQ4Warps * NB * 512 + wid * (RING * STEP);
   uint4 *xs = reinterpret_cast<uint4 *>(smem + RS * kQ4Warps * NB * 512 + kQ4Warps * RING * STEP);
-  const uint32_t full_at = tc::smem_u32(sh.full), empty_at = tc::smem_u32(sh.empty);
+  const uint32_t full_at = tc::smem_u32(sh.full[SECOND]),
+                 empty_at = tc::smem_u32(sh.empty[SECOND]);
 
   if (tid < 4 * TB) (&sh.amax[0][0])[tid] = 0u;
   // offs may come from the kernel before this one (Q4_W13); before Q4_W2 lies
   // the Q4_W13 launch, which passed its own wait before triggering this one,
   // so what offs holds is complete and the weights can be fetched ahead.
-  if (a.mode != Q4_W2) {
+  if (MODE != Q4_W2) {
     pdl_wait();
     pdl_launch_dependents();
   }
   // token blocks of each expert and their prefix
-  {
+  if (!SECOND) {
     int lo = 0, nb = 0;
     if (a.offs == nullptr) {
       if (tid == 0) nb = (int)((a.N + TB - 1) / TB);
@@ -386,7 +387,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
 
   // ---- weights on their way: step after step, RING steps ahead of the
   // products, by an iterator over (block, tile, chunk, slab)
-  const bool gated = a.mode == Q4_W13 && a.act != MOE_ACT_RELU2;
+  const bool gated = MODE == Q4_W13 && a.act != MOE_ACT_RELU2;
   const bool split = gated && a.ap.layout == MOE_W13_PACKED;  // up rows I below the gate rows
   // Row r (0..15) of a tile. Fragment rows g and g + 8 are gate and up of one
   // column of h for a gated w13. Rows past the end read the last row; their
@@ -597,15 +598,12 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
       nt = max(min(TB, sh.cnt[cur_e + 1] - cur_p0), 0);
       part = (part + 1) & 3;
       if (tid < nt)  // a row in range whatever col_sorted holds
-        sh.row[tid] = a.mode != Q4_W13
+        sh.row[tid] = MODE != Q4_W13
                           ? cur_p0 + tid
                           : min(max(__ldg(a.col_sorted + cur_p0 + tid), 0), (int)a.N - 1) / a.k;
     }
     __syncthreads();  // the previous fragments are no longer read
-    if (a.x_dtype == MOE_FP32)
-      load_rows(std::integral_constant<int, 4>{}, ch, fresh);
-    else
-      load_rows(std::integral_constant<int, 2>{}, ch, fresh);
+    load_rows(std::integral_constant<int, MODE == Q4_W2 ? 4 : 2>{}, ch, fresh);
     __syncthreads();
     // the block before the last has been stored by every warp: its part of
     // amax is free for the block after the next, past another barrier
@@ -613,20 +611,24 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
   };
 
   // The first block's activations come before the weights, whose copies would
-  // keep them waiting; but the Q4_W2 launch may only fetch weights until the
-  // one before it is done.
+  // keep them waiting; but Q4_W2 may only fetch weights until Q4_W13 is done.
   if (b0 <= b1) {
-    if (a.mode != Q4_W2) load_x(0, true);
+    if (MODE != Q4_W2) load_x(0, true);
     enter();
     if (p_tile < p_end) point();
   }
 #pragma unroll 1
   for (int d = 0; d < RING; ++d) fetch(d * STEP);
-  if (a.mode == Q4_W2) {
+  if (SECOND) {
+    if (!grid_wait(a.ctrl, arrived, kWaitTimeoutNs)) {  // every thread of the CTA: no result
+      copies_wait<0>();
+      return;
+    }
+  } else if (MODE == Q4_W2) {
     pdl_wait();
     pdl_launch_dependents();
-    if (b0 <= b1) load_x(0, true);
   }
+  if (MODE == Q4_W2 && b0 <= b1) load_x(0, true);
 
   constexpr int NS = Q4Sums<NB>::N;
   Q4Sums<NB> acc = {};
@@ -697,7 +699,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
       const float lo = v[j] * ms * s, hi = v[2 + j] * ms * s;
       const int64_t p = (int64_t)p0 + t;
       const int row = tile * 16 + g;
-      if (a.mode == Q4_W13) {
+      if (MODE == Q4_W13) {
         float *h = static_cast<float *>(a.out);
         if (gated) {
           const int I = a.R >> 1, col = tile * 8 + g;
@@ -815,7 +817,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
     join(u - 1, rs == 0 ? RS - 1 : rs - 1, rs == 0 ? rs_phase ^ 1u : rs_phase);
   copies_wait<0>();
 
-  if (a.mode == Q4_W2) {  // rows of no kept slot
+  if (MODE == Q4_W2) {  // rows of no kept slot
     const int64_t words = (a.N - sh.cnt[a.E]) * a.R / 2;  // R is even: 4-byte words
     uint32_t *z = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) +
                                                (int64_t)sh.cnt[a.E] * a.R);
@@ -823,6 +825,23 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
          i += (int64_t)gridDim.x * kQ4Threads)
       z[i] = 0u;
   }
+}
+
+template <int FMT, int NB, bool CHUNKS, int MODE>
+__global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
+  __shared__ Q4Shared<NB> sh;
+  q4_run<FMT, NB, CHUNKS, MODE, false>(a, sh, 0u);
+}
+
+// Both products of the experts in one launch: a CTA that is done with its
+// share of w13 fetches its first w2 weights while the others finish. The grid
+// barrier needs all CTAs resident (one per SM); it is bounded like every wait.
+template <int FMT, int NB>
+__global__ void __launch_bounds__(kQ4Threads, 1) q4_ffn_kernel(const Q4Args a, const Q4Args b) {
+  __shared__ Q4Shared<NB> sh;
+  q4_run<FMT, NB, false, Q4_W13, false>(a, sh, 0u);
+  const uint32_t arrived = grid_arrive(a.ctrl);
+  q4_run<FMT, NB, false, Q4_W2, true>(b, sh, arrived);
 }
 
 // Slabs whose activations fit beside the ring and the partial sums.
@@ -833,41 +852,103 @@ constexpr int slabs_that_fit() {
          (NB * kSlabXBytes);
 }
 
-template <int FMT, int NB, bool CHUNKS>
-cudaError_t launch(Q4Args &a, cudaStream_t s) {
+template <int FMT, int NB>
+constexpr int fixed_smem() {
+  return kQ4Warps * (ring_steps(FMT) * step_bytes(FMT) + red_slots(NB) * NB * 512);
+}
+
+// Fills in what follows from the sizes; returns the dynamic shared memory.
+template <int FMT, int NB>
+size_t plan(Q4Args &a) {
   constexpr int fit = slabs_that_fit<FMT, NB>();
-  constexpr int fixed = kQ4Warps * (ring_steps(FMT) * step_bytes(FMT) + red_slots(NB) * NB * 512);
   a.chunk = a.slabs < fit ? a.slabs : fit;
-  a.chunks = (a.slabs + a.chunk - 1) / a.chunk;  // 1 unless CHUNKS
+  a.chunks = (a.slabs + a.chunk - 1) / a.chunk;
   a.scale_bytes = (int64_t)a.E * a.R * (a.C / (FMT == MOE_Q4_MXFP4 ? 32 : 16));
+  return fixed_smem<FMT, NB>() + (size_t)a.chunk * NB * kSlabXBytes;
+}
+
+// The kernel of both products waits for all its CTAs: a cooperative launch has
+// them resident together or not at all, whatever other streams run.
+template <int FMT, int NB, auto Kern, typename... Args>
+cudaError_t go(size_t smem, cudaStream_t s, const Args &...args) {
+  constexpr bool cooperative = sizeof...(Args) == 2;
   static PerDeviceOnce configured;
   cudaError_t err = configured.run([] {
-    cudaError_t e = uniform_carveout(q4_kernel<FMT, NB, CHUNKS>);
+    cudaError_t e = uniform_carveout(Kern);
     if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(q4_kernel<FMT, NB, CHUNKS>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                fixed + fit * NB * kSlabXBytes);
+    return cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                fixed_smem<FMT, NB>() +
+                                    slabs_that_fit<FMT, NB>() * NB * kSlabXBytes);
   });
   if (err != cudaSuccess) return err;
-  err = launch_dependent(q4_kernel<FMT, NB, CHUNKS>, dim3((unsigned)device_sm_count()),
-                         dim3(kQ4Threads), (size_t)(fixed + a.chunk * NB * kSlabXBytes), s, a);
+  const dim3 grid((unsigned)device_sm_count()), block(kQ4Threads);
+  if constexpr (cooperative) {
+    void *params[] = {const_cast<Args *>(&args)...};
+    err = cudaLaunchCooperativeKernel(Kern, grid, block, params, smem, s);
+  } else {
+    err = launch_dependent(Kern, grid, block, smem, s, args...);
+  }
   return err == cudaSuccess ? cudaGetLastError() : err;
 }
 
 // Two token blocks per unit where experts have more than 8 tokens on average
 // or nearly so, if a row's activations then stay resident.
 template <int FMT>
-cudaError_t launch_sized(Q4Args &a, cudaStream_t s) {
-  a.slabs = (a.C + kSlab - 1) / kSlab;
-  const bool two = a.N > 8 * (int64_t)(a.offs ? a.E / 2 : 1);
-  if (two && a.slabs <= slabs_that_fit<FMT, 2>()) return launch<FMT, 2, false>(a, s);
-  if (a.slabs <= slabs_that_fit<FMT, 1>()) return launch<FMT, 1, false>(a, s);
-  return launch<FMT, 1, true>(a, s);
+bool two_blocks(const Q4Args &a) {
+  return a.N > 8 * (int64_t)(a.offs ? a.E / 2 : 1) && a.slabs <= slabs_that_fit<FMT, 2>();
 }
 
-cudaError_t launch_format(Q4Args &a, int format, cudaStream_t s) {
-  return format == MOE_Q4_MXFP4 ? launch_sized<MOE_Q4_MXFP4>(a, s)
-                                : launch_sized<MOE_Q4_NVFP4>(a, s);
+template <int FMT, int MODE>
+cudaError_t launch(Q4Args &a, cudaStream_t s) {
+  a.slabs = (a.C + kSlab - 1) / kSlab;
+  if (two_blocks<FMT>(a)) {
+    const size_t smem = plan<FMT, 2>(a);
+    return go<FMT, 2, q4_kernel<FMT, 2, false, MODE>>(smem, s, a);
+  }
+  const size_t smem = plan<FMT, 1>(a);
+  if (a.chunks > 1) return go<FMT, 1, q4_kernel<FMT, 1, true, MODE>>(smem, s, a);
+  return go<FMT, 1, q4_kernel<FMT, 1, false, MODE>>(smem, s, a);
+}
+
+template <int MODE>
+cudaError_t launch(Q4Args &a, int format, cudaStream_t s) {
+  return format == MOE_Q4_MXFP4 ? launch<MOE_Q4_MXFP4, MODE>(a, s)
+                                : launch<MOE_Q4_NVFP4, MODE>(a, s);
+}
+
+cudaError_t launch_dense(Q4Args &a, int format, cudaStream_t s) {
+  return launch<Q4_DENSE>(a, format, s);
+}
+
+// w13 and w2 in one launch, where both take the same variant without chunks;
+// *done says whether.
+template <int FMT>
+cudaError_t launch_both(Q4Args &a, Q4Args &b, cudaStream_t s, bool *done) {
+  a.slabs = (a.C + kSlab - 1) / kSlab;
+  b.slabs = (b.C + kSlab - 1) / kSlab;
+  *done = true;
+  if (two_blocks<FMT>(a) && two_blocks<FMT>(b)) {
+    const size_t sa = plan<FMT, 2>(a), sb = plan<FMT, 2>(b);
+    return go<FMT, 2, q4_ffn_kernel<FMT, 2>>(sa > sb ? sa : sb, s, a, b);
+  }
+  if (!two_blocks<FMT>(a) && !two_blocks<FMT>(b)) {
+    const size_t sa = plan<FMT, 1>(a), sb = plan<FMT, 1>(b);
+    if (a.chunks == 1 && b.chunks == 1)
+      return go<FMT, 1, q4_ffn_kernel<FMT, 1>>(sa > sb ? sa : sb, s, a, b);
+  }
+  *done = false;
+  return cudaSuccess;
+}
+
+cudaError_t launch_experts(Q4Args &a, Q4Args &b, int format13, int format2, cudaStream_t s) {
+  if (format13 == format2) {
+    bool done = false;
+    const cudaError_t err = format13 == MOE_Q4_MXFP4 ? launch_both<MOE_Q4_MXFP4>(a, b, s, &done)
+                                                     : launch_both<MOE_Q4_NVFP4>(a, b, s, &done);
+    if (done) return err;
+  }
+  const cudaError_t err = launch<Q4_W13>(a, format13, s);
+  return err == cudaSuccess ? launch<Q4_W2>(b, format2, s) : err;
 }
 
 }  // namespace
@@ -886,8 +967,7 @@ cudaError_t launch_linear_q4(const void *x, const moe_q4_matrix &w, int64_t n, i
   a.R = R;
   a.C = C;
   a.x_dtype = a.out_dtype = dtype;
-  a.mode = Q4_DENSE;
-  return launch_format(a, w.format, s);
+  return launch_dense(a, w.format, s);
 }
 
 cudaError_t launch_ffn_q4(const void *x, const moe_routing_meta &m, const moe_q4_matrix &w13,
@@ -910,11 +990,8 @@ cudaError_t launch_ffn_q4(const void *x, const moe_routing_meta &m, const moe_q4
   a.C = H;
   a.x_dtype = dtype;
   a.out_dtype = MOE_FP32;
-  a.mode = Q4_W13;
   a.act = act.act;
   a.ap = act;
-  cudaError_t err = launch_format(a, w13.format, s);
-  if (err != cudaSuccess) return err;
   Q4Args b = a;
   b.codes = w2.codes;
   b.scales = w2.scales;
@@ -925,8 +1002,7 @@ cudaError_t launch_ffn_q4(const void *x, const moe_routing_meta &m, const moe_q4
   b.C = I;
   b.x_dtype = MOE_FP32;
   b.out_dtype = dtype;
-  b.mode = Q4_W2;
-  return launch_format(b, w2.format, s);
+  return launch_experts(a, b, w13.format, w2.format, s);
 }
 
 }  // namespace moe

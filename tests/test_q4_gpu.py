@@ -308,6 +308,7 @@ def test_broken_metadata_stays_inside_the_buffers():
     N, size = n * k, moe.workspace_q4_size(n, E, k, H, I)
     raw = torch.full((size + 8192,), 0xA5, dtype=torch.uint8, device="cuda")
     ws = raw[4096:4096 + size]
+    assert moe.lib().moe_workspace_init(ws.data_ptr(), size, None) == 0
     out_raw = torch.full((N * H + 4096,), 7.0, dtype=BF16, device="cuda")
     out = out_raw[2048:2048 + N * H].view(N, H)
     for offs in ([0, 5, 3, 2 ** 31 - 1, 12], [-9, -9, 40, 1, -1], [12, 12, 0, 0, 12]):
