@@ -11,7 +11,7 @@ of the router's weights, are the library's calls:
     d_out -> combine_weighted_backward -> experts' backward -> dispatch_backward
           -> d_x; the weights' gradient -> route_backward -> d_logits
 
-Serving quantises the experts once and calls forward_q4 for every step: four
+Serving quantises the experts once and calls forward_q4 for every step: three
 kernels, no host synchronisation.
 """
 import os

@@ -466,8 +466,9 @@ moe_status moe_linear_q4(const void *x, const moe_q4_matrix *w, int64_t n, int32
                          int32_t dtype, void *y, moe_stream stream);
 
 /* Bytes of workspace for moe_grouped_ffn_q4 and moe_forward_q4 (prepared by
- * moe_workspace_init): routing results, the fp32 intermediate h [n*k, I],
- * the experts' outputs. 0 for invalid sizes. */
+ * moe_workspace_init): control block, routing results, the fp32 intermediate
+ * h [n*k, I], the experts' outputs. One workspace serves one stream at a
+ * time. 0 for invalid sizes. */
 size_t moe_q4_workspace_size(int64_t n, int32_t E, int32_t k, int32_t H, int32_t I);
 
 /* The experts of a decode step with 4-bit weights: for every kept slot, at
@@ -479,7 +480,10 @@ size_t moe_q4_workspace_size(int64_t n, int32_t E, int32_t k, int32_t H, int32_t
  * [n*k, H] of dtype; rows past the kept slots are zero. No gate weight is
  * applied (moe_combine_weighted does). E may be less than k: a rank that
  * holds few of the experts. h stays fp32 up to the second product,
- * which takes it as scaled fp16. params: activation, layout and the values of
+ * which takes it as scaled fp16. One cooperative launch with a bounded grid
+ * barrier between the products (MOE_ERR_TIMEOUT in the status word if it
+ * gives up); two launches where w13 and w2 differ in format or a row is too
+ * long for its activations to stay in shared memory. params: activation, layout and the values of
  * `set`; gating, ffn_kernel and expert_map are not used. */
 moe_status moe_grouped_ffn_q4(const void *x, const moe_routing_meta *meta,
                               const moe_q4_matrix *w13, const moe_q4_matrix *w2, int64_t n,
@@ -489,8 +493,8 @@ moe_status moe_grouped_ffn_q4(const void *x, const moe_routing_meta *meta,
 
 /* The layer with 4-bit experts: moe_route_metadata, moe_grouped_ffn_q4,
  * moe_combine_weighted, with the optional outputs and the expert map of
- * moe_forward (w13 / w2 then hold the local experts). 4 launches while the
- * routing is one kernel. */
+ * moe_forward (w13 / w2 then hold the local experts). 3 launches where
+ * the routing and the experts are one kernel each. */
 moe_status moe_forward_q4(const void *x, const float *logits, const moe_q4_matrix *w13,
                           const moe_q4_matrix *w2, int64_t n, int32_t E, int32_t k, int32_t H,
                           int32_t I, const moe_params *params, int32_t dtype, void *out,

@@ -423,7 +423,7 @@ def _need_weights(weights: torch.Tensor, device: int) -> None:
 
 def _out_rows(out: Optional[torch.Tensor], name: str, shape, like: torch.Tensor) -> torch.Tensor:
     if out is None:
-        return torch.empty(shape, dtype=like.dtype, device=like.device)
+        return like.new_empty(shape)
     _need_on(out, name, like.dtype, like.get_device(), shape)
     return out
 
@@ -504,7 +504,7 @@ def combine_weighted_backward(d_out: torch.Tensor, y_sorted: torch.Tensor, meta:
         raise ValueError(f"d_out must have {n} rows, got {d_out.shape[0]}")
     _need_on(y_sorted, "y_sorted", d_out.dtype, device, (n * k, H))
     _need_slots(meta, n * k, device)
-    d_sorted = torch.empty((n * k, H), dtype=d_out.dtype, device=d_out.device)
+    d_sorted = d_out.new_empty((n * k, H))
     d_weights = torch.empty((n, k), dtype=torch.float32, device=d_out.device)
     _run("moe_combine_weighted_backward", device, d_out.data_ptr(), y_sorted.data_ptr(),
          meta["row_sorted"].data_ptr(), weights.data_ptr(), DTYPE[weights.dtype], _kept(meta), n,
@@ -525,7 +525,7 @@ def route_backward(logits: torch.Tensor, topk_indx: torch.Tensor, d_vals: torch.
         raise ValueError(f"topk_indx must have shape [n, k], got {tuple(topk_indx.shape)}")
     k = topk_indx.shape[1]
     _need_on(d_vals, "d_vals", torch.float32, device, (n, k))
-    d_logits = torch.empty((n, E), dtype=torch.float32, device=logits.device)
+    d_logits = logits.new_empty((n, E))
     _run("moe_route_backward", device, logits.data_ptr(), topk_indx.data_ptr(),
          d_vals.data_ptr(), n, E, k, GATING[gating], d_logits.data_ptr())
     return d_logits

@@ -43,8 +43,8 @@ constexpr int kSlabXBytes = 2048;  // fp16 fragments of 8 tokens x 128 columns
 constexpr int kSmemMax = 226 * 1024;  // dynamic and static shared memory of a CTA
 
 // Slabs per step. Two halve the waits and the ring's bookkeeping: NVFP4, 64
-// tokens of the GPT-OSS experts, 170 -> 154 us. MXFP4 needs more registers for
-// its scales and spills with two: 154 -> 199 us, so it takes one.
+// tokens of the GPT-OSS experts, 170 -> 158 us. MXFP4 gains nothing (156 us
+// either way: its checks of the scales are per slab), so it takes one.
 __host__ __device__ constexpr int step_slabs(int fmt) { return fmt == MOE_Q4_MXFP4 ? 1 : 2; }
 // Shared memory of one step: the lanes' codes of two rows each, 16 bytes a
 // lane, row and slab, then the 16 rows' scales (4 bytes; 16) as whole 4-byte

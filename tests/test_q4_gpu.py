@@ -387,6 +387,27 @@ def test_streams_graphs_and_repeats():
     assert torch.equal(out, moe.forward_q4(x, z, w13, w2, k, p, ws))
 
 
+def test_two_streams_at_a_time():
+    """Layers on two streams, each with a workspace of its own, do not wait
+    for one another's halves (a launch has all its blocks resident)."""
+    n, H, I, E, k = 4, 256, 256, 8, 2
+    w13, w2 = random_q4((2 * I, H), "mxfp4", 64, count=E), random_q4((H, I), "mxfp4", 65, count=E)
+    p = moe.make_params()
+    x, z = tokens(n, H, BF16, 66, 0.1), torch.randn(n, E, device="cuda")
+    spaces = [moe.workspace_q4(n, E, k, H, I) for _ in range(2)]
+    want = moe.forward_q4(x, z, w13, w2, k, p, spaces[0])
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in range(2)], []
+    for i in range(40):
+        with torch.cuda.stream(streams[i % 2]):
+            outs.append(moe.forward_q4(x, z, w13, w2, k, p, spaces[i % 2]))
+    torch.cuda.synchronize()
+    for ws in spaces:
+        assert moe.read_status(ws) == 0
+    for out in outs:
+        assert torch.equal(out, want)
+
+
 @pytest.mark.parametrize("n,local", [(1, 16), (7, 16), (64, 16), (40, 5)])
 @pytest.mark.parametrize("gating", ["softmax_topk", "softmax_all"])
 def test_forward_is_its_stages(n, local, gating):
