@@ -199,6 +199,72 @@ def test_bases_off_the_vector_width(dtype):
     assert ((a[1] - b[1]).abs() <= 2 * (H + 1) * U32 * H * mag).all()
 
 
+class Guarded:
+    """An array `off` elements past a 16-byte boundary, ones of 7 before and after it."""
+
+    def __init__(self, shape, dtype, off):
+        size = int(np.prod(shape))
+        self.buf = torch.full((size + 64,), 7.0, dtype=dtype, device="cuda")
+        self.lo, self.hi = 16 + off, 16 + off + size
+        self.t = self.buf[self.lo:self.hi].view(shape)
+
+    def untouched(self):
+        return bool((self.buf[:self.lo] == 7).all() and (self.buf[self.hi:] == 7).all())
+
+
+def surrounded(t, off):
+    """A copy of t at such a place, between NaN."""
+    g = Guarded(t.shape, t.dtype, off)
+    g.buf.fill_(float("nan"))
+    g.t.copy_(t)
+    return g.t
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+@pytest.mark.parametrize("H", [1, 2, 3, 4, 7, 9, 12, 31, 255, 1442, 4099, 8200])
+@pytest.mark.parametrize("k", [1, 4, 7])
+def test_rows_at_every_alignment(H, dtype, k):
+    """Rows and arrays that start anywhere: what lies around an array is
+    neither used nor written, and copies and scaled copies have their exact
+    bits (one product in fp32, one rounding)."""
+    n, E, per = 13, 9, 16 // torch.finfo(dtype).bits * 8
+    _, meta = make_meta(n, E, k, 50, 6)
+    row, kept = meta["row_sorted"].long(), int(meta["offs"][-1])
+    x, y, d_out = rows((n, H), dtype, 51), rows((n * k, H), dtype, 52), rows((n, H), dtype, 53)
+    y[kept:] = float("nan")
+    w = torch.softmax(rows((n, k), FP32, 54), 1)
+    live = row >= 0
+    token = torch.arange(n, device="cuda").repeat_interleave(k)[live]
+    want = torch.zeros(n * k, H, dtype=dtype, device="cuda")
+    want[row[live]] = x[token]
+    scaled = torch.zeros_like(want)
+    scaled[row[live]] = (w.reshape(-1, 1)[live] * d_out[token].float()).to(dtype)
+    ref, mag, src, _ = combine64(torch.where(torch.isnan(y), 0.0, y), meta, w)
+    up = d_out.double().repeat_interleave(k, 0)
+    ref_w, mag_w = (up * src).sum(1) * live, (up * src).abs().sum(1) * live
+    for a, b, c in [(0, 0, 0), (1, 0, 0), (0, 1, 0), (0, 0, 1), (1, 1, 1), (3, 2, 1),
+                    (per - 1, 1, per - 1), (2, per - 1, 2)]:
+        g = Guarded((n * k, H), dtype, b)
+        moe.dispatch(surrounded(x, a), meta, k, out=g.t)
+        assert g.untouched() and torch.equal(g.t, want)
+
+        yy, g = surrounded(y, a), Guarded((n, H), dtype, b)
+        moe.combine_weighted(yy, meta, w, out=g.t)
+        err = (g.t.double() - ref).abs()
+        assert g.untouched()
+        assert (err <= u(dtype) * ref.abs() * (1 + U32) + 2 * (k + 1) * U32 * mag +
+                TINY[dtype]).all()
+
+        g, d_w = Guarded((n * k, H), dtype, c), torch.empty(n, k, device="cuda")
+        code = {BF16: 0, FP16: 1, FP32: 2}
+        moe._binding._run("moe_combine_weighted_backward", 0, surrounded(d_out, b).data_ptr(),
+                          yy.data_ptr(), meta["row_sorted"].data_ptr(), w.data_ptr(), code[FP32],
+                          moe._binding._kept(meta), n, k, H, code[dtype], g.t.data_ptr(),
+                          d_w.data_ptr())
+        assert g.untouched() and torch.equal(g.t, scaled)
+        assert ((d_w.double().reshape(-1) - ref_w).abs() <= (H + 1) * U32 * mag_w).all()
+
+
 def test_dropped_slots_are_not_read():
     """A dropped slot (-1, or an index past the rows) adds nothing even where
     its weight is NaN; a token without a kept slot gets zeros; rows past the
