@@ -265,6 +265,26 @@ def test_rows_at_every_alignment(H, dtype, k):
         assert ((d_w.double().reshape(-1) - ref_w).abs() <= (H + 1) * U32 * mag_w).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("n,k,local", [(2047, 1, 5), (2051, 1, 5), (2049, 2, 6), (5001, 2, 8),
+                                       (4097, 1, 8)])
+def test_many_tokens_of_one_or_two_slots(n, k, local, dtype):
+    """Several tokens share a thread here; the last ones are no full group."""
+    H, E = 264, 8
+    _, meta = make_meta(n, E, k, 55, local)
+    y, w = rows((n * k, H), dtype, 56), rows((n, k), FP32, 57)
+    y[int(meta["offs"][-1]):] = float("nan")
+    ref, mag, _, _ = combine64(torch.where(torch.isnan(y), 0.0, y), meta, w)
+    g = Guarded((n, H), dtype, 0)
+    moe.combine_weighted(y, meta, w, out=g.t)
+    assert g.untouched()
+    err = (g.t.double() - ref).abs()
+    assert (err <= u(dtype) * ref.abs() * (1 + U32) + 2 * (k + 1) * U32 * mag + TINY[dtype]).all()
+    ref, mag, _, _ = combine64(torch.where(torch.isnan(y), 0.0, y), meta, torch.ones_like(w))
+    err = (moe.dispatch_backward(y, meta, k).double() - ref).abs()
+    assert (err <= u(dtype) * ref.abs() * (1 + U32) + 2 * (k + 1) * U32 * mag + TINY[dtype]).all()
+
+
 def test_dropped_slots_are_not_read():
     """A dropped slot (-1, or an index past the rows) adds nothing even where
     its weight is NaN; a token without a kept slot gets zeros; rows past the
