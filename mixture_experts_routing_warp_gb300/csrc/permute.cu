@@ -191,15 +191,17 @@ combine_weighted_kernel(const void *y_sorted, const int32_t *row_sorted, const v
 
 // A row's threads read their share of d_out[t] once, write the k scaled
 // copies and add up the k dot products with the sorted rows; those are joined
-// over lanes, then over the row's warps. K: 4, or 8 where k > 4. The register
-// limits keep five CTAs of 128 threads on an SM (K = 4, U = 3: 67.5 us for
-// 8192 tokens, H 2880; 72.8 with the compiler's own 127 registers).
+// over lanes, then over the row's warps. K: 1, 2, 4 or 8, the least that holds
+// k. The register limits keep five CTAs of 128 threads on an SM (K = 4, U = 3:
+// 67.5 us for 8192 tokens, H 2880; 72.8 with the compiler's own 127 registers),
+// seven with K = 2 and nine with K = 1 (16384 tokens, H 1440, k 1: 32.5 us with
+// K = 4's kernel, 22.0 so; 8192, k 2: 22.0 and 17.9).
 template <typename T, int U, int K>
-__global__ void __maxnreg__(K == 4 ? (U == 3 ? 96 : 80) : (U == 3 ? 128 : 104))
+__global__ void __maxnreg__(K == 1 ? 56 : K == 2 ? 72 : K == 4 ? (U == 3 ? 96 : 80) : (U == 3 ? 128 : 104))
 combine_backward_kernel(const void *d_out, const void *y_sorted, const int32_t *row_sorted,
                         const void *w, int w_dtype, const int32_t *n_kept, int64_t n, int k,
                         RowMap m, void *d_sorted, float *d_weights) {
-  constexpr int EPV = 16 / sizeof(T);
+  constexpr int EPV = 16 / sizeof(T), J = K < 4 ? K : 4;
   __shared__ float s_dot[kMaxThreads / 32][K];
   pdl_wait();
   pdl_launch_dependents();
@@ -216,14 +218,14 @@ combine_backward_kernel(const void *d_out, const void *y_sorted, const int32_t *
                    ? __ldcs(static_cast<const uint4 *>(d_out) + t * m.vpr + c0 + u * m.lanes)
                    : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-      for (int j0 = 0; j0 < K; j0 += 4) {
+      for (int j0 = 0; j0 < K; j0 += J) {
         if (j0 >= k) break;
-        uint4 v[4][U];
+        uint4 v[J][U];
         int64_t p[4];
         float wj[4];
-        load_slots(row_sorted, w, w_dtype, t * k + j0, k - j0, N, p, wj);
+        load_slots(row_sorted, w, w_dtype, t * k + j0, min(J, k - j0), N, p, wj);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < J; ++j)
 #pragma unroll
           for (int u = 0; u < U; ++u)
             v[j][u] = p[j] >= 0 && c0 + u * m.lanes < m.vpr
@@ -231,7 +233,7 @@ combine_backward_kernel(const void *d_out, const void *y_sorted, const int32_t *
                                    u * m.lanes)
                           : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < J; ++j)
           if (p[j] >= 0)
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -496,11 +498,12 @@ __device__ __forceinline__ float backward_vector(const uint4 &gv, const uint4 &y
 // SAME: y_sorted and d_sorted have the same address modulo 16, so that the
 // vectors of their rows are words of both.
 template <typename T, int K, bool SAME>
-__global__ void __launch_bounds__(kShiftThreads, SAME ? 5 : 4)
+__global__ void __launch_bounds__(kShiftThreads, (SAME ? 5 : 4) + (K == 1 ? 4 : K == 2 ? 2 : 0))
 combine_backward_shift_kernel(const void *d_out, const void *y_sorted, const int32_t *row_sorted,
                               const void *w, int w_dtype, const int32_t *n_kept, int64_t n, int k,
                               int rb, int margin, void *d_sorted, float *d_weights) {
-  constexpr bool FEW = K == 4;
+  constexpr bool FEW = K <= 4;
+  constexpr int J = K < 4 ? K : 4;
   __shared__ float s_dot[kShiftThreads / 32][K];
   pdl_wait();
   pdl_launch_dependents();
@@ -509,16 +512,16 @@ combine_backward_shift_kernel(const void *d_out, const void *y_sorted, const int
                   g_row = (uintptr_t)d_out + t * rb;
   float dot[K] = {};
   if (t < n) {
-    uintptr_t to[4];  // the written row's first word; yd on from it, the read one's
-    int h[4];         // the rows start so many bytes on; a dropped slot's never do
+    uintptr_t to[J];  // the written row's first word; yd on from it, the read one's
+    int h[J];         // the rows start so many bytes on; a dropped slot's never do
     float wj[4];
     bool inner = true;
     auto place = [&](int j0) {
       int64_t p[4];
-      load_slots(row_sorted, w, w_dtype, t * k + j0, k - j0, N, p, wj);
+      load_slots(row_sorted, w, w_dtype, t * k + j0, min(J, k - j0), N, p, wj);
       inner = t >= margin && t < n - margin;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < J; ++j) {
         to[j] = d0 + p[j] * rb;
         h[j] = p[j] >= 0 ? (int)(to[j] & 15) : -rb;
         to[j] &= ~(uintptr_t)15;
@@ -529,20 +532,20 @@ combine_backward_shift_kernel(const void *d_out, const void *y_sorted, const int
 #pragma unroll 1
     for (int c = 16 * threadIdx.x; c < rb + 15; c += 16 * blockDim.x) {
 #pragma unroll
-      for (int j0 = 0; j0 < K; j0 += 4) {
+      for (int j0 = 0; j0 < K; j0 += J) {
         if (j0 >= k) break;
         if (!FEW) place(j0);
         bool inside = true;
         if (!inner) {  // vectors start c - 15 to c bytes into the row
           inside = words_inside(t * rb + c - 15, n * rb - 15);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < J; ++j)
             inside &= c >= rb + h[j] || words_inside((int64_t)(to[j] - d0) + c, N * rb);
         }
         if (inside) {
-          Window g[4], v[4];
+          Window g[J], v[J];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < J; ++j)
             if (c < rb + h[j]) {
               if (SAME)
                 v[j].a = __ldcs(reinterpret_cast<const uint4 *>(to[j] + yd + c));
@@ -551,7 +554,7 @@ combine_backward_shift_kernel(const void *d_out, const void *y_sorted, const int
               g[j] = load_window(g_row - h[j], c);
             }
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < J; ++j)
             if (c < rb + h[j])
               dot[j0 + j] = backward_vector<T>(
                   join_window(g[j], g_row - h[j]),
@@ -559,7 +562,7 @@ combine_backward_shift_kernel(const void *d_out, const void *y_sorted, const int
                   rb, dot[j0 + j]);
         } else {  // an array's first or last words: one slot at a time
 #pragma unroll 1
-          for (int j = 0; j < min(4, k - j0); ++j) {
+          for (int j = 0; j < min(J, k - j0); ++j) {
             int64_t p[4];
             float w1[4];
             load_slots(row_sorted, w, w_dtype, t * k + j0 + j, 1, N, p, w1);
@@ -571,7 +574,7 @@ combine_backward_shift_kernel(const void *d_out, const void *y_sorted, const int
                                                  load_part(row + yd, at, rb), w1[0], row, at, rb,
                                                  0.f);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < J; ++i)
               if (i == j) dot[j0 + i] += add;
           }
         }
@@ -810,6 +813,10 @@ static cudaError_t backward_typed(const void *d_out, const void *y, const int32_
                                                          row_sorted, w, wd, n_kept, n, k,    \
                                                          (int)rb, row_margin((int)rb),       \
                                                          d_sorted, dw)
+    if (k == 1 && same) MOE_BACKWARD(1, true);
+    if (k == 1) MOE_BACKWARD(1, false);
+    if (k == 2 && same) MOE_BACKWARD(2, true);
+    if (k == 2) MOE_BACKWARD(2, false);
     if (k <= 4 && same) MOE_BACKWARD(4, true);
     if (k <= 4) MOE_BACKWARD(4, false);
     if (same) MOE_BACKWARD(8, true);
@@ -817,6 +824,12 @@ static cudaError_t backward_typed(const void *d_out, const void *y, const int32_
 #undef MOE_BACKWARD
   }
   const RowMap m = row_map((int)(rb / 16));
+  if (k == 1)
+    return go_rows<Backward<T, 1>::template F>(n, m, s, d_out, y, row_sorted, w, wd, n_kept, n, k,
+                                               m, d_sorted, dw);
+  if (k == 2)
+    return go_rows<Backward<T, 2>::template F>(n, m, s, d_out, y, row_sorted, w, wd, n_kept, n, k,
+                                               m, d_sorted, dw);
   if (k <= 4)
     return go_rows<Backward<T, 4>::template F>(n, m, s, d_out, y, row_sorted, w, wd, n_kept, n, k,
                                                m, d_sorted, dw);

@@ -222,7 +222,7 @@ def surrounded(t, off):
 
 @pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
 @pytest.mark.parametrize("H", [1, 2, 3, 4, 7, 9, 12, 31, 255, 1442, 4099, 8200])
-@pytest.mark.parametrize("k", [1, 4, 7])
+@pytest.mark.parametrize("k", [1, 2, 4, 7])
 def test_rows_at_every_alignment(H, dtype, k):
     """Rows and arrays that start anywhere: what lies around an array is
     neither used nor written, and copies and scaled copies have their exact
