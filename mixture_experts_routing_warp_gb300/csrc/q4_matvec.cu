@@ -25,8 +25,13 @@
 //  - Activations become fp16 once per CTA, each token's row scaled by a power
 //    of two so that its largest magnitude lies in [2^14, 2^15): bf16's 8 (or
 //    fp16's 11) significant bits stay exact down to 2^-28 of the row's
-//    maximum (fp32 h: 11 bits, half an fp16 step), values below 2^-39 of it
-//    vanish. The sum is scaled back in fp32.
+//    maximum, values below 2^-39 of it vanish. The sum is scaled back in fp32.
+//  - The fp32 h of the experts takes two of the 8 token columns, its fp16 value
+//    and what that leaves, 22 bits in all (with one term, 11 bits, the error of
+//    an fp16 result was that of h). So w2's units hold half as many tokens as
+//    w13's. Up to 4 slots per expert that costs nothing; beyond it w2's codes
+//    are converted once per 8 tokens and not per 16 (GPT-OSS experts, 64 tokens,
+//    one term and two: NVFP4 143 and 156 us, MXFP4 155 and 163).
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -159,15 +164,19 @@ __device__ __forceinline__ float exp2i(int e) {
   return e == -127 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-template <int NB>
+// Tokens per unit: 8 token columns a block, two of them for one of h.
+__host__ __device__ constexpr int block_tokens(int mode) { return mode == Q4_W2 ? 4 : 8; }
+
+// BOTH: the launch runs both products of the experts.
+template <int NB, bool BOTH>
 struct Q4Shared {
   unsigned long long full[2][red_slots(NB)], empty[2][red_slots(NB)];  // mbarriers, by product
   int4 info[red_slots(NB)];  // unit in a slot: expert, first token slot, tokens, first tile
   int tile_end[red_slots(NB)];  // tiles from here on are not the unit's
   int part[red_slots(NB)];   // and its part of amax
   int cnt[kMaxExperts + 1];  // first slot of each expert (offs)
-  int blk[kMaxExperts + 1];  // exclusive prefix of the experts' token blocks
-  int warp_sum[kQ4Warps];
+  int blk[BOTH + 1][kMaxExperts + 1];  // exclusive prefix of the experts' units, by product
+  int warp_sum[BOTH + 1][kQ4Warps];
   int64_t t0, t1;            // the CTA's row tiles
   int row[8 * NB];           // the block's rows of x
   uint32_t amax[4][8 * NB];  // largest magnitude of each token's row (bits), by block
@@ -264,9 +273,9 @@ __device__ __forceinline__ void products_far(Q4Sums<NB> &acc, const unsigned cha
 // rows may be too long for all their activations to be resident; SECOND: after
 // a Q4_W13 in the same launch, whose h is complete when the grid barrier that
 // this CTA arrived at (`arrived`) opens.
-template <int FMT, int NB, bool CHUNKS, int MODE, bool SECOND>
-__device__ __forceinline__ void q4_run(const Q4Args &a, Q4Shared<NB> &sh, uint32_t arrived) {
-  constexpr int TB = 8 * NB;                        // tokens per unit
+template <int FMT, int NB, bool CHUNKS, int MODE, bool SECOND, bool BOTH>
+__device__ __forceinline__ void q4_run(const Q4Args &a, Q4Shared<NB, BOTH> &sh, uint32_t arrived) {
+  constexpr int TB = block_tokens(MODE) * NB;       // tokens per unit
   constexpr int G = FMT == MOE_Q4_MXFP4 ? 32 : 16;  // columns per scale
   constexpr int SW = scale_words(FMT), RS = red_slots(NB), STEP = step_bytes(FMT);
   constexpr int SL = step_slabs(FMT), RING = ring_steps(FMT);
@@ -288,9 +297,11 @@ __device__ __forceinline__ void q4_run(const Q4Args &a, Q4Shared<NB> &sh, uint32
     pdl_wait();
     pdl_launch_dependents();
   }
-  // token blocks of each expert and their prefix
+  // units of tokens of each expert and their prefix, for the second product too
+  const auto &blk = sh.blk[SECOND];
   if (!SECOND) {
-    int lo = 0, nb = 0;
+    constexpr int TB2 = block_tokens(Q4_W2) * NB;
+    int lo = 0, nb = 0, nb2 = 0;
     if (a.offs == nullptr) {
       if (tid == 0) nb = (int)((a.N + TB - 1) / TB);
       if (tid <= 1) sh.cnt[tid] = tid == 0 ? 0 : (int)a.N;
@@ -299,23 +310,38 @@ __device__ __forceinline__ void q4_run(const Q4Args &a, Q4Shared<NB> &sh, uint32
       lo = min(max(__ldg(a.offs + tid), 0), (int)a.N);
       const int hi = min(max(__ldg(a.offs + tid + 1), lo), (int)a.N);
       nb = (hi - lo + TB - 1) / TB;
+      if (BOTH) nb2 = (hi - lo + TB2 - 1) / TB2;
       sh.cnt[tid] = lo;
       if (tid == a.E - 1) sh.cnt[a.E] = hi;
     }
-    int inc = nb;
+    int inc = nb, inc2 = nb2;
     if (a.E > 1) {
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += v;
+        if (BOTH) {
+          const int v2 = __shfl_up_sync(0xffffffffu, inc2, o);
+          if (lane >= o) inc2 += v2;
+        }
       }
-      if (lane == 31) sh.warp_sum[wid] = inc;
+      if (lane == 31) {
+        sh.warp_sum[0][wid] = inc;
+        if (BOTH) sh.warp_sum[BOTH][wid] = inc2;
+      }
       __syncthreads();
-      for (int w = 0; w < wid && w < kMaxExperts / 32; ++w) inc += sh.warp_sum[w];
+      for (int w = 0; w < wid && w < kMaxExperts / 32; ++w) {
+        inc += sh.warp_sum[0][w];
+        if (BOTH) inc2 += sh.warp_sum[BOTH][w];
+      }
     }
     if (tid < a.E) {
-      sh.blk[tid] = inc - nb;
-      if (tid == a.E - 1) sh.blk[a.E] = inc;
+      sh.blk[0][tid] = inc - nb;
+      if (BOTH) sh.blk[BOTH][tid] = inc2 - nb2;
+      if (tid == a.E - 1) {
+        sh.blk[0][a.E] = inc;
+        if (BOTH) sh.blk[BOTH][a.E] = inc2;
+      }
     }
     __syncthreads();
   }
@@ -325,7 +351,7 @@ __device__ __forceinline__ void q4_run(const Q4Args &a, Q4Shared<NB> &sh, uint32
   // one block, kw warps along each row. More warps along a row leave fewer
   // idle at the end of the CTA's tiles, but cost a join and, for each unit,
   // about the time of two steps.
-  const int blocks = sh.blk[a.E], tiles = (a.R + 15) / 16, in_row = min(a.slabs, a.chunk);
+  const int blocks = blk[a.E], tiles = (a.R + 15) / 16, in_row = min(a.slabs, a.chunk);
   int kw = 1;
   const int64_t all = (int64_t)blocks * tiles;
   const int64_t share = all >> 32 ? all / gridDim.x : (uint32_t)all / gridDim.x;
@@ -371,10 +397,10 @@ __device__ __forceinline__ void q4_run(const Q4Args &a, Q4Shared<NB> &sh, uint32
     int lo = 0, hi = a.E;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (sh.blk[mid] <= b) lo = mid; else hi = mid;
+      if (blk[mid] <= b) lo = mid; else hi = mid;
     }
     e = lo;
-    tb = b - sh.blk[lo];
+    tb = b - blk[lo];
   };
   // this warp's slabs of a chunk: n of them from lo
   auto slabs_of = [&](int ch, int &lo, int &n) {
@@ -490,10 +516,11 @@ __device__ __forceinline__ void q4_run(const Q4Args &a, Q4Shared<NB> &sh, uint32
   const int s_at1 =
       1024 * SL + frag1 * (4 * SW) + ((uint32_t)tile_row(rw, frag1) * (a.C / G) & 3) + c * (32 / G);
 
-  // ---- activations of a token block as fp16 B fragments: for slab s, quarter
-  // q and token block b, lane (g, c) finds columns 128 s + 32 c + 8 q .. + 7 of
-  // token 8 b + g in its 16 bytes. What lies there for tokens past the block's
-  // end reaches only sums that are dropped.
+  // ---- activations of a unit's tokens as fp16 B fragments: for slab s, quarter
+  // q and block b, lane (g, c) finds columns 128 s + 32 c + 8 q .. + 7 of
+  // token 8 b + g in its 16 bytes; of h, token 4 b + g / 2, the fp16 value where
+  // g is even and what it leaves where g is odd. What lies there for tokens
+  // past the unit's end reaches only sums that are dropped.
   int nt = 0, part = 3, cur_e = 0, cur_p0 = 0;  // tokens of the block; its part of sh.amax
   int cur_b = b0;
   // BYTES of an activation: 4 warps (fp32; 2 for 16 bits) take a token's row
@@ -585,7 +612,22 @@ __device__ __forceinline__ void q4_run(const Q4Args &a, Q4Shared<NB> &sh, uint32
           uint4 v;
           memcpy(&v, h, 16);
           // at = 16 slab + 4 c + quarter
-          xs[(((at >> 4) * 4 + (at & 3)) * NB + (t >> 3)) * 32 + (t & 7) * 4 + ((at >> 2) & 3)] = v;
+          constexpr int BT = block_tokens(MODE), COLS = 8 / BT;
+          uint4 *to = xs + (((at >> 4) * 4 + (at & 3)) * NB + (uint32_t)t / BT) * 32 +
+                      (t & (BT - 1)) * (4 * COLS) + ((at >> 2) & 3);
+          to[0] = v;
+          if constexpr (MODE == Q4_W2) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 d = __half22float2(h[j]);
+              // an infinity or NaN leaves nothing (inf - inf would be NaN)
+              const float lo = fabsf(d.x) < INFINITY ? x[2 * j] * f - d.x : 0.f;
+              const float hi = fabsf(d.y) < INFINITY ? x[2 * j + 1] * f - d.y : 0.f;
+              h[j] = __floats2half2_rn(lo, hi);
+            }
+            memcpy(&v, h, 16);
+            to[4] = v;
+          }
         }
       }
     }
@@ -688,15 +730,16 @@ __device__ __forceinline__ void q4_run(const Q4Args &a, Q4Shared<NB> &sh, uint32
     }
   };
   // The finished sums v of one row tile and token block: fragment rows g and
-  // g + 8 of tokens 2 c and 2 c + 1.
+  // g + 8 of columns 2 c and 2 c + 1, two tokens or the two terms of one.
   auto store = [&](const float *v, int e, int p0, int q_nt, int q_part, int tile, int b) {
     const float ms = a.mscale ? __ldg(a.mscale + e) : 1.f;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int t = b * 8 + c * 2 + j;
+    for (int j = 0; j < (MODE == Q4_W2 ? 1 : 2); ++j) {
+      const int t = MODE == Q4_W2 ? b * 4 + c : b * 8 + c * 2 + j;
       if (t >= q_nt) continue;
       const float s = exp2i(-row_exponent(sh.amax[q_part][t]));
-      const float lo = v[j] * ms * s, hi = v[2 + j] * ms * s;
+      const float lo = (MODE == Q4_W2 ? v[0] + v[1] : v[j]) * ms * s;
+      const float hi = (MODE == Q4_W2 ? v[2] + v[3] : v[2 + j]) * ms * s;
       const int64_t p = (int64_t)p0 + t;
       const int row = tile * 16 + g;
       if (MODE == Q4_W13) {
@@ -829,7 +872,7 @@ __device__ __forceinline__ void q4_run(const Q4Args &a, Q4Shared<NB> &sh, uint32
 
 template <int FMT, int NB, bool CHUNKS, int MODE>
 __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
-  __shared__ Q4Shared<NB> sh;
+  __shared__ Q4Shared<NB, false> sh;
   q4_run<FMT, NB, CHUNKS, MODE, false>(a, sh, 0u);
 }
 
@@ -838,7 +881,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a) {
 // barrier needs all CTAs resident (one per SM); it is bounded like every wait.
 template <int FMT, int NB>
 __global__ void __launch_bounds__(kQ4Threads, 1) q4_ffn_kernel(const Q4Args a, const Q4Args b) {
-  __shared__ Q4Shared<NB> sh;
+  __shared__ Q4Shared<NB, true> sh;
   q4_run<FMT, NB, false, Q4_W13, false>(a, sh, 0u);
   const uint32_t arrived = grid_arrive(a.ctrl);
   q4_run<FMT, NB, false, Q4_W2, true>(b, sh, arrived);
@@ -847,7 +890,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_ffn_kernel(const Q4Args a, c
 // Slabs whose activations fit beside the ring and the partial sums.
 template <int FMT, int NB>
 constexpr int slabs_that_fit() {
-  return (kSmemMax - (int)sizeof(Q4Shared<NB>) -
+  return (kSmemMax - (int)sizeof(Q4Shared<NB, true>) -
           kQ4Warps * (ring_steps(FMT) * step_bytes(FMT) + red_slots(NB) * NB * 512)) /
          (NB * kSlabXBytes);
 }
