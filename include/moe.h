@@ -480,7 +480,9 @@ size_t moe_q4_workspace_size(int64_t n, int32_t E, int32_t k, int32_t H, int32_t
  * [n*k, H] of dtype; rows past the kept slots are zero. No gate weight is
  * applied (moe_combine_weighted does). E may be less than k: a rank that
  * holds few of the experts. h stays fp32 up to the second product,
- * which takes it as two scaled fp16 terms (22 bits). One cooperative launch with a bounded grid
+ * which takes it as two scaled fp16 terms (22 bits). A NaN in x, a scale or
+ * a matrix_scale reaches every result whose sum has it, through the clamps and
+ * max(a, 0) of the activations too. One cooperative launch with a bounded grid
  * barrier between the products (MOE_ERR_TIMEOUT in the status word if it
  * gives up); two launches where w13 and w2 differ in format or a row is too
  * long for its activations to stay in shared memory. params: activation, layout and the values of

@@ -269,6 +269,14 @@ __device__ __forceinline__ void products_far(Q4Sums<NB> &acc, const unsigned cha
   }
 }
 
+// The activations with NaN passed on: the layer's own take minima and maxima,
+// which drop it, and a corrupt token or scale would go on as a finite number.
+__device__ __forceinline__ float activate_or_nan(float g, float u, const ActParams &p) {
+  const float h = activate(g, u, p);
+  return isnan(g) || isnan(u) ? NAN : h;
+}
+__device__ __forceinline__ float relu2_or_nan(float a) { return isnan(a) ? a : relu2(a); }
+
 // One product. FMT: moe_q4_format; NB: blocks of 8 tokens per unit; CHUNKS:
 // rows may be too long for all their activations to be resident; SECOND: after
 // a Q4_W13 in the same launch, whose h is complete when the grid barrier that
@@ -746,10 +754,10 @@ __device__ __forceinline__ void q4_run(const Q4Args &a, Q4Shared<NB, BOTH> &sh, 
         float *h = static_cast<float *>(a.out);
         if (gated) {
           const int I = a.R >> 1, col = tile * 8 + g;
-          if (col < I) h[p * I + col] = activate(lo, hi, a.ap);
+          if (col < I) h[p * I + col] = activate_or_nan(lo, hi, a.ap);
         } else {
-          if (row < a.R) h[p * a.R + row] = relu2(lo);
-          if (row + 8 < a.R) h[p * a.R + row + 8] = relu2(hi);
+          if (row < a.R) h[p * a.R + row] = relu2_or_nan(lo);
+          if (row + 8 < a.R) h[p * a.R + row + 8] = relu2_or_nan(hi);
         }
       } else {
         uint16_t *o = static_cast<uint16_t *>(a.out) + p * a.R;
