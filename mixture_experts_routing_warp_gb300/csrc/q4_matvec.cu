@@ -226,8 +226,9 @@ __device__ __forceinline__ void products(Q4Sums<NB> &d, const uint4 &c0, const u
 }
 
 // An MXFP4 slab whose scales do not fit one reference: one group per row at a
-// time, the lanes c = j. Rare (no quantiser spreads a row's scales over 2^26),
-// so it is kept small: a quarter at a time, codes read where they are used.
+// time, the lanes c = j; the other lanes' activations count as zeros (their
+// weights may not: an infinity would meet a zero there). Rare, so it is kept
+// small: a quarter at a time, codes read where they are used.
 template <int NB>
 __device__ __forceinline__ void products_far(Q4Sums<NB> &acc, const unsigned char *codes,
                                              const uint4 *x, uint32_t s0, uint32_t s1,
@@ -235,7 +236,7 @@ __device__ __forceinline__ void products_far(Q4Sums<NB> &acc, const unsigned cha
   const int lane = threadIdx.x & 31;
 #pragma unroll 1
   for (int j = 0; j < 4; ++j) {
-    const uint32_t one = (lane & 3) == j ? 0x3c003c00u : 0u;
+    const uint32_t mine = (lane & 3) == j ? 0xffffffffu : 0u;
     float d[NB][4] = {};
 #pragma unroll 1
     for (int q = 0; q < 4; ++q) {
@@ -244,12 +245,11 @@ __device__ __forceinline__ void products_far(Q4Sums<NB> &acc, const unsigned cha
       e2m1x8_to_half2(*reinterpret_cast<const uint32_t *>(codes + 512 + 4 * q), v1);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint32_t A[4] = {hmul2(v0[2 * i], one), hmul2(v1[2 * i], one),
-                               hmul2(v0[2 * i + 1], one), hmul2(v1[2 * i + 1], one)};
+        const uint32_t A[4] = {v0[2 * i], v1[2 * i], v0[2 * i + 1], v1[2 * i + 1]};
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           const uint4 f = x[(q * NB + b) * 32];
-          mma16816(d[b], A, i ? f.z : f.x, i ? f.w : f.y);
+          mma16816(d[b], A, (i ? f.z : f.x) & mine, (i ? f.w : f.y) & mine);
         }
       }
     }
@@ -725,16 +725,24 @@ __device__ __forceinline__ void q4_run(const Q4Args &a, Q4Shared<NB, BOTH> &sh, 
         s0 = ref0;
         s1 = ref1;
       }
-      const uint32_t d0 = s0 - ref0 + 14u, d1 = s1 - ref1 + 14u;
-      uint32_t e0 = d0 * 0x04000400u + 0x04000400u, e1 = d1 * 0x04000400u + 0x04000400u;
-      if (__any_sync(0xffffffffu, d0 > 26u || d1 > 26u)) {
+      const bool far = __any_sync(0xffffffffu, s0 - ref0 + 14u > 26u || s1 - ref1 + 14u > 26u);
+      if (far) {
+        // in place of the products below, whose zero weights would meet infinities.
+        // With one block the step ends here, a second copy of the refill: a test
+        // after the first one keeps the products from overlapping it (GPT-OSS
+        // experts, 8 tokens: 95 us, 87 so); with two blocks the copy costs spills
+        // (64 tokens: 168 us, 175 with it).
         products_far<NB>(acc, codes, x, s0, s1, ref0, ref1);
-        e0 = e1 = 0u;  // what follows adds zeros
+        if (NB == 1) {
+          refill();
+          return;
+        }
       }
+      const uint32_t e0 = (s0 - ref0 + 15u) * 0x04000400u, e1 = (s1 - ref1 + 15u) * 0x04000400u;
       const uint32_t m0[2] = {e0, e0}, m1[2] = {e1, e1};
       const uint4 c0 = code(0, 0), c1 = code(0, 1);
       refill();
-      products<NB>(acc, c0, c1, x, m0, m1);
+      if (NB == 1 || !far) products<NB>(acc, c0, c1, x, m0, m1);
     }
   };
   // The finished sums v of one row tile and token block: fragment rows g and
