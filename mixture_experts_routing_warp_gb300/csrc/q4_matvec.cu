@@ -19,9 +19,10 @@
 //    four lanes of a row hold different groups: an E4M3 scale times an E2M1
 //    value has 6 significant bits and fits fp16's range, so the product is
 //    exact. E8M0 scales span 2^-127 .. 2^127: each row takes its scales
-//    relative to one reference 2^(r - 127), its own first scale, and 2^(s - r)
-//    is exact in fp16 for -14 <= s - r <= 12; the row's sum is scaled by the
-//    reference in fp32. Steps with a scale outside that run group by group.
+//    relative to one reference 2^(r - 127), the largest of its first slab, and
+//    2^(s - r) is exact in fp16 for -14 <= s - r <= 12; the row's sum is scaled
+//    by the reference in fp32. Steps with a scale outside that, in a group that
+//    is not all zeros, run group by group.
 //  - Activations become fp16 once per CTA, each token's row scaled by a power
 //    of two so that its largest magnitude lies in [2^14, 2^15): bf16's 8 (or
 //    fp16's 11) significant bits stay exact down to 2^-28 of the row's
@@ -223,6 +224,22 @@ __device__ __forceinline__ void products(Q4Sums<NB> &d, const uint4 &c0, const u
       mma16816(d.v[NB == 1 ? 1 : b], A[1], f.z, f.w);
     }
   }
+}
+
+// Whether a lane's 32 codes are all zeros, of either sign.
+__device__ __forceinline__ bool all_zeros(const uint4 &c) {
+  return ((c.x | c.y | c.z | c.w) & 0x77777777u) == 0u;
+}
+
+// A row's reference from its first slab (scale s and codes c of this lane's
+// group): the largest scale but those of groups of zeros, which quantisers give
+// a scale far below the others', and NaN; about a trained weight's where all
+// four are such.
+__device__ __forceinline__ uint32_t row_reference(uint32_t s, const uint4 &c) {
+  uint32_t top = s == 255u || all_zeros(c) ? 0u : s;
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  return top == 0u ? 120u : min(max(top, 96u), 158u);
 }
 
 // An MXFP4 slab whose scales do not fit one reference: one group per row at a
@@ -717,23 +734,31 @@ __device__ __forceinline__ void q4_run(const Q4Args &a, Q4Shared<NB, BOTH> &sh, 
       }
     } else {
       uint32_t s0 = st[s_at0], s1 = st[s_at1];
-      if (fresh) {  // the unit's first step: each row's reference, where 2^(s - ref) has room
-        ref0 = min(max(__shfl_sync(0xffffffffu, s0, lane & ~3), 96u), 158u);
-        ref1 = min(max(__shfl_sync(0xffffffffu, s1, lane & ~3), 96u), 158u);
+      if (left <= 0) s0 = s1 = 0u;  // (of stale codes: no part of a reference)
+      if (fresh) {  // the unit's first step
+        ref0 = row_reference(s0, code(0, 0));
+        ref1 = row_reference(s1, code(0, 1));
       }
       if (left <= 0) {
         s0 = ref0;
         s1 = ref1;
       }
-      const bool far = __any_sync(0xffffffffu, s0 - ref0 + 14u > 26u || s1 - ref1 + 14u > 26u);
-      if (far) {
-        // in place of the products below, whose zero weights would meet infinities.
+      auto apart = [&] {
+        return __any_sync(0xffffffffu, s0 - ref0 + 14u > 26u || s1 - ref1 + 14u > 26u);
+      };
+      bool far = false;
+      if (apart()) {
+        // groups of zeros take any scale but NaN; what is still apart takes the
+        // place of the products below, whose zero weights would meet infinities.
         // With one block the step ends here, a second copy of the refill: a test
         // after the first one keeps the products from overlapping it (GPT-OSS
         // experts, 8 tokens: 95 us, 87 so); with two blocks the copy costs spills
         // (64 tokens: 168 us, 175 with it).
-        products_far<NB>(acc, codes, x, s0, s1, ref0, ref1);
-        if (NB == 1) {
+        if (s0 != 255u && all_zeros(code(0, 0))) s0 = ref0;
+        if (s1 != 255u && all_zeros(code(0, 1))) s1 = ref1;
+        far = apart();
+        if (far) products_far<NB>(acc, codes, x, s0, s1, ref0, ref1);
+        if (NB == 1 && far) {
           refill();
           return;
         }

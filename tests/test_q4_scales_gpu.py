@@ -27,6 +27,21 @@ def test_infinity_beside_far_scales(n):
 
 
 @pytest.mark.parametrize("n", [1, 12])
+@pytest.mark.parametrize("zero_scale", [25, 85, 0])
+def test_groups_of_zeros(n, zero_scale):
+    """A quantiser gives a group of zeros a scale far below the others': first
+    in a row, in the middle, whole slabs of them, whole rows."""
+    C, R = 1024, 48
+    w, x = random_q4((R, C), "mxfp4", 180), tokens(n, C, BF16, 181)
+    codes, scales = w.codes.view(R, C // 32, 16), w.scales
+    for r, groups in ((0, [0]), (1, [0, 1, 2, 3]), (2, [5]), (3, range(8, 16)), (4, range(32)),
+                      (5, range(31)), (21, [31]), (40, range(0, 32, 2))):
+        for j in groups:
+            codes[r, j], scales[r, j] = 0x80 if r % 2 else 0, zero_scale
+    check(moe.linear_q4(x, w), *product64(x.double(), decode64(w)))
+
+
+@pytest.mark.parametrize("n", [1, 12])
 def test_scales_that_climb_and_fall(n):
     """Rows whose scales rise or fall along the row by more than one
     reference holds, with activations on the small groups alone too."""
