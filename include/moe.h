@@ -442,7 +442,8 @@ moe_status moe_route_backward(const float *logits, const int32_t *topk_indx, con
  *   MOE_Q4_NVFP4  groups of 16, scale byte an E4M3 value, times the matrix's
  *                 matrix_scale ([R3] title: NVFP4 MoE weights)
  * A matrix of R rows and C columns (C a multiple of 32): codes [R, C/2] and
- * scales [R, C/group] bytes, row-major; E matrices follow one another. The
+ * scales [R, C/group] bytes, row-major; E matrices follow one another. R * C
+ * is at most 2^36 (for the experts H * I at most 2^35). The
  * products are exact in the weights, summed in fp32; activations enter as
  * fp16 scaled by a power of two per row (what lies below 2^-28 of a row's
  * largest magnitude loses bits, below 2^-39 it vanishes). Right for any number

@@ -619,7 +619,7 @@ moe_status moe_forward_q4(const void *x, const float *logits, const moe_q4_matri
                           int32_t *topk_indx, uint16_t *topk_vals, const moe_routing_meta *meta,
                           void *workspace, size_t workspace_bytes, moe_stream stream) {
   moe_status st = check_sizes(n, E, k, H, I, true);
-  if (st != MOE_OK) return st;
+  if (st != MOE_OK || (st = check_q4_sizes(n, E, k, H, I)) != MOE_OK) return st;
   ActParams act;
   int gating = 0;
   if ((st = resolve_params(params, act, &gating)) != MOE_OK) return st;
