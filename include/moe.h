@@ -426,7 +426,9 @@ moe_status moe_combine_weighted_backward(const void *d_out, const void *y_sorted
  * over the k selected experts (MOE_GATING_SOFTMAX_TOPK; 0 at the others) or
  * over all E (MOE_GATING_SOFTMAX_ALL). The selection itself is piecewise
  * constant and has no gradient. An expert id outside [0, E) counts as no
- * selection. */
+ * selection. A logit or gradient that is not finite goes through the formula
+ * and reaches its own token alone: NaN where p is (a NaN or +inf among the
+ * softmax's logits, or all of them -inf), still 0 at experts outside it. */
 moe_status moe_route_backward(const float *logits, const int32_t *topk_indx, const float *d_vals,
                               int64_t n, int32_t E, int32_t k, int32_t gating, float *d_logits,
                               moe_stream stream);

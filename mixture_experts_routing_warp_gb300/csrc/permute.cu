@@ -670,7 +670,9 @@ route_backward_kernel(const float *logits, const int32_t *topk_indx, const float
     den += __shfl_xor_sync(0xffffffffu, den, o);
     dot += __shfl_xor_sync(0xffffffffu, dot, o);
   }
-  const float scale = den > 0.f ? 1.f / den : 0.f, mean = dot * scale;
+  // den is NaN beside a NaN or +inf logit and 0 where every one is -inf: NaN for
+  // the softmax's support, like the gate weights themselves
+  const float scale = 1.f / den, mean = dot * scale;
 #pragma unroll
   for (int q = 0; q < NQ; ++q) {
     const int e = (q * G + g) * V;
@@ -682,6 +684,18 @@ route_backward_kernel(const float *logits, const int32_t *topk_indx, const float
       *reinterpret_cast<float4 *>(d_logits + t * E + e) = make_float4(o[0], o[1], o[2], o[3]);
     else
       d_logits[t * E + e] = o[0];
+  }
+  // Experts outside the support stay 0 beside such a logit or gradient too: the
+  // rare token looks its experts up once more (a mask kept for every token took
+  // 7.3 us for 6.5 at 16384 tokens and 128 experts).
+  if (on && !all && !(fabsf(mean) < INFINITY)) {
+#pragma unroll 1
+    for (int q = 0; q < NQ * V; ++q) {
+      const int e = (q / V * G + g) * V + q % V;
+      bool chosen = e >= E;
+      for (int j = 0; j < k; ++j) chosen |= __ldg(topk_indx + t * k + j) == e;
+      if (!chosen) d_logits[t * E + e] = 0.f;
+    }
   }
 }
 
