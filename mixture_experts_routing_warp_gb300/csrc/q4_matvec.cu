@@ -975,11 +975,25 @@ cudaError_t go(size_t smem, cudaStream_t s, const Args &...args) {
   return err == cudaSuccess ? cudaGetLastError() : err;
 }
 
-// Two token blocks per unit where experts have more than 8 tokens on average
-// or nearly so, if a row's activations then stay resident.
+// Two token blocks per unit for more than 8 tokens of one matrix, and for
+// experts of 7 or more on average, if a row's activations then stay resident.
+// One and two blocks in us, MXFP4 / NVFP4:
+//   one matrix 16384 x 2880, 8 tokens     13.4 14.9 / 12.3 14.5
+//                            9            23.8 15.9 / 20.4 15.6
+//   GPT-OSS experts, average of 5         138.9 153.2 / 136.4 141.4
+//                               6         151.9 153.5 / 152.4 143.7
+//                               8         180.0 170.5 / 173.0 157.8
+//   8 experts of 2880 x 2880,   6         54.5 59.1 / 47.4 54.5
+//                               8         65.3 65.5 / 55.0 58.3
+//                               10        75.4 68.5 / 64.3 64.3
+// A single expert does not mind the second reading of its weights: 15.4 and
+// 17.1 for one token, 22.7 and 22.8 for 16. The average counts dropped slots too,
+// as the host does not know how many a rank keeps: with 4 of 32 experts and 8
+// tokens that takes 30.5 us for 27.3 (the layer). The layer does know what to
+// expect, but its rows would then not be moe_grouped_ffn_q4's bit for bit.
 template <int FMT>
 bool two_blocks(const Q4Args &a) {
-  return a.N > 8 * (int64_t)(a.offs ? a.E / 2 : 1) && a.slabs <= slabs_that_fit<FMT, 2>();
+  return (a.offs ? a.N >= 7 * (int64_t)a.E : a.N > 8) && a.slabs <= slabs_that_fit<FMT, 2>();
 }
 
 template <int FMT, int MODE>
