@@ -792,9 +792,10 @@ static cudaError_t combine_typed(const void *y, const int32_t *row_sorted, const
                                               (int)rb, margin, out);
   }
   const int vpr = (int)(rb / 16);
-  // H 1440, bf16: 16384 tokens, k 1, 26 -> 15 us with four tokens a thread;
-  // few tokens are better spread over the SMs (300: 2.6 us with one)
-  const int tok = n >= 2048 && k <= 2 ? 4 / k : 1;
+  // bf16, k 1, one and four tokens a thread: H 1440, 512 tokens 2.2 and 2.0 us,
+  // 1024 3.2 and 2.4, 16384 24.6 and 13.7; H 512, 512 tokens 1.6 and 2.0, 1024
+  // 1.8 and 2.0, 2048 3.1 and 2.3 (few are better spread over the SMs)
+  const int tok = n >= 1024 && k <= 2 ? 4 / k : 1;
   const RowBlock b((n + tok - 1) / tok, vpr, kMaxRowThreads);
 #define MOE_COMBINE(TOK_) \
   return go<combine_weighted_kernel<T, TOK_>>(b.grid, b.block, s, y, row_sorted, w, wd, n, k, vpr, out)
