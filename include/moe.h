@@ -377,7 +377,7 @@ moe_status moe_forward_gate(const uint16_t *x, const uint16_t *w_gate, const uin
  * metadata's last offset, &offs[E] or &offs[n_local_experts]); the rows of
  * positions [*n_kept, n*k) are then set to zero. NULL = no such rows.
  *
- * Rows are [., H] row-major of `dtype` (any H >= 1), every base aligned to
+ * Rows are [., H] row-major of `dtype` (H from 1 to 65536), every base aligned to
  * its element; 16-byte aligned rows (H * size and the bases) run fastest.
  * Sums run in fp32 in slot order and are rounded once: no atomics, the bits
  * depend on the inputs only. No workspace. n = 0 is a no-op. An input and an

@@ -419,9 +419,10 @@ inline cudaError_t launch_dependent(void (*kern)(KArgs...), dim3 grid, dim3 bloc
   return cudaLaunchKernelEx(&cfg, kern, static_cast<Args &&>(args)...);
 }
 
-// Every kernel of the library asks for the same L1 / shared-memory split
-// (all shared: the grouped GEMM needs ~200 KB), so that consecutive kernels
-// never wait for an SM to drain and reconfigure. Call once per kernel and
+// Every kernel of moe_forward, and the 4-bit products, ask for the same L1 /
+// shared-memory split (all shared: the grouped GEMM needs ~200 KB), so that
+// consecutive kernels never wait for an SM to drain and reconfigure. (The
+// sorted-row kernels keep the default: they live on L1.) Call once per kernel and
 // device before its first launch there (through PerDeviceOnce).
 template <typename Kern>
 inline cudaError_t uniform_carveout(Kern kern) {

@@ -147,10 +147,11 @@ dispatch_kernel(const void *x, const int32_t *row_sorted, const int32_t *n_kept,
 
 // One vector per thread and row, four rows in flight; blockDim.x threads along
 // the row, blockDim.y tokens. `w` null: all weights 1 (the dispatch's backward
-// pass). One vector a thread keeps the kernel at 40 registers and the SM full:
-// three vectors a thread measured 98 us where this takes 70 (16384 tokens,
-// H 2880, k 4). The sums leave by streaming stores (74 us without). TOK: tokens
-// per thread, 1, or for k = 4 / TOK so many that four rows are in flight.
+// pass). One vector a thread keeps the kernel at 40 registers (16-bit rows: at
+// the price of 24 bytes of spills) and the SM full: three vectors a thread
+// measured 98 us where this takes 76 (16384 tokens, H 2880, k 4). The sums leave
+// by streaming stores (81 us without). TOK: tokens per thread, 1, or for
+// k = 4 / TOK so many that four rows are in flight.
 template <typename T, int TOK>
 __global__ void __launch_bounds__(kMaxRowThreads, TOK == 1 ? 3 : 2)
 combine_weighted_kernel(const void *y_sorted, const int32_t *row_sorted, const void *w,
@@ -279,7 +280,9 @@ combine_backward_kernel(const void *d_out, const void *y_sorted, const int32_t *
 // it lies away from the array's ends) is worked out once and not per vector,
 // and the register limits below trade rows in flight per thread for threads:
 // dispatch two and 10 CTAs of 128 (four and 8: 46.5 us), combine four and 7
-// (four and 6: 50; two and 9: 50), gradients four and 5 (two and 7: 103).
+// (four and 6: 50; two and 9: 50), gradients four and 5 (two and 7: 103). They
+// cost spills: 40 bytes in the combine of 16-bit rows (92 with k > 4), 36 to 88
+// in the gradients of k > 4.
 struct Window {
   uint4 a, b;
 };
@@ -732,7 +735,8 @@ inline RowMap row_map(int vpr) {
 
 // These kernels keep the default split of L1 and shared memory: with the
 // library's usual one (all shared) L1 is too small for the rows in flight, and
-// the combine above takes 96 us in place of 70.
+// the combine above takes 99 us in place of 76, its gradients (8192 tokens) 81
+// in place of 69.
 template <auto Kern, typename... Args>
 cudaError_t go(dim3 grid, dim3 block, cudaStream_t s, Args... args) {
   const cudaError_t err = launch_dependent(Kern, grid, block, 0, s, args...);
