@@ -5,7 +5,7 @@
 #include <math.h>
 #include <string.h>
 
-#include "moe_internal.cuh"
+#include "operators.cuh"
 
 using namespace moe;
 

@@ -13,7 +13,7 @@
 // is token-major, so that the token-side row crosses HBM once whatever k is,
 // and every sum runs in slot order in fp32: no atomics, so the bits of a
 // result depend on its inputs only.
-#include "moe_internal.cuh"
+#include "operators.cuh"
 
 #include <cuda_fp16.h>
 

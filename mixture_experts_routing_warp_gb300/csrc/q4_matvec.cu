@@ -40,6 +40,7 @@
 
 #include <type_traits>
 
+#include "operators.cuh"
 #include "tc_ptx.cuh"
 
 namespace moe {
