@@ -330,14 +330,29 @@ def _plain(st):
 
 # -------------------------------------------------------- the user's calls --
 
+def _handles(st):
+    """The row handles and the parameters that a user's program keeps."""
+    if "handles" not in st:
+        import mixture_experts_routing_warp_gb300 as moe
+
+        case, h = st["case"], {}
+        for name in ("x", "w", "w13"):
+            if isinstance(st.get(name), dict):
+                h[name] = moe.Mx8(st[name]["codes"], st[name]["scales"])
+        if case["op"].startswith("gated"):
+            h["params"] = moe.make_params(act=case["act"], layout=case["layout"])
+        st["handles"] = h
+    return st["handles"]
+
+
 def _calls(st):
     import mixture_experts_routing_warp_gb300 as moe
 
-    case = st["case"]
+    case, kept = st["case"], _handles(st)
     op = case["op"]
 
-    def rows(v):
-        return moe.Mx8(v["codes"], v["scales"]) if isinstance(v, dict) else v
+    def rows(name):
+        return kept[name] if name in kept else st[name]
 
     def plain(y):
         if isinstance(y, moe.Mx8):
@@ -355,7 +370,7 @@ def _calls(st):
                                               d_sum=st.get("d_sum"))
         return {"d_x": d_x, "d_weight": d_weight}
     if op == "linear":
-        return moe.linear(rows(st["x"]), rows(st["w"]), bias=st.get("bias"), act=case["act"],
+        return moe.linear(rows("x"), rows("w"), bias=st.get("bias"), act=case["act"],
                           residual=st.get("residual"))
     if op == "linear_grad":
         d_x, d_w, d_bias = moe.linear_backward(st["d_y"], st["x"], st["w"], bias=st.get("bias"),
@@ -364,11 +379,10 @@ def _calls(st):
         if case["bias"]:
             out["d_bias"] = d_bias
         return out
-    params = moe.make_params(act=case["act"], layout=case["layout"])
     if op == "gated":
-        return plain(moe.gated_linear(rows(st["x"]), rows(st["w13"]), params,
+        return plain(moe.gated_linear(rows("x"), rows("w13"), kept["params"],
                                       mx8=case["out"] == "mx8"))
-    d_x, d_w13 = moe.gated_linear_backward(st["d_h"], st["x"], st["w13"], params)
+    d_x, d_w13 = moe.gated_linear_backward(st["d_h"], st["x"], st["w13"], kept["params"])
     return {"d_x": d_x, "d_w13": d_w13}
 
 
