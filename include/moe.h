@@ -23,6 +23,8 @@
  * moe_combine_weighted, moe_combine_weighted_backward, moe_route_backward),
  * products with 4-bit weights for decode (moe_linear_q4, moe_grouped_ffn_q4,
  * the layer moe_forward_q4, moe_q4_workspace_size),
+ * the dense blocks beside the experts, with gradients (moe_rms_norm,
+ * moe_linear, moe_gated_linear, their _backward and _mx8 forms),
  * the workspace calls (moe_workspace_size, moe_workspace_init,
  * moe_workspace_regions), moe_read_status and moe_selftest_wait_timeout.
  *
@@ -505,6 +507,116 @@ moe_status moe_forward_q4(const void *x, const float *logits, const moe_q4_matri
                           int32_t I, const moe_params *params, int32_t dtype, void *out,
                           int32_t *topk_indx, uint16_t *topk_vals, const moe_routing_meta *meta,
                           void *workspace, size_t workspace_bytes, moe_stream stream);
+
+/* ---- The dense blocks beside the experts ---------------------------------
+ * A transformer block's norm, its dense feed-forward block (or a shared
+ * expert beside the routed ones) and the projections onto the residual
+ * stream, with their gradients. No counterpart on the pages.
+ *
+ * Rows are [n, features] row-major and contiguous, features at most 65536 and
+ * a matrix below 2^38 elements; 16-bit rows are MOE_BF16 or MOE_FP16. The
+ * products' operands x, w, w13 and the gradients d_x, d_w, d_w13 (and d_y of
+ * a backward pass) are 16-byte aligned, and the features they sum over are a
+ * multiple of 8; other arrays need their element's alignment (rows that start
+ * on 16 bytes run fastest). Sums run in fp32 in an order that depends on the
+ * sizes alone, and are rounded once. An input and an output may not overlap.
+ * n = 0 writes zeros to the gradients of weights, and nothing else.
+ *
+ * MXFP8 rows: E4M3 codes [rows, C] and E8M0 scale bytes [rows, C / 32], one
+ * per group of 32 values (2^(byte - 127); 255 = NaN), C a multiple of 32. As
+ * an output a group's scale is the least power of two under which none of its
+ * values exceeds 448; values are rounded to the nearest code; a group with an
+ * infinity or a NaN gets the scale 255, so that all of it reads as NaN.
+ *
+ * workspace: scratch of the size that the call's _workspace_size gives (0:
+ * none, NULL is fine), 256-byte aligned; it needs no preparation and keeps
+ * nothing between calls, but calls that may overlap need one each.
+ * status: optional device int32, 0 before its first use (NULL = not
+ * reported): a bounded wait that gives up records MOE_ERR_TIMEOUT there and
+ * leaves the call's outputs undefined. */
+typedef struct {
+  uint8_t *codes;   /* device, 16-byte aligned */
+  uint8_t *scales;  /* device */
+} moe_mx8_rows;
+
+typedef enum {
+  MOE_LINEAR_NONE = 0,
+  MOE_LINEAR_SILU = 1,  /* v sigmoid(v) */
+  MOE_LINEAR_GELU = 2,  /* v (1 + erf(v / sqrt 2)) / 2 */
+  MOE_LINEAR_RELU2 = 3  /* max(v, 0)^2 */
+} moe_linear_act;
+
+/* y[t] = s[t] / sqrt(mean(s[t]^2) + eps) * weight, s = x + residual rounded to
+ * `dtype` (MOE_BF16, MOE_FP16 or MOE_FP32; s = x without a residual): x, residual, y, sum
+ * [n, H], any H. weight [H] of `dtype` or MOE_FP32, NULL = ones. sum: optional
+ * output s (needs a residual). The result goes to exactly one of y and y_mx8
+ * (H a multiple of 32). eps >= 0. */
+moe_status moe_rms_norm(const void *x, const void *residual, const void *weight,
+                        int32_t weight_dtype, int64_t n, int32_t H, int32_t dtype, float eps,
+                        void *y, const moe_mx8_rows *y_mx8, void *sum, moe_stream stream);
+
+/* Gradients of moe_rms_norm; x is what it normalised (its sum, with a
+ * residual). With v = x / rms:
+ *   d_x[t] = (d w - v mean(d w v)) / rms + d_sum[t]      (the gradient of x and
+ *            of residual alike; d_sum, the gradient of sum, may be NULL)
+ *   d_weight = sum_t d_y v, of weight_dtype (NULL = not wanted, and then no
+ *            workspace). */
+size_t moe_rms_norm_backward_workspace_size(int64_t n, int32_t H);
+moe_status moe_rms_norm_backward(const void *d_y, const void *x, const void *weight,
+                                 int32_t weight_dtype, const void *d_sum, int64_t n, int32_t H,
+                                 int32_t dtype, float eps, void *d_x, void *d_weight,
+                                 void *workspace, size_t workspace_bytes, moe_stream stream);
+
+/* y = act(x w^T + bias) + residual: x [n, C], w [R, C], bias [R], residual
+ * and y [n, R], all of `dtype`; any R >= 1 (at most 131072); bias and residual may be NULL.
+ * act: moe_linear_act. _mx8: x and w in 8 bits, bias, residual and y of
+ * `dtype`; the products are exact, the sums fp32. */
+size_t moe_linear_workspace_size(int64_t n, int32_t R, int32_t C);
+moe_status moe_linear(const void *x, const void *w, const void *bias, const void *residual,
+                      int64_t n, int32_t R, int32_t C, int32_t dtype, int32_t act, void *y,
+                      void *workspace, size_t workspace_bytes, int32_t *status,
+                      moe_stream stream);
+moe_status moe_linear_mx8(const moe_mx8_rows *x, const moe_mx8_rows *w, const void *bias,
+                          const void *residual, int64_t n, int32_t R, int32_t C, int32_t dtype,
+                          int32_t act, void *y, void *workspace, size_t workspace_bytes,
+                          int32_t *status, moe_stream stream);
+
+/* Gradients of moe_linear for d_y [n, R] (the residual's is d_y itself), each
+ * NULL where it is not wanted; R a multiple of 8. With an activation its
+ * argument is computed again, and d = d_y act'(x w^T + bias) is rounded to
+ * `dtype` (as any 16-bit gradient between two layers) before
+ *   d_x = d w [n, C],   d_w = d^T x [R, C],   d_bias = sum_t d [R]. */
+size_t moe_linear_backward_workspace_size(int64_t n, int32_t R, int32_t C, int32_t act);
+moe_status moe_linear_backward(const void *d_y, const void *x, const void *w, const void *bias,
+                               int64_t n, int32_t R, int32_t C, int32_t dtype, int32_t act,
+                               void *d_x, void *d_w, void *d_bias, void *workspace,
+                               size_t workspace_bytes, int32_t *status, moe_stream stream);
+
+/* h = activation of (gate, up) = x w13^T, both projections in one product:
+ * x [n, H], w13 [2I, H] in params->w13_layout order, h [n, I] of `dtype` or
+ * h_mx8 (exactly one; I a multiple of 8, with h_mx8 of 32). params: activation
+ * (MOE_ACT_SWIGLU or MOE_ACT_SWIGLU_OAI; MOE_ACT_RELU2 has no gate:
+ * moe_linear), layout and the values of `set`. A NaN passes the clamps. */
+size_t moe_gated_linear_workspace_size(int64_t n, int32_t H, int32_t I);
+moe_status moe_gated_linear(const void *x, const void *w13, int64_t n, int32_t H, int32_t I,
+                            const moe_params *params, int32_t dtype, void *h,
+                            const moe_mx8_rows *h_mx8, void *workspace, size_t workspace_bytes,
+                            int32_t *status, moe_stream stream);
+moe_status moe_gated_linear_mx8(const moe_mx8_rows *x, const moe_mx8_rows *w13, int64_t n,
+                                int32_t H, int32_t I, const moe_params *params, int32_t dtype,
+                                void *h, const moe_mx8_rows *h_mx8, void *workspace,
+                                size_t workspace_bytes, int32_t *status, moe_stream stream);
+
+/* Gradients of moe_gated_linear for d_h [n, I], each NULL where it is not
+ * wanted: (gate, up) are computed again in fp32, their gradients (0 where a
+ * value was clamped) rounded to `dtype` in w13's row order, d [n, 2I], then
+ *   d_x = d w13 [n, H],   d_w13 = d^T x [2I, H]. */
+size_t moe_gated_linear_backward_workspace_size(int64_t n, int32_t H, int32_t I);
+moe_status moe_gated_linear_backward(const void *d_h, const void *x, const void *w13, int64_t n,
+                                     int32_t H, int32_t I, const moe_params *params,
+                                     int32_t dtype, void *d_x, void *d_w13, void *workspace,
+                                     size_t workspace_bytes, int32_t *status,
+                                     moe_stream stream);
 
 /* Stage kernels of moe_forward, in launch order (indices of the events of
  * moe_forward_timed). */

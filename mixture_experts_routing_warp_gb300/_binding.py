@@ -24,6 +24,7 @@ SET_ALPHA, SET_BETA, SET_LIMIT = 1, 2, 4
 FFN_KERNEL = {"auto": 0, "tiled": 1, "swap": 2}
 Q4_FORMAT = {"mxfp4": 0, "nvfp4": 1}
 Q4_GROUP = {"mxfp4": 32, "nvfp4": 16}
+LINEAR_ACT = {"none": 0, "silu": 1, "gelu": 2, "relu2": 3}
 DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 ABI_VERSION = 4
 
@@ -57,6 +58,10 @@ class Q4Matrix(ctypes.Structure):
                 ("matrix_scale", ctypes.c_void_p), ("format", ctypes.c_int32)]
 
 
+class Mx8Rows(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
 _LIB = None
 
 # name -> (restype, argtypes)
@@ -65,6 +70,8 @@ _P, _I64, _I32, _SZ, _U64 = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ct
 _PP = ctypes.POINTER(MoeParams)
 _PM = ctypes.POINTER(RoutingMeta)
 _PQ = ctypes.POINTER(Q4Matrix)
+_P8 = ctypes.POINTER(Mx8Rows)
+_F32 = ctypes.c_float
 SIGNATURES = {
     "moe_abi_version": (_I32, []),
     "moe_status_string": (ctypes.c_char_p, [_I32]),
@@ -99,6 +106,24 @@ SIGNATURES = {
                                   _P, _SZ, _P]),
     "moe_forward_q4": (_I32, [_P, _P, _PQ, _PQ, _I64, _I32, _I32, _I32, _I32, _PP, _I32, _P, _P,
                               _P, _PM, _P, _SZ, _P]),
+    "moe_rms_norm": (_I32, [_P, _P, _P, _I32, _I64, _I32, _I32, _F32, _P, _P8, _P, _P]),
+    "moe_rms_norm_backward_workspace_size": (_SZ, [_I64, _I32]),
+    "moe_rms_norm_backward": (_I32, [_P, _P, _P, _I32, _P, _I64, _I32, _I32, _F32, _P, _P, _P,
+                                     _SZ, _P]),
+    "moe_linear_workspace_size": (_SZ, [_I64, _I32, _I32]),
+    "moe_linear": (_I32, [_P, _P, _P, _P, _I64, _I32, _I32, _I32, _I32, _P, _P, _SZ, _P, _P]),
+    "moe_linear_mx8": (_I32, [_P8, _P8, _P, _P, _I64, _I32, _I32, _I32, _I32, _P, _P, _SZ, _P,
+                              _P]),
+    "moe_linear_backward_workspace_size": (_SZ, [_I64, _I32, _I32, _I32]),
+    "moe_linear_backward": (_I32, [_P, _P, _P, _P, _I64, _I32, _I32, _I32, _I32, _P, _P, _P, _P,
+                                   _SZ, _P, _P]),
+    "moe_gated_linear_workspace_size": (_SZ, [_I64, _I32, _I32]),
+    "moe_gated_linear": (_I32, [_P, _P, _I64, _I32, _I32, _PP, _I32, _P, _P8, _P, _SZ, _P, _P]),
+    "moe_gated_linear_mx8": (_I32, [_P8, _P8, _I64, _I32, _I32, _PP, _I32, _P, _P8, _P, _SZ, _P,
+                                    _P]),
+    "moe_gated_linear_backward_workspace_size": (_SZ, [_I64, _I32, _I32]),
+    "moe_gated_linear_backward": (_I32, [_P, _P, _P, _I64, _I32, _I32, _PP, _I32, _P, _P, _P,
+                                         _SZ, _P, _P]),
     "moe_read_status": (_I32, [_P, _SZ, _I32, _P]),
     "moe_selftest_wait_timeout": (_I32, [_P, _SZ, _U64, _P]),
 }
@@ -673,6 +698,273 @@ def forward_q4(x: torch.Tensor, logits: torch.Tensor, w13: Q4Weight, w2: Q4Weigh
          ctypes.byref(params), DTYPE[x.dtype], out.data_ptr(), _ptr(indx), _ptr(vals), mstruct,
          ws.data_ptr(), ws.numel())
     return out
+
+
+class Mx8:
+    """MXFP8 rows: codes float8_e4m3fn [rows, C] and scales uint8 [rows, C/32]
+    (E8M0), C a multiple of 32. The tensors are used where they lie; the
+    handle keeps them alive."""
+
+    __slots__ = ("codes", "scales", "device", "shape", "_as_parameter_")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
+        self.device = codes.get_device() if isinstance(codes, torch.Tensor) else -1
+        _need_on(codes, "codes", torch.float8_e4m3fn, self.device)
+        if codes.dim() != 2 or codes.shape[1] == 0 or codes.shape[1] % 32:
+            raise ValueError(f"codes must have shape [rows, C], C a multiple of 32, got "
+                             f"{tuple(codes.shape)}")
+        self.shape = codes.shape
+        _need_on(scales, "scales", torch.uint8, self.device, (self.shape[0], self.shape[1] // 32))
+        self.codes, self.scales = codes, scales
+        self._as_parameter_ = ctypes.byref(Mx8Rows(codes.data_ptr(), scales.data_ptr()))
+
+
+def _empty_mx8(rows: int, cols: int, like: torch.Tensor) -> Mx8:
+    return Mx8(torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=like.device),
+               torch.empty((rows, cols // 32), dtype=torch.uint8, device=like.device))
+
+
+def _need_rows16(t: torch.Tensor, name: str) -> int:
+    device = _need_rows(t, name)
+    if t.dtype is torch.float32:
+        raise ValueError(f"{name} must be bfloat16 or float16")
+    return device
+
+
+def _need_vector(t: torch.Tensor, name: str, dtypes: tuple, device: int, size: int) -> int:
+    """A [size] vector of one of the types; its address."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
+        raise ValueError(f"{name} must be a tensor of {' or '.join(map(str, dtypes))}")
+    _need_on(t, name, t.dtype, device, (size,))
+    return t.data_ptr()
+
+
+def _need_status(status: Optional[torch.Tensor], device: int):
+    """Address of the optional status word (int32 [1], zeroed by the caller)."""
+    if status is None:
+        return None
+    _need_on(status, "status", torch.int32, device, (1,))
+    return status.data_ptr()
+
+
+def _scratch(ws: Optional[torch.Tensor], size: int, like: torch.Tensor, device: int):
+    """(workspace tensor or None, address, bytes): the caller's, or a new one."""
+    if ws is None:
+        if size == 0:
+            return None, None, 0
+        ws = torch.empty(size, dtype=torch.uint8, device=like.device)
+    else:
+        _need_on(ws, "ws", torch.uint8, device)
+    return ws, ws.data_ptr(), ws.numel()
+
+
+def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float = 1e-5,
+             residual: Optional[torch.Tensor] = None, mx8: bool = False, out=None,
+             sum_out: Optional[torch.Tensor] = None):
+    """Root-mean-square norm of the rows x [n, H] (bf16, fp16 or fp32) times
+    weight [H] (of x's type or fp32; None: ones). With a residual [n, H] the
+    norm is of s = x + residual, rounded to x's type, and the result is (y, s).
+    mx8: y is Mx8 rows (H a multiple of 32). out, sum_out: where y and s go."""
+    device = _need_rows(x, "x")
+    n, H = x.shape
+    w_dtype, w = DTYPE[x.dtype], None
+    if weight is not None:
+        w = _need_vector(weight, "weight", (x.dtype, torch.float32), device, H)
+        w_dtype = DTYPE[weight.dtype]
+    total = None
+    if residual is not None:
+        _need_on(residual, "residual", x.dtype, device, (n, H))
+        total = _out_rows(sum_out, "sum_out", (n, H), x)
+    elif sum_out is not None:
+        raise ValueError("sum_out needs a residual")
+    if mx8:
+        y = _empty_mx8(n, H, x) if out is None else out
+        _need_mx8(y, "out", device, (n, H))
+    else:
+        y = _out_rows(out, "out", (n, H), x)
+    _run("moe_rms_norm", device, x.data_ptr(), None if residual is None else residual.data_ptr(),
+         w, w_dtype, n, H, DTYPE[x.dtype], eps, None if mx8 else y.data_ptr(),
+         y if mx8 else None, None if total is None else total.data_ptr())
+    return y if residual is None else (y, total)
+
+
+def _need_mx8(m: Mx8, name: str, device: int, shape=None) -> None:
+    if not isinstance(m, Mx8):
+        raise ValueError(f"{name} must be Mx8 rows")
+    if m.device != device:
+        raise ValueError(f"{name} is on cuda:{m.device}, not on cuda:{device}")
+    if shape is not None and m.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(m.shape)}")
+
+
+def rms_norm_backward(d_y: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor],
+                      eps: float = 1e-5, d_sum: Optional[torch.Tensor] = None,
+                      ws: Optional[torch.Tensor] = None):
+    """Gradients of rms_norm -> (d_x [n, H], d_weight [H] of weight's type, or
+    None without a weight). x is what was normalised (the sum, where there was
+    a residual; d_x is then the gradient of x and of the residual alike), d_sum the
+    gradient that reaches the sum from elsewhere, added to d_x. ws: scratch
+    (rms_norm_backward_workspace_size), allocated where it is None."""
+    device = _need_rows(x, "x")
+    n, H = x.shape
+    _need_on(d_y, "d_y", x.dtype, device, (n, H))
+    if d_sum is not None:
+        _need_on(d_sum, "d_sum", x.dtype, device, (n, H))
+    w_dtype, w, d_weight, size = DTYPE[x.dtype], None, None, 0
+    if weight is not None:
+        w = _need_vector(weight, "weight", (x.dtype, torch.float32), device, H)
+        w_dtype = DTYPE[weight.dtype]
+        d_weight = torch.empty_like(weight)
+        size = rms_norm_backward_workspace_size(n, H)
+    d_x = torch.empty_like(x)
+    ws, p, size = _scratch(ws, size, x, device)
+    _run("moe_rms_norm_backward", device, d_y.data_ptr(), x.data_ptr(), w, w_dtype,
+         None if d_sum is None else d_sum.data_ptr(), n, H, DTYPE[x.dtype], eps, d_x.data_ptr(),
+         None if d_weight is None else d_weight.data_ptr(), p, size)
+    return d_x, d_weight
+
+
+def rms_norm_backward_workspace_size(n: int, H: int) -> int:
+    return int((_LIB or lib()).moe_rms_norm_backward_workspace_size(n, H))
+
+
+def linear_workspace_size(n: int, R: int, C: int) -> int:
+    return int((_LIB or lib()).moe_linear_workspace_size(n, R, C))
+
+
+def linear_backward_workspace_size(n: int, R: int, C: int, act: str = "none") -> int:
+    return int((_LIB or lib()).moe_linear_backward_workspace_size(n, R, C, LINEAR_ACT[act]))
+
+
+def gated_linear_workspace_size(n: int, H: int, I: int) -> int:
+    return int((_LIB or lib()).moe_gated_linear_workspace_size(n, H, I))
+
+
+def gated_linear_backward_workspace_size(n: int, H: int, I: int) -> int:
+    return int((_LIB or lib()).moe_gated_linear_backward_workspace_size(n, H, I))
+
+
+def _need_act(act: str) -> int:
+    if act not in LINEAR_ACT:
+        raise ValueError(f"act must be one of {sorted(LINEAR_ACT)}, got {act!r}")
+    return LINEAR_ACT[act]
+
+
+def _product_operands(x, w, w_name: str, dtype):
+    """(device, rows, features, out features, output type) of x and w, both
+    16-bit tensors of one type or both Mx8."""
+    if isinstance(x, Mx8):
+        device = x.device
+        _need_mx8(w, w_name, device)
+        if w.shape[1] != x.shape[1]:
+            raise ValueError(f"{w_name} must have {x.shape[1]} columns, got {tuple(w.shape)}")
+        dtype = torch.bfloat16 if dtype is None else dtype
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError("dtype must be torch.bfloat16 or torch.float16")
+        return device, x.shape[0], x.shape[1], w.shape[0], dtype
+    device = _need_rows16(x, "x")
+    if dtype is not None and dtype is not x.dtype:
+        raise ValueError(f"dtype is x's, {x.dtype}, unless x is Mx8 rows")
+    _need_on(w, w_name, x.dtype, device)
+    if w.dim() != 2 or w.shape[1] != x.shape[1]:
+        raise ValueError(f"{w_name} must have shape [rows, {x.shape[1]}], got {tuple(w.shape)}")
+    return device, x.shape[0], x.shape[1], w.shape[0], x.dtype
+
+
+def linear(x, w, bias: Optional[torch.Tensor] = None, act: str = "none",
+           residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+           ws: Optional[torch.Tensor] = None, dtype: Optional[torch.dtype] = None,
+           status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """act(x w^T + bias) + residual: x [n, C] and w [R, C] bf16 or fp16, or
+    both Mx8 rows (dtype: that of the result then, bf16 by default). act:
+    "none", "silu", "gelu" or "relu2"; bias [R], residual [n, R]. ws: scratch
+    (linear_workspace_size), allocated where it is None."""
+    act_id = _need_act(act)
+    device, n, C, R, dtype = _product_operands(x, w, "w", dtype)
+    mx = isinstance(x, Mx8)
+    like = x.codes if mx else x
+    b = None if bias is None else _need_vector(bias, "bias", (dtype,), device, R)
+    if residual is not None:
+        _need_on(residual, "residual", dtype, device, (n, R))
+    if out is None:
+        out = torch.empty((n, R), dtype=dtype, device=like.device)
+    else:
+        _need_on(out, "out", dtype, device, (n, R))
+    ws, p, size = _scratch(ws, linear_workspace_size(n, R, C), like, device)
+    _run("moe_linear_mx8" if mx else "moe_linear", device, x if mx else x.data_ptr(),
+         w if mx else w.data_ptr(), b, None if residual is None else residual.data_ptr(), n, R, C,
+         DTYPE[dtype], act_id, out.data_ptr(), p, size, _need_status(status, device))
+    return out
+
+
+def linear_backward(d_y: torch.Tensor, x: torch.Tensor, w: torch.Tensor,
+                    bias: Optional[torch.Tensor] = None, act: str = "none",
+                    ws: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None):
+    """Gradients of linear (16-bit operands) for d_y [n, R] -> (d_x [n, C],
+    d_w [R, C], d_bias [R] or None without a bias). The residual's gradient is
+    d_y. R a multiple of 8. ws: scratch (linear_backward_workspace_size),
+    allocated where it is None."""
+    act_id = _need_act(act)
+    device, n, C, R, dtype = _product_operands(x, w, "w", None)
+    _need_on(d_y, "d_y", dtype, device, (n, R))
+    b = None if bias is None else _need_vector(bias, "bias", (dtype,), device, R)
+    d_x, d_w = torch.empty_like(x), torch.empty_like(w)
+    d_bias = None if bias is None else torch.empty_like(bias)
+    ws, p, size = _scratch(ws, linear_backward_workspace_size(n, R, C, act), x, device)
+    _run("moe_linear_backward", device, d_y.data_ptr(), x.data_ptr(), w.data_ptr(), b, n, R, C,
+         DTYPE[dtype], act_id, d_x.data_ptr(), d_w.data_ptr(),
+         None if d_bias is None else d_bias.data_ptr(), p, size, _need_status(status, device))
+    return d_x, d_w, d_bias
+
+
+def gated_linear(x, w13, params: MoeParams, out=None, mx8: bool = False,
+                 ws: Optional[torch.Tensor] = None, dtype: Optional[torch.dtype] = None,
+                 status: Optional[torch.Tensor] = None):
+    """The gated activation of (gate, up) = x w13^T: x [n, H] and w13 [2I, H]
+    (rows in params' layout) bf16 or fp16, or both Mx8 rows -> h [n, I] of x's
+    type (Mx8 operands: of `dtype`, bf16 by default), or Mx8 rows with mx8 (I a
+    multiple of 32). params: make_params' activation ("swiglu" or
+    "swiglu_oai"), layout and limits. ws: scratch
+    (gated_linear_workspace_size), allocated where it is None."""
+    device, n, H, rows, dtype = _product_operands(x, w13, "w13", dtype)
+    if rows % 2:
+        raise ValueError(f"w13 must have an even number of rows, got {rows}")
+    I = rows // 2
+    mx = isinstance(x, Mx8)
+    like = x.codes if mx else x
+    if mx8:
+        h = _empty_mx8(n, I, like) if out is None else out
+        _need_mx8(h, "out", device, (n, I))
+    elif out is None:
+        h = torch.empty((n, I), dtype=dtype, device=like.device)
+    else:
+        h = out
+        _need_on(h, "out", dtype, device, (n, I))
+    ws, p, size = _scratch(ws, gated_linear_workspace_size(n, H, I), like, device)
+    _run("moe_gated_linear_mx8" if mx else "moe_gated_linear", device, x if mx else x.data_ptr(),
+         w13 if mx else w13.data_ptr(), n, H, I, ctypes.byref(params), DTYPE[dtype],
+         None if mx8 else h.data_ptr(), h if mx8 else None, p, size,
+         _need_status(status, device))
+    return h
+
+
+def gated_linear_backward(d_h: torch.Tensor, x: torch.Tensor, w13: torch.Tensor,
+                          params: MoeParams, ws: Optional[torch.Tensor] = None,
+                          status: Optional[torch.Tensor] = None):
+    """Gradients of gated_linear (16-bit operands) for d_h [n, I] -> (d_x
+    [n, H], d_w13 [2I, H]). ws: scratch (gated_linear_backward_workspace_size),
+    allocated where it is None."""
+    device, n, H, rows, dtype = _product_operands(x, w13, "w13", None)
+    if rows % 2:
+        raise ValueError(f"w13 must have an even number of rows, got {rows}")
+    I = rows // 2
+    _need_on(d_h, "d_h", dtype, device, (n, I))
+    d_x, d_w13 = torch.empty_like(x), torch.empty_like(w13)
+    ws, p, size = _scratch(ws, gated_linear_backward_workspace_size(n, H, I), x, device)
+    _run("moe_gated_linear_backward", device, d_h.data_ptr(), x.data_ptr(), w13.data_ptr(), n, H,
+         I, ctypes.byref(params), DTYPE[dtype], d_x.data_ptr(), d_w13.data_ptr(), p, size,
+         _need_status(status, device))
+    return d_x, d_w13
 
 
 STAGES = ("route", "metadata", "gather", "ffn1", "ffn2", "combine")

@@ -1,0 +1,293 @@
+// dense.cuh -- shared pieces of the dense products beside the experts
+// (moe_linear, moe_gated_linear and their gradients): what becomes of the
+// fp32 sums, the row types, and the launchers' interface.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <string.h>
+
+#include "operators.cuh"
+
+namespace moe {
+
+// What is done with the sums a[row, col] of a product.
+enum DenseKind {
+  EPI_LINEAR = 0,    // out = act(a + bias) + add
+  EPI_DACT = 1,      // out = add * act'(a + bias): add is the gradient of act's result
+  EPI_GATED = 2,     // a holds (gate, up) pairs: out = h
+  EPI_GATED_MX = 3,  // the same, h as E4M3 codes with a scale per 32
+  EPI_DGATED = 4,    // (gate, up) pairs and add = d_h: out = (d_gate, d_up) in w13's row order
+  EPI_PARTIAL = 5    // out = a in fp32, to be joined with the other parts of a split sum
+};
+
+struct DenseEpi {
+  int64_t rows;        // rows of out
+  int cols;            // columns of the sums
+  int half;            // 16-bit values are fp16, else bf16
+  int act;             // moe_linear_act
+  ActParams gate;      // gated kinds
+  const void *bias;    // [cols] or null
+  const void *add;     // [rows, cols] (EPI_DGATED: [rows, cols / 2]) or null
+  void *out;           // [rows, cols] (EPI_GATED: [rows, cols / 2])
+  uint8_t *codes, *scales;  // EPI_GATED_MX
+  int vec;             // every row of bias, add and out starts on 16 bytes
+};
+
+// ------------------------------------------------------------ 16-bit rows --
+__device__ __forceinline__ float from16(uint16_t b, int half) {
+  return half ? __half2float(__ushort_as_half(b)) : bf16_bits_to_float(b);
+}
+__device__ __forceinline__ uint16_t to16(float f, int half) {
+  return half ? __half_as_ushort(__float2half_rn(f)) : float_to_bf16_bits(f);
+}
+
+__device__ __forceinline__ void unpack8(const uint4 &q, int half, float *f) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  if (half) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __half2 h;
+      memcpy(&h, &w[i], 4);
+      const float2 d = __half22float2(h);
+      f[2 * i] = d.x;
+      f[2 * i + 1] = d.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float *f, int half) {
+  uint32_t w[4];
+  if (half) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+      memcpy(&w[i], &h, 4);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      memcpy(&w[i], &h, 4);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// W 16-bit values at element `at` as floats; with `vec` the address is a
+// multiple of 16 bytes. Values from `left` on are not read (0).
+template <int W>
+__device__ __forceinline__ void load_row(const void *base, int64_t at, bool vec, int left,
+                                         int half, float (&f)[W]) {
+  const uint16_t *p = static_cast<const uint16_t *>(base) + at;
+  if (vec && left >= W) {
+    uint4 q[W / 8];
+#pragma unroll
+    for (int i = 0; i < W / 8; ++i) q[i] = *reinterpret_cast<const uint4 *>(p + 8 * i);
+#pragma unroll
+    for (int i = 0; i < W / 8; ++i) unpack8(q[i], half, f + 8 * i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i) f[i] = i < left ? from16(p[i], half) : 0.f;
+  }
+}
+
+template <int W>
+__device__ __forceinline__ void store_row(void *base, int64_t at, bool vec, int left, int half,
+                                          const float (&f)[W]) {
+  uint16_t *p = static_cast<uint16_t *>(base) + at;
+  if (vec && left >= W) {
+#pragma unroll
+    for (int i = 0; i < W / 8; ++i) *reinterpret_cast<uint4 *>(p + 8 * i) = pack8(f + 8 * i, half);
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      if (i < left) p[i] = to16(f[i], half);
+  }
+}
+
+// ------------------------------------------------------------------ MXFP8 --
+// Scale byte of a group whose largest magnitude has the bits `top`: the least
+// power of two 2^(b - 127) under which it is at most 448, E4M3's largest
+// (1.75 * 2^8, so the mantissa decides between two exponents); 255, which
+// reads as NaN, where a value of the group is infinite or NaN.
+__device__ __forceinline__ uint32_t mx8_scale(uint32_t top) {
+  if (top >= 0x7f800000u) return 255u;
+  const int b = (int)(top >> 23) - ((top & 0x7fffffu) <= 0x600000u ? 8 : 7);
+  return b < 0 ? 0u : (uint32_t)b;
+}
+// 2^(127 - b): what a value is multiplied with before it is rounded to a code
+__device__ __forceinline__ float mx8_inverse(uint32_t b) {
+  return __uint_as_float((254u - (b > 253u ? 253u : b)) << 23);
+}
+__device__ __forceinline__ uint32_t mx8_codes4(const float *f, float inv) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[0] * inv, f[1] * inv),
+                                               __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[2] * inv, f[3] * inv),
+                                               __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+// ------------------------------------------------------------ activations --
+__device__ __forceinline__ float linear_act(float v, int act) {
+  if (act == MOE_LINEAR_SILU) return v * sigmoid_fast(v);
+  if (act == MOE_LINEAR_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+  if (act == MOE_LINEAR_RELU2) {
+    const float r = v < 0.f ? 0.f : v;  // NaN stays
+    return r * r;
+  }
+  return v;
+}
+
+__device__ __forceinline__ float linear_slope(float v, int act) {
+  if (act == MOE_LINEAR_SILU) {
+    const float s = sigmoid_fast(v);
+    return s * (1.0f + v * (1.0f - s));
+  }
+  if (act == MOE_LINEAR_GELU)
+    return 0.5f * (1.0f + erff(v * 0.70710678118654752f)) +
+           v * (__expf(-0.5f * v * v) * 0.39894228040143268f);
+  if (act == MOE_LINEAR_RELU2) return 2.f * (v < 0.f ? 0.f : v);
+  return 1.f;
+}
+
+// h of a (gate, up) pair, as activate() but NaN passes the clamps.
+__device__ __forceinline__ float gated(float g, float u, const ActParams &p) {
+  g = g > p.limit ? p.limit : g;
+  u = u > p.limit ? p.limit : (u < -p.limit ? -p.limit : u);
+  return (g * sigmoid_fast(p.alpha * g)) * (u + p.beta);
+}
+
+// The gradients of gated() for d = d_h; a clamped value has none (a value at
+// the limit is not clamped).
+__device__ __forceinline__ void gated_backward(float g, float u, float d, const ActParams &p,
+                                               float &d_g, float &d_u) {
+  const float gc = g > p.limit ? p.limit : g;
+  const float uc = u > p.limit ? p.limit : (u < -p.limit ? -p.limit : u);
+  const float s = sigmoid_fast(p.alpha * gc);
+  d_g = g > p.limit ? 0.f : d * (uc + p.beta) * s * (1.f + p.alpha * gc * (1.f - s));
+  d_u = u > p.limit || u < -p.limit ? 0.f : d * gc * s;
+}
+
+// --------------------------------------------------------------- epilogue --
+// Columns [c, c + W) of a row's sums to where they go. c is a multiple of W
+// and c < e.cols, row < e.rows.
+template <int EPI, int W>
+__device__ __forceinline__ void dense_epilogue(const DenseEpi &e, int64_t row, int c,
+                                               float (&v)[W]) {
+  const int left = e.cols - c;
+  if constexpr (EPI == EPI_LINEAR || EPI == EPI_DACT) {
+    const int64_t at = row * e.cols + c;
+    if (e.bias) {
+      float b[W];
+      load_row<W>(e.bias, c, e.vec, left, e.half, b);
+#pragma unroll
+      for (int i = 0; i < W; ++i) v[i] += b[i];
+    }
+    if constexpr (EPI == EPI_LINEAR) {
+      if (e.act != MOE_LINEAR_NONE) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] = linear_act(v[i], e.act);
+      }
+      if (e.add) {
+        float r[W];
+        load_row<W>(e.add, at, e.vec, left, e.half, r);
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] += r[i];
+      }
+    } else {
+      float d[W];
+      load_row<W>(e.add, at, e.vec, left, e.half, d);
+#pragma unroll
+      for (int i = 0; i < W; ++i) v[i] = d[i] * linear_slope(v[i], e.act);
+    }
+    store_row<W>(e.out, at, e.vec, left, e.half, v);
+  } else if constexpr (EPI == EPI_GATED) {
+    float h[W / 2];
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) h[i] = gated(v[2 * i], v[2 * i + 1], e.gate);
+    store_row<W / 2>(e.out, row * (e.cols / 2) + c / 2, e.vec, left / 2, e.half, h);
+  } else if constexpr (EPI == EPI_GATED_MX) {
+    static_assert(EPI != EPI_GATED_MX || W == 64, "one group of 32 at a time");
+    float h[W / 2];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) {
+      h[i] = gated(v[2 * i], v[2 * i + 1], e.gate);
+      top = max(top, __float_as_uint(h[i]) & 0x7fffffffu);
+    }
+    const uint32_t b = mx8_scale(top);
+    const float inv = mx8_inverse(b);
+    const int64_t at = row * (e.cols / 2) + c / 2;
+    uint32_t q[W / 8];
+#pragma unroll
+    for (int i = 0; i < W / 8; ++i) q[i] = mx8_codes4(h + 4 * i, inv);
+    uint4 *dst = reinterpret_cast<uint4 *>(e.codes + at);
+    dst[0] = make_uint4(q[0], q[1], q[2], q[3]);
+    dst[1] = make_uint4(q[4], q[5], q[6], q[7]);
+    e.scales[at / 32] = (uint8_t)b;
+  } else if constexpr (EPI == EPI_DGATED) {
+    const int I = e.cols / 2;
+    float d[W / 2];
+    load_row<W / 2>(e.add, row * I + c / 2, e.vec, left / 2, e.half, d);
+    if (e.gate.layout == MOE_W13_PACKED) {
+      float g[W / 2], u[W / 2];
+#pragma unroll
+      for (int i = 0; i < W / 2; ++i)
+        gated_backward(v[2 * i], v[2 * i + 1], d[i], e.gate, g[i], u[i]);
+      store_row<W / 2>(e.out, row * e.cols + c / 2, e.vec, left / 2, e.half, g);
+      store_row<W / 2>(e.out, row * e.cols + I + c / 2, e.vec, left / 2, e.half, u);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W / 2; ++i)
+        gated_backward(v[2 * i], v[2 * i + 1], d[i], e.gate, v[2 * i], v[2 * i + 1]);
+      store_row<W>(e.out, row * e.cols + c, e.vec, left, e.half, v);
+    }
+  } else {
+    float *p = static_cast<float *>(e.out) + row * e.cols + c;
+    if (left >= W && e.cols % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < W; i += 4)
+        *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+        if (i < left) p[i] = v[i];
+    }
+  }
+}
+
+// --------------------------------------------------------------- products --
+// D[m, n] = sum_k A(m, k) B(n, k). K-major operands are stored [rows, K] row
+// by row, the others [K, rows].
+struct DenseOperand {
+  const void *p;
+  const uint8_t *scales;  // MXFP8: [rows, K / 32], else null
+  int k_major;
+  int pairs;              // rows 2i, 2i + 1 are rows i and i + rows / 2 of p (a packed w13)
+};
+
+struct DensePlan {
+  int tn;       // columns per tile
+  int m_tiles, n_tiles, splits;
+  size_t partial;  // bytes of fp32 partial sums (0: one part)
+};
+
+struct DenseProduct {
+  DenseOperand a, b;
+  int64_t M, N, K;
+  int kind;       // DenseKind, EPI_PARTIAL excepted
+  DenseEpi epi;
+};
+
+DensePlan dense_plan(int64_t M, int64_t N, int64_t K, int kind, bool mx);
+cudaError_t launch_dense(const DenseProduct &p, const DensePlan &plan, float *partial,
+                         int32_t *status, cudaStream_t s);
+
+}  // namespace moe

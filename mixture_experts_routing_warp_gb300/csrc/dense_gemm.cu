@@ -1,0 +1,503 @@
+// dense_gemm.cu -- the dense products beside the experts on the tcgen05 tensor
+// cores: moe_linear, moe_gated_linear and their gradients.
+//
+//   D[m, n] = sum_k A(m, k) B(n, k)      bf16 or fp16 in, fp32 sums
+// with A and B each stored along k (K-major) or along their rows (M/N-major),
+// so that no gradient needs a transposed copy:
+//   forward   a   = x W^T      A = x [n, C],    B = W [R, C]      both K-major
+//   d_x       dx  = d_a W      A = d_a [n, R],  B = W [R, C]      B N-major
+//   d_w       dw  = d_a^T x    A = d_a [n, R],  B = x [n, C]      both M/N-major
+// and an epilogue on the sums while they are in registers (dense.cuh): bias,
+// activation and residual; the gated product; the gradients of either.
+//
+// A persistent kernel, one CTA pair (cta_group::2) per two SMs: tiles of 256
+// rows (128 per CTA) x tn columns (tn / 2 of B's rows per CTA), K steps of 128
+// bytes through a ring of TMA-fed stages, two accumulators of tn TMEM columns,
+// so that the epilogue of one tile runs under the products of the next.
+//   warp 0      TMA producer (each CTA its own halves; bytes counted on the
+//               leader's barrier)
+//   warp 1      TMEM allocation; the leader's issues the MMAs
+//   warps 2-9   epilogue, two per TMEM lane quarter, alternate column chunks
+// Where the tiles are fewer than the pairs of SMs can take, the K range is
+// split: parts write fp32 sums and a second kernel adds them in order and
+// applies the epilogue. No atomics: the bits depend on the inputs and sizes.
+// Every mbarrier wait is bounded.
+#include "dense.cuh"
+#include "tc_ptx.cuh"
+
+namespace moe {
+namespace {
+
+using namespace tc;
+
+constexpr int kRowsCta = 128;                    // A rows of a CTA's half tile
+constexpr int kStepBytes = 128;                  // K bytes of a stage
+constexpr int kABytes = kRowsCta * kStepBytes;   // 16 KB
+constexpr int kMaxTn = 256;
+constexpr int kEpiWarps = 8;
+constexpr int kGemmThreads = (2 + kEpiWarps) * 32;
+constexpr int kRingBytes = 220 * 1024;
+constexpr int kMaxStages = 8;
+constexpr int kNumBars = 2 * kMaxStages + 2 + 2 + 1;
+constexpr int kGemmSmem = 1024 + kRingBytes + kNumBars * 8 + 16;
+constexpr int kTmemCols = 512;
+static_assert(kGemmSmem <= 227 * 1024, "shared memory per CTA");
+
+struct GemmArgs {
+  DenseEpi e;
+  int64_t part_stride;  // floats between the parts of a split sum
+  int m_tiles, n_tiles, splits;
+  int num_kb;           // K steps of the whole sum
+  int tn, stages, b_bytes;
+  int pairs;            // B rows come interleaved through a 3-D map
+  uint32_t idesc;
+  uint32_t *status;
+  unsigned long long timeout_ns;
+};
+
+// Shared-memory descriptor of an operand stored along its rows (M/N-major),
+// 128-byte swizzle: atoms of 64 rows x 8 k (a 128-byte line per k), 8-k groups
+// 1024 bytes apart (SBO), atoms along the rows 8 KB apart (LBO; a stage holds
+// 64 k of each).
+__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(8192 >> 4) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+struct Unit {
+  int m, n, s, k_lo, k_hi;
+};
+__device__ __forceinline__ Unit unit_of(int u, const GemmArgs &a) {
+  Unit w;
+  const int tiles = a.m_tiles * a.n_tiles;
+  w.s = u / tiles;
+  const int t = u - w.s * tiles;
+  w.m = t / a.n_tiles;
+  w.n = t - w.m * a.n_tiles;
+  w.k_lo = (int)((int64_t)a.num_kb * w.s / a.splits);
+  w.k_hi = (int)((int64_t)a.num_kb * (w.s + 1) / a.splits);
+  return w;
+}
+
+// AK / BK: the operand is K-major.
+template <bool AK, bool BK, int EPI>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    dense_gemm_kernel(const __grid_constant__ CUtensorMap map_a,
+                      const __grid_constant__ CUtensorMap map_b,
+                      const __grid_constant__ GemmArgs args) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kRingBytes);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kNumBars);
+  volatile int *s_abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+  const uint32_t stage0 = smem_u32(smem), full0 = smem_u32(bars);
+  const int stages = args.stages, stage_bytes = kABytes + args.b_bytes;
+  auto full_bar = [&](int s) { return full0 + 8u * s; };
+  auto empty_bar = [&](int s) { return full0 + 8u * (kMaxStages + s); };
+  auto tfull_bar = [&](int b) { return full0 + 8u * (2 * kMaxStages + b); };
+  auto tempty_bar = [&](int b) { return full0 + 8u * (2 * kMaxStages + 2 + b); };
+  const uint32_t drain_bar = full0 + 8u * (2 * kMaxStages + 4);
+  auto a_addr = [&](int s) { return stage0 + (uint32_t)(s * stage_bytes); };
+  auto b_addr = [&](int s) { return stage0 + (uint32_t)(s * stage_bytes + kABytes); };
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const int first = (int)(blockIdx.x >> 1), step = (int)(gridDim.x >> 1);
+  const int total = args.m_tiles * args.n_tiles * args.splits;
+  const int tn = args.tn;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull_bar(b), 1);
+      mbar_init(tempty_bar(b), 2 * kEpiWarps);  // the leader's counts both CTAs
+    }
+    mbar_init(drain_bar, 1);
+    *s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    prefetch_tmap(&map_a);
+    prefetch_tmap(&map_b);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  pdl_launch_dependents();
+  pdl_wait();
+  __syncthreads();
+  tc_fence_before();
+  cluster_sync();  // both CTAs' barriers and TMEM exist before any cross-CTA use
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------ TMA producer --
+    if (lane == 0) {
+      const uint32_t tx = 2u * (uint32_t)stage_bytes;
+      int stage = 0;
+      uint32_t phase = 0, issued = 0;
+      bool ok = true;
+      for (int u = first; ok && u < total; u += step) {
+        const Unit w = unit_of(u, args);
+        const int m0 = w.m * 2 * kRowsCta + (int)rank * kRowsCta;
+        const int n0 = w.n * tn + (int)rank * (tn / 2);
+        for (int kb = w.k_lo; kb < w.k_hi; ++kb) {
+          ok = wait_bounded(empty_bar(stage), phase ^ 1u, s_abort, args.status, args.timeout_ns);
+          if (!ok) break;
+          const uint32_t fb = map_to_rank(full_bar(stage), 0);
+          if (leader) mbar_arrive_expect_tx(full_bar(stage), tx);
+          const int k0 = kb * 64;
+          if constexpr (AK) {
+            tma_load_2d_pair(a_addr(stage), &map_a, fb, k0, m0);
+          } else {
+            tma_load_2d_pair(a_addr(stage), &map_a, fb, m0, k0);
+            tma_load_2d_pair(a_addr(stage) + 8192u, &map_a, fb, m0 + 64, k0);
+          }
+          if constexpr (BK) {
+            if (args.pairs)
+              tma_load_3d_pair(b_addr(stage), &map_b, fb, k0, 0, n0 / 2);
+            else
+              tma_load_2d_pair(b_addr(stage), &map_b, fb, k0, n0);
+          } else {
+            tma_load_2d_pair(b_addr(stage), &map_b, fb, n0, k0);
+            if (args.b_bytes > 8192)
+              tma_load_2d_pair(b_addr(stage) + 8192u, &map_b, fb, n0 + 64, k0);
+          }
+          issued = issued < (uint32_t)stages ? issued + 1 : (uint32_t)stages;
+          if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // a pair's copies complete on the leader's barriers: the leader drains
+      // (the peer stays resident until the final cluster barrier)
+      if (!ok && leader) {
+        for (uint32_t i = 0; i < issued; ++i) {
+          int s = stage - 1 - (int)i;
+          uint32_t ph = phase;
+          if (s < 0) {
+            s += stages;
+            ph ^= 1u;
+          }
+          wait_drain(full_bar(s), ph, 100000000ull);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // --------------------------------------------- MMA issuer (the leader) --
+    if (lane == 0 && leader) {
+      // descriptor steps (16-byte units) between the four MMAs of a stage
+      constexpr uint32_t a_step = AK ? 2u : 128u, b_step = BK ? 2u : 128u;
+      int stage = 0, local = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int u = first; ok && u < total; u += step, ++local) {
+        const Unit w = unit_of(u, args);
+        const int acc = local & 1;
+        if (!wait_bounded(tempty_bar(acc), ((uint32_t)(local >> 1) & 1u) ^ 1u, s_abort,
+                          args.status, args.timeout_ns))
+          break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kMaxTn);
+        for (int kb = w.k_lo; kb < w.k_hi; ++kb) {
+          if (!wait_bounded(full_bar(stage), phase, s_abort, args.status, args.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t ad = AK ? sw128_desc(a_addr(stage)) : sw128_desc_mn(a_addr(stage));
+          const uint64_t bd = BK ? sw128_desc(b_addr(stage)) : sw128_desc_mn(b_addr(stage));
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_bf16_pair(d_tmem, ad + a_step * kk, bd + b_step * kk, args.idesc,
+                           kb != w.k_lo || kk != 0);
+          umma_commit_pair(empty_bar(stage), 0x3);
+          if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (ok) umma_commit_pair(tfull_bar(acc), 0x3);
+      }
+      umma_commit_pair(drain_bar, 0x1);
+      wait_drain(drain_bar, 0, 100000000ull);
+    }
+  } else {
+    // ----------------------------------------------------------- epilogue --
+    constexpr int W = EPI == EPI_GATED_MX ? 64 : 32;
+    const int q = warp & 3;            // TMEM lane quarter this warp may read
+    const int part = (warp - 2) >> 2;  // which of the quarter's two warps
+    int local = 0;
+    for (int u = first; u < total; u += step, ++local) {
+      const Unit w = unit_of(u, args);
+      const int acc = local & 1;
+      if (!wait_bounded(tfull_bar(acc), (uint32_t)(local >> 1) & 1u, s_abort, args.status,
+                        args.timeout_ns))
+        break;
+      tc_fence_after();
+      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kMaxTn);
+      const int64_t row = (int64_t)w.m * 2 * kRowsCta + rank * kRowsCta + q * 32 + lane;
+      const int c0 = w.n * tn;
+      for (int c = part * W; c < tn; c += 2 * W) {
+        if (c0 + c >= args.e.cols) break;
+        float v[W];
+        uint32_t r[32];
+#pragma unroll
+        for (int i = 0; i < W; i += 32) {
+          TMEM_LD32(taddr + c + i, r);
+          tmem_wait_ld(r);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[i + j] = __uint_as_float(r[j]);
+        }
+        if (row < args.e.rows) {
+          if constexpr (EPI == EPI_PARTIAL) {
+            DenseEpi e = args.e;
+            e.out = static_cast<float *>(e.out) + w.s * args.part_stride;
+            dense_epilogue<EPI, W>(e, row, c0 + c, v);
+          } else {
+            dense_epilogue<EPI, W>(args.e, row, c0 + c, v);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (leader)
+          mbar_arrive(tempty_bar(acc));
+        else
+          mbar_arrive_cluster(map_to_rank(tempty_bar(acc), 0));
+      }
+    }
+  }
+
+  tc_fence_before();
+  cluster_sync();  // the leader's MMAs into the peer's TMEM are complete
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                 "r"(kTmemCols)
+                 : "memory");
+  }
+}
+
+// The parts of a split sum, added in order, and the epilogue. One thread per
+// W columns.
+template <int EPI>
+__global__ void __launch_bounds__(256)
+dense_join_kernel(const float *part, int64_t stride, int splits, const __grid_constant__ DenseEpi e) {
+  constexpr int W = EPI == EPI_GATED_MX ? 64 : EPI == EPI_GATED || EPI == EPI_DGATED ? 16 : 8;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int chunks = (e.cols + W - 1) / W;
+  const int64_t total = e.rows * chunks;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t row = i / chunks;
+    const int c = (int)(i - row * chunks) * W;
+    float v[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) v[j] = 0.f;
+    const float *p = part + row * e.cols + c;
+    const bool full = c + W <= e.cols && e.cols % 4 == 0;
+    for (int s = 0; s < splits; ++s, p += stride) {
+      if (full) {
+#pragma unroll
+        for (int j = 0; j < W; j += 4) {
+          const float4 f = __ldcg(reinterpret_cast<const float4 *>(p + j));
+          v[j] += f.x;
+          v[j + 1] += f.y;
+          v[j + 2] += f.z;
+          v[j + 3] += f.w;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+          if (c + j < e.cols) v[j] += __ldcg(p + j);
+      }
+    }
+    dense_epilogue<EPI, W>(e, row, c, v);
+  }
+}
+
+// 16-bit [rows, cols] row-major in boxes of 64 columns x box_rows rows (fp16
+// and bf16 are copied alike).
+bool map_rows(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int box_rows) {
+  return map_2d(m, base, (uint64_t)rows, (uint64_t)cols, (uint32_t)box_rows);
+}
+
+// A packed w13 [2, I, cols]: rows gate_i, up_i alternate in the box of
+// 64 columns x 2 x box_pairs.
+bool map_pairs(CUtensorMap *m, const void *base, int64_t I, int64_t cols, int box_pairs) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, 2, (cuuint64_t)I};
+  cuuint64_t strides[2] = {(cuuint64_t)(I * cols * 2), (cuuint64_t)(cols * 2)};
+  cuuint32_t box[3] = {64, 2, (cuuint32_t)box_pairs};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool AK, bool BK, int EPI>
+cudaError_t launch_gemm(const CUtensorMap &ma, const CUtensorMap &mb, const GemmArgs &a,
+                        cudaStream_t s) {
+  auto kern = dense_gemm_kernel<AK, BK, EPI>;
+  static PerDeviceOnce once;
+  static std::atomic<int> resident[PerDeviceOnce::kMaxDevices] = {};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(device_sm_count() & ~1);
+  cfg.blockDim = dim3(kGemmThreads);
+  cfg.dynamicSmemBytes = kGemmSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  err = once.run([&] {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kGemmSmem);
+    if (e == cudaSuccess) e = uniform_carveout(kern);
+    int n = 0;
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+    if (e == cudaSuccess) resident[dev].store(n < 1 ? 1 : n, std::memory_order_relaxed);
+    return e;
+  });
+  if (err != cudaSuccess) return err;
+  const int64_t units = (int64_t)a.m_tiles * a.n_tiles * a.splits;
+  int64_t pairs = resident[dev].load(std::memory_order_relaxed);
+  if (units < pairs) pairs = units;
+  cfg.gridDim = dim3((unsigned)(2 * pairs));
+  err = cudaLaunchKernelEx(&cfg, kern, ma, mb, a);
+  return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+template <int EPI>
+cudaError_t launch_join(const float *part, int64_t stride, int splits, const DenseEpi &e,
+                        cudaStream_t s) {
+  constexpr int W = EPI == EPI_GATED_MX ? 64 : EPI == EPI_GATED || EPI == EPI_DGATED ? 16 : 8;
+  const int64_t threads = e.rows * ((e.cols + W - 1) / W);
+  int64_t blocks = (threads + 255) / 256;
+  const int64_t cap = (int64_t)device_sm_count() * 8;
+  if (blocks > cap) blocks = cap;
+  return launch_dependent(dense_join_kernel<EPI>, dim3((unsigned)blocks), dim3(256), 0, s, part,
+                          stride, splits, e);
+}
+
+template <bool AK, bool BK>
+cudaError_t launch_kind(int kind, const CUtensorMap &ma, const CUtensorMap &mb, const GemmArgs &a,
+                        cudaStream_t s) {
+  if constexpr (AK && BK) {
+    switch (kind) {
+      case EPI_DACT: return launch_gemm<AK, BK, EPI_DACT>(ma, mb, a, s);
+      case EPI_GATED: return launch_gemm<AK, BK, EPI_GATED>(ma, mb, a, s);
+      case EPI_GATED_MX: return launch_gemm<AK, BK, EPI_GATED_MX>(ma, mb, a, s);
+      case EPI_DGATED: return launch_gemm<AK, BK, EPI_DGATED>(ma, mb, a, s);
+    }
+  }
+  if (kind == EPI_PARTIAL) return launch_gemm<AK, BK, EPI_PARTIAL>(ma, mb, a, s);
+  return launch_gemm<AK, BK, EPI_LINEAR>(ma, mb, a, s);
+}
+
+}  // namespace
+
+// Tile width and number of parts of the sum: the choice with the least
+// estimated time, in SM cycles. A K step of a pair takes 2 cycles per column
+// (256 x tn x 64 products at 8192 per cycle and SM) and no less than its
+// shared-memory reads; a unit costs about 1200 cycles beside its steps; a
+// split costs its partial sums' way through L2 and the joining kernel.
+DensePlan dense_plan(int64_t M, int64_t N, int64_t K, int kind, bool mx) {
+  constexpr int kPairs = 76;  // of the GB300's 152 SMs: a plan does not depend on the device
+  DensePlan best{};
+  double best_t = 1e300;
+  const int gran = kind == EPI_GATED_MX ? 64 : 32;
+  const int64_t kb = (K + 63) / 64, mt = (M + 255) / 256;
+  for (int tn = kMaxTn; tn >= 64; tn -= gran) {
+    const int64_t nt = (N + tn - 1) / tn;
+    const int64_t tiles = mt * nt;
+    const double step = 2.0 * tn > 150.0 + tn ? 2.0 * tn : 150.0 + tn;
+    for (int s = 1; s <= 16; ++s) {
+      if (s > 1 && (kb / s < 4 || tiles * s > 2 * kPairs)) break;
+      const int64_t waves = (tiles * s + kPairs - 1) / kPairs;
+      double t = (double)waves * ((double)((kb + s - 1) / s) * step + 1200.0);
+      if (s > 1) t += 5000.0 + (double)M * N * 4.0 * (s + 1) / 2500.0;
+      if (t < best_t) {
+        best_t = t;
+        best.tn = tn;
+        best.m_tiles = (int)mt;
+        best.n_tiles = (int)nt;
+        best.splits = s;
+      }
+    }
+  }
+  best.partial = best.splits > 1 ? (size_t)M * N * 4 * best.splits : 0;
+  (void)mx;
+  return best;
+}
+
+cudaError_t launch_dense(const DenseProduct &p, const DensePlan &plan, float *partial,
+                         int32_t *status, cudaStream_t s) {
+  if (p.a.scales || p.b.scales) return cudaErrorNotSupported;
+  CUtensorMap ma, mb;
+  const int tn = plan.tn;
+  const bool ak = p.a.k_major, bk = p.b.k_major;
+  bool ok = ak ? map_rows(&ma, p.a.p, p.M, p.K, kRowsCta) : map_rows(&ma, p.a.p, p.K, p.M, 64);
+  if (p.b.pairs)
+    ok = ok && map_pairs(&mb, p.b.p, p.N / 2, p.K, tn / 4);
+  else
+    ok = ok && (bk ? map_rows(&mb, p.b.p, p.N, p.K, tn / 2) : map_rows(&mb, p.b.p, p.K, p.N, 64));
+  if (!ok) return cudaErrorInvalidValue;
+  GemmArgs a{};
+  a.e = p.epi;
+  a.m_tiles = plan.m_tiles;
+  a.n_tiles = plan.n_tiles;
+  a.splits = plan.splits;
+  a.num_kb = (int)((p.K + 63) / 64);
+  a.tn = tn;
+  a.b_bytes = bk ? tn / 2 * kStepBytes : (tn / 2 + 63) / 64 * 8192;
+  a.stages = kRingBytes / (kABytes + a.b_bytes);
+  if (a.stages > kMaxStages) a.stages = kMaxStages;
+  a.pairs = p.b.pairs;
+  const uint32_t type = p.epi.half ? 0u : 1u;  // fp16 / bf16
+  a.idesc = (1u << 4) | (type << 7) | (type << 10) | ((ak ? 0u : 1u) << 15) |
+            ((bk ? 0u : 1u) << 16) | ((uint32_t)(tn >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
+  a.status = reinterpret_cast<uint32_t *>(status);
+  a.timeout_ns = kWaitTimeoutNs;
+  int kind = p.kind;
+  if (plan.splits > 1) {
+    kind = EPI_PARTIAL;
+    a.e.out = partial;
+    a.part_stride = p.M * p.N;
+  }
+  cudaError_t err = ak && bk ? launch_kind<true, true>(kind, ma, mb, a, s)
+                    : ak     ? launch_kind<true, false>(kind, ma, mb, a, s)
+                             : launch_kind<false, false>(kind, ma, mb, a, s);
+  if (err != cudaSuccess || plan.splits == 1) return err;
+  switch (p.kind) {
+    case EPI_DACT: return launch_join<EPI_DACT>(partial, p.M * p.N, plan.splits, p.epi, s);
+    case EPI_GATED: return launch_join<EPI_GATED>(partial, p.M * p.N, plan.splits, p.epi, s);
+    case EPI_GATED_MX: return launch_join<EPI_GATED_MX>(partial, p.M * p.N, plan.splits, p.epi, s);
+    case EPI_DGATED: return launch_join<EPI_DGATED>(partial, p.M * p.N, plan.splits, p.epi, s);
+    default: return launch_join<EPI_LINEAR>(partial, p.M * p.N, plan.splits, p.epi, s);
+  }
+}
+
+}  // namespace moe

@@ -9,22 +9,7 @@
 
 using namespace moe;
 
-namespace {
-
-inline bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
-moe_status check_sizes(int64_t n, int E, int k, int H, int I, bool need_hi) {
-  if (n < 0 || E < 1 || E > kMaxExperts || k < 1 || k > kMaxTopk || k > E)
-    return MOE_ERR_INVALID_ARG;
-  if (n * (int64_t)k >= (int64_t)INT32_MAX) return MOE_ERR_INVALID_ARG;
-  if (need_hi) {
-    if (H < 64 || I < 64 || H % 64 != 0 || I % 64 != 0) return MOE_ERR_INVALID_ARG;
-    if ((int64_t)2 * I > (int64_t)INT32_MAX / 2 || H > 65536) return MOE_ERR_INVALID_ARG;
-  }
-  return MOE_OK;
-}
-
-moe_status resolve_params(const moe_params *p, ActParams &out, int *gating) {
+moe_status moe::resolve_params(const moe_params *p, ActParams &out, int *gating) {
   if (!p) return MOE_ERR_INVALID_ARG;
   if (p->gating != MOE_GATING_SOFTMAX_TOPK && p->gating != MOE_GATING_SOFTMAX_ALL)
     return MOE_ERR_INVALID_ARG;
@@ -61,6 +46,21 @@ moe_status resolve_params(const moe_params *p, ActParams &out, int *gating) {
     out.limit = INFINITY;
   }
   if (gating) *gating = p->gating;
+  return MOE_OK;
+}
+
+namespace {
+
+inline bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+moe_status check_sizes(int64_t n, int E, int k, int H, int I, bool need_hi) {
+  if (n < 0 || E < 1 || E > kMaxExperts || k < 1 || k > kMaxTopk || k > E)
+    return MOE_ERR_INVALID_ARG;
+  if (n * (int64_t)k >= (int64_t)INT32_MAX) return MOE_ERR_INVALID_ARG;
+  if (need_hi) {
+    if (H < 64 || I < 64 || H % 64 != 0 || I % 64 != 0) return MOE_ERR_INVALID_ARG;
+    if ((int64_t)2 * I > (int64_t)INT32_MAX / 2 || H > 65536) return MOE_ERR_INVALID_ARG;
+  }
   return MOE_OK;
 }
 

@@ -30,4 +30,21 @@ cudaError_t launch_ffn_q4(const void *x, const moe_routing_meta &m, const moe_q4
                           const ActParams &act, int dtype, float *h, void *y_sorted,
                           uint32_t *ctrl, cudaStream_t s);
 
+// moe_params checked and resolved (moe_api.cu).
+moe_status resolve_params(const moe_params *p, ActParams &out, int *gating);
+
+// The norm in front of a layer and column sums (norm.cu). codes null: y, else
+// codes and scales. Scratch sizes in bytes.
+cudaError_t launch_rms_norm(const void *x, const void *residual, const void *weight, int w_dtype,
+                            int64_t n, int H, int dtype, float eps, void *y, void *sum,
+                            uint8_t *codes, uint8_t *scales, cudaStream_t s);
+size_t rms_norm_backward_scratch(int64_t n, int H);
+cudaError_t launch_rms_norm_backward(const void *d_y, const void *x, const void *weight,
+                                     int w_dtype, const void *d_sum, int64_t n, int H, int dtype,
+                                     float eps, void *d_x, void *d_weight, float *scratch,
+                                     cudaStream_t s);
+size_t column_sum_scratch(int cols);
+cudaError_t launch_column_sum(const void *d, int64_t n, int cols, int dtype, void *out,
+                              float *scratch, cudaStream_t s);
+
 }  // namespace moe
