@@ -54,6 +54,22 @@ moe_status check_workspace(const void *ws, size_t have, size_t need) {
 char *at(void *ws, size_t off) { return static_cast<char *>(ws) + off; }
 
 // --------------------------------------------------------------- products --
+// A forward product's workspace: the 8-bit scales in the tensor core's
+// layout, then the parts of a split sum.
+size_t forward_bytes(const DensePlan &p) { return align_up(p.blocks, kAlign) + p.partial; }
+
+moe_status run_forward(const DenseProduct &p, const DensePlan &plan, void *workspace,
+                       size_t workspace_bytes, int32_t *status, moe_stream stream) {
+  const moe_status st = check_workspace(workspace, workspace_bytes, forward_bytes(plan));
+  if (st != MOE_OK) return st;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (!p.a.scales)
+    return from_cuda(launch_dense(p, plan, static_cast<float *>(workspace), status, s));
+  return from_cuda(launch_dense_mx8(
+      p, plan, static_cast<uint8_t *>(workspace),
+      reinterpret_cast<float *>(at(workspace, align_up(plan.blocks, kAlign))), status, s));
+}
+
 DenseProduct forward_product(const void *x, const void *w, int64_t n, int64_t out, int64_t in,
                              int kind) {
   DenseProduct p{};
@@ -146,10 +162,7 @@ moe_status run_linear(const void *x, const uint8_t *x_scales, const void *w,
   p.epi.out = y;
   p.epi.vec = R % 8 == 0 && aligned(bias, 16) && aligned(residual, 16) && aligned(y, 16);
   const DensePlan plan = dense_plan(n, R, C, EPI_LINEAR, x_scales != nullptr);
-  const moe_status st = check_workspace(workspace, workspace_bytes, plan.partial);
-  if (st != MOE_OK) return st;
-  return from_cuda(launch_dense(p, plan, static_cast<float *>(workspace), status,
-                                (cudaStream_t)stream));
+  return run_forward(p, plan, workspace, workspace_bytes, status, stream);
 }
 
 moe_status run_gated(const void *x, const uint8_t *x_scales, const void *w13,
@@ -177,10 +190,7 @@ moe_status run_gated(const void *x, const uint8_t *x_scales, const void *w13,
   }
   p.epi.vec = aligned(h, 16);
   const DensePlan plan = dense_plan(n, 2 * (int64_t)I, H, kind, x_scales != nullptr);
-  const moe_status st = check_workspace(workspace, workspace_bytes, plan.partial);
-  if (st != MOE_OK) return st;
-  return from_cuda(launch_dense(p, plan, static_cast<float *>(workspace), status,
-                                (cudaStream_t)stream));
+  return run_forward(p, plan, workspace, workspace_bytes, status, stream);
 }
 
 }  // namespace
@@ -249,7 +259,8 @@ size_t moe_linear_workspace_size(int64_t n, int32_t R, int32_t C) {
   if (check_product(n, R, C, MOE_BF16, false) != MOE_OK) return 0;
   const DensePlan a = dense_plan(n, R, C, EPI_LINEAR, false);
   const DensePlan b = dense_plan(n, R, C, EPI_LINEAR, true);
-  return align_up(a.partial > b.partial ? a.partial : b.partial, kAlign);
+  const size_t need = C % 32 == 0 && forward_bytes(b) > a.partial ? forward_bytes(b) : a.partial;
+  return align_up(need, kAlign);
 }
 
 moe_status moe_linear(const void *x, const void *w, const void *bias, const void *residual,
@@ -339,7 +350,8 @@ size_t moe_gated_linear_workspace_size(int64_t n, int32_t H, int32_t I) {
   size_t most = 0;
   for (int k = 0; k < 4; ++k) {
     const DensePlan p = dense_plan(n, 2 * (int64_t)I, H, k & 1 ? EPI_GATED_MX : EPI_GATED, k > 1);
-    most = p.partial > most ? p.partial : most;
+    if (k > 1 && H % 32 != 0) break;
+    most = forward_bytes(p) > most ? forward_bytes(p) : most;
   }
   return align_up(most, kAlign);
 }
