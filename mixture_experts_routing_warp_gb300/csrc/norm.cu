@@ -36,59 +36,69 @@ __device__ __forceinline__ T from_float(float f) {
   else return __float2bfloat16_rn(f);
 }
 
-// VEC elements of T as one load: 16 bytes, or one element.
+// VEC elements of T, 16 bytes or one element, as they lie in memory: rows wait
+// in registers in this form (half the registers of floats for 16-bit types).
 template <typename T, int VEC>
-struct Pack {
-  T v[VEC];
-};
-template <typename T, int VEC>
-__device__ __forceinline__ void load_pack(const T *p, float (&f)[VEC]) {
-  if constexpr (VEC == 1) {
-    f[0] = to_float(*p);
-  } else {
-    static_assert(VEC * sizeof(T) == 16, "a 16-byte vector");
-    const uint4 q = *reinterpret_cast<const uint4 *>(p);
+struct Raw {
+  static_assert(VEC * sizeof(T) == 16, "a 16-byte vector");
+  uint4 q;
+  __device__ __forceinline__ void load(const T *p) { q = *reinterpret_cast<const uint4 *>(p); }
+  __device__ __forceinline__ void store(T *p) const { *reinterpret_cast<uint4 *>(p) = q; }
+  __device__ __forceinline__ void zero() { q = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void get(float (&f)[VEC]) const {
     if constexpr (sizeof(T) == 4) memcpy(f, &q, 16);
     else unpack8(q, std::is_same_v<T, __half>, f);
   }
+  __device__ __forceinline__ void set(const float (&f)[VEC]) {
+    if constexpr (sizeof(T) == 4) memcpy(&q, f, 16);
+    else q = pack8(f, std::is_same_v<T, __half>);
+  }
+};
+template <typename T>
+struct Raw<T, 1> {
+  T q;
+  __device__ __forceinline__ void load(const T *p) { q = *p; }
+  __device__ __forceinline__ void store(T *p) const { *p = q; }
+  __device__ __forceinline__ void zero() { q = from_float<T>(0.f); }
+  __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = to_float(q); }
+  __device__ __forceinline__ void set(const float (&f)[1]) { q = from_float<T>(f[0]); }
+};
+template <typename T, int VEC>
+__device__ __forceinline__ void load_pack(const T *p, float (&f)[VEC]) {
+  Raw<T, VEC> r;
+  r.load(p);
+  r.get(f);
 }
 template <typename T, int VEC>
 __device__ __forceinline__ void store_pack(T *p, const float (&f)[VEC]) {
-  if constexpr (VEC == 1) {
-    *p = from_float<T>(f[0]);
-  } else {
-    uint4 q;
-    if constexpr (sizeof(T) == 4) memcpy(&q, f, 16);
-    else q = pack8(f, std::is_same_v<T, __half>);
-    *reinterpret_cast<uint4 *>(p) = q;
-  }
+  Raw<T, VEC> r;
+  r.set(f);
+  r.store(p);
 }
-// VEC weights of T or, with w32, of fp32.
-template <typename T, int VEC>
-__device__ __forceinline__ void load_weight(const void *w, bool w32, int c, float (&f)[VEC]) {
+// VEC weights of WT (the rows' type or fp32); ones where there are none.
+template <typename WT, int VEC>
+__device__ __forceinline__ void load_weight(const void *w, int c, float (&f)[VEC]) {
+  const WT *p = static_cast<const WT *>(w) + c;
   if (!w) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) f[i] = 1.f;
-  } else if (w32 && !std::is_same_v<T, float>) {
-    const float *p = static_cast<const float *>(w) + c;
-    if constexpr (VEC == 1) {
-      f[0] = __ldg(p);
-    } else {
-#pragma unroll
-      for (int i = 0; i < VEC; i += 4) {
-        const float4 q = __ldg(reinterpret_cast<const float4 *>(p + i));
-        f[i] = q.x;
-        f[i + 1] = q.y;
-        f[i + 2] = q.z;
-        f[i + 3] = q.w;
-      }
-    }
+  } else if constexpr (VEC * sizeof(WT) <= 16) {
+    load_pack<WT, VEC>(p, f);
   } else {
-    load_pack<T, VEC>(static_cast<const T *>(w) + c, f);
+#pragma unroll
+    for (int i = 0; i < VEC; i += 4) {
+      const float4 q = *reinterpret_cast<const float4 *>(p + i);
+      memcpy(f + i, &q, 16);
+    }
   }
 }
 
-// Sums of up to two values over the group of G threads (a power of two, 32 or
+// 1 / rms: rsqrt.approx, good to 2^-22
+__device__ __forceinline__ float inverse_rms(float squares, float inv_h, float eps) {
+  return rsqrtf(fmaf(squares, inv_h, eps));
+}
+
+// Sums of up to two values over the group of G threads (whole warps, 32 or
 // more); `slot` alternates between the two halves of the scratch, so that one
 // barrier per call is enough.
 template <int N>
@@ -99,16 +109,19 @@ __device__ __forceinline__ void group_sum(float (&v)[N], int G, int group, int s
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
   if (G == 32) return;
-  const int warp = threadIdx.x >> 5, warps = G >> 5, w0 = group * warps;
-  if ((threadIdx.x & 31) == 0)
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = G >> 5;
+  if (lane == 0)
 #pragma unroll
     for (int i = 0; i < N; ++i) scratch[slot][warp][i] = v[i];
   asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(G) : "memory");
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = 0.f;
-  for (int w = 0; w < warps; ++w)
+  for (int i = 0; i < N; ++i) v[i] = lane < warps ? scratch[slot][group * warps + lane][i] : 0.f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += scratch[slot][w0 + w][i];
+  for (int off = kNormThreads / 64; off > 0; off >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, v[i], 0);
 }
 
 struct NormArgs {
@@ -116,8 +129,8 @@ struct NormArgs {
   void *y, *sum;
   uint8_t *codes, *scales;
   int64_t n;
-  int H, G, w32;
-  float eps;
+  int H, G;
+  float eps, inv_h;
 };
 
 // VEC values of a row to 8-bit codes; the 32 / VEC lanes of a group of 32
@@ -145,8 +158,11 @@ __device__ __forceinline__ void store_mx8(const NormArgs &a, int64_t row, int c,
   if (c % 32 == 0) a.scales[at / 32] = (uint8_t)b;
 }
 
-template <typename T, int VEC, int V, bool MX>
-__global__ void __launch_bounds__(kNormThreads)
+// Blocks per SM that a kernel with V vectors per thread leaves registers for.
+constexpr int norm_blocks(int V) { return V == 1 ? 3 : V <= 4 ? 2 : 1; }
+
+template <typename T, typename WT, int VEC, int V, bool MX>
+__global__ void __launch_bounds__(kNormThreads, norm_blocks(V))
 rms_norm_kernel(const NormArgs a) {
   __shared__ float scratch[2][kNormThreads / 32][1];
   pdl_launch_dependents();
@@ -157,60 +173,63 @@ rms_norm_kernel(const NormArgs a) {
   for (int64_t row = (int64_t)blockIdx.x * per_block + group; row < a.n;
        row += (int64_t)gridDim.x * per_block, slot ^= 1) {
     const T *x = static_cast<const T *>(a.x) + row * a.H;
-    float s[V][VEC];
+    Raw<T, VEC> s[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = (t + v * G) * VEC;
-      if (c < a.H) {
-        load_pack<T, VEC>(x + c, s[v]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) s[v][i] = 0.f;
-      }
+      if (c < a.H) s[v].load(x + c);
+      else s[v].zero();
     }
     if (a.residual) {
       const T *res = static_cast<const T *>(a.residual) + row * a.H;
-      float d[V][VEC];
+      Raw<T, VEC> d[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int c = (t + v * G) * VEC;
-        if (c < a.H) load_pack<T, VEC>(res + c, d[v]);
+        if (c < a.H) d[v].load(res + c);
+        else d[v].zero();
       }
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int c = (t + v * G) * VEC;
-        if (c < a.H) {
+        float f[VEC], g[VEC];
+        s[v].get(f);
+        d[v].get(g);
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) s[v][i] = to_float(from_float<T>(s[v][i] + d[v][i]));
-          if (a.sum) store_pack<T, VEC>(static_cast<T *>(a.sum) + row * a.H + c, s[v]);
-        }
+        for (int i = 0; i < VEC; ++i) f[i] += g[i];
+        s[v].set(f);
+        if (a.sum && c < a.H) s[v].store(static_cast<T *>(a.sum) + row * a.H + c);
       }
     }
     float q[1] = {0.f};
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v) {
+      float f[VEC];
+      s[v].get(f);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) q[0] += s[v][i] * s[v][i];
+      for (int i = 0; i < VEC; ++i) q[0] += f[i] * f[i];
+    }
     group_sum<1>(q, G, group, slot, scratch);
-    const float r = 1.0f / sqrtf(q[0] / (float)a.H + a.eps);
+    const float r = inverse_rms(q[0], a.inv_h, a.eps);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = (t + v * G) * VEC;
       const bool live = c < a.H;
-      float w[VEC];
-      if (live) load_weight<T, VEC>(a.weight, a.w32, c, w);
+      float f[VEC], w[VEC];
+      s[v].get(f);
+      if (live) load_weight<WT, VEC>(a.weight, c, w);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) s[v][i] = live ? s[v][i] * r * w[i] : 0.f;
+      for (int i = 0; i < VEC; ++i) f[i] = live ? f[i] * r * w[i] : 0.f;
       if constexpr (MX)
-        store_mx8<VEC>(a, row, c, live, s[v]);
+        store_mx8<VEC>(a, row, c, live, f);
       else if (live)
-        store_pack<T, VEC>(static_cast<T *>(a.y) + row * a.H + c, s[v]);
+        store_pack<T, VEC>(static_cast<T *>(a.y) + row * a.H + c, f);
     }
   }
 }
 
 // Rows that the registers do not hold: read twice, element by element.
-template <typename T, bool MX>
+template <typename T, typename WT, bool MX>
 __global__ void __launch_bounds__(kNormThreads)
 rms_norm_long_kernel(const NormArgs a) {
   __shared__ float scratch[2][kNormThreads / 32][1];
@@ -230,7 +249,7 @@ rms_norm_long_kernel(const NormArgs a) {
       q[0] += s * s;
     }
     group_sum<1>(q, kNormThreads, 0, slot, scratch);
-    const float r = 1.0f / sqrtf(q[0] / (float)a.H + a.eps);
+    const float r = inverse_rms(q[0], a.inv_h, a.eps);
     for (int c0 = 0; c0 < a.H; c0 += kNormThreads) {
       const int c = c0 + (int)threadIdx.x;
       const bool live = c < a.H;
@@ -238,7 +257,7 @@ rms_norm_long_kernel(const NormArgs a) {
       if (live) {
         s = value(c);
         if (res && a.sum) static_cast<T *>(a.sum)[row * a.H + c] = from_float<T>(s);
-        load_weight<T, 1>(a.weight, a.w32, c, w);
+        load_weight<WT, 1>(a.weight, c, w);
       }
       float f[1] = {live ? s * r * w[0] : 0.f};
       if constexpr (MX)
@@ -255,12 +274,21 @@ struct NormGradArgs {
   float *part;   // [blocks, H] sums of d v over a block's rows, or null
   float *rstd;   // [n], rows read twice only
   int64_t n;
-  int H, G, w32;
-  float eps;
+  int H, G;
+  float eps, inv_h;
 };
 
-template <typename T, int VEC, int V>
-__global__ void __launch_bounds__(kNormThreads)
+#ifndef GRAD_THREADS2
+#define GRAD_THREADS2 384
+#endif
+#ifndef GRAD_KEEP
+#define GRAD_KEEP 1
+#endif
+// Threads of a block at V vectors per thread, two blocks per SM up to V = 2.
+constexpr int grad_threads(int V) { return V == 2 ? GRAD_THREADS2 : kNormThreads; }
+
+template <typename T, typename WT, int VEC, int V>
+__global__ void __launch_bounds__(grad_threads(V), V <= 2 ? 2 : 1)
 rms_norm_backward_kernel(const NormGradArgs a) {
   __shared__ float scratch[2][kNormThreads / 32][2];
   extern __shared__ float s_acc[];  // [groups, H]: the groups' d_w, where there are several
@@ -273,59 +301,74 @@ rms_norm_backward_kernel(const NormGradArgs a) {
   for (int v = 0; v < V; ++v)
 #pragma unroll
     for (int i = 0; i < VEC; ++i) acc[v][i] = 0.f;
-  int slot = 0;
-  for (int64_t row = (int64_t)blockIdx.x * per_block + group; row < a.n;
-       row += (int64_t)gridDim.x * per_block, slot ^= 1) {
-    const T *x = static_cast<const T *>(a.x) + row * a.H;
-    const T *dy = static_cast<const T *>(a.d_y) + row * a.H;
-    float s[V][VEC], d[V][VEC];
+  // the weights of this thread's columns: kept for all rows where they are of
+  // the rows' type, else loaded again (from L1)
+  constexpr bool kKeep = std::is_same_v<T, WT> && V <= GRAD_KEEP;
+  Raw<T, VEC> kept[kKeep ? V : 1];
+  if constexpr (kKeep) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = (t + v * G) * VEC;
-      if (c < a.H) {
-        load_pack<T, VEC>(x + c, s[v]);
-        load_pack<T, VEC>(dy + c, d[v]);
-      } else {
+      float one[VEC];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) s[v][i] = d[v][i] = 0.f;
+      for (int i = 0; i < VEC; ++i) one[i] = 1.f;
+      kept[v].set(one);
+      if (a.weight && c < a.H) kept[v].load(static_cast<const T *>(a.weight) + c);
+    }
+  }
+  auto weights = [&](int v, float (&w)[VEC]) {
+    if constexpr (kKeep) kept[v].get(w);
+    else load_weight<WT, VEC>((t + v * G) * VEC < a.H ? a.weight : nullptr, (t + v * G) * VEC, w);
+  };
+  int slot = 0;
+  for (int64_t row = (int64_t)blockIdx.x * per_block + group; row < a.n;
+       row += (int64_t)gridDim.x * per_block, slot ^= 1) {
+    const int64_t at = row * a.H;
+    Raw<T, VEC> s[V], d[V], e[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (t + v * G) * VEC;
+      e[v].zero();
+      if (c < a.H) {
+        s[v].load(static_cast<const T *>(a.x) + at + c);
+        d[v].load(static_cast<const T *>(a.d_y) + at + c);
+        if (a.d_sum) e[v].load(static_cast<const T *>(a.d_sum) + at + c);
+      } else {
+        s[v].zero();
+        d[v].zero();
       }
     }
     float q[2] = {0.f, 0.f};
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = (t + v * G) * VEC;
-      float w[VEC];
-      if (c < a.H) {
-        load_weight<T, VEC>(a.weight, a.w32, c, w);
+      float f[VEC], g[VEC], w[VEC];
+      s[v].get(f);
+      d[v].get(g);
+      weights(v, w);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          q[0] += s[v][i] * s[v][i];
-          q[1] += s[v][i] * (d[v][i] * w[i]);
-        }
+      for (int i = 0; i < VEC; ++i) {
+        q[0] += f[i] * f[i];
+        q[1] += f[i] * (g[i] * w[i]);
       }
     }
     group_sum<2>(q, G, group, slot, scratch);
-    const float r = 1.0f / sqrtf(q[0] / (float)a.H + a.eps);
-    const float m = r * r * (q[1] / (float)a.H);  // mean(d w v) r, to be times s
+    const float r = inverse_rms(q[0], a.inv_h, a.eps);
+    const float m = -(r * r) * (r * q[1] * a.inv_h);  // d_x = r d w + m x
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = (t + v * G) * VEC;
-      if (c < a.H) {
-        float w[VEC], o[VEC];
-        load_weight<T, VEC>(a.weight, a.w32, c, w);
+      float f[VEC], g[VEC], w[VEC], o[VEC];
+      s[v].get(f);
+      d[v].get(g);
+      e[v].get(o);
+      weights(v, w);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          o[i] = r * (d[v][i] * w[i] - s[v][i] * m);
-          acc[v][i] += d[v][i] * (s[v][i] * r);
-        }
-        if (a.d_sum) {
-          float e[VEC];
-          load_pack<T, VEC>(static_cast<const T *>(a.d_sum) + row * a.H + c, e);
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) o[i] += e[i];
-        }
-        store_pack<T, VEC>(static_cast<T *>(a.d_x) + row * a.H + c, o);
+      for (int i = 0; i < VEC; ++i) {
+        const float p = g[i] * r;
+        o[i] = fmaf(m, f[i], fmaf(p, w[i], o[i]));
+        acc[v][i] = fmaf(p, f[i], acc[v][i]);
       }
+      if (c < a.H) store_pack<T, VEC>(static_cast<T *>(a.d_x) + at + c, o);
     }
   }
   if (!a.part) return;
@@ -348,7 +391,7 @@ rms_norm_backward_kernel(const NormGradArgs a) {
   }
 }
 
-template <typename T>
+template <typename T, typename WT>
 __global__ void __launch_bounds__(kNormThreads)
 rms_norm_backward_long_kernel(const NormGradArgs a) {
   __shared__ float scratch[2][kNormThreads / 32][2];
@@ -360,17 +403,17 @@ rms_norm_backward_long_kernel(const NormGradArgs a) {
     const T *dy = static_cast<const T *>(a.d_y) + row * a.H;
     float q[2] = {0.f, 0.f}, w[1];
     for (int c = threadIdx.x; c < a.H; c += kNormThreads) {
-      load_weight<T, 1>(a.weight, a.w32, c, w);
+      load_weight<WT, 1>(a.weight, c, w);
       const float s = to_float(x[c]);
       q[0] += s * s;
       q[1] += s * (to_float(dy[c]) * w[0]);
     }
     group_sum<2>(q, kNormThreads, 0, slot, scratch);
-    const float r = 1.0f / sqrtf(q[0] / (float)a.H + a.eps);
-    const float m = r * r * (q[1] / (float)a.H);
+    const float r = inverse_rms(q[0], a.inv_h, a.eps);
+    const float m = r * r * (q[1] * a.inv_h);
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = r;
     for (int c = threadIdx.x; c < a.H; c += kNormThreads) {
-      load_weight<T, 1>(a.weight, a.w32, c, w);
+      load_weight<WT, 1>(a.weight, c, w);
       float o = r * (to_float(dy[c]) * w[0] - to_float(x[c]) * m);
       if (a.d_sum) o += to_float(static_cast<const T *>(a.d_sum)[row * a.H + c]);
       static_cast<T *>(a.d_x)[row * a.H + c] = from_float<T>(o);
@@ -422,115 +465,135 @@ column_sum_kernel(const void *d, const void *x, const float *rstd, int64_t n, in
   }
 }
 
-// out[c] = sum over the P rows of part [P, cols]: 32 columns per block, eight
-// rows at a time, then over the eight.
-__global__ void __launch_bounds__(256)
+// out[c] = sum over the P rows of part [P, cols]: 32 columns per block, one row
+// per warp at a time (all of a warp's loads in flight), then over the warps.
+constexpr int kJoinThreads = 1024;
+__global__ void __launch_bounds__(kJoinThreads)
 column_join_kernel(const float *part, int P, int cols, int dtype, void *out) {
-  __shared__ float s_sum[8][32];
+  __shared__ float s_sum[kJoinThreads / 32][33];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = (int)blockIdx.x * 32 + lane;
   float acc = 0.f;
   if (c < cols) {
-#pragma unroll 8
-    for (int p = warp; p < P; p += 8) acc += __ldcg(part + (int64_t)p * cols + c);
+#pragma unroll 10
+    for (int p = warp; p < P; p += kJoinThreads / 32) acc += __ldcg(part + (int64_t)p * cols + c);
   }
   s_sum[warp][lane] = acc;
   __syncthreads();
-  if (warp == 0 && c < cols) {
-    float f = 0.f;
+  float f = s_sum[lane][warp];  // column `warp` of the block, one row's sum per lane
 #pragma unroll
-    for (int w = 0; w < 8; ++w) f += s_sum[w][lane];
-    if (dtype == MOE_FP32) static_cast<float *>(out)[c] = f;
-    else static_cast<uint16_t *>(out)[c] = to16(f, dtype == MOE_FP16);
+  for (int off = 16; off > 0; off >>= 1) f += __shfl_xor_sync(0xffffffffu, f, off);
+  const int mine = (int)blockIdx.x * 32 + warp;
+  if (lane == 0 && mine < cols) {
+    if (dtype == MOE_FP32) static_cast<float *>(out)[mine] = f;
+    else static_cast<uint16_t *>(out)[mine] = to16(f, dtype == MOE_FP16);
   }
 }
 
 // ------------------------------------------------------------------- host --
-// Threads per row (a power of two from 32 to 512) and vectors per thread.
+// Threads per row (whole warps, at most 512) and vectors per thread, at most
+// `most`; V = 0: the row does not stay in registers. Few rows take one vector
+// per thread, for latency.
+#ifndef NORM_TARGET
+#define NORM_TARGET 3
+#endif
+#ifndef NORM_GRAD_TARGET
+#define NORM_GRAD_TARGET 2
+#endif
 struct RowShape {
   int G, V;
 };
-// Few rows: as many threads per row as have a vector, for latency; many:
-// about three vectors per thread.
-RowShape row_shape(int64_t n, int64_t vectors, int most) {
-  const int target = n <= 2 * 152 ? 1 : 3;
-  RowShape s{32, 1};
-  while (s.G < kNormThreads && (int64_t)s.G * target < vectors) s.G *= 2;
-  s.V = (int)((vectors + s.G - 1) / s.G);
-  if (s.V > most) s.V = 0;  // not in registers
-  return s;
+RowShape row_shape(int64_t n, int64_t vectors, int target, int most, int two = kNormThreads) {
+  if (n <= 2 * 152) target = 1;
+  const int64_t fit = (vectors + kNormThreads - 1) / kNormThreads;
+  int V = (int)(fit > target ? fit : target);
+  if (V == 2 && vectors > 2 * two) V = 3;
+  if (fit > most) return {kNormThreads, 0};
+  if (vectors < 32 * V) V = (int)((vectors + 31) / 32);
+  const int64_t per = (vectors + V - 1) / V;
+  return {(int)((per + 31) / 32 * 32), V};
 }
 
-template <typename T, int VEC, bool MX>
+template <typename T, typename WT, int VEC, bool MX>
 cudaError_t norm_v(const NormArgs &a, int V, dim3 grid, cudaStream_t s) {
-  const dim3 block(kNormThreads);
+  const dim3 block((unsigned)(kNormThreads / a.G * a.G));  // whole groups
   switch (V) {
-    case 1: return launch_dependent(rms_norm_kernel<T, VEC, 1, MX>, grid, block, 0, s, a);
-    case 2: return launch_dependent(rms_norm_kernel<T, VEC, 2, MX>, grid, block, 0, s, a);
-    case 3: return launch_dependent(rms_norm_kernel<T, VEC, 3, MX>, grid, block, 0, s, a);
-    case 4: return launch_dependent(rms_norm_kernel<T, VEC, 4, MX>, grid, block, 0, s, a);
-    default: return launch_dependent(rms_norm_kernel<T, VEC, 8, MX>, grid, block, 0, s, a);
+    case 1: return launch_dependent(rms_norm_kernel<T, WT, VEC, 1, MX>, grid, block, 0, s, a);
+    case 2: return launch_dependent(rms_norm_kernel<T, WT, VEC, 2, MX>, grid, block, 0, s, a);
+    case 3: return launch_dependent(rms_norm_kernel<T, WT, VEC, 3, MX>, grid, block, 0, s, a);
+    case 4: return launch_dependent(rms_norm_kernel<T, WT, VEC, 4, MX>, grid, block, 0, s, a);
+    case 5:
+    case 6: return launch_dependent(rms_norm_kernel<T, WT, VEC, 6, MX>, grid, block, 0, s, a);
+    case 7:
+    case 8: return launch_dependent(rms_norm_kernel<T, WT, VEC, 8, MX>, grid, block, 0, s, a);
+    default: return launch_dependent(rms_norm_kernel<T, WT, VEC, 12, MX>, grid, block, 0, s, a);
   }
 }
 
 inline bool on16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
-template <typename T, bool MX>
+template <typename T, typename WT, bool MX>
 cudaError_t norm_t(NormArgs a, cudaStream_t s) {
   constexpr int VEC = 16 / sizeof(T);
   const bool wide = a.H % VEC == 0 && on16(a.x) && on16(a.residual) && on16(a.weight) &&
                     on16(a.y) && on16(a.sum);
-  const RowShape r = row_shape(a.n, wide ? a.H / VEC : a.H, 8);
+  const RowShape r = row_shape(a.n, wide ? a.H / VEC : a.H, NORM_TARGET, 12);
   const int64_t cap = (int64_t)device_sm_count() * 4 * 16;
   if (r.V == 0) {
     const dim3 grid((unsigned)(a.n < cap ? a.n : cap));
-    return launch_dependent(rms_norm_long_kernel<T, MX>, grid, dim3(kNormThreads), 0, s, a);
+    return launch_dependent(rms_norm_long_kernel<T, WT, MX>, grid, dim3(kNormThreads), 0, s, a);
   }
   a.G = r.G;
-  int64_t blocks = (a.n * r.G + kNormThreads - 1) / kNormThreads;
+  const int per_block = kNormThreads / r.G;
+  int64_t blocks = (a.n + per_block - 1) / per_block;
   if (blocks > cap) blocks = cap;
-  return wide ? norm_v<T, VEC, MX>(a, r.V, dim3((unsigned)blocks), s)
-              : norm_v<T, 1, MX>(a, r.V, dim3((unsigned)blocks), s);
+  return wide ? norm_v<T, WT, VEC, MX>(a, r.V, dim3((unsigned)blocks), s)
+              : norm_v<T, WT, 1, MX>(a, r.V, dim3((unsigned)blocks), s);
 }
 
-template <typename T, int VEC, int V>
+template <typename T, typename WT>
+cudaError_t norm_w(const NormArgs &a, cudaStream_t s) {
+  return a.codes ? norm_t<T, WT, true>(a, s) : norm_t<T, WT, false>(a, s);
+}
+
+template <typename T, typename WT, int VEC, int V>
 cudaError_t norm_grad_k(const NormGradArgs &a, dim3 grid, size_t smem, cudaStream_t s) {
-  auto kern = rms_norm_backward_kernel<T, VEC, V>;
+  auto kern = rms_norm_backward_kernel<T, WT, VEC, V>;
   static PerDeviceOnce once;  // 512 threads x V vectors of fp32 sums: up to 64 KB
   const cudaError_t err = once.run([&] {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 kNormThreads * V * VEC * 4);
   });
   if (err != cudaSuccess) return err;
-  return launch_dependent(kern, grid, dim3(kNormThreads), smem, s, a);
+  return launch_dependent(kern, grid, dim3((unsigned)(grad_threads(V) / a.G * a.G)), smem, s, a);
 }
 
-template <typename T, int VEC>
+template <typename T, typename WT, int VEC>
 cudaError_t norm_grad_v(const NormGradArgs &a, int V, dim3 grid, size_t smem, cudaStream_t s) {
   switch (V) {
-    case 1: return norm_grad_k<T, VEC, 1>(a, grid, smem, s);
-    case 2: return norm_grad_k<T, VEC, 2>(a, grid, smem, s);
-    case 3: return norm_grad_k<T, VEC, 3>(a, grid, smem, s);
-    default: return norm_grad_k<T, VEC, 4>(a, grid, smem, s);
+    case 1: return norm_grad_k<T, WT, VEC, 1>(a, grid, smem, s);
+    case 2: return norm_grad_k<T, WT, VEC, 2>(a, grid, smem, s);
+    case 3: return norm_grad_k<T, WT, VEC, 3>(a, grid, smem, s);
+    default: return norm_grad_k<T, WT, VEC, 4>(a, grid, smem, s);
   }
 }
 
 constexpr int kPartRows = 2 * 152;  // blocks of the backward pass, and rows of their sums
 
-template <typename T>
+template <typename T, typename WT>
 cudaError_t norm_grad_t(NormGradArgs a, int w_dtype, void *d_weight, cudaStream_t s) {
   constexpr int VEC = 16 / sizeof(T);
   const bool wide = a.H % VEC == 0 && on16(a.x) && on16(a.d_y) && on16(a.weight) &&
                     on16(a.d_sum) && on16(a.d_x);
-  const RowShape r = row_shape(a.n, wide ? a.H / VEC : a.H, 4);
+  const RowShape r = row_shape(a.n, wide ? a.H / VEC : a.H, NORM_GRAD_TARGET, 4, grad_threads(2));
   int P;
   cudaError_t err;
   if (r.V == 0) {
     const int64_t cap = (int64_t)device_sm_count() * 4;
     if (d_weight) a.rstd = a.part + (int64_t)kPartRows * a.H;
-    err = launch_dependent(rms_norm_backward_long_kernel<T>,
+    err = launch_dependent(rms_norm_backward_long_kernel<T, WT>,
                            dim3((unsigned)(a.n < cap ? a.n : cap)), dim3(kNormThreads), 0, s, a);
     if (err != cudaSuccess || !d_weight) return err;
     P = (int)(a.n < 64 ? a.n : 64);
@@ -540,16 +603,16 @@ cudaError_t norm_grad_t(NormGradArgs a, int w_dtype, void *d_weight, cudaStream_
   } else {
     a.G = r.G;
     if (!d_weight) a.part = nullptr;
-    const int per_block = kNormThreads / r.G;
+    const int per_block = grad_threads(r.V) / r.G;
     int64_t blocks = (a.n + per_block - 1) / per_block;
     P = (int)(blocks < kPartRows ? blocks : kPartRows);
     const size_t smem = d_weight && per_block > 1 ? (size_t)per_block * a.H * 4 : 0;
-    err = wide ? norm_grad_v<T, VEC>(a, r.V, dim3((unsigned)P), smem, s)
-               : norm_grad_v<T, 1>(a, r.V, dim3((unsigned)P), smem, s);
+    err = wide ? norm_grad_v<T, WT, VEC>(a, r.V, dim3((unsigned)P), smem, s)
+               : norm_grad_v<T, WT, 1>(a, r.V, dim3((unsigned)P), smem, s);
   }
   if (err != cudaSuccess || !d_weight) return err;
-  return launch_dependent(column_join_kernel, dim3((unsigned)((a.H + 31) / 32)), dim3(256), 0, s,
-                          (const float *)a.part, P, a.H, w_dtype, d_weight);
+  return launch_dependent(column_join_kernel, dim3((unsigned)((a.H + 31) / 32)),
+                          dim3(kJoinThreads), 0, s, (const float *)a.part, P, a.H, w_dtype, d_weight);
 }
 
 }  // namespace
@@ -557,11 +620,12 @@ cudaError_t norm_grad_t(NormGradArgs a, int w_dtype, void *d_weight, cudaStream_
 cudaError_t launch_rms_norm(const void *x, const void *residual, const void *weight, int w_dtype,
                             int64_t n, int H, int dtype, float eps, void *y, void *sum,
                             uint8_t *codes, uint8_t *scales, cudaStream_t s) {
-  NormArgs a{x, residual, weight, y, sum, codes, scales, n, H, 0, w_dtype == MOE_FP32, eps};
+  const NormArgs a{x, residual, weight, y, sum, codes, scales, n, H, 0, eps, 1.0f / (float)H};
+  const bool w32 = weight && w_dtype == MOE_FP32;
   switch (dtype) {
-    case MOE_BF16: return codes ? norm_t<__nv_bfloat16, true>(a, s) : norm_t<__nv_bfloat16, false>(a, s);
-    case MOE_FP16: return codes ? norm_t<__half, true>(a, s) : norm_t<__half, false>(a, s);
-    default: return codes ? norm_t<float, true>(a, s) : norm_t<float, false>(a, s);
+    case MOE_BF16: return w32 ? norm_w<__nv_bfloat16, float>(a, s) : norm_w<__nv_bfloat16, __nv_bfloat16>(a, s);
+    case MOE_FP16: return w32 ? norm_w<__half, float>(a, s) : norm_w<__half, __half>(a, s);
+    default: return norm_w<float, float>(a, s);
   }
 }
 
@@ -574,11 +638,16 @@ cudaError_t launch_rms_norm_backward(const void *d_y, const void *x, const void 
                                      int w_dtype, const void *d_sum, int64_t n, int H, int dtype,
                                      float eps, void *d_x, void *d_weight, float *scratch,
                                      cudaStream_t s) {
-  NormGradArgs a{d_y, x, weight, d_sum, d_x, scratch, nullptr, n, H, 0, w_dtype == MOE_FP32, eps};
+  const NormGradArgs a{d_y, x, weight, d_sum, d_x, scratch, nullptr, n, H, 0, eps, 1.0f / (float)H};
+  const bool w32 = weight && w_dtype == MOE_FP32;
   switch (dtype) {
-    case MOE_BF16: return norm_grad_t<__nv_bfloat16>(a, w_dtype, d_weight, s);
-    case MOE_FP16: return norm_grad_t<__half>(a, w_dtype, d_weight, s);
-    default: return norm_grad_t<float>(a, w_dtype, d_weight, s);
+    case MOE_BF16:
+      return w32 ? norm_grad_t<__nv_bfloat16, float>(a, w_dtype, d_weight, s)
+                 : norm_grad_t<__nv_bfloat16, __nv_bfloat16>(a, w_dtype, d_weight, s);
+    case MOE_FP16:
+      return w32 ? norm_grad_t<__half, float>(a, w_dtype, d_weight, s)
+                 : norm_grad_t<__half, __half>(a, w_dtype, d_weight, s);
+    default: return norm_grad_t<float, float>(a, w_dtype, d_weight, s);
   }
 }
 
@@ -609,8 +678,8 @@ cudaError_t launch_column_sum(const void *d, int64_t n, int cols, int dtype, voi
                                   s, d, (const void *)nullptr, (const float *)nullptr, n, cols,
                                   scratch);
   if (err != cudaSuccess) return err;
-  return launch_dependent(column_join_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(256), 0, s,
-                          (const float *)scratch, (int)P, cols, dtype, out);
+  return launch_dependent(column_join_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(kJoinThreads), 0,
+                          s, (const float *)scratch, (int)P, cols, dtype, out);
 }
 
 }  // namespace moe
