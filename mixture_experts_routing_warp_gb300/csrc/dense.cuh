@@ -263,6 +263,22 @@ __device__ __forceinline__ void dense_epilogue(const DenseEpi &e, int64_t row, i
   }
 }
 
+// ----------------------------------------------------------- warp roles --
+// The producer and MMA roles run as whole warps whose every value is the same
+// in all lanes, and one elected lane issues: addresses and descriptors then
+// stay in uniform registers. (With the loop in lane 0 alone an MMA took 60
+// cycles to issue and a K step 570, whatever its width.)
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // --------------------------------------------------------------- products --
 // D[m, n] = sum_k A(m, k) B(n, k). K-major operands are stored [rows, K] row
 // by row, the others [K, rows].

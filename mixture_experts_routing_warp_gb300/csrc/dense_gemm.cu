@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   auto a_addr = [&](int s) { return stage0 + (uint32_t)(s * stage_bytes); };
   auto b_addr = [&](int s) { return stage0 + (uint32_t)(s * stage_bytes + kABytes); };
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
   const int first = (int)(blockIdx.x >> 1), step = (int)(gridDim.x >> 1);
@@ -137,22 +137,23 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   tc_fence_before();
   cluster_sync();  // both CTAs' barriers and TMEM exist before any cross-CTA use
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t tmem_base = (uint32_t)uniform((int)*tmem_slot);
 
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer --
-    if (lane == 0) {
-      const uint32_t tx = 2u * (uint32_t)stage_bytes;
-      int stage = 0;
-      uint32_t phase = 0, issued = 0;
-      bool ok = true;
-      for (int u = first; ok && u < total; u += step) {
-        const Unit w = unit_of(u, args);
-        const int m0 = w.m * 2 * kRowsCta + (int)rank * kRowsCta;
-        const int n0 = w.n * tn + (int)rank * (tn / 2);
-        for (int kb = w.k_lo; kb < w.k_hi; ++kb) {
-          ok = wait_bounded(empty_bar(stage), phase ^ 1u, s_abort, args.status, args.timeout_ns);
-          if (!ok) break;
+    const uint32_t tx = 2u * (uint32_t)stage_bytes;
+    int stage = 0;
+    uint32_t phase = 0, issued = 0;
+    bool ok = true;
+    for (int u = first; ok && u < total; u += step) {
+      const Unit w = unit_of(u, args);
+      const int m0 = w.m * 2 * kRowsCta + (int)rank * kRowsCta;
+      const int n0 = w.n * tn + (int)rank * (tn / 2);
+      for (int kb = w.k_lo; kb < w.k_hi; ++kb) {
+        ok = wait_bounded(empty_bar(stage), phase ^ 1u, s_abort, args.status, args.timeout_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (elect_one()) {
           const uint32_t fb = map_to_rank(full_bar(stage), 0);
           if (leader) mbar_arrive_expect_tx(full_bar(stage), tx);
           const int k0 = kb * 64;
@@ -172,30 +173,30 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             if (args.b_bytes > 8192)
               tma_load_2d_pair(b_addr(stage) + 8192u, &map_b, fb, n0 + 64, k0);
           }
-          issued = issued < (uint32_t)stages ? issued + 1 : (uint32_t)stages;
-          if (++stage == stages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        issued = issued < (uint32_t)stages ? issued + 1 : (uint32_t)stages;
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      // a pair's copies complete on the leader's barriers: the leader drains
-      // (the peer stays resident until the final cluster barrier)
-      if (!ok && leader) {
-        for (uint32_t i = 0; i < issued; ++i) {
-          int s = stage - 1 - (int)i;
-          uint32_t ph = phase;
-          if (s < 0) {
-            s += stages;
-            ph ^= 1u;
-          }
-          wait_drain(full_bar(s), ph, 100000000ull);
+    }
+    // a pair's copies complete on the leader's barriers: the leader drains
+    // (the peer stays resident until the final cluster barrier)
+    if (!ok && leader) {
+      for (uint32_t i = 0; i < issued; ++i) {
+        int s = stage - 1 - (int)i;
+        uint32_t ph = phase;
+        if (s < 0) {
+          s += stages;
+          ph ^= 1u;
         }
+        wait_drain(full_bar(s), ph, 100000000ull);
       }
     }
   } else if (warp == 1) {
     // --------------------------------------------- MMA issuer (the leader) --
-    if (lane == 0 && leader) {
+    if (leader) {
       // descriptor steps (16-byte units) between the four MMAs of a stage
       constexpr uint32_t a_step = AK ? 2u : 128u, b_step = BK ? 2u : 128u;
       int stage = 0, local = 0;
@@ -204,32 +205,37 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       for (int u = first; ok && u < total; u += step, ++local) {
         const Unit w = unit_of(u, args);
         const int acc = local & 1;
-        if (!wait_bounded(tempty_bar(acc), ((uint32_t)(local >> 1) & 1u) ^ 1u, s_abort,
-                          args.status, args.timeout_ns))
-          break;
+        ok = wait_bounded(tempty_bar(acc), ((uint32_t)(local >> 1) & 1u) ^ 1u, s_abort,
+                          args.status, args.timeout_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kMaxTn);
         for (int kb = w.k_lo; kb < w.k_hi; ++kb) {
-          if (!wait_bounded(full_bar(stage), phase, s_abort, args.status, args.timeout_ns)) {
-            ok = false;
-            break;
-          }
+          ok = wait_bounded(full_bar(stage), phase, s_abort, args.status, args.timeout_ns);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           tc_fence_after();
           const uint64_t ad = AK ? sw128_desc(a_addr(stage)) : sw128_desc_mn(a_addr(stage));
           const uint64_t bd = BK ? sw128_desc(b_addr(stage)) : sw128_desc_mn(b_addr(stage));
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_bf16_pair(d_tmem, ad + a_step * kk, bd + b_step * kk, args.idesc,
-                           kb != w.k_lo || kk != 0);
-          umma_commit_pair(empty_bar(stage), 0x3);
+            for (int kk = 0; kk < 4; ++kk)
+              umma_bf16_pair(d_tmem, ad + a_step * kk, bd + b_step * kk, args.idesc,
+                             kb != w.k_lo || kk != 0);
+            umma_commit_pair(empty_bar(stage), 0x3);
+          }
+          __syncwarp();
           if (++stage == stages) {
             stage = 0;
             phase ^= 1u;
           }
         }
-        if (ok) umma_commit_pair(tfull_bar(acc), 0x3);
+        if (ok && elect_one()) umma_commit_pair(tfull_bar(acc), 0x3);
+        __syncwarp();
       }
-      umma_commit_pair(drain_bar, 0x1);
+      if (elect_one()) umma_commit_pair(drain_bar, 0x1);
+      __syncwarp();
       wait_drain(drain_bar, 0, 100000000ull);
     }
   } else {

@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto b_addr = [&](int s) { return stage0 + (uint32_t)(s * kStageBytes + kABytes); };
   auto scale_addr = [&](int s) { return scale0 + (uint32_t)(s * kScaleBytes); };
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int total = args.m_tiles * args.n_tiles * args.splits;
   const int tn = args.tn;
 
@@ -149,20 +149,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t tmem_base = (uint32_t)uniform((int)*tmem_slot);
 
   if (warp == 0) {
-    if (lane == 0) {
-      const uint32_t sb_bytes = tn > 128 ? 1024u : 512u;
-      const uint32_t tx = (uint32_t)(kABytes + tn * kStep + kScaleA) + sb_bytes;
-      int stage = 0;
-      uint32_t phase = 0, issued = 0;
-      bool ok = true;
-      for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
-        const Unit w = unit_of(u, args);
-        for (int kb = w.k_lo; kb < w.k_hi; ++kb) {
-          ok = wait_bounded(empty_bar(stage), phase ^ 1u, s_abort, args.status, args.timeout_ns);
-          if (!ok) break;
+    const uint32_t sb_bytes = tn > 128 ? 1024u : 512u;
+    const uint32_t tx = (uint32_t)(kABytes + tn * kStep + kScaleA) + sb_bytes;
+    int stage = 0;
+    uint32_t phase = 0, issued = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
+      const Unit w = unit_of(u, args);
+      for (int kb = w.k_lo; kb < w.k_hi; ++kb) {
+        ok = wait_bounded(empty_bar(stage), phase ^ 1u, s_abort, args.status, args.timeout_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (elect_one()) {
           const uint32_t fb = full_bar(stage);
           mbar_arrive_expect_tx(fb, tx);
           tma_load_2d(a_addr(stage), &map_a, fb, kb * kStep, w.m * kRows);
@@ -174,67 +175,70 @@ __global__ void __launch_bounds__(kThreads, 1)
                     kScaleA, fb);
           bulk_load(scale_addr(stage) + kScaleA,
                     args.sb + ((int64_t)w.n * args.num_kb + kb) * kScaleB, sb_bytes, fb);
-          issued = issued < (uint32_t)kStages ? issued + 1 : (uint32_t)kStages;
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
         }
-      }
-      if (!ok) {
-        for (uint32_t i = 0; i < issued; ++i) {
-          int s = stage - 1 - (int)i;
-          uint32_t ph = phase;
-          if (s < 0) {
-            s += kStages;
-            ph ^= 1u;
-          }
-          wait_drain(full_bar(s), ph, 100000000ull);
+        issued = issued < (uint32_t)kStages ? issued + 1 : (uint32_t)kStages;
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
     }
+    if (!ok) {
+      for (uint32_t i = 0; i < issued; ++i) {
+        int s = stage - 1 - (int)i;
+        uint32_t ph = phase;
+        if (s < 0) {
+          s += kStages;
+          ph ^= 1u;
+        }
+        wait_drain(full_bar(s), ph, 100000000ull);
+      }
+    }
   } else if (warp == 1) {
-    if (lane == 0) {
-      int stage = 0, local = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int u = blockIdx.x; ok && u < total; u += gridDim.x, ++local) {
-        const Unit w = unit_of(u, args);
-        const int acc = local & 1;
-        if (!wait_bounded(tempty_bar(acc), ((uint32_t)(local >> 1) & 1u) ^ 1u, s_abort,
-                          args.status, args.timeout_ns))
-          break;
+    int stage = 0, local = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < total; u += gridDim.x, ++local) {
+      const Unit w = unit_of(u, args);
+      const int acc = local & 1;
+      ok = wait_bounded(tempty_bar(acc), ((uint32_t)(local >> 1) & 1u) ^ 1u, s_abort, args.status,
+                        args.timeout_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kMaxTn);
+      for (int kb = w.k_lo; kb < w.k_hi; ++kb) {
+        ok = wait_bounded(full_bar(stage), phase, s_abort, args.status, args.timeout_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kMaxTn);
-        for (int kb = w.k_lo; kb < w.k_hi; ++kb) {
-          if (!wait_bounded(full_bar(stage), phase, s_abort, args.status, args.timeout_ns)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          // the scales' columns belong to the stage: the MMAs that read them
-          // last were complete before the stage was filled again
-          const uint32_t sfa = tmem_base + 2u * kMaxTn + (uint32_t)(stage * kScaleCols);
-          const uint32_t sfb = sfa + 4u;
+        // the scales' columns belong to the stage: the MMAs that read them
+        // last were complete before the stage was filled again
+        const uint32_t sfa = tmem_base + 2u * kMaxTn + (uint32_t)(stage * kScaleCols);
+        const uint32_t sfb = sfa + 4u;
+        const uint64_t ad = sw128_desc(a_addr(stage)), bd = sw128_desc(b_addr(stage));
+        if (elect_one()) {
           copy_scales(sfa, scale_addr(stage));
           copy_scales(sfb, scale_addr(stage) + kScaleA);
           if (tn > 128) copy_scales(sfb + 4u, scale_addr(stage) + kScaleA + 512u);
-          const uint64_t ad = sw128_desc(a_addr(stage)), bd = sw128_desc(b_addr(stage));
 #pragma unroll
           for (uint32_t kk = 0; kk < 4; ++kk)  // the kk-th byte of each scale word
             umma_mx8(d_tmem, ad + 2u * kk, bd + 2u * kk, args.idesc | (kk << 4) | (kk << 29), sfa,
                      sfb, kb != w.k_lo || kk != 0);
           umma_commit(empty_bar(stage));
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
         }
-        if (ok) umma_commit(tfull_bar(acc));
+        __syncwarp();
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      umma_commit(drain_bar);
-      wait_drain(drain_bar, 0, 100000000ull);
+      if (ok && elect_one()) umma_commit(tfull_bar(acc));
+      __syncwarp();
     }
+    if (elect_one()) umma_commit(drain_bar);
+    __syncwarp();
+    wait_drain(drain_bar, 0, 100000000ull);
   } else {
     constexpr int W = EPI == EPI_GATED_MX ? 64 : 32;
     const int q = warp & 3, part = (warp - 2) >> 2;
