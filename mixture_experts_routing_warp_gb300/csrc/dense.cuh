@@ -98,13 +98,32 @@ __device__ __forceinline__ void load_row(const void *base, int64_t at, bool vec,
   }
 }
 
+// One 32-byte store: a thread of an epilogue writes its own row, and L2 takes
+// whole sectors at half the transactions of 16-byte pieces.
+__device__ __forceinline__ void store32(void *p, const uint4 &a, const uint4 &b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x),
+               "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+
 template <int W>
 __device__ __forceinline__ void store_row(void *base, int64_t at, bool vec, int left, int half,
                                           const float (&f)[W]) {
   uint16_t *p = static_cast<uint16_t *>(base) + at;
   if (vec && left >= W) {
+    bool done = false;
+    if constexpr (W % 16 == 0) {
+      if (((uintptr_t)p & 31) == 0) {  // whole sectors
+        done = true;
 #pragma unroll
-    for (int i = 0; i < W / 8; ++i) *reinterpret_cast<uint4 *>(p + 8 * i) = pack8(f + 8 * i, half);
+        for (int i = 0; i < W; i += 16) store32(p + i, pack8(f + i, half), pack8(f + i + 8, half));
+      }
+    }
+    if (!done) {
+#pragma unroll
+      for (int i = 0; i < W / 8; ++i)
+        *reinterpret_cast<uint4 *>(p + 8 * i) = pack8(f + 8 * i, half);
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < W; ++i)
@@ -159,8 +178,10 @@ __device__ __forceinline__ float linear_slope(float v, int act) {
 
 // h of a (gate, up) pair, as activate() but NaN passes the clamps.
 __device__ __forceinline__ float gated(float g, float u, const ActParams &p) {
-  g = g > p.limit ? p.limit : g;
-  u = u > p.limit ? p.limit : (u < -p.limit ? -p.limit : u);
+  if (p.limit < INFINITY) {
+    g = g > p.limit ? p.limit : g;
+    u = u > p.limit ? p.limit : (u < -p.limit ? -p.limit : u);
+  }
   return (g * sigmoid_fast(p.alpha * g)) * (u + p.beta);
 }
 
@@ -176,14 +197,47 @@ __device__ __forceinline__ void gated_backward(float g, float u, float d, const 
 }
 
 // --------------------------------------------------------------- epilogue --
+// What the epilogue reads of e.add for W columns of the sums: fetched ahead,
+// while the sums are still being made.
+template <int EPI, int W>
+struct Addend {
+  static constexpr bool kUsed = EPI == EPI_LINEAR || EPI == EPI_DACT || EPI == EPI_DGATED;
+  static constexpr int kWide = EPI == EPI_DGATED ? W / 2 : W;
+  uint4 q[kUsed ? kWide / 8 : 1];
+};
+template <int EPI, int W>
+__device__ __forceinline__ void fetch_addend(const DenseEpi &e, int64_t row, int c,
+                                             Addend<EPI, W> &a) {
+  if constexpr (Addend<EPI, W>::kUsed) {
+    if (e.add && e.vec && c + W <= e.cols) {
+      const int64_t at = EPI == EPI_DGATED ? row * (e.cols / 2) + c / 2 : row * e.cols + c;
+      const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(e.add) + at);
+#pragma unroll
+      for (int i = 0; i < Addend<EPI, W>::kWide / 8; ++i) a.q[i] = __ldg(p + i);
+    }
+  }
+}
+template <int EPI, int W>
+__device__ __forceinline__ void addend(const DenseEpi &e, int64_t row, int c,
+                                       const Addend<EPI, W> &a,
+                                       float (&f)[Addend<EPI, W>::kWide]) {
+  constexpr int N = Addend<EPI, W>::kWide;
+  if (e.vec && c + W <= e.cols) {
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i) unpack8(a.q[i], e.half, f + 8 * i);
+  } else {
+    const int64_t at = EPI == EPI_DGATED ? row * (e.cols / 2) + c / 2 : row * e.cols + c;
+    load_row<N>(e.add, at, false, EPI == EPI_DGATED ? (e.cols - c) / 2 : e.cols - c, e.half, f);
+  }
+}
+
 // Columns [c, c + W) of a row's sums to where they go. c is a multiple of W
 // and c < e.cols, row < e.rows.
 template <int EPI, int W>
 __device__ __forceinline__ void dense_epilogue(const DenseEpi &e, int64_t row, int c,
-                                               float (&v)[W]) {
+                                               float (&v)[W], const Addend<EPI, W> &a) {
   const int left = e.cols - c;
   if constexpr (EPI == EPI_LINEAR || EPI == EPI_DACT) {
-    const int64_t at = row * e.cols + c;
     if (e.bias) {
       float b[W];
       load_row<W>(e.bias, c, e.vec, left, e.half, b);
@@ -197,17 +251,17 @@ __device__ __forceinline__ void dense_epilogue(const DenseEpi &e, int64_t row, i
       }
       if (e.add) {
         float r[W];
-        load_row<W>(e.add, at, e.vec, left, e.half, r);
+        addend<EPI, W>(e, row, c, a, r);
 #pragma unroll
         for (int i = 0; i < W; ++i) v[i] += r[i];
       }
     } else {
       float d[W];
-      load_row<W>(e.add, at, e.vec, left, e.half, d);
+      addend<EPI, W>(e, row, c, a, d);
 #pragma unroll
       for (int i = 0; i < W; ++i) v[i] = d[i] * linear_slope(v[i], e.act);
     }
-    store_row<W>(e.out, at, e.vec, left, e.half, v);
+    store_row<W>(e.out, row * e.cols + c, e.vec, left, e.half, v);
   } else if constexpr (EPI == EPI_GATED) {
     float h[W / 2];
 #pragma unroll
@@ -229,13 +283,18 @@ __device__ __forceinline__ void dense_epilogue(const DenseEpi &e, int64_t row, i
 #pragma unroll
     for (int i = 0; i < W / 8; ++i) q[i] = mx8_codes4(h + 4 * i, inv);
     uint4 *dst = reinterpret_cast<uint4 *>(e.codes + at);
-    dst[0] = make_uint4(q[0], q[1], q[2], q[3]);
-    dst[1] = make_uint4(q[4], q[5], q[6], q[7]);
+    const uint4 lo = make_uint4(q[0], q[1], q[2], q[3]), hi = make_uint4(q[4], q[5], q[6], q[7]);
+    if (((uintptr_t)dst & 31) == 0) {
+      store32(dst, lo, hi);
+    } else {
+      dst[0] = lo;
+      dst[1] = hi;
+    }
     e.scales[at / 32] = (uint8_t)b;
   } else if constexpr (EPI == EPI_DGATED) {
     const int I = e.cols / 2;
     float d[W / 2];
-    load_row<W / 2>(e.add, row * I + c / 2, e.vec, left / 2, e.half, d);
+    addend<EPI, W>(e, row, c, a, d);
     if (e.gate.layout == MOE_W13_PACKED) {
       float g[W / 2], u[W / 2];
 #pragma unroll
@@ -290,7 +349,7 @@ struct DenseOperand {
 };
 
 struct DensePlan {
-  int tn;       // columns per tile
+  int tn, tn_last;  // columns per tile, and of the last one of a row of tiles
   int m_tiles, n_tiles, splits;
   size_t partial;  // bytes of fp32 partial sums (0: one part)
   size_t blocks;   // bytes of the MXFP8 scales in the tensor core's layout

@@ -17,13 +17,17 @@
 //   warp 0      TMA producer (each CTA its own halves; bytes counted on the
 //               leader's barrier)
 //   warp 1      TMEM allocation; the leader's issues the MMAs
-//   warps 2-9   epilogue, two per TMEM lane quarter, alternate column chunks
+//   warps 2..   epilogue, two or four per TMEM lane quarter, column chunks in turn
 // Where the tiles are fewer than the pairs of SMs can take, the K range is
 // split: parts write fp32 sums and a second kernel adds them in order and
 // applies the epilogue. No atomics: the bits depend on the inputs and sizes.
 // Every mbarrier wait is bounded.
 #include "dense.cuh"
 #include "tc_ptx.cuh"
+#ifdef DENSE_TUNE
+#include <stdio.h>
+#include <stdlib.h>
+#endif
 
 namespace moe {
 namespace {
@@ -34,8 +38,14 @@ constexpr int kRowsCta = 128;                    // A rows of a CTA's half tile
 constexpr int kStepBytes = 128;                  // K bytes of a stage
 constexpr int kABytes = kRowsCta * kStepBytes;   // 16 KB
 constexpr int kMaxTn = 256;
-constexpr int kEpiWarps = 8;
-constexpr int kGemmThreads = (2 + kEpiWarps) * 32;
+// Epilogue warps, two or four per TMEM lane quarter: with four a tile's
+// epilogue has the latency of two column chunks; a group of 32 8-bit results
+// takes 64 columns and twice the registers.
+#ifndef EPI_WARPS
+#define EPI_WARPS 16
+#endif
+constexpr int epi_warps(int epi) { return epi == EPI_GATED_MX ? 8 : EPI_WARPS; }
+constexpr int gemm_threads(int epi) { return (2 + epi_warps(epi)) * 32; }
 constexpr int kRingBytes = 220 * 1024;
 constexpr int kMaxStages = 8;
 constexpr int kNumBars = 2 * kMaxStages + 2 + 2 + 1;
@@ -49,6 +59,7 @@ struct GemmArgs {
   int m_tiles, n_tiles, splits;
   int num_kb;           // K steps of the whole sum
   int tn, stages, b_bytes;
+  int tn_last, b_bytes_last, n_full;  // the last tile of a row of tiles, if narrower
   int pairs;            // B rows come interleaved through a 3-D map
   uint32_t idesc;
   uint32_t *status;
@@ -64,16 +75,27 @@ __device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr) {
          ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
+// Unit u: a tile and its part of the sum. The narrow last tiles come behind
+// all others, to fill what the last wave of whole tiles leaves idle.
 struct Unit {
-  int m, n, s, k_lo, k_hi;
+  int m, n, s, k_lo, k_hi, tn, b_bytes;
 };
 __device__ __forceinline__ Unit unit_of(int u, const GemmArgs &a) {
   Unit w;
-  const int tiles = a.m_tiles * a.n_tiles;
+  const int tiles = a.m_tiles * a.n_tiles, full = a.m_tiles * a.n_full;
   w.s = u / tiles;
   const int t = u - w.s * tiles;
-  w.m = t / a.n_tiles;
-  w.n = t - w.m * a.n_tiles;
+  if (t < full) {
+    w.m = t / a.n_full;
+    w.n = t - w.m * a.n_full;
+    w.tn = a.tn;
+    w.b_bytes = a.b_bytes;
+  } else {
+    w.m = t - full;
+    w.n = a.n_full;
+    w.tn = a.tn_last;
+    w.b_bytes = a.b_bytes_last;
+  }
   w.k_lo = (int)((int64_t)a.num_kb * w.s / a.splits);
   w.k_hi = (int)((int64_t)a.num_kb * (w.s + 1) / a.splits);
   return w;
@@ -81,9 +103,10 @@ __device__ __forceinline__ Unit unit_of(int u, const GemmArgs &a) {
 
 // AK / BK: the operand is K-major.
 template <bool AK, bool BK, int EPI>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+__global__ void __launch_bounds__(gemm_threads(EPI), 1)
     dense_gemm_kernel(const __grid_constant__ CUtensorMap map_a,
                       const __grid_constant__ CUtensorMap map_b,
+                      const __grid_constant__ CUtensorMap map_b_last,
                       const __grid_constant__ GemmArgs args) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -115,7 +138,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull_bar(b), 1);
-      mbar_init(tempty_bar(b), 2 * kEpiWarps);  // the leader's counts both CTAs
+      mbar_init(tempty_bar(b), 2 * epi_warps(EPI));  // the leader's counts both CTAs
     }
     mbar_init(drain_bar, 1);
     *s_abort = 0;
@@ -123,6 +146,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     prefetch_tmap(&map_a);
     prefetch_tmap(&map_b);
+    prefetch_tmap(&map_b_last);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -141,14 +165,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer --
-    const uint32_t tx = 2u * (uint32_t)stage_bytes;
     int stage = 0;
     uint32_t phase = 0, issued = 0;
     bool ok = true;
     for (int u = first; ok && u < total; u += step) {
       const Unit w = unit_of(u, args);
       const int m0 = w.m * 2 * kRowsCta + (int)rank * kRowsCta;
-      const int n0 = w.n * tn + (int)rank * (tn / 2);
+      const int n0 = w.n * tn + (int)rank * (w.tn / 2);
+      const uint32_t tx = 2u * (uint32_t)(kABytes + w.b_bytes);
+      const CUtensorMap *mb = w.n < args.n_full ? &map_b : &map_b_last;
       for (int kb = w.k_lo; kb < w.k_hi; ++kb) {
         ok = wait_bounded(empty_bar(stage), phase ^ 1u, s_abort, args.status, args.timeout_ns);
         ok = __all_sync(0xffffffffu, ok);
@@ -165,12 +190,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           }
           if constexpr (BK) {
             if (args.pairs)
-              tma_load_3d_pair(b_addr(stage), &map_b, fb, k0, 0, n0 / 2);
+              tma_load_3d_pair(b_addr(stage), mb, fb, k0, 0, n0 / 2);
             else
-              tma_load_2d_pair(b_addr(stage), &map_b, fb, k0, n0);
+              tma_load_2d_pair(b_addr(stage), mb, fb, k0, n0);
           } else {
             tma_load_2d_pair(b_addr(stage), &map_b, fb, n0, k0);
-            if (args.b_bytes > 8192)
+            if (w.b_bytes > 8192)
               tma_load_2d_pair(b_addr(stage) + 8192u, &map_b, fb, n0 + 64, k0);
           }
         }
@@ -211,6 +236,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kMaxTn);
+        const uint32_t idesc = args.idesc | ((uint32_t)(w.tn >> 3) << 17);
         for (int kb = w.k_lo; kb < w.k_hi; ++kb) {
           ok = wait_bounded(full_bar(stage), phase, s_abort, args.status, args.timeout_ns);
           ok = __all_sync(0xffffffffu, ok);
@@ -221,7 +247,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              umma_bf16_pair(d_tmem, ad + a_step * kk, bd + b_step * kk, args.idesc,
+              umma_bf16_pair(d_tmem, ad + a_step * kk, bd + b_step * kk, idesc,
                              kb != w.k_lo || kk != 0);
             umma_commit_pair(empty_bar(stage), 0x3);
           }
@@ -242,19 +268,27 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     // ----------------------------------------------------------- epilogue --
     constexpr int W = EPI == EPI_GATED_MX ? 64 : 32;
     const int q = warp & 3;            // TMEM lane quarter this warp may read
-    const int part = (warp - 2) >> 2;  // which of the quarter's two warps
+    const int part = (warp - 2) >> 2;  // which of the quarter's warps
+    constexpr int kHop = epi_warps(EPI) / 4 * W;  // columns from one of its chunks to the next
     int local = 0;
     for (int u = first; u < total; u += step, ++local) {
       const Unit w = unit_of(u, args);
       const int acc = local & 1;
+      const int64_t row = (int64_t)w.m * 2 * kRowsCta + rank * kRowsCta + q * 32 + lane;
+      const int c0 = w.n * tn;
+      const bool live = row < args.e.rows;
+      Addend<EPI, W> add;  // of the first columns, while the last products run
+      if (live && part * W < w.tn && c0 + part * W < args.e.cols)
+        fetch_addend<EPI, W>(args.e, row, c0 + part * W, add);
       if (!wait_bounded(tfull_bar(acc), (uint32_t)(local >> 1) & 1u, s_abort, args.status,
                         args.timeout_ns))
         break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kMaxTn);
-      const int64_t row = (int64_t)w.m * 2 * kRowsCta + rank * kRowsCta + q * 32 + lane;
-      const int c0 = w.n * tn;
-      for (int c = part * W; c < tn; c += 2 * W) {
+      DenseEpi e = args.e;
+      if constexpr (EPI == EPI_PARTIAL) e.out = static_cast<float *>(e.out) + w.s * args.part_stride;
+#pragma unroll 1
+      for (int c = part * W; c < w.tn; c += kHop) {
         if (c0 + c >= args.e.cols) break;
         float v[W];
         uint32_t r[32];
@@ -265,14 +299,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[i + j] = __uint_as_float(r[j]);
         }
-        if (row < args.e.rows) {
-          if constexpr (EPI == EPI_PARTIAL) {
-            DenseEpi e = args.e;
-            e.out = static_cast<float *>(e.out) + w.s * args.part_stride;
-            dense_epilogue<EPI, W>(e, row, c0 + c, v);
-          } else {
-            dense_epilogue<EPI, W>(args.e, row, c0 + c, v);
-          }
+        if (live) {
+          const Addend<EPI, W> now = add;
+          if (c + kHop < w.tn && c0 + c + kHop < args.e.cols)
+            fetch_addend<EPI, W>(e, row, c0 + c + kHop, add);
+          dense_epilogue<EPI, W>(e, row, c0 + c, v, now);
         }
       }
       tc_fence_before();
@@ -314,6 +345,8 @@ dense_join_kernel(const float *part, int64_t stride, int splits, const __grid_co
 #pragma unroll
     for (int j = 0; j < W; ++j) v[j] = 0.f;
     const float *p = part + row * e.cols + c;
+    Addend<EPI, W> add;
+    fetch_addend<EPI, W>(e, row, c, add);
     const bool full = c + W <= e.cols && e.cols % 4 == 0;
     for (int s = 0; s < splits; ++s, p += stride) {
       if (full) {
@@ -331,7 +364,7 @@ dense_join_kernel(const float *part, int64_t stride, int splits, const __grid_co
           if (c + j < e.cols) v[j] += __ldcg(p + j);
       }
     }
-    dense_epilogue<EPI, W>(e, row, c, v);
+    dense_epilogue<EPI, W>(e, row, c, v, add);
   }
 }
 
@@ -356,14 +389,14 @@ bool map_pairs(CUtensorMap *m, const void *base, int64_t I, int64_t cols, int bo
 }
 
 template <bool AK, bool BK, int EPI>
-cudaError_t launch_gemm(const CUtensorMap &ma, const CUtensorMap &mb, const GemmArgs &a,
-                        cudaStream_t s) {
+cudaError_t launch_gemm(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &ml,
+                        const GemmArgs &a, cudaStream_t s) {
   auto kern = dense_gemm_kernel<AK, BK, EPI>;
   static PerDeviceOnce once;
   static std::atomic<int> resident[PerDeviceOnce::kMaxDevices] = {};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(device_sm_count() & ~1);
-  cfg.blockDim = dim3(kGemmThreads);
+  cfg.blockDim = dim3(gemm_threads(EPI));
   cfg.dynamicSmemBytes = kGemmSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -392,7 +425,7 @@ cudaError_t launch_gemm(const CUtensorMap &ma, const CUtensorMap &mb, const Gemm
   int64_t pairs = resident[dev].load(std::memory_order_relaxed);
   if (units < pairs) pairs = units;
   cfg.gridDim = dim3((unsigned)(2 * pairs));
-  err = cudaLaunchKernelEx(&cfg, kern, ma, mb, a);
+  err = cudaLaunchKernelEx(&cfg, kern, ma, mb, ml, a);
   return err != cudaSuccess ? err : cudaGetLastError();
 }
 
@@ -409,18 +442,18 @@ cudaError_t launch_join(const float *part, int64_t stride, int splits, const Den
 }
 
 template <bool AK, bool BK>
-cudaError_t launch_kind(int kind, const CUtensorMap &ma, const CUtensorMap &mb, const GemmArgs &a,
-                        cudaStream_t s) {
+cudaError_t launch_kind(int kind, const CUtensorMap &ma, const CUtensorMap &mb,
+                        const CUtensorMap &ml, const GemmArgs &a, cudaStream_t s) {
   if constexpr (AK && BK) {
     switch (kind) {
-      case EPI_DACT: return launch_gemm<AK, BK, EPI_DACT>(ma, mb, a, s);
-      case EPI_GATED: return launch_gemm<AK, BK, EPI_GATED>(ma, mb, a, s);
-      case EPI_GATED_MX: return launch_gemm<AK, BK, EPI_GATED_MX>(ma, mb, a, s);
-      case EPI_DGATED: return launch_gemm<AK, BK, EPI_DGATED>(ma, mb, a, s);
+      case EPI_DACT: return launch_gemm<AK, BK, EPI_DACT>(ma, mb, ml, a, s);
+      case EPI_GATED: return launch_gemm<AK, BK, EPI_GATED>(ma, mb, ml, a, s);
+      case EPI_GATED_MX: return launch_gemm<AK, BK, EPI_GATED_MX>(ma, mb, ml, a, s);
+      case EPI_DGATED: return launch_gemm<AK, BK, EPI_DGATED>(ma, mb, ml, a, s);
     }
   }
-  if (kind == EPI_PARTIAL) return launch_gemm<AK, BK, EPI_PARTIAL>(ma, mb, a, s);
-  return launch_gemm<AK, BK, EPI_LINEAR>(ma, mb, a, s);
+  if (kind == EPI_PARTIAL) return launch_gemm<AK, BK, EPI_PARTIAL>(ma, mb, ml, a, s);
+  return launch_gemm<AK, BK, EPI_LINEAR>(ma, mb, ml, a, s);
 }
 
 }  // namespace
@@ -428,30 +461,51 @@ cudaError_t launch_kind(int kind, const CUtensorMap &ma, const CUtensorMap &mb, 
 // Tile width and number of parts of the sum: the choice with the least
 // estimated time, in SM cycles. A K step of a pair takes 2 cycles per column
 // (256 x tn x 64 products at 8192 per cycle and SM) and no less than its
-// shared-memory reads; a unit costs about 1200 cycles beside its steps; a
-// split costs its partial sums' way through L2 and the joining kernel. MXFP8:
-// single CTAs of 128 rows and steps of 128 codes at twice the rate, the same
-// 2 cycles per column.
+// operands' way into shared memory (kIngress bytes per cycle and SM) nor than
+// its issue; a unit costs about kUnit cycles beside its steps; a split costs
+// its partial sums' way through L2 and the joining kernel. MXFP8: single CTAs
+// of 128 rows and steps of 128 codes at twice the rate, the same 2 cycles per
+// column.
 DensePlan dense_plan(int64_t M, int64_t N, int64_t K, int kind, bool mx) {
   constexpr int kSms = 152;  // the GB300's: a plan does not depend on the device
+  constexpr double kIngress = 60.0, kIssue = 200.0, kUnit = 800.0;
   DensePlan best{};
   double best_t = 1e300;
   const int gran = kind == EPI_GATED_MX ? 64 : 32;
   const int workers = mx ? kSms : kSms / 2, rows = mx ? 128 : 256;
   const int64_t kb = mx ? (K + 127) / 128 : (K + 63) / 64, mt = (M + rows - 1) / rows;
+  auto step = [&](int tn) {
+    const double mma = 2.0 * tn, load = (16384.0 + (mx ? 128.0 : 64.0) * tn) / kIngress;
+    const double t = mma > load ? mma : load;
+    return t > kIssue ? t : kIssue;
+  };
+#ifdef DENSE_TUNE
+  const char *env_tn = getenv("DENSE_TN"), *env_s = getenv("DENSE_SPLIT");
+#endif
   for (int tn = mx ? 192 : kMaxTn; tn >= 64; tn -= gran) {
+#ifdef DENSE_TUNE
+    if (env_tn && atoi(env_tn) != tn) continue;
+#endif
     const int64_t nt = (N + tn - 1) / tn;
-    const int64_t tiles = mt * nt;
-    const double reads = mx ? 150.0 + tn : 150.0 + tn / 2;
-    const double step = 2.0 * tn > reads ? 2.0 * tn : reads;
+    const int last = (int)((N - (nt - 1) * tn + gran - 1) / gran * gran);
+    const int64_t nf = last == tn ? nt : nt - 1;
     for (int s = 1; s <= 16; ++s) {
-      if (s > 1 && (kb / s < 4 || tiles * s > 2 * workers)) break;
-      const int64_t waves = (tiles * s + workers - 1) / workers;
-      double t = (double)waves * ((double)((kb + s - 1) / s) * step + 1200.0);
+#ifdef DENSE_TUNE
+      if (env_s && atoi(env_s) != s) continue;
+#endif
+      if (s > 1 && (kb / s < 4 || mt * nt * s > 2 * workers)) break;
+      const double steps = (double)((kb + s - 1) / s);
+      // whole tiles in waves, the narrow ones in the room that the last leaves
+      const int64_t full = mt * nf * s, waves = (full + workers - 1) / workers;
+      int64_t narrow = (nt - nf) * mt * s - (waves * workers - full);
+      if (narrow < 0) narrow = 0;
+      double t = (double)waves * (steps * step(tn) + kUnit) +
+                 (double)((narrow + workers - 1) / workers) * (steps * step(last) + kUnit);
       if (s > 1) t += 5000.0 + (double)M * N * 4.0 * (s + 1) / 2500.0;
       if (t < best_t) {
         best_t = t;
         best.tn = tn;
+        best.tn_last = mx ? tn : last;
         best.m_tiles = (int)mt;
         best.n_tiles = (int)nt;
         best.splits = s;
@@ -460,19 +514,25 @@ DensePlan dense_plan(int64_t M, int64_t N, int64_t K, int kind, bool mx) {
   }
   best.partial = best.splits > 1 ? (size_t)M * N * 4 * best.splits : 0;
   best.blocks = mx ? mx8_scale_blocks(best, K) : 0;
+#ifdef DENSE_TUNE
+  if (getenv("DENSE_SHOW")) fprintf(stderr, "plan M %ld N %ld K %ld: tn %d last %d splits %d tiles %dx%d est %.0f\n", (long)M, (long)N, (long)K, best.tn, best.tn_last, best.splits, best.m_tiles, best.n_tiles, best_t);
+#endif
   return best;
 }
 
 cudaError_t launch_dense(const DenseProduct &p, const DensePlan &plan, float *partial,
                          int32_t *status, cudaStream_t s) {
-  CUtensorMap ma, mb;
+  CUtensorMap ma, mb, ml;
   const int tn = plan.tn;
   const bool ak = p.a.k_major, bk = p.b.k_major;
   bool ok = ak ? map_rows(&ma, p.a.p, p.M, p.K, kRowsCta) : map_rows(&ma, p.a.p, p.K, p.M, 64);
-  if (p.b.pairs)
-    ok = ok && map_pairs(&mb, p.b.p, p.N / 2, p.K, tn / 4);
-  else
-    ok = ok && (bk ? map_rows(&mb, p.b.p, p.N, p.K, tn / 2) : map_rows(&mb, p.b.p, p.K, p.N, 64));
+  auto map_b = [&](CUtensorMap *m, int cols) {
+    if (p.b.pairs) return map_pairs(m, p.b.p, p.N / 2, p.K, cols / 4);
+    return bk ? map_rows(m, p.b.p, p.N, p.K, cols / 2) : map_rows(m, p.b.p, p.K, p.N, 64);
+  };
+  ok = ok && map_b(&mb, tn);
+  ml = mb;
+  if (plan.tn_last != tn) ok = ok && map_b(&ml, plan.tn_last);
   if (!ok) return cudaErrorInvalidValue;
   GemmArgs a{};
   a.e = p.epi;
@@ -481,13 +541,17 @@ cudaError_t launch_dense(const DenseProduct &p, const DensePlan &plan, float *pa
   a.splits = plan.splits;
   a.num_kb = (int)((p.K + 63) / 64);
   a.tn = tn;
-  a.b_bytes = bk ? tn / 2 * kStepBytes : (tn / 2 + 63) / 64 * 8192;
+  auto b_bytes = [&](int cols) { return bk ? cols / 2 * kStepBytes : (cols / 2 + 63) / 64 * 8192; };
+  a.b_bytes = b_bytes(tn);
+  a.tn_last = plan.tn_last;
+  a.b_bytes_last = b_bytes(plan.tn_last);
+  a.n_full = plan.tn_last == tn ? plan.n_tiles : plan.n_tiles - 1;
   a.stages = kRingBytes / (kABytes + a.b_bytes);
   if (a.stages > kMaxStages) a.stages = kMaxStages;
   a.pairs = p.b.pairs;
   const uint32_t type = p.epi.half ? 0u : 1u;  // fp16 / bf16
   a.idesc = (1u << 4) | (type << 7) | (type << 10) | ((ak ? 0u : 1u) << 15) |
-            ((bk ? 0u : 1u) << 16) | ((uint32_t)(tn >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
+            ((bk ? 0u : 1u) << 16) | ((uint32_t)(256 >> 4) << 24);
   a.status = reinterpret_cast<uint32_t *>(status);
   a.timeout_ns = kWaitTimeoutNs;
   int kind = p.kind;
@@ -496,9 +560,9 @@ cudaError_t launch_dense(const DenseProduct &p, const DensePlan &plan, float *pa
     a.e.out = partial;
     a.part_stride = p.M * p.N;
   }
-  cudaError_t err = ak && bk ? launch_kind<true, true>(kind, ma, mb, a, s)
-                    : ak     ? launch_kind<true, false>(kind, ma, mb, a, s)
-                             : launch_kind<false, false>(kind, ma, mb, a, s);
+  cudaError_t err = ak && bk ? launch_kind<true, true>(kind, ma, mb, ml, a, s)
+                    : ak     ? launch_kind<true, false>(kind, ma, mb, ml, a, s)
+                             : launch_kind<false, false>(kind, ma, mb, ml, a, s);
   return err != cudaSuccess || plan.splits == 1 ? err : launch_dense_join(p, plan, partial, s);
 }
 

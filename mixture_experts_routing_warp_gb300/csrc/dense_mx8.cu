@@ -246,13 +246,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int u = blockIdx.x; u < total; u += gridDim.x, ++local) {
       const Unit w = unit_of(u, args);
       const int acc = local & 1;
+      const int64_t row = (int64_t)w.m * kRows + q * 32 + lane;
+      const int c0 = w.n * tn;
+      const bool live = row < args.e.rows;
+      Addend<EPI, W> add;  // of the first columns, while the last products run
+      if (live && c0 + part * W < args.e.cols) fetch_addend<EPI, W>(args.e, row, c0 + part * W, add);
       if (!wait_bounded(tfull_bar(acc), (uint32_t)(local >> 1) & 1u, s_abort, args.status,
                         args.timeout_ns))
         break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kMaxTn);
-      const int64_t row = (int64_t)w.m * kRows + q * 32 + lane;
-      const int c0 = w.n * tn;
+      DenseEpi e = args.e;
+      if constexpr (EPI == EPI_PARTIAL) e.out = static_cast<float *>(e.out) + w.s * args.part_stride;
+#pragma unroll 1
       for (int c = part * W; c < tn; c += 2 * W) {
         if (c0 + c >= args.e.cols) break;
         float v[W];
@@ -264,14 +270,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[i + j] = __uint_as_float(r[j]);
         }
-        if (row < args.e.rows) {
-          if constexpr (EPI == EPI_PARTIAL) {
-            DenseEpi e = args.e;
-            e.out = static_cast<float *>(e.out) + w.s * args.part_stride;
-            dense_epilogue<EPI, W>(e, row, c0 + c, v);
-          } else {
-            dense_epilogue<EPI, W>(args.e, row, c0 + c, v);
-          }
+        if (live) {
+          const Addend<EPI, W> now = add;
+          if (c + 2 * W < tn && c0 + c + 2 * W < args.e.cols)
+            fetch_addend<EPI, W>(e, row, c0 + c + 2 * W, add);
+          dense_epilogue<EPI, W>(e, row, c0 + c, v, now);
         }
       }
       tc_fence_before();
