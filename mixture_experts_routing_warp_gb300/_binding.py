@@ -9,6 +9,7 @@ call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Optional
@@ -457,7 +458,7 @@ def _run(name: str, device: int, *args) -> None:
     """The library call `name`(*args, stream) on the device's current stream,
     with that device current."""
     fn = getattr(_LIB or lib(), name)
-    if device == torch.cuda.current_device():
+    if device == torch._C._cuda_getDevice():
         status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
     else:
         with torch.cuda.device(device):
@@ -719,9 +720,25 @@ class Mx8:
         self._as_parameter_ = ctypes.byref(Mx8Rows(codes.data_ptr(), scales.data_ptr()))
 
 
-def _empty_mx8(rows: int, cols: int, like: torch.Tensor) -> Mx8:
-    return Mx8(torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=like.device),
-               torch.empty((rows, cols // 32), dtype=torch.uint8, device=like.device))
+def _empty_mx8(rows: int, cols: int, like: torch.Tensor, device: int) -> Mx8:
+    if cols % 32:
+        raise ValueError(f"8-bit rows need a multiple of 32 columns, got {cols}")
+    m = Mx8.__new__(Mx8)
+    on = like.device
+    m.codes = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=on)
+    m.scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=on)
+    m.device, m.shape = device, m.codes.shape
+    m._as_parameter_ = ctypes.byref(Mx8Rows(m.codes.data_ptr(), m.scales.data_ptr()))
+    return m
+
+
+def _out_like(out: Optional[torch.Tensor], name: str, like: torch.Tensor) -> torch.Tensor:
+    """`out`, or a new tensor, of like's shape and type (empty_like costs the
+    host 2 us less than new_empty)."""
+    if out is None:
+        return torch.empty_like(like)
+    _need_on(out, name, like.dtype, like.get_device(), like.shape)
+    return out
 
 
 def _need_rows16(t: torch.Tensor, name: str) -> int:
@@ -774,14 +791,17 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float = 1e-5,
     total = None
     if residual is not None:
         _need_on(residual, "residual", x.dtype, device, (n, H))
-        total = _out_rows(sum_out, "sum_out", (n, H), x)
+        total = _out_like(sum_out, "sum_out", x)
     elif sum_out is not None:
         raise ValueError("sum_out needs a residual")
     if mx8:
-        y = _empty_mx8(n, H, x) if out is None else out
-        _need_mx8(y, "out", device, (n, H))
+        if out is None:
+            y = _empty_mx8(n, H, x, device)
+        else:
+            y = out
+            _need_mx8(y, "out", device, (n, H))
     else:
-        y = _out_rows(out, "out", (n, H), x)
+        y = _out_like(out, "out", x)
     _run("moe_rms_norm", device, x.data_ptr(), None if residual is None else residual.data_ptr(),
          w, w_dtype, n, H, DTYPE[x.dtype], eps, None if mx8 else y.data_ptr(),
          y if mx8 else None, None if total is None else total.data_ptr())
@@ -824,36 +844,43 @@ def rms_norm_backward(d_y: torch.Tensor, x: torch.Tensor, weight: Optional[torch
     return d_x, d_weight
 
 
+@functools.lru_cache(maxsize=4096)
 def rms_norm_backward_workspace_size(n: int, H: int) -> int:
     return int((_LIB or lib()).moe_rms_norm_backward_workspace_size(n, H))
 
 
+@functools.lru_cache(maxsize=4096)
 def linear_workspace_size(n: int, R: int, C: int) -> int:
     return int((_LIB or lib()).moe_linear_workspace_size(n, R, C))
 
 
+@functools.lru_cache(maxsize=4096)
 def linear_backward_workspace_size(n: int, R: int, C: int, act: str = "none") -> int:
     return int((_LIB or lib()).moe_linear_backward_workspace_size(n, R, C, LINEAR_ACT[act]))
 
 
+@functools.lru_cache(maxsize=4096)
 def gated_linear_workspace_size(n: int, H: int, I: int) -> int:
     return int((_LIB or lib()).moe_gated_linear_workspace_size(n, H, I))
 
 
+@functools.lru_cache(maxsize=4096)
 def gated_linear_backward_workspace_size(n: int, H: int, I: int) -> int:
     return int((_LIB or lib()).moe_gated_linear_backward_workspace_size(n, H, I))
 
 
 def _need_act(act: str) -> int:
-    if act not in LINEAR_ACT:
+    act_id = LINEAR_ACT.get(act)
+    if act_id is None:
         raise ValueError(f"act must be one of {sorted(LINEAR_ACT)}, got {act!r}")
-    return LINEAR_ACT[act]
+    return act_id
 
 
 def _product_operands(x, w, w_name: str, dtype):
     """(device, rows, features, out features, output type) of x and w, both
-    16-bit tensors of one type or both Mx8."""
-    if isinstance(x, Mx8):
+    16-bit tensors of one type or both Mx8. One expression checks the common
+    case; what it refuses is then named."""
+    if type(x) is Mx8:
         device = x.device
         _need_mx8(w, w_name, device)
         if w.shape[1] != x.shape[1]:
@@ -862,13 +889,19 @@ def _product_operands(x, w, w_name: str, dtype):
         if dtype not in (torch.bfloat16, torch.float16):
             raise ValueError("dtype must be torch.bfloat16 or torch.float16")
         return device, x.shape[0], x.shape[1], w.shape[0], dtype
+    if isinstance(x, torch.Tensor) and isinstance(w, torch.Tensor) and x.dim() == 2 == w.dim():
+        dt, device = x.dtype, x.get_device()
+        n, C = x.shape
+        R, columns = w.shape
+        if ((dt is torch.bfloat16 or dt is torch.float16) and w.dtype is dt and columns == C > 0
+                and w.get_device() == device >= 0 and x.is_contiguous() and w.is_contiguous()
+                and (dtype is None or dtype is dt)):
+            return device, n, C, R, dt
     device = _need_rows16(x, "x")
     if dtype is not None and dtype is not x.dtype:
         raise ValueError(f"dtype is x's, {x.dtype}, unless x is Mx8 rows")
     _need_on(w, w_name, x.dtype, device)
-    if w.dim() != 2 or w.shape[1] != x.shape[1]:
-        raise ValueError(f"{w_name} must have shape [rows, {x.shape[1]}], got {tuple(w.shape)}")
-    return device, x.shape[0], x.shape[1], w.shape[0], x.dtype
+    raise ValueError(f"{w_name} must have shape [rows, {x.shape[1]}], got {tuple(w.shape)}")
 
 
 def linear(x, w, bias: Optional[torch.Tensor] = None, act: str = "none",
@@ -881,19 +914,26 @@ def linear(x, w, bias: Optional[torch.Tensor] = None, act: str = "none",
     (linear_workspace_size), allocated where it is None."""
     act_id = _need_act(act)
     device, n, C, R, dtype = _product_operands(x, w, "w", dtype)
-    mx = isinstance(x, Mx8)
-    like = x.codes if mx else x
+    if type(x) is Mx8:
+        name, like, xp, wp = "moe_linear_mx8", x.codes, x, w
+    else:
+        name, like, xp, wp = "moe_linear", x, x.data_ptr(), w.data_ptr()
     b = None if bias is None else _need_vector(bias, "bias", (dtype,), device, R)
     if residual is not None:
         _need_on(residual, "residual", dtype, device, (n, R))
+        residual = residual.data_ptr()
     if out is None:
         out = torch.empty((n, R), dtype=dtype, device=like.device)
     else:
         _need_on(out, "out", dtype, device, (n, R))
-    ws, p, size = _scratch(ws, linear_workspace_size(n, R, C), like, device)
-    _run("moe_linear_mx8" if mx else "moe_linear", device, x if mx else x.data_ptr(),
-         w if mx else w.data_ptr(), b, None if residual is None else residual.data_ptr(), n, R, C,
-         DTYPE[dtype], act_id, out.data_ptr(), p, size, _need_status(status, device))
+    size = linear_workspace_size(n, R, C)
+    p = None
+    if size or ws is not None:
+        ws, p, size = _scratch(ws, size, like, device)
+    if status is not None:
+        status = _need_status(status, device)
+    _run(name, device, xp, wp, b, residual, n, R, C, DTYPE[dtype], act_id, out.data_ptr(), p, size,
+         status)
     return out
 
 
@@ -930,22 +970,30 @@ def gated_linear(x, w13, params: MoeParams, out=None, mx8: bool = False,
     if rows % 2:
         raise ValueError(f"w13 must have an even number of rows, got {rows}")
     I = rows // 2
-    mx = isinstance(x, Mx8)
-    like = x.codes if mx else x
-    if mx8:
-        h = _empty_mx8(n, I, like) if out is None else out
-        _need_mx8(h, "out", device, (n, I))
-    elif out is None:
-        h = torch.empty((n, I), dtype=dtype, device=like.device)
+    if type(x) is Mx8:
+        name, like, xp, wp = "moe_gated_linear_mx8", x.codes, x, w13
     else:
-        h = out
-        _need_on(h, "out", dtype, device, (n, I))
-    ws, p, size = _scratch(ws, gated_linear_workspace_size(n, H, I), like, device)
-    _run("moe_gated_linear_mx8" if mx else "moe_gated_linear", device, x if mx else x.data_ptr(),
-         w13 if mx else w13.data_ptr(), n, H, I, ctypes.byref(params), DTYPE[dtype],
-         None if mx8 else h.data_ptr(), h if mx8 else None, p, size,
-         _need_status(status, device))
-    return h
+        name, like, xp, wp = "moe_gated_linear", x, x.data_ptr(), w13.data_ptr()
+    if mx8:
+        if out is None:
+            out = _empty_mx8(n, I, like, device)
+        else:
+            _need_mx8(out, "out", device, (n, I))
+        hp, h8 = None, out
+    else:
+        if out is None:
+            out = torch.empty((n, I), dtype=dtype, device=like.device)
+        else:
+            _need_on(out, "out", dtype, device, (n, I))
+        hp, h8 = out.data_ptr(), None
+    size = gated_linear_workspace_size(n, H, I)
+    p = None
+    if size or ws is not None:
+        ws, p, size = _scratch(ws, size, like, device)
+    if status is not None:
+        status = _need_status(status, device)
+    _run(name, device, xp, wp, n, H, I, ctypes.byref(params), DTYPE[dtype], hp, h8, p, size, status)
+    return out
 
 
 def gated_linear_backward(d_h: torch.Tensor, x: torch.Tensor, w13: torch.Tensor,
