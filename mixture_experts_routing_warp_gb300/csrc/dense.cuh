@@ -363,14 +363,11 @@ struct DenseProduct {
 };
 
 DensePlan dense_plan(int64_t M, int64_t N, int64_t K, int kind, bool mx);
-cudaError_t launch_dense(const DenseProduct &p, const DensePlan &plan, float *partial,
-                         int32_t *status, cudaStream_t s);
+// blocks and partial: scratch of plan.blocks and plan.partial bytes.
+cudaError_t launch_dense(const DenseProduct &p, const DensePlan &plan, uint8_t *blocks,
+                         float *partial, int32_t *status, cudaStream_t s);
 // The parts of a split sum joined, with the product's epilogue.
 cudaError_t launch_dense_join(const DenseProduct &p, const DensePlan &plan, const float *partial,
                               cudaStream_t s);
-// MXFP8 operands: blocks is scratch for the scales in the tensor core's layout.
-size_t mx8_scale_blocks(const DensePlan &plan, int64_t K);
-cudaError_t launch_dense_mx8(const DenseProduct &p, const DensePlan &plan, uint8_t *blocks,
-                             float *partial, int32_t *status, cudaStream_t s);
 
 }  // namespace moe

@@ -62,12 +62,10 @@ moe_status run_forward(const DenseProduct &p, const DensePlan &plan, void *works
                        size_t workspace_bytes, int32_t *status, moe_stream stream) {
   const moe_status st = check_workspace(workspace, workspace_bytes, forward_bytes(plan));
   if (st != MOE_OK) return st;
-  cudaStream_t s = (cudaStream_t)stream;
-  if (!p.a.scales)
-    return from_cuda(launch_dense(p, plan, static_cast<float *>(workspace), status, s));
-  return from_cuda(launch_dense_mx8(
-      p, plan, static_cast<uint8_t *>(workspace),
-      reinterpret_cast<float *>(at(workspace, align_up(plan.blocks, kAlign))), status, s));
+  return from_cuda(
+      launch_dense(p, plan, static_cast<uint8_t *>(workspace),
+                   reinterpret_cast<float *>(at(workspace, align_up(plan.blocks, kAlign))), status,
+                   (cudaStream_t)stream));
 }
 
 DenseProduct forward_product(const void *x, const void *w, int64_t n, int64_t out, int64_t in,
@@ -329,13 +327,13 @@ moe_status moe_linear_backward(const void *d_y, const void *x, const void *w, co
     p.epi.add = d_y;
     p.epi.out = at(workspace, g.d);
     p.epi.vec = aligned(bias, 16);
-    e = launch_dense(p, g.sums, partial, status, s);
+    e = launch_dense(p, g.sums, nullptr, partial, status, s);
     d = p.epi.out;
   }
   if (e == cudaSuccess && d_x)
-    e = launch_dense(input_gradient(d, w, n, R, C, half, d_x), g.d_x, partial, status, s);
+    e = launch_dense(input_gradient(d, w, n, R, C, half, d_x), g.d_x, nullptr, partial, status, s);
   if (e == cudaSuccess && d_w)
-    e = launch_dense(weight_gradient(d, x, n, R, C, half, d_w), g.d_w, partial, status, s);
+    e = launch_dense(weight_gradient(d, x, n, R, C, half, d_w), g.d_w, nullptr, partial, status, s);
   if (e == cudaSuccess && d_bias)
     e = launch_column_sum(d, n, R, dtype, d_bias, reinterpret_cast<float *>(at(workspace, g.columns)),
                           s);
@@ -418,12 +416,12 @@ moe_status moe_gated_linear_backward(const void *d_h, const void *x, const void 
   p.epi.add = d_h;
   p.epi.out = at(workspace, g.d);
   p.epi.vec = aligned(d_h, 16);
-  cudaError_t e = launch_dense(p, g.sums, partial, status, s);
+  cudaError_t e = launch_dense(p, g.sums, nullptr, partial, status, s);
   const void *d = p.epi.out;
   if (e == cudaSuccess && d_x)
-    e = launch_dense(input_gradient(d, w13, n, out, H, half, d_x), g.d_x, partial, status, s);
+    e = launch_dense(input_gradient(d, w13, n, out, H, half, d_x), g.d_x, nullptr, partial, status, s);
   if (e == cudaSuccess && d_w13)
-    e = launch_dense(weight_gradient(d, x, n, out, H, half, d_w13), g.d_w, partial, status, s);
+    e = launch_dense(weight_gradient(d, x, n, out, H, half, d_w13), g.d_w, nullptr, partial, status, s);
   return from_cuda(e);
 }
 

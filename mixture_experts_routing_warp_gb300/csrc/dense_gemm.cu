@@ -18,6 +18,14 @@
 //               leader's barrier)
 //   warp 1      TMEM allocation; the leader's issues the MMAs
 //   warps 2..   epilogue, two or four per TMEM lane quarter, column chunks in turn
+// MXFP8 operands (moe_linear_mx8, moe_gated_linear_mx8) take the same kernel:
+// E4M3 codes with one power of two per 32 of them, which the tensor core
+// applies itself (kind::mxf8f6f4, block_scale), so nothing is converted and
+// the rate is twice that of bf16. A stage then holds 128 codes of each row and
+// the rows' four scales, which tcgen05.cp spreads into TMEM beside the
+// accumulators (224 columns each, so that both fit). The scales come row by
+// row with C / 32 bytes at no alignment: a small kernel lays them out in the
+// blocks that the copy wants first, x and w together.
 // Where the tiles are fewer than the pairs of SMs can take, the K range is
 // split: parts write fp32 sums and a second kernel adds them in order and
 // applies the epilogue. No atomics: the bits depend on the inputs and sizes.
@@ -51,6 +59,18 @@ constexpr int kMaxStages = 8;
 constexpr int kNumBars = 2 * kMaxStages + 2 + 2 + 1;
 constexpr int kGemmSmem = 1024 + kRingBytes + kNumBars * 8 + 16;
 constexpr int kTmemCols = 512;
+// MXFP8: stages, accumulator columns, and the scales of a stage: blocks of 512
+// bytes (128 rows, 4 scales each; 4 TMEM columns), one of x and two of w.
+constexpr int kMxStages = 5;
+constexpr int kMxTn = 224;
+constexpr int kScaleBlock = 512;
+constexpr int kScaleBytes = 3 * kScaleBlock;
+constexpr int kScaleCols = 12;
+constexpr int kScaleOffset = kRingBytes - kMxStages * kScaleBytes;
+static_assert(2 * kMxTn + kMxStages * kScaleCols <= kTmemCols, "TMEM columns");
+static_assert(kMxStages * (kABytes + kMxTn / 2 * kStepBytes) <= kScaleOffset, "stages and scales");
+static_assert(kScaleOffset % kScaleBlock == 0, "scale blocks");
+constexpr int acc_cols(bool mx) { return mx ? kMxTn : kMaxTn; }
 static_assert(kGemmSmem <= 227 * 1024, "shared memory per CTA");
 
 struct GemmArgs {
@@ -77,6 +97,27 @@ __device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr) {
 
 // Unit u: a tile and its part of the sum. The narrow last tiles come behind
 // all others, to fill what the last wave of whole tiles leaves idle.
+// 512 bytes (32 lines of 16: line l holds the scales of rows l, l + 32, l + 64
+// and l + 96) to 4 TMEM columns of all lane quarters, in both CTAs of the pair
+// from their own shared memory.
+__device__ __forceinline__ void copy_scales_pair(uint32_t tmem, uint32_t saddr) {
+  const uint64_t desc = (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) |
+                        ((uint64_t)1 << 46);
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+               : "memory");
+}
+
+__device__ __forceinline__ void umma_mx8_pair(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc,
+                                              uint32_t sa, uint32_t sb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], "
+      "[%5], p;\n\t}" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+      : "memory");
+}
+
 struct Unit {
   int m, n, s, k_lo, k_hi, tn, b_bytes;
 };
@@ -101,13 +142,16 @@ __device__ __forceinline__ Unit unit_of(int u, const GemmArgs &a) {
   return w;
 }
 
-// AK / BK: the operand is K-major.
-template <bool AK, bool BK, int EPI>
+// AK / BK: the operand is K-major. MX: both are MXFP8.
+template <bool AK, bool BK, int EPI, bool MX>
 __global__ void __launch_bounds__(gemm_threads(EPI), 1)
     dense_gemm_kernel(const __grid_constant__ CUtensorMap map_a,
                       const __grid_constant__ CUtensorMap map_b,
                       const __grid_constant__ CUtensorMap map_b_last,
+                      const __grid_constant__ CUtensorMap map_sa,
+                      const __grid_constant__ CUtensorMap map_sb,
                       const __grid_constant__ GemmArgs args) {
+  constexpr int kStepK = MX ? 128 : 64;  // elements of a K step
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kRingBytes);
@@ -123,6 +167,7 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
   const uint32_t drain_bar = full0 + 8u * (2 * kMaxStages + 4);
   auto a_addr = [&](int s) { return stage0 + (uint32_t)(s * stage_bytes); };
   auto b_addr = [&](int s) { return stage0 + (uint32_t)(s * stage_bytes + kABytes); };
+  auto scale_addr = [&](int s) { return stage0 + (uint32_t)(kScaleOffset + s * kScaleBytes); };
 
   const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -147,6 +192,10 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
     prefetch_tmap(&map_a);
     prefetch_tmap(&map_b);
     prefetch_tmap(&map_b_last);
+    if constexpr (MX) {
+      prefetch_tmap(&map_sa);
+      prefetch_tmap(&map_sb);
+    }
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -172,7 +221,7 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
       const Unit w = unit_of(u, args);
       const int m0 = w.m * 2 * kRowsCta + (int)rank * kRowsCta;
       const int n0 = w.n * tn + (int)rank * (w.tn / 2);
-      const uint32_t tx = 2u * (uint32_t)(kABytes + w.b_bytes);
+      const uint32_t tx = 2u * (uint32_t)(kABytes + w.b_bytes + (MX ? kScaleBytes : 0));
       const CUtensorMap *mb = w.n < args.n_full ? &map_b : &map_b_last;
       for (int kb = w.k_lo; kb < w.k_hi; ++kb) {
         ok = wait_bounded(empty_bar(stage), phase ^ 1u, s_abort, args.status, args.timeout_ns);
@@ -181,7 +230,7 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
         if (elect_one()) {
           const uint32_t fb = map_to_rank(full_bar(stage), 0);
           if (leader) mbar_arrive_expect_tx(full_bar(stage), tx);
-          const int k0 = kb * 64;
+          const int k0 = kb * kStepK;
           if constexpr (AK) {
             tma_load_2d_pair(a_addr(stage), &map_a, fb, k0, m0);
           } else {
@@ -197,6 +246,12 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
             tma_load_2d_pair(b_addr(stage), &map_b, fb, n0, k0);
             if (w.b_bytes > 8192)
               tma_load_2d_pair(b_addr(stage) + 8192u, &map_b, fb, n0 + 64, k0);
+          }
+          if constexpr (MX) {  // x's own rows, w's all: each CTA multiplies every column
+            tma_load_2d_pair(scale_addr(stage), &map_sa, fb, 0,
+                             (w.m * 2 + (int)rank) * args.num_kb + kb);
+            tma_load_2d_pair(scale_addr(stage) + kScaleBlock, &map_sb, fb, 0,
+                             (w.n * args.num_kb + kb) * 2);
           }
         }
         issued = issued < (uint32_t)stages ? issued + 1 : (uint32_t)stages;
@@ -235,7 +290,7 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kMaxTn);
+        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * acc_cols(MX));
         const uint32_t idesc = args.idesc | ((uint32_t)(w.tn >> 3) << 17);
         for (int kb = w.k_lo; kb < w.k_hi; ++kb) {
           ok = wait_bounded(full_bar(stage), phase, s_abort, args.status, args.timeout_ns);
@@ -245,10 +300,24 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
           const uint64_t ad = AK ? sw128_desc(a_addr(stage)) : sw128_desc_mn(a_addr(stage));
           const uint64_t bd = BK ? sw128_desc(b_addr(stage)) : sw128_desc_mn(b_addr(stage));
           if (elect_one()) {
+            if constexpr (MX) {
+              // the columns belong to the stage: the MMAs that read them last
+              // were complete before the stage was filled again
+              const uint32_t sa = tmem_base + 2u * kMxTn + (uint32_t)(stage * kScaleCols);
+              copy_scales_pair(sa, scale_addr(stage));
+              copy_scales_pair(sa + 4u, scale_addr(stage) + kScaleBlock);
+              if (w.tn > 128) copy_scales_pair(sa + 8u, scale_addr(stage) + 2 * kScaleBlock);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_bf16_pair(d_tmem, ad + a_step * kk, bd + b_step * kk, idesc,
-                             kb != w.k_lo || kk != 0);
+              for (uint32_t kk = 0; kk < 4; ++kk)  // the kk-th byte of each scale word
+                umma_mx8_pair(d_tmem, ad + a_step * kk, bd + b_step * kk,
+                              idesc | (kk << 4) | (kk << 29), sa, sa + 4u,
+                              kb != w.k_lo || kk != 0);
+            } else {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_bf16_pair(d_tmem, ad + a_step * kk, bd + b_step * kk, idesc,
+                               kb != w.k_lo || kk != 0);
+            }
             umma_commit_pair(empty_bar(stage), 0x3);
           }
           __syncwarp();
@@ -284,7 +353,7 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
                         args.timeout_ns))
         break;
       tc_fence_after();
-      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kMaxTn);
+      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * acc_cols(MX));
       DenseEpi e = args.e;
       if constexpr (EPI == EPI_PARTIAL) e.out = static_cast<float *>(e.out) + w.s * args.part_stride;
 #pragma unroll 1
@@ -388,10 +457,98 @@ bool map_pairs(CUtensorMap *m, const void *base, int64_t I, int64_t cols, int bo
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool AK, bool BK, int EPI>
-cudaError_t launch_gemm(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &ml,
-                        const GemmArgs &a, cudaStream_t s) {
-  auto kern = dense_gemm_kernel<AK, BK, EPI>;
+// Scale bytes [rows, G] to blocks: one thread per line of a block (four rows'
+// four scales), K steps fastest, so that a warp reads its rows' bytes in a
+// piece. Rows and groups that do not exist get 1 (their codes are zeros).
+struct ScaleLayout {
+  const uint8_t *src;
+  uint8_t *dst;
+  int64_t rows;
+  int tiles, tile_rows, blocks;  // blocks of 128 rows per tile
+  int pairs;                     // tile rows 2i, 2i + 1 are rows i and i + rows / 2
+};
+// Bytes of the widest load that every row's scales allow (4, 2 or 1).
+template <int BYTES>
+__device__ __forceinline__ uint32_t scale_word(const uint8_t *p, int left) {
+  uint32_t word = 0;
+#pragma unroll
+  for (int t = 0; t < 4; t += BYTES) {
+    uint32_t part;
+    if constexpr (BYTES == 4) part = left >= 4 ? __ldg(reinterpret_cast<const uint32_t *>(p)) : 0u;
+    else if constexpr (BYTES == 2)
+      part = t < left ? __ldg(reinterpret_cast<const uint16_t *>(p + t)) : 0x7f7fu;
+    else part = t < left ? __ldg(p + t) : 0x7fu;
+    word |= part << (8 * t);
+  }
+  return word;
+}
+template <int BYTES>
+__global__ void __launch_bounds__(256)
+mx8_layout_kernel(const ScaleLayout a, const ScaleLayout b, int G, int num_kb) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t na = (int64_t)a.tiles * a.blocks * num_kb * 32;
+  const int64_t nb = (int64_t)b.tiles * b.blocks * num_kb * 32;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < na + nb;
+       i += (int64_t)gridDim.x * blockDim.x) {
+    const ScaleLayout &l = i < na ? a : b;
+    const int64_t j = i < na ? i : i - na;  // [tile][block][line][kb]
+    const int64_t lines = j / num_kb;
+    const int kb = (int)(j - lines * num_kb), left = G - kb * 4;
+    const int line = (int)(lines & 31);
+    const int64_t tb = lines >> 5, tile = tb / l.blocks;
+    const int block = (int)(tb - tile * l.blocks);
+    uint32_t word[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int r = block * 128 + q * 32 + line;
+      const int64_t row = tile * l.tile_rows + r;
+      word[q] = 0x7f7f7f7fu;
+      if (r < l.tile_rows && row < l.rows) {
+        const int64_t from = l.pairs ? (row >> 1) + (row & 1) * (l.rows / 2) : row;
+        word[q] = scale_word<BYTES>(l.src + from * G + kb * 4, left);
+      }
+    }
+    reinterpret_cast<uint4 *>(l.dst)[((tile * num_kb + kb) * l.blocks + block) * 32 + line] =
+        make_uint4(word[0], word[1], word[2], word[3]);
+  }
+}
+
+// MXFP8 codes [rows, cols] in boxes of 128 columns; with `pairs` as map_pairs.
+bool map_codes(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int box_rows,
+               bool pairs) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const int64_t I = rows / 2;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, pairs ? 2 : (cuuint64_t)rows, (cuuint64_t)I};
+  cuuint64_t strides[2] = {(cuuint64_t)(pairs ? I * cols : cols), (cuuint64_t)cols};
+  cuuint32_t box[3] = {128, pairs ? 2 : (cuuint32_t)box_rows, (cuuint32_t)(box_rows / 2)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, pairs ? 3 : 2, const_cast<void *>(base), dims,
+             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Scale blocks, `box` of them at a time.
+bool map_blocks(CUtensorMap *m, const void *base, int64_t blocks, int box_blocks) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {kScaleBlock / 4, (cuuint64_t)blocks};
+  cuuint64_t strides[1] = {kScaleBlock};
+  cuuint32_t box[2] = {kScaleBlock / 4, (cuuint32_t)box_blocks};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void *>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct GemmMaps {
+  CUtensorMap a, b, b_last, sa, sb;
+};
+
+template <bool AK, bool BK, int EPI, bool MX = false>
+cudaError_t launch_gemm(const GemmMaps &m, const GemmArgs &a, cudaStream_t s) {
+  auto kern = dense_gemm_kernel<AK, BK, EPI, MX>;
   static PerDeviceOnce once;
   static std::atomic<int> resident[PerDeviceOnce::kMaxDevices] = {};
   cudaLaunchConfig_t cfg = {};
@@ -425,7 +582,7 @@ cudaError_t launch_gemm(const CUtensorMap &ma, const CUtensorMap &mb, const CUte
   int64_t pairs = resident[dev].load(std::memory_order_relaxed);
   if (units < pairs) pairs = units;
   cfg.gridDim = dim3((unsigned)(2 * pairs));
-  err = cudaLaunchKernelEx(&cfg, kern, ma, mb, ml, a);
+  err = cudaLaunchKernelEx(&cfg, kern, m.a, m.b, m.b_last, m.sa, m.sb, a);
   return err != cudaSuccess ? err : cudaGetLastError();
 }
 
@@ -442,47 +599,53 @@ cudaError_t launch_join(const float *part, int64_t stride, int splits, const Den
 }
 
 template <bool AK, bool BK>
-cudaError_t launch_kind(int kind, const CUtensorMap &ma, const CUtensorMap &mb,
-                        const CUtensorMap &ml, const GemmArgs &a, cudaStream_t s) {
+cudaError_t launch_kind(int kind, const GemmMaps &m, const GemmArgs &a, cudaStream_t s) {
   if constexpr (AK && BK) {
     switch (kind) {
-      case EPI_DACT: return launch_gemm<AK, BK, EPI_DACT>(ma, mb, ml, a, s);
-      case EPI_GATED: return launch_gemm<AK, BK, EPI_GATED>(ma, mb, ml, a, s);
-      case EPI_GATED_MX: return launch_gemm<AK, BK, EPI_GATED_MX>(ma, mb, ml, a, s);
-      case EPI_DGATED: return launch_gemm<AK, BK, EPI_DGATED>(ma, mb, ml, a, s);
+      case EPI_DACT: return launch_gemm<AK, BK, EPI_DACT>(m, a, s);
+      case EPI_GATED: return launch_gemm<AK, BK, EPI_GATED>(m, a, s);
+      case EPI_GATED_MX: return launch_gemm<AK, BK, EPI_GATED_MX>(m, a, s);
+      case EPI_DGATED: return launch_gemm<AK, BK, EPI_DGATED>(m, a, s);
     }
   }
-  if (kind == EPI_PARTIAL) return launch_gemm<AK, BK, EPI_PARTIAL>(ma, mb, ml, a, s);
-  return launch_gemm<AK, BK, EPI_LINEAR>(ma, mb, ml, a, s);
+  if (kind == EPI_PARTIAL) return launch_gemm<AK, BK, EPI_PARTIAL>(m, a, s);
+  return launch_gemm<AK, BK, EPI_LINEAR>(m, a, s);
+}
+
+cudaError_t launch_mx(int kind, const GemmMaps &m, const GemmArgs &a, cudaStream_t s) {
+  switch (kind) {
+    case EPI_GATED: return launch_gemm<true, true, EPI_GATED, true>(m, a, s);
+    case EPI_GATED_MX: return launch_gemm<true, true, EPI_GATED_MX, true>(m, a, s);
+    case EPI_PARTIAL: return launch_gemm<true, true, EPI_PARTIAL, true>(m, a, s);
+    default: return launch_gemm<true, true, EPI_LINEAR, true>(m, a, s);
+  }
 }
 
 }  // namespace
 
 // Tile width and number of parts of the sum: the choice with the least
 // estimated time, in SM cycles. A K step of a pair takes 2 cycles per column
-// (256 x tn x 64 products at 8192 per cycle and SM) and no less than its
-// operands' way into shared memory (kIngress bytes per cycle and SM) nor than
-// its issue; a unit costs about kUnit cycles beside its steps; a split costs
-// its partial sums' way through L2 and the joining kernel. MXFP8: single CTAs
-// of 128 rows and steps of 128 codes at twice the rate, the same 2 cycles per
-// column.
+// (256 x tn x 64 products at 8192 per cycle and SM; MXFP8 twice the products at
+// twice the rate) and no less than its operands' way into shared memory
+// (kIngress bytes per cycle and SM) nor than its issue; a unit costs about
+// kUnit cycles beside its steps; a split costs its partial sums' way through
+// L2 and the joining kernel.
 DensePlan dense_plan(int64_t M, int64_t N, int64_t K, int kind, bool mx) {
-  constexpr int kSms = 152;  // the GB300's: a plan does not depend on the device
+  constexpr int kPairs = 76;  // of the GB300's 152 SMs: a plan does not depend on the device
   constexpr double kIngress = 60.0, kIssue = 200.0, kUnit = 800.0;
   DensePlan best{};
   double best_t = 1e300;
   const int gran = kind == EPI_GATED_MX ? 64 : 32;
-  const int workers = mx ? kSms : kSms / 2, rows = mx ? 128 : 256;
-  const int64_t kb = mx ? (K + 127) / 128 : (K + 63) / 64, mt = (M + rows - 1) / rows;
+  const int64_t kb = mx ? (K + 127) / 128 : (K + 63) / 64, mt = (M + 255) / 256;
   auto step = [&](int tn) {
-    const double mma = 2.0 * tn, load = (16384.0 + (mx ? 128.0 : 64.0) * tn) / kIngress;
+    const double mma = 2.0 * tn, load = (16384.0 + (mx ? kScaleBytes : 0) + 64.0 * tn) / kIngress;
     const double t = mma > load ? mma : load;
     return t > kIssue ? t : kIssue;
   };
 #ifdef DENSE_TUNE
   const char *env_tn = getenv("DENSE_TN"), *env_s = getenv("DENSE_SPLIT");
 #endif
-  for (int tn = mx ? 192 : kMaxTn; tn >= 64; tn -= gran) {
+  for (int tn = acc_cols(mx) / gran * gran; tn >= 64; tn -= gran) {
 #ifdef DENSE_TUNE
     if (env_tn && atoi(env_tn) != tn) continue;
 #endif
@@ -493,19 +656,19 @@ DensePlan dense_plan(int64_t M, int64_t N, int64_t K, int kind, bool mx) {
 #ifdef DENSE_TUNE
       if (env_s && atoi(env_s) != s) continue;
 #endif
-      if (s > 1 && (kb / s < 4 || mt * nt * s > 2 * workers)) break;
+      if (s > 1 && (kb / s < 4 || mt * nt * s > 2 * kPairs)) break;
       const double steps = (double)((kb + s - 1) / s);
       // whole tiles in waves, the narrow ones in the room that the last leaves
-      const int64_t full = mt * nf * s, waves = (full + workers - 1) / workers;
-      int64_t narrow = (nt - nf) * mt * s - (waves * workers - full);
+      const int64_t full = mt * nf * s, waves = (full + kPairs - 1) / kPairs;
+      int64_t narrow = (nt - nf) * mt * s - (waves * kPairs - full);
       if (narrow < 0) narrow = 0;
       double t = (double)waves * (steps * step(tn) + kUnit) +
-                 (double)((narrow + workers - 1) / workers) * (steps * step(last) + kUnit);
+                 (double)((narrow + kPairs - 1) / kPairs) * (steps * step(last) + kUnit);
       if (s > 1) t += 5000.0 + (double)M * N * 4.0 * (s + 1) / 2500.0;
       if (t < best_t) {
         best_t = t;
         best.tn = tn;
-        best.tn_last = mx ? tn : last;
+        best.tn_last = last;
         best.m_tiles = (int)mt;
         best.n_tiles = (int)nt;
         best.splits = s;
@@ -513,33 +676,24 @@ DensePlan dense_plan(int64_t M, int64_t N, int64_t K, int kind, bool mx) {
     }
   }
   best.partial = best.splits > 1 ? (size_t)M * N * 4 * best.splits : 0;
-  best.blocks = mx ? mx8_scale_blocks(best, K) : 0;
+  best.blocks = mx ? (size_t)kb * kScaleBlock * 2 * ((size_t)best.m_tiles + (size_t)best.n_tiles) : 0;
 #ifdef DENSE_TUNE
   if (getenv("DENSE_SHOW")) fprintf(stderr, "plan M %ld N %ld K %ld: tn %d last %d splits %d tiles %dx%d est %.0f\n", (long)M, (long)N, (long)K, best.tn, best.tn_last, best.splits, best.m_tiles, best.n_tiles, best_t);
 #endif
   return best;
 }
 
-cudaError_t launch_dense(const DenseProduct &p, const DensePlan &plan, float *partial,
-                         int32_t *status, cudaStream_t s) {
-  CUtensorMap ma, mb, ml;
+cudaError_t launch_dense(const DenseProduct &p, const DensePlan &plan, uint8_t *blocks,
+                         float *partial, int32_t *status, cudaStream_t s) {
+  GemmMaps m;
   const int tn = plan.tn;
-  const bool ak = p.a.k_major, bk = p.b.k_major;
-  bool ok = ak ? map_rows(&ma, p.a.p, p.M, p.K, kRowsCta) : map_rows(&ma, p.a.p, p.K, p.M, 64);
-  auto map_b = [&](CUtensorMap *m, int cols) {
-    if (p.b.pairs) return map_pairs(m, p.b.p, p.N / 2, p.K, cols / 4);
-    return bk ? map_rows(m, p.b.p, p.N, p.K, cols / 2) : map_rows(m, p.b.p, p.K, p.N, 64);
-  };
-  ok = ok && map_b(&mb, tn);
-  ml = mb;
-  if (plan.tn_last != tn) ok = ok && map_b(&ml, plan.tn_last);
-  if (!ok) return cudaErrorInvalidValue;
+  const bool ak = p.a.k_major, bk = p.b.k_major, mx = p.a.scales != nullptr;
   GemmArgs a{};
   a.e = p.epi;
   a.m_tiles = plan.m_tiles;
   a.n_tiles = plan.n_tiles;
   a.splits = plan.splits;
-  a.num_kb = (int)((p.K + 63) / 64);
+  a.num_kb = (int)((p.K + (mx ? 127 : 63)) / (mx ? 128 : 64));
   a.tn = tn;
   auto b_bytes = [&](int cols) { return bk ? cols / 2 * kStepBytes : (cols / 2 + 63) / 64 * 8192; };
   a.b_bytes = b_bytes(tn);
@@ -547,22 +701,61 @@ cudaError_t launch_dense(const DenseProduct &p, const DensePlan &plan, float *pa
   a.b_bytes_last = b_bytes(plan.tn_last);
   a.n_full = plan.tn_last == tn ? plan.n_tiles : plan.n_tiles - 1;
   a.stages = kRingBytes / (kABytes + a.b_bytes);
-  if (a.stages > kMaxStages) a.stages = kMaxStages;
+  const int most = mx ? kMxStages : kMaxStages;
+  if (a.stages > most) a.stages = most;
   a.pairs = p.b.pairs;
-  const uint32_t type = p.epi.half ? 0u : 1u;  // fp16 / bf16
-  a.idesc = (1u << 4) | (type << 7) | (type << 10) | ((ak ? 0u : 1u) << 15) |
-            ((bk ? 0u : 1u) << 16) | ((uint32_t)(256 >> 4) << 24);
   a.status = reinterpret_cast<uint32_t *>(status);
   a.timeout_ns = kWaitTimeoutNs;
+
+  auto map_b = [&](CUtensorMap *t, int cols) {
+    if (mx) return map_codes(t, p.b.p, p.N, p.K, cols / 2, p.b.pairs);
+    if (p.b.pairs) return map_pairs(t, p.b.p, p.N / 2, p.K, cols / 4);
+    return bk ? map_rows(t, p.b.p, p.N, p.K, cols / 2) : map_rows(t, p.b.p, p.K, p.N, 64);
+  };
+  bool ok = mx   ? map_codes(&m.a, p.a.p, p.M, p.K, kRowsCta, false)
+            : ak ? map_rows(&m.a, p.a.p, p.M, p.K, kRowsCta)
+                 : map_rows(&m.a, p.a.p, p.K, p.M, 64);
+  ok = ok && map_b(&m.b, tn);
+  m.b_last = m.b;
+  if (plan.tn_last != tn) ok = ok && map_b(&m.b_last, plan.tn_last);
+  m.sa = m.sb = m.a;
+  if (mx) {
+    // scale type E8M0 (bit 23); both codes E4M3
+    a.idesc = (1u << 23) | ((uint32_t)(256 >> 4) << 24);
+    const int64_t a_blocks = (int64_t)2 * plan.m_tiles * a.num_kb;
+    const int64_t b_blocks = (int64_t)2 * plan.n_tiles * a.num_kb;
+    uint8_t *sb = blocks + a_blocks * kScaleBlock;
+    ok = ok && map_blocks(&m.sa, blocks, a_blocks, 1) && map_blocks(&m.sb, sb, b_blocks, 2);
+    if (!ok) return cudaErrorInvalidValue;
+    const ScaleLayout la{p.a.scales, blocks, p.M, 2 * plan.m_tiles, kRowsCta, 1, 0};
+    const ScaleLayout lb{p.b.scales, sb, p.N, plan.n_tiles, tn, 2, p.b.pairs};
+    int64_t grid = ((a_blocks + b_blocks) * 32 + 255) / 256;
+    const int64_t cap = (int64_t)device_sm_count() * 8;
+    if (grid > cap) grid = cap;
+    const int G = (int)(p.K / 32);
+    const uintptr_t bits = (uintptr_t)p.a.scales | (uintptr_t)p.b.scales | (uintptr_t)G;
+    const cudaError_t err =
+        launch_dependent(bits % 4 == 0   ? mx8_layout_kernel<4>
+                         : bits % 2 == 0 ? mx8_layout_kernel<2>
+                                         : mx8_layout_kernel<1>,
+                         dim3((unsigned)grid), dim3(256), 0, s, la, lb, G, a.num_kb);
+    if (err != cudaSuccess) return err;
+  } else {
+    const uint32_t type = p.epi.half ? 0u : 1u;  // fp16 / bf16
+    a.idesc = (1u << 4) | (type << 7) | (type << 10) | ((ak ? 0u : 1u) << 15) |
+              ((bk ? 0u : 1u) << 16) | ((uint32_t)(256 >> 4) << 24);
+  }
+  if (!ok) return cudaErrorInvalidValue;
   int kind = p.kind;
   if (plan.splits > 1) {
     kind = EPI_PARTIAL;
     a.e.out = partial;
     a.part_stride = p.M * p.N;
   }
-  cudaError_t err = ak && bk ? launch_kind<true, true>(kind, ma, mb, ml, a, s)
-                    : ak     ? launch_kind<true, false>(kind, ma, mb, ml, a, s)
-                             : launch_kind<false, false>(kind, ma, mb, ml, a, s);
+  const cudaError_t err = mx         ? launch_mx(kind, m, a, s)
+                          : ak && bk ? launch_kind<true, true>(kind, m, a, s)
+                          : ak       ? launch_kind<true, false>(kind, m, a, s)
+                                     : launch_kind<false, false>(kind, m, a, s);
   return err != cudaSuccess || plan.splits == 1 ? err : launch_dense_join(p, plan, partial, s);
 }
 
