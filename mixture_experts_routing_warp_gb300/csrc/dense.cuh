@@ -18,7 +18,8 @@ enum DenseKind {
   EPI_GATED = 2,     // a holds (gate, up) pairs: out = h
   EPI_GATED_MX = 3,  // the same, h as E4M3 codes with a scale per 32
   EPI_DGATED = 4,    // (gate, up) pairs and add = d_h: out = (d_gate, d_up) in w13's row order
-  EPI_PARTIAL = 5    // out = a in fp32, to be joined with the other parts of a split sum
+  EPI_PARTIAL = 5,   // fp32 parts of a split sum, whose joining kernel has the epilogue
+  EPI_GRAD = 6       // out = a (of two products at a time), or the same parts
 };
 
 struct DenseEpi {
@@ -31,6 +32,7 @@ struct DenseEpi {
   const void *add;     // [rows, cols] (EPI_DGATED: [rows, cols / 2]) or null
   void *out;           // [rows, cols] (EPI_GATED: [rows, cols / 2])
   uint8_t *codes, *scales;  // EPI_GATED_MX
+  float *column_part;  // EPI_DACT: [rows / 32, cols] sums of out before its rounding, or null
   int vec;             // every row of bias, add and out starts on 16 bytes
 };
 
@@ -308,17 +310,24 @@ __device__ __forceinline__ void dense_epilogue(const DenseEpi &e, int64_t row, i
         gated_backward(v[2 * i], v[2 * i + 1], d[i], e.gate, v[2 * i], v[2 * i + 1]);
       store_row<W>(e.out, row * e.cols + c, e.vec, left, e.half, v);
     }
+  } else if constexpr (EPI == EPI_GRAD) {
+    store_row<W>(e.out, row * e.cols + c, e.vec, left, e.half, v);
+  }
+}
+
+// W fp32 sums of a part [., cols].
+template <int W>
+__device__ __forceinline__ void store_partial(float *part, int64_t row, int c, int cols,
+                                              const float (&v)[W]) {
+  float *p = part + row * cols + c;
+  if (c + W <= cols && cols % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < W; i += 4)
+      *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
   } else {
-    float *p = static_cast<float *>(e.out) + row * e.cols + c;
-    if (left >= W && e.cols % 4 == 0) {
 #pragma unroll
-      for (int i = 0; i < W; i += 4)
-        *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < W; ++i)
-        if (i < left) p[i] = v[i];
-    }
+    for (int i = 0; i < W; ++i)
+      if (c + i < cols) p[i] = v[i];
   }
 }
 
@@ -366,8 +375,15 @@ DensePlan dense_plan(int64_t M, int64_t N, int64_t K, int kind, bool mx);
 // blocks and partial: scratch of plan.blocks and plan.partial bytes.
 cudaError_t launch_dense(const DenseProduct &p, const DensePlan &plan, uint8_t *blocks,
                          float *partial, int32_t *status, cudaStream_t s);
-// The parts of a split sum joined, with the product's epilogue.
-cudaError_t launch_dense_join(const DenseProduct &p, const DensePlan &plan, const float *partial,
-                              cudaStream_t s);
+// Plans of two gradients that go in one launch.
+void dense_plan_two(int64_t M0, int64_t N0, int64_t K0, int64_t M1, int64_t N1, int64_t K1,
+                    DensePlan *plan0, DensePlan *plan1);
+// One or two gradients (EPI_LINEAR without bias, activation or addend; B
+// stored along its rows) in one launch, which with column_out also adds up the
+// rows of column_part [column_rows, columns].
+cudaError_t launch_dense_gradients(const DenseProduct *const *p, const DensePlan *const *plan,
+                                   float *const *partial, int count, const float *column_part,
+                                   int column_rows, int columns, int half, void *column_out,
+                                   int32_t *status, cudaStream_t s);
 
 }  // namespace moe

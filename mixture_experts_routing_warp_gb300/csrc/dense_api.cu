@@ -122,25 +122,53 @@ DenseProduct weight_gradient(const void *d, const void *x, int64_t n, int64_t ou
 // the caller's), the parts of split sums, the column sums' scratch.
 struct GradLayout {
   DensePlan sums, d_x, d_w;  // of the recomputed sums and of both gradients
-  size_t d, partial, columns, total;
+  size_t d, partial, partial_w, columns, total;
 };
 GradLayout grad_layout(int64_t n, int64_t out, int64_t in, int kind, bool own_d, bool columns) {
   GradLayout g{};
-  size_t most = 0;
-  auto need = [&](const DensePlan &p) { most = p.partial > most ? p.partial : most; };
-  if (own_d) {
-    g.sums = dense_plan(n, out, in, kind, false);
-    need(g.sums);
-  }
-  g.d_x = dense_plan(n, in, out, EPI_LINEAR, false);
-  g.d_w = dense_plan(out, in, n, EPI_LINEAR, false);
-  need(g.d_x);
-  need(g.d_w);
-  g.d = 0;
+  if (own_d) g.sums = dense_plan(n, out, in, kind, false);
+  dense_plan_two(n, in, out, out, in, n, &g.d_x, &g.d_w);
   g.partial = own_d ? align_up((size_t)n * out * 2, kAlign) : 0;
-  g.columns = g.partial + align_up(most, kAlign);
-  g.total = g.columns + (columns ? align_up(column_sum_scratch((int)out), kAlign) : 0);
+  g.partial_w = g.partial + align_up(g.d_x.partial, kAlign);
+  const size_t both = g.partial_w + align_up(g.d_w.partial, kAlign);
+  const size_t first = g.partial + align_up(g.sums.partial, kAlign);
+  g.columns = both > first ? both : first;
+  const int64_t rows = (n + 31) / 32;
+  const size_t sums = (size_t)rows * out * 4, other = column_sum_scratch((int)out);
+  g.total = g.columns + (columns ? align_up(sums > other ? sums : other, kAlign) : 0);
   return g;
+}
+
+// d_x and d_w of d, each where it is wanted; with column_rows, d_bias from
+// the column sums that d's epilogue left, in the same launch.
+cudaError_t run_gradients(const void *d, const void *x, const void *w, int64_t n, int64_t out,
+                          int64_t in, int half, void *d_x, void *d_w, const GradLayout &g,
+                          void *workspace, int column_rows, void *d_bias, int32_t *status,
+                          cudaStream_t s) {
+  const DenseProduct px = input_gradient(d, w, n, out, in, half, d_x);
+  const DenseProduct pw = weight_gradient(d, x, n, out, in, half, d_w);
+  const DenseProduct *p[2];
+  const DensePlan *plan[2];
+  float *part[2];
+  int count = 0;
+  if (d_x) {
+    p[count] = &px;
+    plan[count] = &g.d_x;
+    part[count++] = reinterpret_cast<float *>(at(workspace, g.partial));
+  }
+  if (d_w) {
+    p[count] = &pw;
+    plan[count] = &g.d_w;
+    part[count++] = reinterpret_cast<float *>(at(workspace, g.partial_w));
+  }
+  const float *columns = reinterpret_cast<const float *>(at(workspace, g.columns));
+  void *joined = column_rows ? d_bias : nullptr;
+  if (count == 0)
+    return joined ? launch_column_join(columns, column_rows, (int)out, half ? MOE_FP16 : MOE_BF16,
+                                       joined, s)
+                  : cudaSuccess;
+  return launch_dense_gradients(p, plan, part, count, columns, column_rows, (int)out, half, joined,
+                                status, s);
 }
 
 moe_status run_linear(const void *x, const uint8_t *x_scales, const void *w,
@@ -316,8 +344,8 @@ moe_status moe_linear_backward(const void *d_y, const void *x, const void *w, co
   const GradLayout g = grad_layout(n, R, C, EPI_DACT, own_d, true);
   if ((st = check_workspace(workspace, workspace_bytes, g.total)) != MOE_OK) return st;
   const int half = dtype == MOE_FP16;
-  float *partial = reinterpret_cast<float *>(at(workspace, g.partial));
   const void *d = d_y;
+  int column_rows = 0;
   cudaError_t e = cudaSuccess;
   if (own_d) {
     DenseProduct p = forward_product(x, w, n, R, C, EPI_DACT);
@@ -327,16 +355,20 @@ moe_status moe_linear_backward(const void *d_y, const void *x, const void *w, co
     p.epi.add = d_y;
     p.epi.out = at(workspace, g.d);
     p.epi.vec = aligned(bias, 16);
-    e = launch_dense(p, g.sums, nullptr, partial, status, s);
+    if (d_bias && g.sums.splits == 1) {
+      p.epi.column_part = reinterpret_cast<float *>(at(workspace, g.columns));
+      column_rows = (int)((n + 31) / 32);
+    }
+    e = launch_dense(p, g.sums, nullptr, reinterpret_cast<float *>(at(workspace, g.partial)),
+                     status, s);
     d = p.epi.out;
   }
-  if (e == cudaSuccess && d_x)
-    e = launch_dense(input_gradient(d, w, n, R, C, half, d_x), g.d_x, nullptr, partial, status, s);
-  if (e == cudaSuccess && d_w)
-    e = launch_dense(weight_gradient(d, x, n, R, C, half, d_w), g.d_w, nullptr, partial, status, s);
-  if (e == cudaSuccess && d_bias)
-    e = launch_column_sum(d, n, R, dtype, d_bias, reinterpret_cast<float *>(at(workspace, g.columns)),
-                          s);
+  if (e == cudaSuccess && d_bias && !column_rows)
+    e = launch_column_sum(d, n, R, dtype, d_bias,
+                          reinterpret_cast<float *>(at(workspace, g.columns)), s);
+  if (e == cudaSuccess)
+    e = run_gradients(d, x, w, n, R, C, half, d_x, d_w, g, workspace, column_rows, d_bias, status,
+                      s);
   return from_cuda(e);
 }
 
@@ -408,7 +440,6 @@ moe_status moe_gated_linear_backward(const void *d_h, const void *x, const void 
   const GradLayout g = grad_layout(n, out, H, EPI_DGATED, true, false);
   if ((st = check_workspace(workspace, workspace_bytes, g.total)) != MOE_OK) return st;
   const int half = dtype == MOE_FP16;
-  float *partial = reinterpret_cast<float *>(at(workspace, g.partial));
   DenseProduct p = forward_product(x, w13, n, out, H, EPI_DGATED);
   p.b.pairs = act.layout == MOE_W13_PACKED;
   p.epi.half = half;
@@ -416,12 +447,12 @@ moe_status moe_gated_linear_backward(const void *d_h, const void *x, const void 
   p.epi.add = d_h;
   p.epi.out = at(workspace, g.d);
   p.epi.vec = aligned(d_h, 16);
-  cudaError_t e = launch_dense(p, g.sums, nullptr, partial, status, s);
-  const void *d = p.epi.out;
-  if (e == cudaSuccess && d_x)
-    e = launch_dense(input_gradient(d, w13, n, out, H, half, d_x), g.d_x, nullptr, partial, status, s);
-  if (e == cudaSuccess && d_w13)
-    e = launch_dense(weight_gradient(d, x, n, out, H, half, d_w13), g.d_w, nullptr, partial, status, s);
+  if (!d_x && !d_w13) return MOE_OK;
+  cudaError_t e = launch_dense(p, g.sums, nullptr,
+                               reinterpret_cast<float *>(at(workspace, g.partial)), status, s);
+  if (e == cudaSuccess)
+    e = run_gradients(p.epi.out, x, w13, n, out, H, half, d_x, d_w13, g, workspace, 0, nullptr,
+                      status, s);
   return from_cuda(e);
 }
 

@@ -7,6 +7,7 @@
 //   forward   a   = x W^T      A = x [n, C],    B = W [R, C]      both K-major
 //   d_x       dx  = d_a W      A = d_a [n, R],  B = W [R, C]      B N-major
 //   d_w       dw  = d_a^T x    A = d_a [n, R],  B = x [n, C]      both M/N-major
+// (the two gradients in one launch, which also adds up a bias's gradient)
 // and an epilogue on the sums while they are in registers (dense.cuh): bias,
 // activation and residual; the gated product; the gradients of either.
 //
@@ -32,10 +33,6 @@
 // Every mbarrier wait is bounded.
 #include "dense.cuh"
 #include "tc_ptx.cuh"
-#ifdef DENSE_TUNE
-#include <stdio.h>
-#include <stdlib.h>
-#endif
 
 namespace moe {
 namespace {
@@ -49,10 +46,7 @@ constexpr int kMaxTn = 256;
 // Epilogue warps, two or four per TMEM lane quarter: with four a tile's
 // epilogue has the latency of two column chunks; a group of 32 8-bit results
 // takes 64 columns and twice the registers.
-#ifndef EPI_WARPS
-#define EPI_WARPS 16
-#endif
-constexpr int epi_warps(int epi) { return epi == EPI_GATED_MX ? 8 : EPI_WARPS; }
+constexpr int epi_warps(int epi) { return epi == EPI_GATED_MX ? 8 : 16; }
 constexpr int gemm_threads(int epi) { return (2 + epi_warps(epi)) * 32; }
 constexpr int kRingBytes = 220 * 1024;
 constexpr int kMaxStages = 8;
@@ -73,17 +67,41 @@ static_assert(kScaleOffset % kScaleBlock == 0, "scale blocks");
 constexpr int acc_cols(bool mx) { return mx ? kMxTn : kMaxTn; }
 static_assert(kGemmSmem <= 227 * 1024, "shared memory per CTA");
 
-struct GemmArgs {
+// One product. Gradients come two at a time.
+struct GemmProblem {
   DenseEpi e;
   int64_t part_stride;  // floats between the parts of a split sum
   int m_tiles, n_tiles, splits;
   int num_kb;           // K steps of the whole sum
-  int tn, stages, b_bytes;
+  int tn, b_bytes;      // columns of a tile, B bytes per CTA and stage
   int tn_last, b_bytes_last, n_full;  // the last tile of a row of tiles, if narrower
-  int pairs;            // B rows come interleaved through a 3-D map
+  int a_k_major, partial;             // gradients: how A is stored; fp32 parts of a split sum
+  int units;            // tiles x parts
   uint32_t idesc;
+};
+
+// Sums over the rows of part [rows, cols], for the epilogue warps to make while
+// the first products run (a bias's gradient).
+struct ColumnJoin {
+  const float *part;
+  void *out;  // null: none
+  int rows, cols, half;
+};
+
+struct GemmArgs {
+  GemmProblem p[2];
+  ColumnJoin join;
+  int stages, stage_bytes;
+  int pairs;  // B rows come interleaved through a 3-D map
   uint32_t *status;
   unsigned long long timeout_ns;
+};
+
+// Tensor maps of a launch: A, B, B of narrow last tiles, scale blocks of A and
+// of B; or A and B of two gradients.
+enum { kMapA = 0, kMapB = 1, kMapBLast = 2, kMapSa = 3, kMapSb = 4, kMaps = 5 };
+struct GemmMaps {
+  CUtensorMap m[kMaps];
 };
 
 // Shared-memory descriptor of an operand stored along its rows (M/N-major),
@@ -95,8 +113,6 @@ __device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr) {
          ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-// Unit u: a tile and its part of the sum. The narrow last tiles come behind
-// all others, to fill what the last wave of whole tiles leaves idle.
 // 512 bytes (32 lines of 16: line l holds the scales of rows l, l + 32, l + 64
 // and l + 96) to 4 TMEM columns of all lane quarters, in both CTAs of the pair
 // from their own shared memory.
@@ -118,11 +134,17 @@ __device__ __forceinline__ void umma_mx8_pair(uint32_t d, uint64_t ad, uint64_t 
       : "memory");
 }
 
+// Unit u: a tile of a product and its part of the sum. The narrow last tiles
+// come behind all others, to fill what the last wave of whole tiles leaves.
 struct Unit {
-  int m, n, s, k_lo, k_hi, tn, b_bytes;
+  int p, m, n, s, k_lo, k_hi, tn, b_bytes;
 };
-__device__ __forceinline__ Unit unit_of(int u, const GemmArgs &a) {
+template <bool GRAD>
+__device__ __forceinline__ Unit unit_of(int u, const GemmArgs &args) {
   Unit w;
+  w.p = GRAD && u >= args.p[0].units ? 1 : 0;
+  const GemmProblem &a = args.p[w.p];
+  if (w.p) u -= args.p[0].units;
   const int tiles = a.m_tiles * a.n_tiles, full = a.m_tiles * a.n_full;
   w.s = u / tiles;
   const int t = u - w.s * tiles;
@@ -142,16 +164,53 @@ __device__ __forceinline__ Unit unit_of(int u, const GemmArgs &a) {
   return w;
 }
 
-// AK / BK: the operand is K-major. MX: both are MXFP8.
-template <bool AK, bool BK, int EPI, bool MX>
+// Sums of 32 columns over the 32 lanes: lane l gets that of v[l]. Each step
+// halves the columns a lane holds.
+__device__ __forceinline__ float column_sums(float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int h = 16; h > 0; h >>= 1)
+#pragma unroll
+    for (int i = 0; i < h; ++i) {
+      const float send = lane & h ? v[i] : v[i + h], keep = lane & h ? v[i + h] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, h);
+    }
+  return v[0];
+}
+
+// The epilogue warps' share of a ColumnJoin: 32 columns per CTA at a time, one
+// row per warp, then over the warps.
+template <int WARPS>
+__device__ __forceinline__ void join_columns(const ColumnJoin &j, int warp, int lane,
+                                             float (*s_sum)[33]) {
+  for (int c0 = (int)blockIdx.x * 32; c0 < j.cols; c0 += (int)gridDim.x * 32) {
+    float acc = 0.f;
+    if (c0 + lane < j.cols) {
+#pragma unroll 8
+      for (int r = warp; r < j.rows; r += WARPS)
+        acc += __ldcg(j.part + (int64_t)r * j.cols + c0 + lane);
+    }
+    s_sum[warp][lane] = acc;
+    asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
+    if (warp == 0 && c0 + lane < j.cols) {
+      acc = 0.f;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) acc += s_sum[w][lane];
+      static_cast<uint16_t *>(j.out)[c0 + lane] = to16(acc, j.half);
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
+  }
+}
+
+// GRAD: up to two gradients, B stored along its rows, A either way; else both
+// operands K-major. MX: both are MXFP8.
+template <bool GRAD, int EPI, bool MX>
 __global__ void __launch_bounds__(gemm_threads(EPI), 1)
-    dense_gemm_kernel(const __grid_constant__ CUtensorMap map_a,
-                      const __grid_constant__ CUtensorMap map_b,
-                      const __grid_constant__ CUtensorMap map_b_last,
-                      const __grid_constant__ CUtensorMap map_sa,
-                      const __grid_constant__ CUtensorMap map_sb,
+    dense_gemm_kernel(const __grid_constant__ GemmMaps maps,
                       const __grid_constant__ GemmArgs args) {
+  static_assert(GRAD == (EPI == EPI_GRAD), "gradients have an epilogue of their own");
   constexpr int kStepK = MX ? 128 : 64;  // elements of a K step
+  __shared__ float s_join[GRAD ? epi_warps(EPI) : 1][33];
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kRingBytes);
@@ -159,7 +218,7 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
   volatile int *s_abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
   const uint32_t stage0 = smem_u32(smem), full0 = smem_u32(bars);
-  const int stages = args.stages, stage_bytes = kABytes + args.b_bytes;
+  const int stages = args.stages, stage_bytes = args.stage_bytes;
   auto full_bar = [&](int s) { return full0 + 8u * s; };
   auto empty_bar = [&](int s) { return full0 + 8u * (kMaxStages + s); };
   auto tfull_bar = [&](int b) { return full0 + 8u * (2 * kMaxStages + b); };
@@ -173,8 +232,7 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
   const int first = (int)(blockIdx.x >> 1), step = (int)(gridDim.x >> 1);
-  const int total = args.m_tiles * args.n_tiles * args.splits;
-  const int tn = args.tn;
+  const int total = args.p[0].units + (GRAD ? args.p[1].units : 0);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -189,13 +247,8 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
     *s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    prefetch_tmap(&map_a);
-    prefetch_tmap(&map_b);
-    prefetch_tmap(&map_b_last);
-    if constexpr (MX) {
-      prefetch_tmap(&map_sa);
-      prefetch_tmap(&map_sb);
-    }
+    prefetch_tmap(&maps.m[kMapA]);
+    prefetch_tmap(&maps.m[kMapB]);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -218,11 +271,15 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
     uint32_t phase = 0, issued = 0;
     bool ok = true;
     for (int u = first; ok && u < total; u += step) {
-      const Unit w = unit_of(u, args);
+      const Unit w = unit_of<GRAD>(u, args);
+      const GemmProblem &p = args.p[w.p];
       const int m0 = w.m * 2 * kRowsCta + (int)rank * kRowsCta;
-      const int n0 = w.n * tn + (int)rank * (w.tn / 2);
+      const int n0 = w.n * p.tn + (int)rank * (w.tn / 2);
       const uint32_t tx = 2u * (uint32_t)(kABytes + w.b_bytes + (MX ? kScaleBytes : 0));
-      const CUtensorMap *mb = w.n < args.n_full ? &map_b : &map_b_last;
+      const CUtensorMap *ma = &maps.m[2 * w.p + kMapA];
+      const CUtensorMap *mb = GRAD              ? &maps.m[2 * w.p + kMapB]
+                              : w.n < p.n_full ? &maps.m[kMapB]
+                                               : &maps.m[kMapBLast];
       for (int kb = w.k_lo; kb < w.k_hi; ++kb) {
         ok = wait_bounded(empty_bar(stage), phase ^ 1u, s_abort, args.status, args.timeout_ns);
         ok = __all_sync(0xffffffffu, ok);
@@ -231,27 +288,26 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
           const uint32_t fb = map_to_rank(full_bar(stage), 0);
           if (leader) mbar_arrive_expect_tx(full_bar(stage), tx);
           const int k0 = kb * kStepK;
-          if constexpr (AK) {
-            tma_load_2d_pair(a_addr(stage), &map_a, fb, k0, m0);
+          if (!GRAD || p.a_k_major) {
+            tma_load_2d_pair(a_addr(stage), ma, fb, k0, m0);
           } else {
-            tma_load_2d_pair(a_addr(stage), &map_a, fb, m0, k0);
-            tma_load_2d_pair(a_addr(stage) + 8192u, &map_a, fb, m0 + 64, k0);
+            tma_load_2d_pair(a_addr(stage), ma, fb, m0, k0);
+            tma_load_2d_pair(a_addr(stage) + 8192u, ma, fb, m0 + 64, k0);
           }
-          if constexpr (BK) {
-            if (args.pairs)
-              tma_load_3d_pair(b_addr(stage), mb, fb, k0, 0, n0 / 2);
-            else
-              tma_load_2d_pair(b_addr(stage), mb, fb, k0, n0);
-          } else {
-            tma_load_2d_pair(b_addr(stage), &map_b, fb, n0, k0);
+          if constexpr (GRAD) {
+            tma_load_2d_pair(b_addr(stage), mb, fb, n0, k0);
             if (w.b_bytes > 8192)
-              tma_load_2d_pair(b_addr(stage) + 8192u, &map_b, fb, n0 + 64, k0);
+              tma_load_2d_pair(b_addr(stage) + 8192u, mb, fb, n0 + 64, k0);
+          } else if (args.pairs) {
+            tma_load_3d_pair(b_addr(stage), mb, fb, k0, 0, n0 / 2);
+          } else {
+            tma_load_2d_pair(b_addr(stage), mb, fb, k0, n0);
           }
           if constexpr (MX) {  // x's own rows, w's all: each CTA multiplies every column
-            tma_load_2d_pair(scale_addr(stage), &map_sa, fb, 0,
-                             (w.m * 2 + (int)rank) * args.num_kb + kb);
-            tma_load_2d_pair(scale_addr(stage) + kScaleBlock, &map_sb, fb, 0,
-                             (w.n * args.num_kb + kb) * 2);
+            tma_load_2d_pair(scale_addr(stage), &maps.m[kMapSa], fb, 0,
+                             (w.m * 2 + (int)rank) * p.num_kb + kb);
+            tma_load_2d_pair(scale_addr(stage) + kScaleBlock, &maps.m[kMapSb], fb, 0,
+                             (w.n * p.num_kb + kb) * 2);
           }
         }
         issued = issued < (uint32_t)stages ? issued + 1 : (uint32_t)stages;
@@ -277,13 +333,16 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
   } else if (warp == 1) {
     // --------------------------------------------- MMA issuer (the leader) --
     if (leader) {
-      // descriptor steps (16-byte units) between the four MMAs of a stage
-      constexpr uint32_t a_step = AK ? 2u : 128u, b_step = BK ? 2u : 128u;
       int stage = 0, local = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int u = first; ok && u < total; u += step, ++local) {
-        const Unit w = unit_of(u, args);
+        const Unit w = unit_of<GRAD>(u, args);
+        const GemmProblem &p = args.p[w.p];
+        const bool a_k = !GRAD || p.a_k_major;
+        // descriptor steps (16-byte units) between the four MMAs of a stage
+        const uint32_t a_step = a_k ? 2u : 128u;
+        constexpr uint32_t b_step = GRAD ? 128u : 2u;
         const int acc = local & 1;
         ok = wait_bounded(tempty_bar(acc), ((uint32_t)(local >> 1) & 1u) ^ 1u, s_abort,
                           args.status, args.timeout_ns);
@@ -291,14 +350,14 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
         if (!ok) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * acc_cols(MX));
-        const uint32_t idesc = args.idesc | ((uint32_t)(w.tn >> 3) << 17);
+        const uint32_t idesc = p.idesc | ((uint32_t)(w.tn >> 3) << 17);
         for (int kb = w.k_lo; kb < w.k_hi; ++kb) {
           ok = wait_bounded(full_bar(stage), phase, s_abort, args.status, args.timeout_ns);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t ad = AK ? sw128_desc(a_addr(stage)) : sw128_desc_mn(a_addr(stage));
-          const uint64_t bd = BK ? sw128_desc(b_addr(stage)) : sw128_desc_mn(b_addr(stage));
+          const uint64_t ad = a_k ? sw128_desc(a_addr(stage)) : sw128_desc_mn(a_addr(stage));
+          const uint64_t bd = GRAD ? sw128_desc_mn(b_addr(stage)) : sw128_desc(b_addr(stage));
           if (elect_one()) {
             if constexpr (MX) {
               // the columns belong to the stage: the MMAs that read them last
@@ -339,26 +398,29 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
     const int q = warp & 3;            // TMEM lane quarter this warp may read
     const int part = (warp - 2) >> 2;  // which of the quarter's warps
     constexpr int kHop = epi_warps(EPI) / 4 * W;  // columns from one of its chunks to the next
+    if constexpr (GRAD)
+      if (args.join.out) join_columns<epi_warps(EPI)>(args.join, warp - 2, lane, s_join);
     int local = 0;
     for (int u = first; u < total; u += step, ++local) {
-      const Unit w = unit_of(u, args);
+      const Unit w = unit_of<GRAD>(u, args);
+      const GemmProblem &p = args.p[w.p];
       const int acc = local & 1;
-      const int64_t row = (int64_t)w.m * 2 * kRowsCta + rank * kRowsCta + q * 32 + lane;
-      const int c0 = w.n * tn;
-      const bool live = row < args.e.rows;
+      const int64_t row0 = (int64_t)w.m * 2 * kRowsCta + rank * kRowsCta + q * 32;
+      const int64_t row = row0 + lane;
+      const int c0 = w.n * p.tn;
+      const bool live = row < p.e.rows;
       Addend<EPI, W> add;  // of the first columns, while the last products run
-      if (live && part * W < w.tn && c0 + part * W < args.e.cols)
-        fetch_addend<EPI, W>(args.e, row, c0 + part * W, add);
+      if (live && part * W < w.tn && c0 + part * W < p.e.cols)
+        fetch_addend<EPI, W>(p.e, row, c0 + part * W, add);
       if (!wait_bounded(tfull_bar(acc), (uint32_t)(local >> 1) & 1u, s_abort, args.status,
                         args.timeout_ns))
         break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * acc_cols(MX));
-      DenseEpi e = args.e;
-      if constexpr (EPI == EPI_PARTIAL) e.out = static_cast<float *>(e.out) + w.s * args.part_stride;
+      const bool partial = EPI == EPI_PARTIAL || (GRAD && p.partial);
 #pragma unroll 1
       for (int c = part * W; c < w.tn; c += kHop) {
-        if (c0 + c >= args.e.cols) break;
+        if (c0 + c >= p.e.cols) break;
         float v[W];
         uint32_t r[32];
 #pragma unroll
@@ -370,9 +432,22 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
         }
         if (live) {
           const Addend<EPI, W> now = add;
-          if (c + kHop < w.tn && c0 + c + kHop < args.e.cols)
-            fetch_addend<EPI, W>(e, row, c0 + c + kHop, add);
-          dense_epilogue<EPI, W>(e, row, c0 + c, v, now);
+          if (c + kHop < w.tn && c0 + c + kHop < p.e.cols)
+            fetch_addend<EPI, W>(p.e, row, c0 + c + kHop, add);
+          if (partial)
+            store_partial<W>(static_cast<float *>(p.e.out) + w.s * p.part_stride, row, c0 + c,
+                             p.e.cols, v);
+          else
+            dense_epilogue<EPI, W>(p.e, row, c0 + c, v, now);
+        }
+        if constexpr (EPI == EPI_DACT) {
+          if (p.e.column_part && row0 < p.e.rows) {
+#pragma unroll
+            for (int i = 0; i < W; ++i) v[i] = live ? v[i] : 0.f;
+            const float sum = column_sums(v);
+            if (c0 + c + lane < p.e.cols)
+              p.e.column_part[row0 / 32 * p.e.cols + c0 + c + lane] = sum;
+          }
         }
       }
       tc_fence_before();
@@ -542,13 +617,9 @@ bool map_blocks(CUtensorMap *m, const void *base, int64_t blocks, int box_blocks
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-struct GemmMaps {
-  CUtensorMap a, b, b_last, sa, sb;
-};
-
-template <bool AK, bool BK, int EPI, bool MX = false>
+template <bool GRAD, int EPI, bool MX>
 cudaError_t launch_gemm(const GemmMaps &m, const GemmArgs &a, cudaStream_t s) {
-  auto kern = dense_gemm_kernel<AK, BK, EPI, MX>;
+  auto kern = dense_gemm_kernel<GRAD, EPI, MX>;
   static PerDeviceOnce once;
   static std::atomic<int> resident[PerDeviceOnce::kMaxDevices] = {};
   cudaLaunchConfig_t cfg = {};
@@ -578,11 +649,11 @@ cudaError_t launch_gemm(const GemmMaps &m, const GemmArgs &a, cudaStream_t s) {
     return e;
   });
   if (err != cudaSuccess) return err;
-  const int64_t units = (int64_t)a.m_tiles * a.n_tiles * a.splits;
+  const int64_t units = (int64_t)a.p[0].units + a.p[1].units;
   int64_t pairs = resident[dev].load(std::memory_order_relaxed);
   if (units < pairs) pairs = units;
   cfg.gridDim = dim3((unsigned)(2 * pairs));
-  err = cudaLaunchKernelEx(&cfg, kern, m.a, m.b, m.b_last, m.sa, m.sb, a);
+  err = cudaLaunchKernelEx(&cfg, kern, m, a);
   return err != cudaSuccess ? err : cudaGetLastError();
 }
 
@@ -598,137 +669,212 @@ cudaError_t launch_join(const float *part, int64_t stride, int splits, const Den
                           stride, splits, e);
 }
 
-template <bool AK, bool BK>
+template <bool MX>
 cudaError_t launch_kind(int kind, const GemmMaps &m, const GemmArgs &a, cudaStream_t s) {
-  if constexpr (AK && BK) {
-    switch (kind) {
-      case EPI_DACT: return launch_gemm<AK, BK, EPI_DACT>(m, a, s);
-      case EPI_GATED: return launch_gemm<AK, BK, EPI_GATED>(m, a, s);
-      case EPI_GATED_MX: return launch_gemm<AK, BK, EPI_GATED_MX>(m, a, s);
-      case EPI_DGATED: return launch_gemm<AK, BK, EPI_DGATED>(m, a, s);
-    }
+  if constexpr (!MX) {
+    if (kind == EPI_DACT) return launch_gemm<false, EPI_DACT, MX>(m, a, s);
+    if (kind == EPI_DGATED) return launch_gemm<false, EPI_DGATED, MX>(m, a, s);
   }
-  if (kind == EPI_PARTIAL) return launch_gemm<AK, BK, EPI_PARTIAL>(m, a, s);
-  return launch_gemm<AK, BK, EPI_LINEAR>(m, a, s);
+  switch (kind) {
+    case EPI_GATED: return launch_gemm<false, EPI_GATED, MX>(m, a, s);
+    case EPI_GATED_MX: return launch_gemm<false, EPI_GATED_MX, MX>(m, a, s);
+    case EPI_PARTIAL: return launch_gemm<false, EPI_PARTIAL, MX>(m, a, s);
+    default: return launch_gemm<false, EPI_LINEAR, MX>(m, a, s);
+  }
 }
 
-cudaError_t launch_mx(int kind, const GemmMaps &m, const GemmArgs &a, cudaStream_t s) {
-  switch (kind) {
-    case EPI_GATED: return launch_gemm<true, true, EPI_GATED, true>(m, a, s);
-    case EPI_GATED_MX: return launch_gemm<true, true, EPI_GATED_MX, true>(m, a, s);
-    case EPI_PARTIAL: return launch_gemm<true, true, EPI_PARTIAL, true>(m, a, s);
-    default: return launch_gemm<true, true, EPI_LINEAR, true>(m, a, s);
+cudaError_t join_parts(const DenseProduct &p, const DensePlan &plan, const float *partial,
+                       cudaStream_t s) {
+  switch (p.kind) {
+    case EPI_DACT: return launch_join<EPI_DACT>(partial, p.M * p.N, plan.splits, p.epi, s);
+    case EPI_GATED: return launch_join<EPI_GATED>(partial, p.M * p.N, plan.splits, p.epi, s);
+    case EPI_GATED_MX: return launch_join<EPI_GATED_MX>(partial, p.M * p.N, plan.splits, p.epi, s);
+    case EPI_DGATED: return launch_join<EPI_DGATED>(partial, p.M * p.N, plan.splits, p.epi, s);
+    default: return launch_join<EPI_LINEAR>(partial, p.M * p.N, plan.splits, p.epi, s);
   }
+}
+
+// Estimated SM cycles of a K step of a tile of tn columns on a CTA pair: 2 per
+// column (256 x tn x 64 products at 8192 per cycle and SM; MXFP8 twice the
+// products at twice the rate) and no less than its operands' way into shared
+// memory, which 74 bytes per cycle and SM fit over tiles of 64 to 256 columns
+// (2048 x 2880 x 2880: 36, 26, 22 and 30 us at 64, 128, 160 and 256 columns).
+double step_cycles(int tn, bool mx) {
+  const double mma = 2.08 * tn, load = (16384.0 + (mx ? kScaleBytes : 0) + 64.0 * tn) / 74.0;
+  return mma > load ? mma : load;
+}
+constexpr double kUnitCycles = 800.0;   // of a unit beside its steps
+constexpr double kJoinCycles = 5000.0;  // of the kernel that joins the parts
+constexpr int kPairs = 76;  // of the GB300's 152 SMs: a plan does not depend on the device
+
+DensePlan plan_of(int64_t M, int64_t N, int tn, int last, int splits) {
+  DensePlan p{};
+  p.tn = tn;
+  p.tn_last = last;
+  p.m_tiles = (int)((M + 255) / 256);
+  p.n_tiles = (int)((N + tn - 1) / tn);
+  p.splits = splits;
+  p.partial = splits > 1 ? (size_t)M * N * 4 * splits : 0;
+  return p;
+}
+
+void set_problem(GemmProblem &g, const DenseProduct &p, const DensePlan &plan, bool grad, bool mx,
+                 float *partial) {
+  auto b_bytes = [&](int cols) {
+    return grad ? (cols / 2 + 63) / 64 * 8192 : cols / 2 * kStepBytes;
+  };
+  g.e = p.epi;
+  g.m_tiles = plan.m_tiles;
+  g.n_tiles = plan.n_tiles;
+  g.splits = plan.splits;
+  g.num_kb = (int)((p.K + (mx ? 127 : 63)) / (mx ? 128 : 64));
+  g.tn = plan.tn;
+  g.b_bytes = b_bytes(plan.tn);
+  g.tn_last = plan.tn_last;
+  g.b_bytes_last = b_bytes(plan.tn_last);
+  g.n_full = plan.tn_last == plan.tn ? plan.n_tiles : plan.n_tiles - 1;
+  g.a_k_major = p.a.k_major;
+  g.units = plan.m_tiles * plan.n_tiles * plan.splits;
+  if (mx) {  // scale type E8M0 (bit 23); both codes E4M3
+    g.idesc = (1u << 23) | ((uint32_t)(256 >> 4) << 24);
+  } else {
+    const uint32_t type = p.epi.half ? 0u : 1u;  // fp16 / bf16
+    g.idesc = (1u << 4) | (type << 7) | (type << 10) | ((p.a.k_major ? 0u : 1u) << 15) |
+              ((p.b.k_major ? 0u : 1u) << 16) | ((uint32_t)(256 >> 4) << 24);
+  }
+  if (plan.splits > 1) {
+    g.partial = 1;
+    g.e.out = partial;
+    g.part_stride = p.M * p.N;
+  }
+}
+
+void set_ring(GemmArgs &a, int b_bytes, bool mx, int32_t *status) {
+  a.stage_bytes = kABytes + b_bytes;
+  const int most = mx ? kMxStages : kMaxStages;
+  a.stages = kRingBytes / a.stage_bytes < most ? kRingBytes / a.stage_bytes : most;
+  a.status = reinterpret_cast<uint32_t *>(status);
+  a.timeout_ns = kWaitTimeoutNs;
 }
 
 }  // namespace
 
 // Tile width and number of parts of the sum: the choice with the least
-// estimated time, in SM cycles. A K step of a pair takes 2 cycles per column
-// (256 x tn x 64 products at 8192 per cycle and SM; MXFP8 twice the products at
-// twice the rate) and no less than its operands' way into shared memory
-// (kIngress bytes per cycle and SM) nor than its issue; a unit costs about
-// kUnit cycles beside its steps; a split costs its partial sums' way through
-// L2 and the joining kernel.
+// estimated time. A split costs its partial sums' way through L2 and the
+// joining kernel.
 DensePlan dense_plan(int64_t M, int64_t N, int64_t K, int kind, bool mx) {
-  constexpr int kPairs = 76;  // of the GB300's 152 SMs: a plan does not depend on the device
-  constexpr double kIngress = 60.0, kIssue = 200.0, kUnit = 800.0;
   DensePlan best{};
   double best_t = 1e300;
   const int gran = kind == EPI_GATED_MX ? 64 : 32;
   const int64_t kb = mx ? (K + 127) / 128 : (K + 63) / 64, mt = (M + 255) / 256;
-  auto step = [&](int tn) {
-    const double mma = 2.0 * tn, load = (16384.0 + (mx ? kScaleBytes : 0) + 64.0 * tn) / kIngress;
-    const double t = mma > load ? mma : load;
-    return t > kIssue ? t : kIssue;
-  };
-#ifdef DENSE_TUNE
-  const char *env_tn = getenv("DENSE_TN"), *env_s = getenv("DENSE_SPLIT");
-#endif
   for (int tn = acc_cols(mx) / gran * gran; tn >= 64; tn -= gran) {
-#ifdef DENSE_TUNE
-    if (env_tn && atoi(env_tn) != tn) continue;
-#endif
     const int64_t nt = (N + tn - 1) / tn;
     const int last = (int)((N - (nt - 1) * tn + gran - 1) / gran * gran);
     const int64_t nf = last == tn ? nt : nt - 1;
     for (int s = 1; s <= 16; ++s) {
-#ifdef DENSE_TUNE
-      if (env_s && atoi(env_s) != s) continue;
-#endif
       if (s > 1 && (kb / s < 4 || mt * nt * s > 2 * kPairs)) break;
       const double steps = (double)((kb + s - 1) / s);
       // whole tiles in waves, the narrow ones in the room that the last leaves
       const int64_t full = mt * nf * s, waves = (full + kPairs - 1) / kPairs;
       int64_t narrow = (nt - nf) * mt * s - (waves * kPairs - full);
       if (narrow < 0) narrow = 0;
-      double t = (double)waves * (steps * step(tn) + kUnit) +
-                 (double)((narrow + kPairs - 1) / kPairs) * (steps * step(last) + kUnit);
-      if (s > 1) t += 5000.0 + (double)M * N * 4.0 * (s + 1) / 2500.0;
+      double t = (double)waves * (steps * step_cycles(tn, mx) + kUnitCycles) +
+                 (double)((narrow + kPairs - 1) / kPairs) *
+                     (steps * step_cycles(last, mx) + kUnitCycles);
+      if (s > 1) t += kJoinCycles + (double)M * N * 4.0 * (s + 1) / 2500.0;
       if (t < best_t) {
         best_t = t;
-        best.tn = tn;
-        best.tn_last = last;
-        best.m_tiles = (int)mt;
-        best.n_tiles = (int)nt;
-        best.splits = s;
+        best = plan_of(M, N, tn, last, s);
       }
     }
   }
-  best.partial = best.splits > 1 ? (size_t)M * N * 4 * best.splits : 0;
-  best.blocks = mx ? (size_t)kb * kScaleBlock * 2 * ((size_t)best.m_tiles + (size_t)best.n_tiles) : 0;
-#ifdef DENSE_TUNE
-  if (getenv("DENSE_SHOW")) fprintf(stderr, "plan M %ld N %ld K %ld: tn %d last %d splits %d tiles %dx%d est %.0f\n", (long)M, (long)N, (long)K, best.tn, best.tn_last, best.splits, best.m_tiles, best.n_tiles, best_t);
-#endif
+  if (mx)
+    best.blocks = (size_t)kb * kScaleBlock * 2 * ((size_t)best.m_tiles + (size_t)best.n_tiles);
   return best;
+}
+
+// The same for two gradients in one launch, whose units are dealt out one
+// after the other to the pairs in turn (x: the one that comes first).
+void dense_plan_two(int64_t M0, int64_t N0, int64_t K0, int64_t M1, int64_t N1, int64_t K1,
+                    DensePlan *plan0, DensePlan *plan1) {
+  struct Choice {
+    int tn, last, splits;
+    int64_t units;
+    double time, extra;
+  };
+  auto choices = [](int64_t M, int64_t N, int64_t K, Choice *out) {
+    int count = 0;
+    const int64_t kb = (K + 63) / 64, mt = (M + 255) / 256;
+    const int splits[] = {1, 2, 3, 4, 6, 8, 12};
+    for (int tn = 256; tn >= 64; tn -= 64) {
+      const int64_t nt = (N + tn - 1) / tn;
+      if (tn > 64 && N <= tn / 2) continue;  // a narrower tile holds all columns
+      const int last = (int)((N - (nt - 1) * tn + 31) / 32 * 32);
+      for (int s : splits) {
+        if (s > 1 && (kb / s < 4 || mt * nt * s > 2 * kPairs)) break;
+        out[count++] = {tn, last, s, mt * nt * s,
+                        (double)((kb + s - 1) / s) * step_cycles(tn, false) + kUnitCycles,
+                        s > 1 ? kJoinCycles + (double)M * N * 4.0 * (s + 1) / 2500.0 : 0.0};
+      }
+    }
+    return count;
+  };
+  Choice c0[28], c1[28];
+  const int n0 = choices(M0, N0, K0, c0), n1 = choices(M1, N1, K1, c1);
+  double best = 1e300;
+  int b0 = 0, b1 = 0;
+  for (int i = 0; i < n0; ++i)
+    for (int j = 0; j < n1; ++j) {
+      const Choice &x = c0[i], &y = c1[j];
+      const int64_t fx = x.units / kPairs, rx = x.units % kPairs;
+      const int64_t fy = y.units / kPairs, ry = y.units % kPairs;
+      // pairs [0, rx) take one unit more of x, the ry pairs behind them (in a
+      // ring) one more of y
+      double t = (double)fx * x.time + (double)fy * y.time;
+      if (rx + ry > kPairs) t += x.time + y.time;
+      else if (rx > 0 && (ry == 0 || x.time >= y.time)) t += x.time;
+      else if (ry > 0) t += y.time;
+      t += x.extra + y.extra;
+      if (t < best) {
+        best = t;
+        b0 = i;
+        b1 = j;
+      }
+    }
+  *plan0 = plan_of(M0, N0, c0[b0].tn, c0[b0].last, c0[b0].splits);
+  *plan1 = plan_of(M1, N1, c1[b1].tn, c1[b1].last, c1[b1].splits);
 }
 
 cudaError_t launch_dense(const DenseProduct &p, const DensePlan &plan, uint8_t *blocks,
                          float *partial, int32_t *status, cudaStream_t s) {
-  GemmMaps m;
-  const int tn = plan.tn;
-  const bool ak = p.a.k_major, bk = p.b.k_major, mx = p.a.scales != nullptr;
+  GemmMaps maps;
+  CUtensorMap *m = maps.m;
+  const bool mx = p.a.scales != nullptr;
   GemmArgs a{};
-  a.e = p.epi;
-  a.m_tiles = plan.m_tiles;
-  a.n_tiles = plan.n_tiles;
-  a.splits = plan.splits;
-  a.num_kb = (int)((p.K + (mx ? 127 : 63)) / (mx ? 128 : 64));
-  a.tn = tn;
-  auto b_bytes = [&](int cols) { return bk ? cols / 2 * kStepBytes : (cols / 2 + 63) / 64 * 8192; };
-  a.b_bytes = b_bytes(tn);
-  a.tn_last = plan.tn_last;
-  a.b_bytes_last = b_bytes(plan.tn_last);
-  a.n_full = plan.tn_last == tn ? plan.n_tiles : plan.n_tiles - 1;
-  a.stages = kRingBytes / (kABytes + a.b_bytes);
-  const int most = mx ? kMxStages : kMaxStages;
-  if (a.stages > most) a.stages = most;
+  set_problem(a.p[0], p, plan, false, mx, partial);
+  set_ring(a, a.p[0].b_bytes, mx, status);
   a.pairs = p.b.pairs;
-  a.status = reinterpret_cast<uint32_t *>(status);
-  a.timeout_ns = kWaitTimeoutNs;
-
+  const GemmProblem &g = a.p[0];
   auto map_b = [&](CUtensorMap *t, int cols) {
     if (mx) return map_codes(t, p.b.p, p.N, p.K, cols / 2, p.b.pairs);
     if (p.b.pairs) return map_pairs(t, p.b.p, p.N / 2, p.K, cols / 4);
-    return bk ? map_rows(t, p.b.p, p.N, p.K, cols / 2) : map_rows(t, p.b.p, p.K, p.N, 64);
+    return map_rows(t, p.b.p, p.N, p.K, cols / 2);
   };
-  bool ok = mx   ? map_codes(&m.a, p.a.p, p.M, p.K, kRowsCta, false)
-            : ak ? map_rows(&m.a, p.a.p, p.M, p.K, kRowsCta)
-                 : map_rows(&m.a, p.a.p, p.K, p.M, 64);
-  ok = ok && map_b(&m.b, tn);
-  m.b_last = m.b;
-  if (plan.tn_last != tn) ok = ok && map_b(&m.b_last, plan.tn_last);
-  m.sa = m.sb = m.a;
+  bool ok = mx ? map_codes(&m[kMapA], p.a.p, p.M, p.K, kRowsCta, false)
+               : map_rows(&m[kMapA], p.a.p, p.M, p.K, kRowsCta);
+  ok = ok && map_b(&m[kMapB], plan.tn);
+  m[kMapBLast] = m[kMapB];
+  if (plan.tn_last != plan.tn) ok = ok && map_b(&m[kMapBLast], plan.tn_last);
+  m[kMapSa] = m[kMapSb] = m[kMapA];
   if (mx) {
-    // scale type E8M0 (bit 23); both codes E4M3
-    a.idesc = (1u << 23) | ((uint32_t)(256 >> 4) << 24);
-    const int64_t a_blocks = (int64_t)2 * plan.m_tiles * a.num_kb;
-    const int64_t b_blocks = (int64_t)2 * plan.n_tiles * a.num_kb;
+    const int64_t a_blocks = (int64_t)2 * plan.m_tiles * g.num_kb;
+    const int64_t b_blocks = (int64_t)2 * plan.n_tiles * g.num_kb;
     uint8_t *sb = blocks + a_blocks * kScaleBlock;
-    ok = ok && map_blocks(&m.sa, blocks, a_blocks, 1) && map_blocks(&m.sb, sb, b_blocks, 2);
+    ok = ok && map_blocks(&m[kMapSa], blocks, a_blocks, 1) &&
+         map_blocks(&m[kMapSb], sb, b_blocks, 2);
     if (!ok) return cudaErrorInvalidValue;
     const ScaleLayout la{p.a.scales, blocks, p.M, 2 * plan.m_tiles, kRowsCta, 1, 0};
-    const ScaleLayout lb{p.b.scales, sb, p.N, plan.n_tiles, tn, 2, p.b.pairs};
+    const ScaleLayout lb{p.b.scales, sb, p.N, plan.n_tiles, plan.tn, 2, p.b.pairs};
     int64_t grid = ((a_blocks + b_blocks) * 32 + 255) / 256;
     const int64_t cap = (int64_t)device_sm_count() * 8;
     if (grid > cap) grid = cap;
@@ -738,36 +884,39 @@ cudaError_t launch_dense(const DenseProduct &p, const DensePlan &plan, uint8_t *
         launch_dependent(bits % 4 == 0   ? mx8_layout_kernel<4>
                          : bits % 2 == 0 ? mx8_layout_kernel<2>
                                          : mx8_layout_kernel<1>,
-                         dim3((unsigned)grid), dim3(256), 0, s, la, lb, G, a.num_kb);
+                         dim3((unsigned)grid), dim3(256), 0, s, la, lb, G, g.num_kb);
     if (err != cudaSuccess) return err;
-  } else {
-    const uint32_t type = p.epi.half ? 0u : 1u;  // fp16 / bf16
-    a.idesc = (1u << 4) | (type << 7) | (type << 10) | ((ak ? 0u : 1u) << 15) |
-              ((bk ? 0u : 1u) << 16) | ((uint32_t)(256 >> 4) << 24);
   }
   if (!ok) return cudaErrorInvalidValue;
-  int kind = p.kind;
-  if (plan.splits > 1) {
-    kind = EPI_PARTIAL;
-    a.e.out = partial;
-    a.part_stride = p.M * p.N;
-  }
-  const cudaError_t err = mx         ? launch_mx(kind, m, a, s)
-                          : ak && bk ? launch_kind<true, true>(kind, m, a, s)
-                          : ak       ? launch_kind<true, false>(kind, m, a, s)
-                                     : launch_kind<false, false>(kind, m, a, s);
-  return err != cudaSuccess || plan.splits == 1 ? err : launch_dense_join(p, plan, partial, s);
+  const int kind = plan.splits > 1 ? (int)EPI_PARTIAL : p.kind;
+  const cudaError_t err = mx ? launch_kind<true>(kind, maps, a, s) : launch_kind<false>(kind, maps, a, s);
+  return err != cudaSuccess || plan.splits == 1 ? err : join_parts(p, plan, partial, s);
 }
 
-cudaError_t launch_dense_join(const DenseProduct &p, const DensePlan &plan, const float *partial,
-                              cudaStream_t s) {
-  switch (p.kind) {
-    case EPI_DACT: return launch_join<EPI_DACT>(partial, p.M * p.N, plan.splits, p.epi, s);
-    case EPI_GATED: return launch_join<EPI_GATED>(partial, p.M * p.N, plan.splits, p.epi, s);
-    case EPI_GATED_MX: return launch_join<EPI_GATED_MX>(partial, p.M * p.N, plan.splits, p.epi, s);
-    case EPI_DGATED: return launch_join<EPI_DGATED>(partial, p.M * p.N, plan.splits, p.epi, s);
-    default: return launch_join<EPI_LINEAR>(partial, p.M * p.N, plan.splits, p.epi, s);
+cudaError_t launch_dense_gradients(const DenseProduct *const *p, const DensePlan *const *plan,
+                                   float *const *partial, int count, const float *column_part,
+                                   int column_rows, int columns, int half, void *column_out,
+                                   int32_t *status, cudaStream_t s) {
+  GemmMaps maps{};
+  GemmArgs a{};
+  int most = 0;
+  for (int i = 0; i < count; ++i) {
+    const DenseProduct &d = *p[i];
+    set_problem(a.p[i], d, *plan[i], true, false, partial[i]);
+    most = a.p[i].b_bytes > most ? a.p[i].b_bytes : most;
+    CUtensorMap *m = maps.m + 2 * i;
+    if (!(d.a.k_major ? map_rows(&m[kMapA], d.a.p, d.M, d.K, kRowsCta)
+                      : map_rows(&m[kMapA], d.a.p, d.K, d.M, 64)) ||
+        !map_rows(&m[kMapB], d.b.p, d.K, d.N, 64))
+      return cudaErrorInvalidValue;
   }
+  for (int i = 2 * count; i < kMaps; ++i) maps.m[i] = maps.m[0];
+  set_ring(a, most, false, status);
+  a.join = {column_part, column_out, column_rows, columns, half};
+  cudaError_t err = launch_gemm<true, EPI_GRAD, false>(maps, a, s);
+  for (int i = 0; i < count && err == cudaSuccess; ++i)
+    if (plan[i]->splits > 1) err = join_parts(*p[i], *plan[i], partial[i], s);
+  return err;
 }
 
 }  // namespace moe

@@ -611,8 +611,7 @@ cudaError_t norm_grad_t(NormGradArgs a, int w_dtype, void *d_weight, cudaStream_
                : norm_grad_v<T, WT, 1>(a, r.V, dim3((unsigned)P), smem, s);
   }
   if (err != cudaSuccess || !d_weight) return err;
-  return launch_dependent(column_join_kernel, dim3((unsigned)((a.H + 31) / 32)),
-                          dim3(kJoinThreads), 0, s, (const float *)a.part, P, a.H, w_dtype, d_weight);
+  return launch_column_join(a.part, P, a.H, w_dtype, d_weight, s);
 }
 
 }  // namespace
@@ -651,6 +650,12 @@ cudaError_t launch_rms_norm_backward(const void *d_y, const void *x, const void 
   }
 }
 
+cudaError_t launch_column_join(const float *part, int rows, int cols, int dtype, void *out,
+                               cudaStream_t s) {
+  return launch_dependent(column_join_kernel, dim3((unsigned)((cols + 31) / 32)),
+                          dim3(kJoinThreads), 0, s, part, rows, cols, dtype, out);
+}
+
 size_t column_sum_scratch(int cols) { return (size_t)64 * cols * 4; }
 
 cudaError_t launch_column_sum(const void *d, int64_t n, int cols, int dtype, void *out,
@@ -678,8 +683,7 @@ cudaError_t launch_column_sum(const void *d, int64_t n, int cols, int dtype, voi
                                   s, d, (const void *)nullptr, (const float *)nullptr, n, cols,
                                   scratch);
   if (err != cudaSuccess) return err;
-  return launch_dependent(column_join_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(kJoinThreads), 0,
-                          s, (const float *)scratch, (int)P, cols, dtype, out);
+  return launch_column_join(scratch, (int)P, cols, dtype, out, s);
 }
 
 }  // namespace moe

@@ -43,6 +43,8 @@ cudaError_t launch_rms_norm_backward(const void *d_y, const void *x, const void 
                                      int w_dtype, const void *d_sum, int64_t n, int H, int dtype,
                                      float eps, void *d_x, void *d_weight, float *scratch,
                                      cudaStream_t s);
+cudaError_t launch_column_join(const float *part, int rows, int cols, int dtype, void *out,
+                               cudaStream_t s);
 size_t column_sum_scratch(int cols);
 cudaError_t launch_column_sum(const void *d, int64_t n, int cols, int dtype, void *out,
                               float *scratch, cudaStream_t s);
