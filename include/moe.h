@@ -570,8 +570,9 @@ moe_status moe_rms_norm_backward(const void *d_y, const void *x, const void *wei
 /* y = act(x w^T + bias) + residual: x [n, C], w [R, C], bias [R], residual
  * and y [n, R], all of `dtype`; any R >= 1 (at most 131072); bias and residual may be NULL.
  * act: moe_linear_act. _mx8: x and w in 8 bits, bias, residual and y of
- * `dtype`; the products are exact, the sums fp32. */
-size_t moe_linear_workspace_size(int64_t n, int32_t R, int32_t C);
+ * `dtype`; the products are exact, the sums fp32. Workspace: mx8 non-zero
+ * for 8-bit operands. */
+size_t moe_linear_workspace_size(int64_t n, int32_t R, int32_t C, int32_t mx8);
 moe_status moe_linear(const void *x, const void *w, const void *bias, const void *residual,
                       int64_t n, int32_t R, int32_t C, int32_t dtype, int32_t act, void *y,
                       void *workspace, size_t workspace_bytes, int32_t *status,
@@ -596,8 +597,10 @@ moe_status moe_linear_backward(const void *d_y, const void *x, const void *w, co
  * x [n, H], w13 [2I, H] in params->w13_layout order, h [n, I] of `dtype` or
  * h_mx8 (exactly one; I a multiple of 8, with h_mx8 of 32). params: activation
  * (MOE_ACT_SWIGLU or MOE_ACT_SWIGLU_OAI; MOE_ACT_RELU2 has no gate:
- * moe_linear), layout and the values of `set`. A NaN passes the clamps. */
-size_t moe_gated_linear_workspace_size(int64_t n, int32_t H, int32_t I);
+ * moe_linear), layout and the values of `set`. A NaN passes the clamps.
+ * Workspace: mx8 / h_mx8 non-zero for 8-bit operands / results. */
+size_t moe_gated_linear_workspace_size(int64_t n, int32_t H, int32_t I, int32_t mx8,
+                                       int32_t h_mx8);
 moe_status moe_gated_linear(const void *x, const void *w13, int64_t n, int32_t H, int32_t I,
                             const moe_params *params, int32_t dtype, void *h,
                             const moe_mx8_rows *h_mx8, void *workspace, size_t workspace_bytes,

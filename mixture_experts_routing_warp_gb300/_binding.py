@@ -111,14 +111,14 @@ SIGNATURES = {
     "moe_rms_norm_backward_workspace_size": (_SZ, [_I64, _I32]),
     "moe_rms_norm_backward": (_I32, [_P, _P, _P, _I32, _P, _I64, _I32, _I32, _F32, _P, _P, _P,
                                      _SZ, _P]),
-    "moe_linear_workspace_size": (_SZ, [_I64, _I32, _I32]),
+    "moe_linear_workspace_size": (_SZ, [_I64, _I32, _I32, _I32]),
     "moe_linear": (_I32, [_P, _P, _P, _P, _I64, _I32, _I32, _I32, _I32, _P, _P, _SZ, _P, _P]),
     "moe_linear_mx8": (_I32, [_P8, _P8, _P, _P, _I64, _I32, _I32, _I32, _I32, _P, _P, _SZ, _P,
                               _P]),
     "moe_linear_backward_workspace_size": (_SZ, [_I64, _I32, _I32, _I32]),
     "moe_linear_backward": (_I32, [_P, _P, _P, _P, _I64, _I32, _I32, _I32, _I32, _P, _P, _P, _P,
                                    _SZ, _P, _P]),
-    "moe_gated_linear_workspace_size": (_SZ, [_I64, _I32, _I32]),
+    "moe_gated_linear_workspace_size": (_SZ, [_I64, _I32, _I32, _I32, _I32]),
     "moe_gated_linear": (_I32, [_P, _P, _I64, _I32, _I32, _PP, _I32, _P, _P8, _P, _SZ, _P, _P]),
     "moe_gated_linear_mx8": (_I32, [_P8, _P8, _I64, _I32, _I32, _PP, _I32, _P, _P8, _P, _SZ, _P,
                                     _P]),
@@ -850,8 +850,9 @@ def rms_norm_backward_workspace_size(n: int, H: int) -> int:
 
 
 @functools.lru_cache(maxsize=4096)
-def linear_workspace_size(n: int, R: int, C: int) -> int:
-    return int((_LIB or lib()).moe_linear_workspace_size(n, R, C))
+def linear_workspace_size(n: int, R: int, C: int, mx8: bool = False) -> int:
+    """Bytes of scratch for linear; mx8: with Mx8 operands."""
+    return int((_LIB or lib()).moe_linear_workspace_size(n, R, C, mx8))
 
 
 @functools.lru_cache(maxsize=4096)
@@ -860,8 +861,10 @@ def linear_backward_workspace_size(n: int, R: int, C: int, act: str = "none") ->
 
 
 @functools.lru_cache(maxsize=4096)
-def gated_linear_workspace_size(n: int, H: int, I: int) -> int:
-    return int((_LIB or lib()).moe_gated_linear_workspace_size(n, H, I))
+def gated_linear_workspace_size(n: int, H: int, I: int, mx8: bool = False,
+                                h_mx8: bool = False) -> int:
+    """Bytes of scratch for gated_linear; mx8 / h_mx8: with Mx8 operands / results."""
+    return int((_LIB or lib()).moe_gated_linear_workspace_size(n, H, I, mx8, h_mx8))
 
 
 @functools.lru_cache(maxsize=4096)
@@ -926,7 +929,7 @@ def linear(x, w, bias: Optional[torch.Tensor] = None, act: str = "none",
         out = torch.empty((n, R), dtype=dtype, device=like.device)
     else:
         _need_on(out, "out", dtype, device, (n, R))
-    size = linear_workspace_size(n, R, C)
+    size = linear_workspace_size(n, R, C, like is not x)
     p = None
     if size or ws is not None:
         ws, p, size = _scratch(ws, size, like, device)
@@ -986,7 +989,7 @@ def gated_linear(x, w13, params: MoeParams, out=None, mx8: bool = False,
         else:
             _need_on(out, "out", dtype, device, (n, I))
         hp, h8 = out.data_ptr(), None
-    size = gated_linear_workspace_size(n, H, I)
+    size = gated_linear_workspace_size(n, H, I, like is not x, mx8)
     p = None
     if size or ws is not None:
         ws, p, size = _scratch(ws, size, like, device)

@@ -54,18 +54,34 @@ moe_status check_workspace(const void *ws, size_t have, size_t need) {
 char *at(void *ws, size_t off) { return static_cast<char *>(ws) + off; }
 
 // --------------------------------------------------------------- products --
-// A forward product's workspace: the 8-bit scales in the tensor core's
-// layout, then the parts of a split sum.
-size_t forward_bytes(const DensePlan &p) { return align_up(p.blocks, kAlign) + p.partial; }
+// How a forward product runs: few 16-bit rows without a workspace, else by a
+// plan, with the 8-bit scales in the tensor core's layout and the parts of a
+// split sum in the workspace.
+struct ForwardPlan {
+  bool skinny;
+  DensePlan plan;
+  size_t bytes;
+};
+ForwardPlan forward_plan(int64_t n, int64_t out, int64_t in, int kind, bool mx) {
+  ForwardPlan f{};
+  f.skinny = !mx && kind != EPI_GATED_MX && dense_skinny(n, out, in);
+  if (f.skinny) return f;
+  f.plan = dense_plan(n, out, in, kind, mx);
+  f.bytes = align_up(f.plan.blocks, kAlign) + align_up(f.plan.partial, kAlign);
+  return f;
+}
 
-moe_status run_forward(const DenseProduct &p, const DensePlan &plan, void *workspace,
-                       size_t workspace_bytes, int32_t *status, moe_stream stream) {
-  const moe_status st = check_workspace(workspace, workspace_bytes, forward_bytes(plan));
+moe_status run_forward(const DenseProduct &p, void *workspace, size_t workspace_bytes,
+                       int32_t *status, moe_stream stream) {
+  const ForwardPlan f = forward_plan(p.M, p.N, p.K, p.kind, p.a.scales != nullptr);
+  const moe_status st = check_workspace(workspace, workspace_bytes, f.bytes);
   if (st != MOE_OK) return st;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (f.skinny) return from_cuda(launch_dense_skinny(p, s));
   return from_cuda(
-      launch_dense(p, plan, static_cast<uint8_t *>(workspace),
-                   reinterpret_cast<float *>(at(workspace, align_up(plan.blocks, kAlign))), status,
-                   (cudaStream_t)stream));
+      launch_dense(p, f.plan, static_cast<uint8_t *>(workspace),
+                   reinterpret_cast<float *>(at(workspace, align_up(f.plan.blocks, kAlign))),
+                   status, s));
 }
 
 DenseProduct forward_product(const void *x, const void *w, int64_t n, int64_t out, int64_t in,
@@ -187,8 +203,7 @@ moe_status run_linear(const void *x, const uint8_t *x_scales, const void *w,
   p.epi.add = residual;
   p.epi.out = y;
   p.epi.vec = R % 8 == 0 && aligned(bias, 16) && aligned(residual, 16) && aligned(y, 16);
-  const DensePlan plan = dense_plan(n, R, C, EPI_LINEAR, x_scales != nullptr);
-  return run_forward(p, plan, workspace, workspace_bytes, status, stream);
+  return run_forward(p, workspace, workspace_bytes, status, stream);
 }
 
 moe_status run_gated(const void *x, const uint8_t *x_scales, const void *w13,
@@ -215,8 +230,7 @@ moe_status run_gated(const void *x, const uint8_t *x_scales, const void *w13,
     p.epi.scales = h_mx8->scales;
   }
   p.epi.vec = aligned(h, 16);
-  const DensePlan plan = dense_plan(n, 2 * (int64_t)I, H, kind, x_scales != nullptr);
-  return run_forward(p, plan, workspace, workspace_bytes, status, stream);
+  return run_forward(p, workspace, workspace_bytes, status, stream);
 }
 
 }  // namespace
@@ -281,12 +295,9 @@ moe_status moe_rms_norm_backward(const void *d_y, const void *x, const void *wei
 }
 
 // ------------------------------------------------------------------ linear --
-size_t moe_linear_workspace_size(int64_t n, int32_t R, int32_t C) {
-  if (check_product(n, R, C, MOE_BF16, false) != MOE_OK) return 0;
-  const DensePlan a = dense_plan(n, R, C, EPI_LINEAR, false);
-  const DensePlan b = dense_plan(n, R, C, EPI_LINEAR, true);
-  const size_t need = C % 32 == 0 && forward_bytes(b) > a.partial ? forward_bytes(b) : a.partial;
-  return align_up(need, kAlign);
+size_t moe_linear_workspace_size(int64_t n, int32_t R, int32_t C, int32_t mx8) {
+  if (check_product(n, R, C, MOE_BF16, mx8) != MOE_OK) return 0;
+  return forward_plan(n, R, C, EPI_LINEAR, mx8).bytes;
 }
 
 moe_status moe_linear(const void *x, const void *w, const void *bias, const void *residual,
@@ -373,17 +384,12 @@ moe_status moe_linear_backward(const void *d_y, const void *x, const void *w, co
 }
 
 // ------------------------------------------------------------ gated linear --
-size_t moe_gated_linear_workspace_size(int64_t n, int32_t H, int32_t I) {
-  if (I < 8 || I > kMaxFeatures || I % 8 != 0 ||
-      check_product(n, 2 * (int64_t)I, H, MOE_BF16, false) != MOE_OK)
+size_t moe_gated_linear_workspace_size(int64_t n, int32_t H, int32_t I, int32_t mx8,
+                                       int32_t h_mx8) {
+  if (I < 8 || I > kMaxFeatures || I % 8 != 0 || (h_mx8 && I % 32 != 0) ||
+      check_product(n, 2 * (int64_t)I, H, MOE_BF16, mx8) != MOE_OK)
     return 0;
-  size_t most = 0;
-  for (int k = 0; k < 4; ++k) {
-    const DensePlan p = dense_plan(n, 2 * (int64_t)I, H, k & 1 ? EPI_GATED_MX : EPI_GATED, k > 1);
-    if (k > 1 && H % 32 != 0) break;
-    most = forward_bytes(p) > most ? forward_bytes(p) : most;
-  }
-  return align_up(most, kAlign);
+  return forward_plan(n, 2 * (int64_t)I, H, h_mx8 ? EPI_GATED_MX : EPI_GATED, mx8).bytes;
 }
 
 moe_status moe_gated_linear(const void *x, const void *w13, int64_t n, int32_t H, int32_t I,
