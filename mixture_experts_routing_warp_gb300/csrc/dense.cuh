@@ -19,7 +19,8 @@ enum DenseKind {
   EPI_GATED_MX = 3,  // the same, h as E4M3 codes with a scale per 32
   EPI_DGATED = 4,    // (gate, up) pairs and add = d_h: out = (d_gate, d_up) in w13's row order
   EPI_PARTIAL = 5,   // fp32 parts of a split sum, whose joining kernel has the epilogue
-  EPI_GRAD = 6       // out = a (of two products at a time), or the same parts
+  EPI_GRAD = 6,      // out = a (of two products at a time), or the same parts
+  EPI_COLUMNS = 7    // EPI_LINEAR where rows do not start on 16 bytes
 };
 
 struct DenseEpi {
@@ -199,14 +200,29 @@ __device__ __forceinline__ void gated_backward(float g, float u, float d, const 
 }
 
 // --------------------------------------------------------------- epilogue --
-// What the epilogue reads of e.add for W columns of the sums: fetched ahead,
-// while the sums are still being made.
+// What the epilogue reads of e.add for W columns of the sums, and of the bias
+// (a lane's own column, in the warps of a tile): fetched ahead, while the sums
+// are still being made. The loads are volatile: as plain ones they were moved
+// down to their use, behind the wait.
 template <int EPI, int W>
 struct Addend {
   static constexpr bool kUsed = EPI == EPI_LINEAR || EPI == EPI_DACT || EPI == EPI_DGATED;
   static constexpr int kWide = EPI == EPI_DGATED ? W / 2 : W;
   uint4 q[kUsed ? kWide / 8 : 1];
+  uint16_t bias;
 };
+__device__ __forceinline__ uint4 load_now(const uint4 *p) {
+  uint4 q;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+               : "l"(p));
+  return q;
+}
+__device__ __forceinline__ uint16_t load_now(const uint16_t *p) {
+  uint16_t v;
+  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
+  return v;
+}
 template <int EPI, int W>
 __device__ __forceinline__ void fetch_addend(const DenseEpi &e, int64_t row, int c,
                                              Addend<EPI, W> &a) {
@@ -215,7 +231,47 @@ __device__ __forceinline__ void fetch_addend(const DenseEpi &e, int64_t row, int
       const int64_t at = EPI == EPI_DGATED ? row * (e.cols / 2) + c / 2 : row * e.cols + c;
       const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(e.add) + at);
 #pragma unroll
-      for (int i = 0; i < Addend<EPI, W>::kWide / 8; ++i) a.q[i] = __ldg(p + i);
+      for (int i = 0; i < Addend<EPI, W>::kWide / 8; ++i) a.q[i] = load_now(p + i);
+    }
+  }
+}
+// The bias of column c + lane, for add_bias by the whole warp.
+template <int EPI, int W>
+__device__ __forceinline__ void fetch_bias(const DenseEpi &e, int c, Addend<EPI, W> &a) {
+  if constexpr (EPI == EPI_LINEAR || EPI == EPI_DACT) {
+    const int col = c + (int)(threadIdx.x & 31);
+    a.bias = 0;
+    if (e.bias && col < e.cols) a.bias = load_now(static_cast<const uint16_t *>(e.bias) + col);
+  }
+}
+template <int EPI, int W>
+__device__ __forceinline__ void add_bias(const DenseEpi &e, const Addend<EPI, W> &a,
+                                         float (&v)[W]) {
+  if constexpr (EPI == EPI_LINEAR || EPI == EPI_DACT) {
+    if (!e.bias) return;
+    const float b = from16(a.bias, e.half);
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] += __shfl_sync(0xffffffffu, b, i);
+  }
+}
+// f on all of v, eight at a time in one copy of its code: unrolled over 32
+// values, erf alone is 30 KB that a tile's epilogue fetches for two passes
+// (4000 x 1000 x 1000 with GELU: 23 us so).
+template <int W, typename F>
+__device__ __forceinline__ void by_eights(float (&v)[W], F f) {
+  if constexpr (W <= 8) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = f(v[i]);
+  } else {
+#pragma unroll 1
+    for (int g = 0; g < W / 8; ++g) {
+      float t[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[i] = f(v[i]);
+#pragma unroll
+      for (int i = 0; i < W - 8; ++i) v[i] = v[i + 8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[W - 8 + i] = t[i];
     }
   }
 }
@@ -233,24 +289,15 @@ __device__ __forceinline__ void addend(const DenseEpi &e, int64_t row, int c,
   }
 }
 
-// Columns [c, c + W) of a row's sums to where they go. c is a multiple of W
-// and c < e.cols, row < e.rows.
+// Columns [c, c + W) of a row's sums (with the bias) to where they go. c is a
+// multiple of W and c < e.cols, row < e.rows.
 template <int EPI, int W>
 __device__ __forceinline__ void dense_epilogue(const DenseEpi &e, int64_t row, int c,
                                                float (&v)[W], const Addend<EPI, W> &a) {
   const int left = e.cols - c;
   if constexpr (EPI == EPI_LINEAR || EPI == EPI_DACT) {
-    if (e.bias) {
-      float b[W];
-      load_row<W>(e.bias, c, e.vec, left, e.half, b);
-#pragma unroll
-      for (int i = 0; i < W; ++i) v[i] += b[i];
-    }
     if constexpr (EPI == EPI_LINEAR) {
-      if (e.act != MOE_LINEAR_NONE) {
-#pragma unroll
-        for (int i = 0; i < W; ++i) v[i] = linear_act(v[i], e.act);
-      }
+      if (e.act != MOE_LINEAR_NONE) by_eights(v, [&](float f) { return linear_act(f, e.act); });
       if (e.add) {
         float r[W];
         addend<EPI, W>(e, row, c, a, r);
@@ -258,10 +305,11 @@ __device__ __forceinline__ void dense_epilogue(const DenseEpi &e, int64_t row, i
         for (int i = 0; i < W; ++i) v[i] += r[i];
       }
     } else {
+      by_eights(v, [&](float f) { return linear_slope(f, e.act); });
       float d[W];
       addend<EPI, W>(e, row, c, a, d);
 #pragma unroll
-      for (int i = 0; i < W; ++i) v[i] = d[i] * linear_slope(v[i], e.act);
+      for (int i = 0; i < W; ++i) v[i] *= d[i];
     }
     store_row<W>(e.out, row * e.cols + c, e.vec, left, e.half, v);
   } else if constexpr (EPI == EPI_GATED) {
@@ -315,20 +363,15 @@ __device__ __forceinline__ void dense_epilogue(const DenseEpi &e, int64_t row, i
   }
 }
 
-// W fp32 sums of a part [., cols].
+// Columns of a row of fp32 partial sums: whole chunks of 64, so that parts are
+// written and read in vectors.
+__host__ __device__ __forceinline__ int64_t part_columns(int cols) { return (cols + 63) / 64 * 64; }
+
 template <int W>
-__device__ __forceinline__ void store_partial(float *part, int64_t row, int c, int cols,
-                                              const float (&v)[W]) {
-  float *p = part + row * cols + c;
-  if (c + W <= cols && cols % 4 == 0) {
+__device__ __forceinline__ void store_partial(float *p, const float (&v)[W]) {
 #pragma unroll
-    for (int i = 0; i < W; i += 4)
-      *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < W; ++i)
-      if (c + i < cols) p[i] = v[i];
-  }
+  for (int i = 0; i < W; i += 4)
+    *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
 }
 
 // ----------------------------------------------------------- warp roles --

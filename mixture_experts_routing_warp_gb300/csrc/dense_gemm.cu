@@ -43,10 +43,12 @@ constexpr int kRowsCta = 128;                    // A rows of a CTA's half tile
 constexpr int kStepBytes = 128;                  // K bytes of a stage
 constexpr int kABytes = kRowsCta * kStepBytes;   // 16 KB
 constexpr int kMaxTn = 256;
-// Epilogue warps, two or four per TMEM lane quarter: with four a tile's
+// Epilogue warps, two to four per TMEM lane quarter: with four a tile's
 // epilogue has the latency of two column chunks; a group of 32 8-bit results
-// takes 64 columns and twice the registers.
-constexpr int epi_warps(int epi) { return epi == EPI_GATED_MX ? 8 : 16; }
+// takes 64 columns and twice the registers, rows off 16 bytes 124 registers
+// (922 x 5281 x 280: 24.9 us with four, where they spill, 16.0 with three,
+// 16.9 with two).
+constexpr int epi_warps(int epi) { return epi == EPI_GATED_MX ? 8 : epi == EPI_COLUMNS ? 12 : 16; }
 constexpr int gemm_threads(int epi) { return (2 + epi_warps(epi)) * 32; }
 constexpr int kRingBytes = 220 * 1024;
 constexpr int kMaxStages = 8;
@@ -176,6 +178,57 @@ __device__ __forceinline__ float column_sums(float (&v)[32]) {
       v[i] = keep + __shfl_xor_sync(0xffffffffu, send, h);
     }
   return v[0];
+}
+
+// v[c] of lane r to v[r] of lane c.
+__device__ __forceinline__ void transpose32(float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int h = 16; h > 0; h >>= 1)
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if ((i & h) == 0) {
+        const float got = __shfl_xor_sync(0xffffffffu, lane & h ? v[i] : v[i + h], h);
+        if (lane & h) v[i] = got;
+        else v[i + h] = got;
+      }
+}
+
+// EPI_COLUMNS, 32 rows x 32 columns of a warp: a lane per column, so that a
+// row's values are read and written side by side (922 x 5281 x 280 with bias
+// and residual: 95 us with a lane per row).
+struct ColumnAddend {
+  uint16_t r[32];
+};
+__device__ __forceinline__ void fetch_columns(const DenseEpi &e, int64_t row0, int c,
+                                              ColumnAddend &a) {
+  const int col = c + (int)(threadIdx.x & 31);
+  const uint16_t *p = static_cast<const uint16_t *>(e.add) + row0 * e.cols + col;
+  if (e.add && col < e.cols) {
+    const int rows = e.rows - row0 < 32 ? (int)(e.rows - row0) : 32;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      a.r[i] = 0;
+      if (i < rows) a.r[i] = load_now(p + (int64_t)i * e.cols);
+    }
+  }
+}
+__device__ __forceinline__ void linear_columns(const DenseEpi &e, int64_t row0, int c,
+                                               float (&v)[32], const ColumnAddend &a) {
+  const int col = c + (int)(threadIdx.x & 31);
+  transpose32(v);
+  if (col >= e.cols) return;
+  const int rows = e.rows - row0 < 32 ? (int)(e.rows - row0) : 32;
+  uint16_t *out = static_cast<uint16_t *>(e.out) + row0 * e.cols + col;
+  const float b = e.bias ? from16(static_cast<const uint16_t *>(e.bias)[col], e.half) : 0.f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] += b;
+  if (e.act != MOE_LINEAR_NONE) by_eights(v, [&](float f) { return linear_act(f, e.act); });
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    if (e.add) v[i] += from16(a.r[i], e.half);
+    if (i < rows) out[(int64_t)i * e.cols] = to16(v[i], e.half);
+  }
 }
 
 // The epilogue warps' share of a ColumnJoin: 32 columns per CTA at a time, one
@@ -410,8 +463,15 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
       const int c0 = w.n * p.tn;
       const bool live = row < p.e.rows;
       Addend<EPI, W> add;  // of the first columns, while the last products run
-      if (live && part * W < w.tn && c0 + part * W < p.e.cols)
-        fetch_addend<EPI, W>(p.e, row, c0 + part * W, add);
+      ColumnAddend column_add;
+      if (part * W < w.tn && c0 + part * W < p.e.cols) {
+        if constexpr (EPI == EPI_COLUMNS) {
+          if (row0 < p.e.rows) fetch_columns(p.e, row0, c0 + part * W, column_add);
+        } else {
+          fetch_bias<EPI, W>(p.e, c0 + part * W, add);
+          if (live) fetch_addend<EPI, W>(p.e, row, c0 + part * W, add);
+        }
+      }
       if (!wait_bounded(tfull_bar(acc), (uint32_t)(local >> 1) & 1u, s_abort, args.status,
                         args.timeout_ns))
         break;
@@ -430,13 +490,26 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[i + j] = __uint_as_float(r[j]);
         }
+        if constexpr (EPI == EPI_COLUMNS) {
+          if (row0 < p.e.rows) {
+            const ColumnAddend now = column_add;
+            if (c + kHop < w.tn && c0 + c + kHop < p.e.cols)
+              fetch_columns(p.e, row0, c0 + c + kHop, column_add);
+            linear_columns(p.e, row0, c0 + c, v, now);
+          }
+          continue;
+        }
+        const Addend<EPI, W> now = add;
+        if (c + kHop < w.tn && c0 + c + kHop < p.e.cols) {
+          fetch_bias<EPI, W>(p.e, c0 + c + kHop, add);
+          if (live) fetch_addend<EPI, W>(p.e, row, c0 + c + kHop, add);
+        }
+        add_bias<EPI, W>(p.e, now, v);
         if (live) {
-          const Addend<EPI, W> now = add;
-          if (c + kHop < w.tn && c0 + c + kHop < p.e.cols)
-            fetch_addend<EPI, W>(p.e, row, c0 + c + kHop, add);
           if (partial)
-            store_partial<W>(static_cast<float *>(p.e.out) + w.s * p.part_stride, row, c0 + c,
-                             p.e.cols, v);
+            store_partial<W>(static_cast<float *>(p.e.out) + w.s * p.part_stride +
+                                 row * part_columns(p.e.cols) + c0 + c,
+                             v);
           else
             dense_epilogue<EPI, W>(p.e, row, c0 + c, v, now);
         }
@@ -471,12 +544,17 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
   }
 }
 
-// The parts of a split sum, added in order, and the epilogue. One thread per
-// W columns.
+// The parts of a split sum [splits][rows, part_columns(cols)], added in order,
+// and the epilogue. One thread per W columns; where rows do not start on 16
+// bytes (EPI_LINEAR only) per column.
 template <int EPI>
+constexpr int join_width(bool vec) {
+  return EPI == EPI_GATED_MX ? 64 : EPI == EPI_GATED || EPI == EPI_DGATED ? 16 : vec ? 8 : 1;
+}
+template <int EPI, bool VEC>
 __global__ void __launch_bounds__(256)
 dense_join_kernel(const float *part, int64_t stride, int splits, const __grid_constant__ DenseEpi e) {
-  constexpr int W = EPI == EPI_GATED_MX ? 64 : EPI == EPI_GATED || EPI == EPI_DGATED ? 16 : 8;
+  constexpr int W = join_width<EPI>(VEC);
   pdl_launch_dependents();
   pdl_wait();
   const int chunks = (e.cols + W - 1) / W;
@@ -485,15 +563,22 @@ dense_join_kernel(const float *part, int64_t stride, int splits, const __grid_co
        i += (int64_t)gridDim.x * blockDim.x) {
     const int64_t row = i / chunks;
     const int c = (int)(i - row * chunks) * W;
-    float v[W];
+    const float *p = part + row * part_columns(e.cols) + c;
+    if constexpr (W == 1) {
+      float v = 0.f;
+      for (int s = 0; s < splits; ++s, p += stride) v += __ldcg(p);
+      const int64_t at = row * e.cols + c;
+      if (e.bias) v += from16(static_cast<const uint16_t *>(e.bias)[c], e.half);
+      if (e.act != MOE_LINEAR_NONE) v = linear_act(v, e.act);
+      if (e.add) v += from16(static_cast<const uint16_t *>(e.add)[at], e.half);
+      static_cast<uint16_t *>(e.out)[at] = to16(v, e.half);
+    } else {
+      float v[W];
 #pragma unroll
-    for (int j = 0; j < W; ++j) v[j] = 0.f;
-    const float *p = part + row * e.cols + c;
-    Addend<EPI, W> add;
-    fetch_addend<EPI, W>(e, row, c, add);
-    const bool full = c + W <= e.cols && e.cols % 4 == 0;
-    for (int s = 0; s < splits; ++s, p += stride) {
-      if (full) {
+      for (int j = 0; j < W; ++j) v[j] = 0.f;
+      Addend<EPI, W> add;
+      fetch_addend<EPI, W>(e, row, c, add);
+      for (int s = 0; s < splits; ++s, p += stride) {
 #pragma unroll
         for (int j = 0; j < W; j += 4) {
           const float4 f = __ldcg(reinterpret_cast<const float4 *>(p + j));
@@ -502,13 +587,17 @@ dense_join_kernel(const float *part, int64_t stride, int splits, const __grid_co
           v[j + 2] += f.z;
           v[j + 3] += f.w;
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < W; ++j)
-          if (c + j < e.cols) v[j] += __ldcg(p + j);
       }
+      if constexpr (EPI == EPI_LINEAR || EPI == EPI_DACT) {
+        if (e.bias) {
+          float b[W];
+          load_row<W>(e.bias, c, e.vec, e.cols - c, e.half, b);
+#pragma unroll
+          for (int j = 0; j < W; ++j) v[j] += b[j];
+        }
+      }
+      dense_epilogue<EPI, W>(e, row, c, v, add);
     }
-    dense_epilogue<EPI, W>(e, row, c, v, add);
   }
 }
 
@@ -657,15 +746,15 @@ cudaError_t launch_gemm(const GemmMaps &m, const GemmArgs &a, cudaStream_t s) {
   return err != cudaSuccess ? err : cudaGetLastError();
 }
 
-template <int EPI>
+template <int EPI, bool VEC = true>
 cudaError_t launch_join(const float *part, int64_t stride, int splits, const DenseEpi &e,
                         cudaStream_t s) {
-  constexpr int W = EPI == EPI_GATED_MX ? 64 : EPI == EPI_GATED || EPI == EPI_DGATED ? 16 : 8;
+  constexpr int W = join_width<EPI>(VEC);
   const int64_t threads = e.rows * ((e.cols + W - 1) / W);
   int64_t blocks = (threads + 255) / 256;
   const int64_t cap = (int64_t)device_sm_count() * 8;
   if (blocks > cap) blocks = cap;
-  return launch_dependent(dense_join_kernel<EPI>, dim3((unsigned)blocks), dim3(256), 0, s, part,
+  return launch_dependent(dense_join_kernel<EPI, VEC>, dim3((unsigned)blocks), dim3(256), 0, s, part,
                           stride, splits, e);
 }
 
@@ -679,18 +768,23 @@ cudaError_t launch_kind(int kind, const GemmMaps &m, const GemmArgs &a, cudaStre
     case EPI_GATED: return launch_gemm<false, EPI_GATED, MX>(m, a, s);
     case EPI_GATED_MX: return launch_gemm<false, EPI_GATED_MX, MX>(m, a, s);
     case EPI_PARTIAL: return launch_gemm<false, EPI_PARTIAL, MX>(m, a, s);
+    case EPI_COLUMNS: return launch_gemm<false, EPI_COLUMNS, MX>(m, a, s);
     default: return launch_gemm<false, EPI_LINEAR, MX>(m, a, s);
   }
 }
 
 cudaError_t join_parts(const DenseProduct &p, const DensePlan &plan, const float *partial,
                        cudaStream_t s) {
+  const int64_t stride = p.M * part_columns((int)p.N);
+  const int n = plan.splits;
   switch (p.kind) {
-    case EPI_DACT: return launch_join<EPI_DACT>(partial, p.M * p.N, plan.splits, p.epi, s);
-    case EPI_GATED: return launch_join<EPI_GATED>(partial, p.M * p.N, plan.splits, p.epi, s);
-    case EPI_GATED_MX: return launch_join<EPI_GATED_MX>(partial, p.M * p.N, plan.splits, p.epi, s);
-    case EPI_DGATED: return launch_join<EPI_DGATED>(partial, p.M * p.N, plan.splits, p.epi, s);
-    default: return launch_join<EPI_LINEAR>(partial, p.M * p.N, plan.splits, p.epi, s);
+    case EPI_DACT: return launch_join<EPI_DACT>(partial, stride, n, p.epi, s);
+    case EPI_GATED: return launch_join<EPI_GATED>(partial, stride, n, p.epi, s);
+    case EPI_GATED_MX: return launch_join<EPI_GATED_MX>(partial, stride, n, p.epi, s);
+    case EPI_DGATED: return launch_join<EPI_DGATED>(partial, stride, n, p.epi, s);
+    default:
+      return p.epi.vec ? launch_join<EPI_LINEAR>(partial, stride, n, p.epi, s)
+                       : launch_join<EPI_LINEAR, false>(partial, stride, n, p.epi, s);
   }
 }
 
@@ -714,7 +808,7 @@ DensePlan plan_of(int64_t M, int64_t N, int tn, int last, int splits) {
   p.m_tiles = (int)((M + 255) / 256);
   p.n_tiles = (int)((N + tn - 1) / tn);
   p.splits = splits;
-  p.partial = splits > 1 ? (size_t)M * N * 4 * splits : 0;
+  p.partial = splits > 1 ? (size_t)M * part_columns((int)N) * 4 * splits : 0;
   return p;
 }
 
@@ -745,7 +839,7 @@ void set_problem(GemmProblem &g, const DenseProduct &p, const DensePlan &plan, b
   if (plan.splits > 1) {
     g.partial = 1;
     g.e.out = partial;
-    g.part_stride = p.M * p.N;
+    g.part_stride = p.M * part_columns((int)p.N);
   }
 }
 
@@ -888,7 +982,9 @@ cudaError_t launch_dense(const DenseProduct &p, const DensePlan &plan, uint8_t *
     if (err != cudaSuccess) return err;
   }
   if (!ok) return cudaErrorInvalidValue;
-  const int kind = plan.splits > 1 ? (int)EPI_PARTIAL : p.kind;
+  const int kind = plan.splits > 1                         ? (int)EPI_PARTIAL
+                   : p.kind == EPI_LINEAR && !p.epi.vec ? (int)EPI_COLUMNS
+                                                        : p.kind;
   const cudaError_t err = mx ? launch_kind<true>(kind, maps, a, s) : launch_kind<false>(kind, maps, a, s);
   return err != cudaSuccess || plan.splits == 1 ? err : join_parts(p, plan, partial, s);
 }
