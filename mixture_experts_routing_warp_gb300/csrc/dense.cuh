@@ -33,7 +33,7 @@ struct DenseEpi {
   const void *add;     // [rows, cols] (EPI_DGATED: [rows, cols / 2]) or null
   void *out;           // [rows, cols] (EPI_GATED: [rows, cols / 2])
   uint8_t *codes, *scales;  // EPI_GATED_MX
-  float *column_part;  // EPI_DACT: [rows / 32, cols] sums of out before its rounding, or null
+  float *column_part;  // EPI_DACT: sums over 32 rows each of out before its rounding, or null
   int vec;             // every row of bias, add and out starts on 16 bytes
 };
 
@@ -200,17 +200,7 @@ __device__ __forceinline__ void gated_backward(float g, float u, float d, const 
 }
 
 // --------------------------------------------------------------- epilogue --
-// What the epilogue reads of e.add for W columns of the sums, and of the bias
-// (a lane's own column, in the warps of a tile): fetched ahead, while the sums
-// are still being made. The loads are volatile: as plain ones they were moved
-// down to their use, behind the wait.
-template <int EPI, int W>
-struct Addend {
-  static constexpr bool kUsed = EPI == EPI_LINEAR || EPI == EPI_DACT || EPI == EPI_DGATED;
-  static constexpr int kWide = EPI == EPI_DGATED ? W / 2 : W;
-  uint4 q[kUsed ? kWide / 8 : 1];
-  uint16_t bias;
-};
+// Loads that stay where they are written.
 __device__ __forceinline__ uint4 load_now(const uint4 *p) {
   uint4 q;
   asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -218,41 +208,15 @@ __device__ __forceinline__ uint4 load_now(const uint4 *p) {
                : "l"(p));
   return q;
 }
+__device__ __forceinline__ uint2 load_now(const uint2 *p) {
+  uint2 q;
+  asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(q.x), "=r"(q.y) : "l"(p));
+  return q;
+}
 __device__ __forceinline__ uint16_t load_now(const uint16_t *p) {
   uint16_t v;
   asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
   return v;
-}
-template <int EPI, int W>
-__device__ __forceinline__ void fetch_addend(const DenseEpi &e, int64_t row, int c,
-                                             Addend<EPI, W> &a) {
-  if constexpr (Addend<EPI, W>::kUsed) {
-    if (e.add && e.vec && c + W <= e.cols) {
-      const int64_t at = EPI == EPI_DGATED ? row * (e.cols / 2) + c / 2 : row * e.cols + c;
-      const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(e.add) + at);
-#pragma unroll
-      for (int i = 0; i < Addend<EPI, W>::kWide / 8; ++i) a.q[i] = load_now(p + i);
-    }
-  }
-}
-// The bias of column c + lane, for add_bias by the whole warp.
-template <int EPI, int W>
-__device__ __forceinline__ void fetch_bias(const DenseEpi &e, int c, Addend<EPI, W> &a) {
-  if constexpr (EPI == EPI_LINEAR || EPI == EPI_DACT) {
-    const int col = c + (int)(threadIdx.x & 31);
-    a.bias = 0;
-    if (e.bias && col < e.cols) a.bias = load_now(static_cast<const uint16_t *>(e.bias) + col);
-  }
-}
-template <int EPI, int W>
-__device__ __forceinline__ void add_bias(const DenseEpi &e, const Addend<EPI, W> &a,
-                                         float (&v)[W]) {
-  if constexpr (EPI == EPI_LINEAR || EPI == EPI_DACT) {
-    if (!e.bias) return;
-    const float b = from16(a.bias, e.half);
-#pragma unroll
-    for (int i = 0; i < W; ++i) v[i] += __shfl_sync(0xffffffffu, b, i);
-  }
 }
 // f on all of v, eight at a time in one copy of its code: unrolled over 32
 // values, erf alone is 30 KB that a tile's epilogue fetches for two passes
@@ -275,39 +239,32 @@ __device__ __forceinline__ void by_eights(float (&v)[W], F f) {
     }
   }
 }
-template <int EPI, int W>
-__device__ __forceinline__ void addend(const DenseEpi &e, int64_t row, int c,
-                                       const Addend<EPI, W> &a,
-                                       float (&f)[Addend<EPI, W>::kWide]) {
-  constexpr int N = Addend<EPI, W>::kWide;
-  if (e.vec && c + W <= e.cols) {
-#pragma unroll
-    for (int i = 0; i < N / 8; ++i) unpack8(a.q[i], e.half, f + 8 * i);
-  } else {
-    const int64_t at = EPI == EPI_DGATED ? row * (e.cols / 2) + c / 2 : row * e.cols + c;
-    load_row<N>(e.add, at, false, EPI == EPI_DGATED ? (e.cols - c) / 2 : e.cols - c, e.half, f);
-  }
-}
-
-// Columns [c, c + W) of a row's sums (with the bias) to where they go. c is a
-// multiple of W and c < e.cols, row < e.rows.
+// Columns [c, c + W) of a row's sums to where they go, by one thread (the
+// gated results of a tile, and joined parts). c is a multiple of W and c <
+// e.cols, row < e.rows.
 template <int EPI, int W>
 __device__ __forceinline__ void dense_epilogue(const DenseEpi &e, int64_t row, int c,
-                                               float (&v)[W], const Addend<EPI, W> &a) {
+                                               float (&v)[W]) {
   const int left = e.cols - c;
   if constexpr (EPI == EPI_LINEAR || EPI == EPI_DACT) {
+    if (e.bias) {
+      float b[W];
+      load_row<W>(e.bias, c, e.vec, left, e.half, b);
+#pragma unroll
+      for (int i = 0; i < W; ++i) v[i] += b[i];
+    }
     if constexpr (EPI == EPI_LINEAR) {
       if (e.act != MOE_LINEAR_NONE) by_eights(v, [&](float f) { return linear_act(f, e.act); });
       if (e.add) {
         float r[W];
-        addend<EPI, W>(e, row, c, a, r);
+        load_row<W>(e.add, row * e.cols + c, e.vec, left, e.half, r);
 #pragma unroll
         for (int i = 0; i < W; ++i) v[i] += r[i];
       }
     } else {
       by_eights(v, [&](float f) { return linear_slope(f, e.act); });
       float d[W];
-      addend<EPI, W>(e, row, c, a, d);
+      load_row<W>(e.add, row * e.cols + c, e.vec, left, e.half, d);
 #pragma unroll
       for (int i = 0; i < W; ++i) v[i] *= d[i];
     }
@@ -344,7 +301,7 @@ __device__ __forceinline__ void dense_epilogue(const DenseEpi &e, int64_t row, i
   } else if constexpr (EPI == EPI_DGATED) {
     const int I = e.cols / 2;
     float d[W / 2];
-    addend<EPI, W>(e, row, c, a, d);
+    load_row<W / 2>(e.add, row * I + c / 2, e.vec, left / 2, e.half, d);
     if (e.gate.layout == MOE_W13_PACKED) {
       float g[W / 2], u[W / 2];
 #pragma unroll
@@ -358,21 +315,12 @@ __device__ __forceinline__ void dense_epilogue(const DenseEpi &e, int64_t row, i
         gated_backward(v[2 * i], v[2 * i + 1], d[i], e.gate, v[2 * i], v[2 * i + 1]);
       store_row<W>(e.out, row * e.cols + c, e.vec, left, e.half, v);
     }
-  } else if constexpr (EPI == EPI_GRAD) {
-    store_row<W>(e.out, row * e.cols + c, e.vec, left, e.half, v);
   }
 }
 
 // Columns of a row of fp32 partial sums: whole chunks of 64, so that parts are
 // written and read in vectors.
 __host__ __device__ __forceinline__ int64_t part_columns(int cols) { return (cols + 63) / 64 * 64; }
-
-template <int W>
-__device__ __forceinline__ void store_partial(float *p, const float (&v)[W]) {
-#pragma unroll
-  for (int i = 0; i < W; i += 4)
-    *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-}
 
 // ----------------------------------------------------------- warp roles --
 // The producer and MMA roles run as whole warps whose every value is the same
@@ -418,7 +366,7 @@ DensePlan dense_plan(int64_t M, int64_t N, int64_t K, int kind, bool mx);
 // blocks and partial: scratch of plan.blocks and plan.partial bytes.
 cudaError_t launch_dense(const DenseProduct &p, const DensePlan &plan, uint8_t *blocks,
                          float *partial, int32_t *status, cudaStream_t s);
-// A product of few rows (16-bit, EPI_LINEAR or EPI_GATED), where dense_skinny
+// A product of few 16-bit rows (any kind but EPI_GATED_MX), where dense_skinny
 // says so (dense_skinny.cu). No scratch.
 bool dense_skinny(int64_t n, int64_t out, int64_t in);
 cudaError_t launch_dense_skinny(const DenseProduct &p, cudaStream_t s);

@@ -137,12 +137,14 @@ DenseProduct weight_gradient(const void *d, const void *x, int64_t n, int64_t ou
 // The backward passes' workspace: the gradient of the sums (where it is not
 // the caller's), the parts of split sums, the column sums' scratch.
 struct GradLayout {
+  bool skinny;               // the recomputed sums take few rows
   DensePlan sums, d_x, d_w;  // of the recomputed sums and of both gradients
   size_t d, partial, partial_w, columns, total;
 };
 GradLayout grad_layout(int64_t n, int64_t out, int64_t in, int kind, bool own_d, bool columns) {
   GradLayout g{};
-  if (own_d) g.sums = dense_plan(n, out, in, kind, false);
+  g.skinny = dense_skinny(n, out, in);
+  if (own_d && !g.skinny) g.sums = dense_plan(n, out, in, kind, false);
   dense_plan_two(n, in, out, out, in, n, &g.d_x, &g.d_w);
   g.partial = own_d ? align_up((size_t)n * out * 2, kAlign) : 0;
   g.partial_w = g.partial + align_up(g.d_x.partial, kAlign);
@@ -153,6 +155,13 @@ GradLayout grad_layout(int64_t n, int64_t out, int64_t in, int kind, bool own_d,
   const size_t sums = (size_t)rows * out * 4, other = column_sum_scratch((int)out);
   g.total = g.columns + (columns ? align_up(sums > other ? sums : other, kAlign) : 0);
   return g;
+}
+
+cudaError_t run_sums(const DenseProduct &p, const GradLayout &g, void *workspace, int32_t *status,
+                     cudaStream_t s) {
+  if (g.skinny) return launch_dense_skinny(p, s);
+  return launch_dense(p, g.sums, nullptr, reinterpret_cast<float *>(at(workspace, g.partial)),
+                      status, s);
 }
 
 // d_x and d_w of d, each where it is wanted; with column_rows, d_bias from
@@ -366,12 +375,11 @@ moe_status moe_linear_backward(const void *d_y, const void *x, const void *w, co
     p.epi.add = d_y;
     p.epi.out = at(workspace, g.d);
     p.epi.vec = aligned(bias, 16);
-    if (d_bias && g.sums.splits == 1) {
+    if (d_bias && g.sums.splits <= 1) {
       p.epi.column_part = reinterpret_cast<float *>(at(workspace, g.columns));
       column_rows = (int)((n + 31) / 32);
     }
-    e = launch_dense(p, g.sums, nullptr, reinterpret_cast<float *>(at(workspace, g.partial)),
-                     status, s);
+    e = run_sums(p, g, workspace, status, s);
     d = p.epi.out;
   }
   if (e == cudaSuccess && d_bias && !column_rows)
@@ -454,8 +462,7 @@ moe_status moe_gated_linear_backward(const void *d_h, const void *x, const void 
   p.epi.out = at(workspace, g.d);
   p.epi.vec = aligned(d_h, 16);
   if (!d_x && !d_w13) return MOE_OK;
-  cudaError_t e = launch_dense(p, g.sums, nullptr,
-                               reinterpret_cast<float *>(at(workspace, g.partial)), status, s);
+  cudaError_t e = run_sums(p, g, workspace, status, s);
   if (e == cudaSuccess)
     e = run_gradients(p.epi.out, x, w13, n, out, H, half, d_x, d_w13, g, workspace, 0, nullptr,
                       status, s);

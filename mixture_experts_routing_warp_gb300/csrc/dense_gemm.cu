@@ -166,18 +166,175 @@ __device__ __forceinline__ Unit unit_of(int u, const GemmArgs &args) {
   return w;
 }
 
-// Sums of 32 columns over the 32 lanes: lane l gets that of v[l]. Each step
-// halves the columns a lane holds.
-__device__ __forceinline__ float column_sums(float (&v)[32]) {
+// ---------------------------------------------- epilogue of the tile's warps --
+// A warp reads 32 rows x 32 columns of sums from TMEM, a row per lane. Before
+// the epilogue the four lanes of a group exchange them, so that a lane has 8
+// columns of its group's 4 rows: v[8 k + i] is row 4 (lane / 4) + k, column 8
+// (lane % 4) + i. Rows are then read and written 64 bytes side by side (128 of
+// fp32) and not 16 per row: 4945 x 3632 x 1152 36 -> 31 us.
+__device__ __forceinline__ void regroup(float (&v)[32]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int h = 16; h > 0; h >>= 1)
+  for (int h = 2; h > 0; h >>= 1)
 #pragma unroll
-    for (int i = 0; i < h; ++i) {
-      const float send = lane & h ? v[i] : v[i + h], keep = lane & h ? v[i + h] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, h);
+    for (int p = 0; p < 4; ++p)
+      if ((p & h) == 0)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float got =
+              __shfl_xor_sync(0xffffffffu, lane & h ? v[8 * p + i] : v[8 * (p + h) + i], h);
+          if (lane & h) v[8 * p + i] = got;
+          else v[8 * (p + h) + i] = got;
+        }
+}
+
+// What a lane's epilogue reads: fetched ahead, while the sums are still being
+// made. The loads are volatile: plain ones were moved down to their use,
+// behind the wait.
+struct RowsAddend {
+  uint4 q[4];  // of e.add, a row each (EPI_DGATED: 4 values, in x and y)
+  uint4 bias;
+};
+template <int EPI>
+__device__ __forceinline__ void fetch_rows(const DenseEpi &e, int64_t row0, int c, RowsAddend &a) {
+  const int lane = threadIdx.x & 31, col = c + (lane & 3) * 8;
+  const int64_t row = row0 + (lane >> 2) * 4;
+  if (col >= e.cols) return;
+  if constexpr (EPI == EPI_LINEAR || EPI == EPI_DACT) {
+    if (e.bias) {
+      const uint16_t *b = static_cast<const uint16_t *>(e.bias) + col;
+      if (e.vec) {
+        a.bias = load_now(reinterpret_cast<const uint4 *>(b));
+      } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = (uint32_t)load_now(b + 2 * i) | (uint32_t)load_now(b + 2 * i + 1) << 16;
+        a.bias = make_uint4(w[0], w[1], w[2], w[3]);
+      }
     }
-  return v[0];
+    if (e.add) {
+      const uint16_t *p = static_cast<const uint16_t *>(e.add) + row * e.cols + col;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (row + k < e.rows) a.q[k] = load_now(reinterpret_cast<const uint4 *>(p + (int64_t)k * e.cols));
+    }
+  } else if constexpr (EPI == EPI_DGATED) {
+    const int I = e.cols / 2;
+    const uint16_t *p = static_cast<const uint16_t *>(e.add) + row * I + col / 2;
+#pragma unroll
+    for (int k = 0; k < 4; ++k, p += I)
+      if (row + k < e.rows) {
+        if (e.vec) {
+          const uint2 w = load_now(reinterpret_cast<const uint2 *>(p));
+          a.q[k].x = w.x;
+          a.q[k].y = w.y;
+        } else {
+          a.q[k].x = (uint32_t)load_now(p) | (uint32_t)load_now(p + 1) << 16;
+          a.q[k].y = (uint32_t)load_now(p + 2) | (uint32_t)load_now(p + 3) << 16;
+        }
+      }
+  }
+}
+
+__device__ __forceinline__ void store4(uint16_t *p, const float (&f)[4], int half) {
+  const float g[8] = {f[0], f[1], f[2], f[3], 0.f, 0.f, 0.f, 0.f};
+  const uint4 q = pack8(g, half);
+  *reinterpret_cast<uint2 *>(p) = make_uint2(q.x, q.y);
+}
+
+// The regrouped sums of columns [c, c + 32) of rows [row0, row0 + 32), row0 <
+// e.rows. Every lane of the warp comes here.
+template <int EPI>
+__device__ __forceinline__ void rows_epilogue(const DenseEpi &e, int64_t row0, int c,
+                                              float (&v)[32], const RowsAddend &a) {
+  const int lane = threadIdx.x & 31, col = c + (lane & 3) * 8;
+  const int64_t row = row0 + (lane >> 2) * 4;
+  const int rows = col >= e.cols ? 0 : e.rows - row >= 4 ? 4 : e.rows > row ? (int)(e.rows - row) : 0;
+  const int64_t at = row * e.cols + col;
+  if constexpr (EPI == EPI_LINEAR || EPI == EPI_DACT) {
+    if (e.bias) {
+      float b[8];
+      unpack8(a.bias, e.half, b);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] += b[i & 7];
+    }
+  }
+  uint16_t *out = static_cast<uint16_t *>(e.out) + at;
+  if constexpr (EPI == EPI_LINEAR) {
+    if (e.act != MOE_LINEAR_NONE) by_eights(v, [&](float f) { return linear_act(f, e.act); });
+  } else if constexpr (EPI == EPI_DACT) {
+    by_eights(v, [&](float f) { return linear_slope(f, e.act); });
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = v[8 * k + i];
+    if constexpr (EPI == EPI_LINEAR || EPI == EPI_DACT) {
+      if (e.add) {
+        float d[8];
+        unpack8(a.q[k], e.half, d);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = EPI == EPI_DACT ? f[i] * d[i] : f[i] + d[i];
+      }
+    }
+    if constexpr (EPI == EPI_DGATED) {
+      const int I = e.cols / 2;
+      float d[8], g[4], u[4];
+      unpack8(make_uint4(a.q[k].x, a.q[k].y, 0u, 0u), e.half, d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        gated_backward(f[2 * i], f[2 * i + 1], d[i], e.gate, g[i], u[i]);
+      if (k < rows) {
+        if (e.gate.layout == MOE_W13_PACKED) {
+          uint16_t *p = static_cast<uint16_t *>(e.out) + (row + k) * e.cols + col / 2;
+          store4(p, g, e.half);
+          store4(p + I, u, e.half);
+        } else {
+          const float o[8] = {g[0], u[0], g[1], u[1], g[2], u[2], g[3], u[3]};
+          *reinterpret_cast<uint4 *>(out + (int64_t)k * e.cols) = pack8(o, e.half);
+        }
+      }
+    } else if (k < rows) {
+      *reinterpret_cast<uint4 *>(out + (int64_t)k * e.cols) = pack8(f, e.half);
+    }
+    if constexpr (EPI == EPI_DACT) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[8 * k + i] = k < rows ? f[i] : 0.f;
+    }
+  }
+  if constexpr (EPI == EPI_DACT) {
+    if (e.column_part) {  // over the lane's rows, then over the groups
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float f = (v[i] + v[8 + i]) + (v[16 + i] + v[24 + i]);
+#pragma unroll
+        for (int h = 4; h < 32; h <<= 1) f += __shfl_xor_sync(0xffffffffu, f, h);
+        v[i] = f;
+      }
+      if (lane < 4 && col < e.cols) {
+        float4 *p = reinterpret_cast<float4 *>(e.column_part + row0 / 32 * e.cols + col);
+        p[0] = make_float4(v[0], v[1], v[2], v[3]);
+        p[1] = make_float4(v[4], v[5], v[6], v[7]);
+      }
+    }
+  }
+}
+
+// The same of a part of a split sum [rows, part_columns(cols)].
+__device__ __forceinline__ void store_partial(float *part, int64_t rows, int cols, int64_t row0,
+                                              int c, const float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = row0 + (lane >> 2) * 4, wide = part_columns(cols);
+  float *p = part + row * wide + c + (lane & 3) * 8;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (row + k < rows) {
+      uint4 q[2];
+      memcpy(q, v + 8 * k, 32);
+      store32(p + k * wide, q[0], q[1]);
+    }
 }
 
 // v[c] of lane r to v[r] of lane c.
@@ -459,18 +616,12 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
       const GemmProblem &p = args.p[w.p];
       const int acc = local & 1;
       const int64_t row0 = (int64_t)w.m * 2 * kRowsCta + rank * kRowsCta + q * 32;
-      const int64_t row = row0 + lane;
       const int c0 = w.n * p.tn;
-      const bool live = row < p.e.rows;
-      Addend<EPI, W> add;  // of the first columns, while the last products run
+      RowsAddend add;  // of the first columns, while the last products run
       ColumnAddend column_add;
-      if (part * W < w.tn && c0 + part * W < p.e.cols) {
-        if constexpr (EPI == EPI_COLUMNS) {
-          if (row0 < p.e.rows) fetch_columns(p.e, row0, c0 + part * W, column_add);
-        } else {
-          fetch_bias<EPI, W>(p.e, c0 + part * W, add);
-          if (live) fetch_addend<EPI, W>(p.e, row, c0 + part * W, add);
-        }
+      if (row0 < p.e.rows && part * W < w.tn && c0 + part * W < p.e.cols) {
+        if constexpr (EPI == EPI_COLUMNS) fetch_columns(p.e, row0, c0 + part * W, column_add);
+        else fetch_rows<EPI>(p.e, row0, c0 + part * W, add);
       }
       if (!wait_bounded(tfull_bar(acc), (uint32_t)(local >> 1) & 1u, s_abort, args.status,
                         args.timeout_ns))
@@ -490,37 +641,23 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[i + j] = __uint_as_float(r[j]);
         }
-        if constexpr (EPI == EPI_COLUMNS) {
-          if (row0 < p.e.rows) {
-            const ColumnAddend now = column_add;
-            if (c + kHop < w.tn && c0 + c + kHop < p.e.cols)
-              fetch_columns(p.e, row0, c0 + c + kHop, column_add);
-            linear_columns(p.e, row0, c0 + c, v, now);
-          }
-          continue;
-        }
-        const Addend<EPI, W> now = add;
-        if (c + kHop < w.tn && c0 + c + kHop < p.e.cols) {
-          fetch_bias<EPI, W>(p.e, c0 + c + kHop, add);
-          if (live) fetch_addend<EPI, W>(p.e, row, c0 + c + kHop, add);
-        }
-        add_bias<EPI, W>(p.e, now, v);
-        if (live) {
+        if (row0 >= p.e.rows) continue;
+        const bool more = c + kHop < w.tn && c0 + c + kHop < p.e.cols;
+        if constexpr (EPI == EPI_GATED || EPI == EPI_GATED_MX) {
+          if (row0 + lane < p.e.rows) dense_epilogue<EPI, W>(p.e, row0 + lane, c0 + c, v);
+        } else if constexpr (EPI == EPI_COLUMNS) {
+          const ColumnAddend now = column_add;
+          if (more) fetch_columns(p.e, row0, c0 + c + kHop, column_add);
+          linear_columns(p.e, row0, c0 + c, v, now);
+        } else {
+          const RowsAddend now = add;
+          if (more) fetch_rows<EPI>(p.e, row0, c0 + c + kHop, add);
+          regroup(v);
           if (partial)
-            store_partial<W>(static_cast<float *>(p.e.out) + w.s * p.part_stride +
-                                 row * part_columns(p.e.cols) + c0 + c,
-                             v);
+            store_partial(static_cast<float *>(p.e.out) + w.s * p.part_stride, p.e.rows, p.e.cols,
+                          row0, c0 + c, v);
           else
-            dense_epilogue<EPI, W>(p.e, row, c0 + c, v, now);
-        }
-        if constexpr (EPI == EPI_DACT) {
-          if (p.e.column_part && row0 < p.e.rows) {
-#pragma unroll
-            for (int i = 0; i < W; ++i) v[i] = live ? v[i] : 0.f;
-            const float sum = column_sums(v);
-            if (c0 + c + lane < p.e.cols)
-              p.e.column_part[row0 / 32 * p.e.cols + c0 + c + lane] = sum;
-          }
+            rows_epilogue<EPI>(p.e, row0, c0 + c, v, now);
         }
       }
       tc_fence_before();
@@ -576,8 +713,6 @@ dense_join_kernel(const float *part, int64_t stride, int splits, const __grid_co
       float v[W];
 #pragma unroll
       for (int j = 0; j < W; ++j) v[j] = 0.f;
-      Addend<EPI, W> add;
-      fetch_addend<EPI, W>(e, row, c, add);
       for (int s = 0; s < splits; ++s, p += stride) {
 #pragma unroll
         for (int j = 0; j < W; j += 4) {
@@ -588,15 +723,7 @@ dense_join_kernel(const float *part, int64_t stride, int splits, const __grid_co
           v[j + 3] += f.w;
         }
       }
-      if constexpr (EPI == EPI_LINEAR || EPI == EPI_DACT) {
-        if (e.bias) {
-          float b[W];
-          load_row<W>(e.bias, c, e.vec, e.cols - c, e.half, b);
-#pragma unroll
-          for (int j = 0; j < W; ++j) v[j] += b[j];
-        }
-      }
-      dense_epilogue<EPI, W>(e, row, c, v, add);
+      dense_epilogue<EPI, W>(e, row, c, v);
     }
   }
 }

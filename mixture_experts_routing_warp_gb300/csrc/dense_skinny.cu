@@ -1,5 +1,6 @@
-// dense_skinny.cu -- moe_linear and moe_gated_linear for a handful of rows
-// (decode): y[t, r] = sum_k x[t, k] w[r, k] with every weight read once.
+// dense_skinny.cu -- moe_linear and moe_gated_linear, and the sums that their
+// gradients compute again, for a handful of rows (decode): y[t, r] = sum_k
+// x[t, k] w[r, k] with every weight read once.
 //
 // Bound by HBM for the weights, and at a few MB by latency: one launch, no
 // partial sums through memory. A CTA takes 16 rows of w (gated: 8 gate and
@@ -57,9 +58,9 @@ struct SkinnyArgs {
 };
 
 // The CTA's weight row j of 16: gated, gates first, then their ups.
-template <bool GATED>
+template <bool PAIRS>
 __device__ __forceinline__ int64_t weight_row(const SkinnyArgs &a, int j, bool &live) {
-  if constexpr (!GATED) {
+  if constexpr (!PAIRS) {
     const int64_t r = (int64_t)blockIdx.x * kRows + j;
     live = r < a.rows;
     return r;
@@ -70,9 +71,11 @@ __device__ __forceinline__ int64_t weight_row(const SkinnyArgs &a, int j, bool &
 }
 
 // NB blocks of 8 tokens; CTAS per SM that registers are left for.
-template <bool GATED, bool HALF, int NB, int CTAS>
+template <int EPI, bool HALF, int NB, int CTAS>
 __global__ void __launch_bounds__(kThreads, CTAS)
     dense_skinny_kernel(const __grid_constant__ SkinnyArgs a) {
+  constexpr bool PAIRS = EPI == EPI_GATED || EPI == EPI_DGATED;
+  __shared__ float s_d[EPI == EPI_DACT ? NB * 8 : 1][kRows + 1];
   constexpr int U = NB == 4 ? 2 : 4;  // blocks of 32 k in flight per warp
   __shared__ float s_sum[kWarps][NB][4][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -81,7 +84,7 @@ __global__ void __launch_bounds__(kThreads, CTAS)
     const int most = lines < kAhead ? lines : kAhead;
     for (int i = threadIdx.x; i < kRows * most; i += kThreads) {
       bool live;
-      const int64_t r = weight_row<GATED>(a, i / most, live);
+      const int64_t r = weight_row<PAIRS>(a, i / most, live);
       const char *p = reinterpret_cast<const char *>(a.w + r * a.K) + (i % most) * 128;
       if (live) asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
     }
@@ -90,8 +93,8 @@ __global__ void __launch_bounds__(kThreads, CTAS)
   pdl_wait();
 
   bool live0, live1;
-  const uint16_t *w0 = a.w + weight_row<GATED>(a, g, live0) * a.K;
-  const uint16_t *w1 = a.w + weight_row<GATED>(a, g + 8, live1) * a.K;
+  const uint16_t *w0 = a.w + weight_row<PAIRS>(a, g, live0) * a.K;
+  const uint16_t *w1 = a.w + weight_row<PAIRS>(a, g + 8, live1) * a.K;
   const int blocks = (a.K + 31) / 32;
   const int b_lo = blocks * warp / kWarps, b_hi = blocks * (warp + 1) / kWarps;
   float acc[NB][4];
@@ -139,22 +142,52 @@ __global__ void __launch_bounds__(kThreads, CTAS)
     return f;
   };
   const DenseEpi &e = a.e;
-  constexpr int kOut = GATED ? kRows / 2 : kRows;  // results per token
+  constexpr int kOut = PAIRS ? kRows / 2 : kRows;  // results per token
   for (int i = threadIdx.x; i < kOut * NB * 8; i += kThreads) {
     const int j = i % kOut, tok = i / kOut;
     const int64_t c = (int64_t)blockIdx.x * kOut + j;
-    if (tok >= a.n || c >= a.rows) continue;
+    const bool live = tok < a.n && c < a.rows;
     const int64_t at = (int64_t)tok * a.rows + c;
-    float v;
-    if constexpr (GATED) {
-      v = gated(total(j, tok), total(j + 8, tok), e.gate);
+    uint16_t *out = static_cast<uint16_t *>(e.out) + at;
+    auto add = [&] { return from16(static_cast<const uint16_t *>(e.add)[at], HALF); };
+    if constexpr (PAIRS) {
+      if (!live) continue;
+      const float g = total(j, tok), u = total(j + 8, tok);
+      if constexpr (EPI == EPI_GATED) {
+        *out = to16(gated(g, u, e.gate), HALF);
+      } else {  // in w13's row order
+        float d_g, d_u;
+        gated_backward(g, u, add(), e.gate, d_g, d_u);
+        uint16_t *d = static_cast<uint16_t *>(e.out) + (int64_t)tok * 2 * a.rows +
+                      (a.packed ? c : 2 * c);
+        d[0] = to16(d_g, HALF);
+        d[a.packed ? a.rows : 1] = to16(d_u, HALF);
+      }
     } else {
-      v = total(j, tok);
-      if (e.bias) v += from16(static_cast<const uint16_t *>(e.bias)[c], HALF);
-      if (e.act != MOE_LINEAR_NONE) v = linear_act(v, e.act);
-      if (e.add) v += from16(static_cast<const uint16_t *>(e.add)[at], HALF);
+      float v = 0.f;
+      if (live) {
+        v = total(j, tok);
+        if (e.bias) v += from16(static_cast<const uint16_t *>(e.bias)[c], HALF);
+        if constexpr (EPI == EPI_DACT) {
+          v = add() * linear_slope(v, e.act);
+        } else {
+          if (e.act != MOE_LINEAR_NONE) v = linear_act(v, e.act);
+          if (e.add) v += add();
+        }
+        *out = to16(v, HALF);
+      }
+      if constexpr (EPI == EPI_DACT) s_d[tok][j] = v;
     }
-    static_cast<uint16_t *>(e.out)[at] = to16(v, HALF);
+  }
+  if constexpr (EPI == EPI_DACT) {
+    if (!e.column_part) return;
+    __syncthreads();
+    const int64_t c = (int64_t)blockIdx.x * kRows + threadIdx.x;
+    if (threadIdx.x < kRows && c < a.rows) {
+      float f = 0.f;
+      for (int tok = 0; tok < a.n; ++tok) f += s_d[tok][threadIdx.x];
+      e.column_part[c] = f;
+    }
   }
 }
 
@@ -163,20 +196,26 @@ __global__ void __launch_bounds__(kThreads, CTAS)
 // 2880 x 5760 gated (360 CTAs) 5.1 us at three CTAs per SM and 6.4 at four,
 // 8192 x 8192 (512) 26.8 and 20.9; 32 rows: 2880 x 2880 (180) 7.9 us at two
 // and 9.5 at three, 2880 x 5760 gated 13.6 and 10.3.
-template <bool GATED, bool HALF, int NB>
+template <int EPI, bool HALF, int NB>
 cudaError_t launch_nb(const SkinnyArgs &a, cudaStream_t s) {
-  constexpr int kFew = NB == 4 ? 2 : 3, per = GATED ? kRows / 2 : kRows;
+  constexpr bool PAIRS = EPI == EPI_GATED || EPI == EPI_DGATED;
+  constexpr int kFew = NB == 4 ? 2 : 3, per = PAIRS ? kRows / 2 : kRows;
   const int ctas = (a.rows + per - 1) / per;
   return launch_dependent(ctas <= kFew * device_sm_count()
-                              ? dense_skinny_kernel<GATED, HALF, NB, kFew>
-                              : dense_skinny_kernel<GATED, HALF, NB, kFew + 1>,
+                              ? dense_skinny_kernel<EPI, HALF, NB, kFew>
+                              : dense_skinny_kernel<EPI, HALF, NB, kFew + 1>,
                           dim3((unsigned)ctas), dim3(kThreads), 0, s, a);
 }
 
-template <bool GATED, bool HALF>
+template <int EPI, bool HALF>
 cudaError_t launch_n(const SkinnyArgs &a, cudaStream_t s) {
-  if (a.n <= 8) return launch_nb<GATED, HALF, 1>(a, s);
-  return a.n <= 16 ? launch_nb<GATED, HALF, 2>(a, s) : launch_nb<GATED, HALF, 4>(a, s);
+  if (a.n <= 8) return launch_nb<EPI, HALF, 1>(a, s);
+  return a.n <= 16 ? launch_nb<EPI, HALF, 2>(a, s) : launch_nb<EPI, HALF, 4>(a, s);
+}
+
+template <int EPI>
+cudaError_t launch_epi(const SkinnyArgs &a, cudaStream_t s) {
+  return a.e.half ? launch_n<EPI, true>(a, s) : launch_n<EPI, false>(a, s);
 }
 
 }  // namespace
@@ -190,11 +229,15 @@ bool dense_skinny(int64_t n, int64_t out, int64_t in) {
 }
 
 cudaError_t launch_dense_skinny(const DenseProduct &p, cudaStream_t s) {
-  const bool gated = p.kind == EPI_GATED;
-  SkinnyArgs a{static_cast<const uint16_t *>(p.a.p), static_cast<const uint16_t *>(p.b.p),
-               (int)p.M, (int)(gated ? p.N / 2 : p.N), (int)p.K, p.b.pairs, p.epi};
-  if (gated) return p.epi.half ? launch_n<true, true>(a, s) : launch_n<true, false>(a, s);
-  return p.epi.half ? launch_n<false, true>(a, s) : launch_n<false, false>(a, s);
+  const bool pairs = p.kind == EPI_GATED || p.kind == EPI_DGATED;
+  const SkinnyArgs a{static_cast<const uint16_t *>(p.a.p), static_cast<const uint16_t *>(p.b.p),
+                     (int)p.M, (int)(pairs ? p.N / 2 : p.N), (int)p.K, p.b.pairs, p.epi};
+  switch (p.kind) {
+    case EPI_GATED: return launch_epi<EPI_GATED>(a, s);
+    case EPI_DGATED: return launch_epi<EPI_DGATED>(a, s);
+    case EPI_DACT: return launch_epi<EPI_DACT>(a, s);
+    default: return launch_epi<EPI_LINEAR>(a, s);
+  }
 }
 
 }  // namespace moe
