@@ -467,8 +467,10 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
+  // MXFP8: the preceding kernel lays out the scales and has itself waited for
+  // all before it, so only the scales' loads wait for it
   pdl_launch_dependents();
-  pdl_wait();
+  if constexpr (!MX) pdl_wait();
   __syncthreads();
   tc_fence_before();
   cluster_sync();  // both CTAs' barriers and TMEM exist before any cross-CTA use
@@ -490,35 +492,54 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
       const CUtensorMap *mb = GRAD              ? &maps.m[2 * w.p + kMapB]
                               : w.n < p.n_full ? &maps.m[kMapB]
                                                : &maps.m[kMapBLast];
-      for (int kb = w.k_lo; kb < w.k_hi; ++kb) {
+      auto load_operands = [&](int s, int kb) {
+        const uint32_t fb = map_to_rank(full_bar(s), 0);
+        if (leader) mbar_arrive_expect_tx(full_bar(s), tx);
+        const int k0 = kb * kStepK;
+        if (!GRAD || p.a_k_major) {
+          tma_load_2d_pair(a_addr(s), ma, fb, k0, m0);
+        } else {
+          tma_load_2d_pair(a_addr(s), ma, fb, m0, k0);
+          tma_load_2d_pair(a_addr(s) + 8192u, ma, fb, m0 + 64, k0);
+        }
+        if constexpr (GRAD) {
+          tma_load_2d_pair(b_addr(s), mb, fb, n0, k0);
+          if (w.b_bytes > 8192) tma_load_2d_pair(b_addr(s) + 8192u, mb, fb, n0 + 64, k0);
+        } else if (args.pairs) {
+          tma_load_3d_pair(b_addr(s), mb, fb, k0, 0, n0 / 2);
+        } else {
+          tma_load_2d_pair(b_addr(s), mb, fb, k0, n0);
+        }
+      };
+      auto load_scales = [&](int s, int kb) {  // x's own rows, w's all: each CTA
+        const uint32_t fb = map_to_rank(full_bar(s), 0);  // multiplies every column
+        tma_load_2d_pair(scale_addr(s), &maps.m[kMapSa], fb, 0,
+                         (w.m * 2 + (int)rank) * p.num_kb + kb);
+        tma_load_2d_pair(scale_addr(s) + kScaleBlock, &maps.m[kMapSb], fb, 0,
+                         (w.n * p.num_kb + kb) * 2);
+      };
+      int kb = w.k_lo;
+      if constexpr (MX) {
+        if (u == first) {  // the ring's first codes, ahead of the scales
+          const int ahead = w.k_hi - w.k_lo < stages ? w.k_hi - w.k_lo : stages;
+          for (int i = 0; i < ahead; ++i)
+            if (elect_one()) load_operands(i, kb + i);
+          pdl_wait();
+          for (int i = 0; i < ahead; ++i)
+            if (elect_one()) load_scales(i, kb + i);
+          kb += ahead;
+          issued = (uint32_t)ahead;
+          stage = ahead == stages ? 0 : ahead;
+          phase = ahead == stages ? 1u : 0u;
+        }
+      }
+      for (; kb < w.k_hi; ++kb) {
         ok = wait_bounded(empty_bar(stage), phase ^ 1u, s_abort, args.status, args.timeout_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (elect_one()) {
-          const uint32_t fb = map_to_rank(full_bar(stage), 0);
-          if (leader) mbar_arrive_expect_tx(full_bar(stage), tx);
-          const int k0 = kb * kStepK;
-          if (!GRAD || p.a_k_major) {
-            tma_load_2d_pair(a_addr(stage), ma, fb, k0, m0);
-          } else {
-            tma_load_2d_pair(a_addr(stage), ma, fb, m0, k0);
-            tma_load_2d_pair(a_addr(stage) + 8192u, ma, fb, m0 + 64, k0);
-          }
-          if constexpr (GRAD) {
-            tma_load_2d_pair(b_addr(stage), mb, fb, n0, k0);
-            if (w.b_bytes > 8192)
-              tma_load_2d_pair(b_addr(stage) + 8192u, mb, fb, n0 + 64, k0);
-          } else if (args.pairs) {
-            tma_load_3d_pair(b_addr(stage), mb, fb, k0, 0, n0 / 2);
-          } else {
-            tma_load_2d_pair(b_addr(stage), mb, fb, k0, n0);
-          }
-          if constexpr (MX) {  // x's own rows, w's all: each CTA multiplies every column
-            tma_load_2d_pair(scale_addr(stage), &maps.m[kMapSa], fb, 0,
-                             (w.m * 2 + (int)rank) * p.num_kb + kb);
-            tma_load_2d_pair(scale_addr(stage) + kScaleBlock, &maps.m[kMapSb], fb, 0,
-                             (w.n * p.num_kb + kb) * 2);
-          }
+          load_operands(stage, kb);
+          if constexpr (MX) load_scales(stage, kb);
         }
         issued = issued < (uint32_t)stages ? issued + 1 : (uint32_t)stages;
         if (++stage == stages) {
@@ -776,8 +797,8 @@ __device__ __forceinline__ uint32_t scale_word(const uint8_t *p, int left) {
 template <int BYTES>
 __global__ void __launch_bounds__(256)
 mx8_layout_kernel(const ScaleLayout a, const ScaleLayout b, int G, int num_kb) {
+  pdl_wait();  // first: the product that follows starts on this kernel's word
   pdl_launch_dependents();
-  pdl_wait();
   const int64_t na = (int64_t)a.tiles * a.blocks * num_kb * 32;
   const int64_t nb = (int64_t)b.tiles * b.blocks * num_kb * 32;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < na + nb;
@@ -1097,7 +1118,7 @@ cudaError_t launch_dense(const DenseProduct &p, const DensePlan &plan, uint8_t *
     const ScaleLayout la{p.a.scales, blocks, p.M, 2 * plan.m_tiles, kRowsCta, 1, 0};
     const ScaleLayout lb{p.b.scales, sb, p.N, plan.n_tiles, plan.tn, 2, p.b.pairs};
     int64_t grid = ((a_blocks + b_blocks) * 32 + 255) / 256;
-    const int64_t cap = (int64_t)device_sm_count() * 8;
+    const int64_t cap = (int64_t)device_sm_count() * 4;  // room for the product's CTAs
     if (grid > cap) grid = cap;
     const int G = (int)(p.K / 32);
     const uintptr_t bits = (uintptr_t)p.a.scales | (uintptr_t)p.b.scales | (uintptr_t)G;
