@@ -1,7 +1,10 @@
-"""A MoE layer trained and then served with 4-bit experts.
+"""A MoE layer trained and then served with 4-bit experts, and the dense block
+(a shared expert) beside it.
 
     python examples/moe_layer.py train     # a few steps of gradient descent
     python examples/moe_layer.py decode    # the layer's experts in MXFP4, token by token
+    python examples/moe_layer.py block     # norm, shared expert, residual: a few training
+                                           # steps, then the same block in MXFP8
 
 Training runs the experts as plain torch products on their contiguous slices
 of the dispatched rows; the way there and back, and the gradients of both and
@@ -13,6 +16,12 @@ of the router's weights, are the library's calls:
 
 Serving quantises the experts once and calls forward_q4 for every step: three
 kernels, no host synchronisation.
+
+The block is three calls forward and three back:
+
+    s, y = rms_norm(x, residual) -> h = gated_linear(y) -> out = linear(h) + s
+    d_out -> linear_backward -> gated_linear_backward -> rms_norm_backward
+          (+ d_out, through the residual) -> d_x
 """
 import os
 import sys
@@ -132,11 +141,83 @@ def decode(H=2880, E=32, I=2880, k=4, tokens=8, seed=0):
     return out, want
 
 
+class Block:
+    """norm [H], w13 [2I, H] (packed gate, up) and w2 [H, I], bf16 with fp32 masters."""
+
+    def __init__(self, H, I, seed=0):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.params = moe.make_params(act="swiglu", layout="packed")
+        self.master = [torch.ones(H, device="cuda"),
+                       torch.randn(2 * I, H, generator=g, device="cuda") * H ** -0.5,
+                       torch.randn(H, I, generator=g, device="cuda") * I ** -0.5]
+        self.cast()
+
+    def cast(self):
+        self.norm, self.w13, self.w2 = (m.to(torch.bfloat16) for m in self.master)
+
+    def forward(self, x, residual):
+        """out, and what the backward pass needs."""
+        y, s = moe.rms_norm(x, self.norm, residual=residual)
+        h = moe.gated_linear(y, self.w13, self.params)
+        return moe.linear(h, self.w2, residual=s), (y, s, h)
+
+    def backward(self, d_out, kept):
+        """(d_x, which is the residual's gradient too, and those of the weights)."""
+        y, s, h = kept
+        d_h, d_w2, _ = moe.linear_backward(d_out, h, self.w2)
+        d_y, d_w13 = moe.gated_linear_backward(d_h, y, self.w13, self.params)
+        d_x, d_norm = moe.rms_norm_backward(d_y, s, self.norm, d_sum=d_out)
+        return d_x, (d_norm, d_w13, d_w2)
+
+
+def quantise_mxfp8(w):
+    """Mx8 rows of float weights [R, C]: E4M3 codes, the least scale of each 32
+    under which none exceeds 448."""
+    v = w.float().view(w.shape[0], -1, 32)
+    e = torch.ceil(torch.log2(v.abs().amax(dim=2).clamp_min(2.0 ** -100) / 448.0))
+    codes = (v / torch.exp2(e)[..., None]).view_as(w).to(torch.float8_e4m3fn)
+    return moe.Mx8(codes, (e + 127.0).to(torch.uint8))
+
+
+def serve_mxfp8(block, x, residual):
+    """The block with 8 bits between its products: the norm and the gated
+    product write them, the next product reads them."""
+    y, s = moe.rms_norm(x, block.norm, residual=residual, mx8=True)
+    h = moe.gated_linear(y, quantise_mxfp8(block.w13), block.params, mx8=True)
+    return moe.linear(h, quantise_mxfp8(block.w2), residual=s)
+
+
+def train_block(H=512, I=1408, n=1024, steps=20, rate=0.5, seed=0):
+    """A block learns another's outputs; returns it, its losses and its inputs."""
+    teacher, block = Block(H, I, seed + 1), Block(H, I, seed)
+    g = torch.Generator(device="cuda").manual_seed(seed + 2)
+    x, residual = (torch.randn(n, H, generator=g, device="cuda").to(torch.bfloat16)
+                   for _ in range(2))
+    target = teacher.forward(x, residual)[0]
+    losses = []
+    for _ in range(steps):
+        out, kept = block.forward(x, residual)
+        off = out.float() - target.float()
+        losses.append((off ** 2).mean().item())
+        _, grads = block.backward((off * (2.0 / n)).to(torch.bfloat16), kept)
+        for m, d in zip(block.master, grads):
+            m -= rate * d.float()
+        block.cast()
+    return block, losses, x, residual
+
+
 if __name__ == "__main__":
     what = sys.argv[1] if len(sys.argv) > 1 else "train"
     if what == "train":
         for i, loss in enumerate(train()):
             print(f"step {i:2d}  loss {loss:.5f}")
+    elif what == "block":
+        block, losses, x, residual = train_block()
+        for i, loss in enumerate(losses):
+            print(f"step {i:2d}  loss {loss:.5f}")
+        a, b = serve_mxfp8(block, x, residual), block.forward(x, residual)[0]
+        err = (a.float() - b.float()).norm() / b.float().norm()
+        print(f"in 8 bits: relative distance to the bf16 block {err:.5f}")
     else:
         a, b = decode()
         err = (a.float() - b.float()).norm() / b.float().norm()
