@@ -417,7 +417,8 @@ def _need_rows(t: torch.Tensor, name: str) -> int:
     if not isinstance(t, torch.Tensor) or t.dtype not in DTYPE:
         raise ValueError(f"{name} must be a bfloat16, float16 or float32 tensor")
     device = t.get_device()
-    _need_on(t, name, t.dtype, device)
+    if device < 0 or not t.is_contiguous():
+        _need_on(t, name, t.dtype, device)
     if t.dim() != 2 or t.shape[1] == 0:
         raise ValueError(f"{name} must have shape [rows, H], got {tuple(t.shape)}")
     return device
@@ -775,6 +776,15 @@ def _scratch(ws: Optional[torch.Tensor], size: int, like: torch.Tensor, device: 
     return ws, ws.data_ptr(), ws.numel()
 
 
+def _weight_vector(weight: torch.Tensor, dt: torch.dtype, device: int, H: int):
+    """(address, type) of a norm's weights: [H] of the rows' type or fp32."""
+    if (isinstance(weight, torch.Tensor) and (weight.dtype is dt or weight.dtype is torch.float32)
+            and weight.dim() == 1 and weight.numel() == H and weight.is_contiguous()
+            and weight.get_device() == device):
+        return weight.data_ptr(), DTYPE[weight.dtype]
+    return _need_vector(weight, "weight", (dt, torch.float32), device, H), DTYPE[weight.dtype]
+
+
 def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float = 1e-5,
              residual: Optional[torch.Tensor] = None, mx8: bool = False, out=None,
              sum_out: Optional[torch.Tensor] = None):
@@ -783,15 +793,17 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float = 1e-5,
     norm is of s = x + residual, rounded to x's type, and the result is (y, s).
     mx8: y is Mx8 rows (H a multiple of 32). out, sum_out: where y and s go."""
     device = _need_rows(x, "x")
-    n, H = x.shape
-    w_dtype, w = DTYPE[x.dtype], None
+    n, H = shape = x.shape
+    dt = x.dtype
+    dtype = w_dtype = DTYPE[dt]
+    w = r = t = total = None
     if weight is not None:
-        w = _need_vector(weight, "weight", (x.dtype, torch.float32), device, H)
-        w_dtype = DTYPE[weight.dtype]
-    total = None
+        w, w_dtype = _weight_vector(weight, dt, device, H)
     if residual is not None:
-        _need_on(residual, "residual", x.dtype, device, (n, H))
-        total = _out_like(sum_out, "sum_out", x)
+        _need_on(residual, "residual", dt, device, shape)
+        r = residual.data_ptr()
+        total = torch.empty_like(x) if sum_out is None else _out_like(sum_out, "sum_out", x)
+        t = total.data_ptr()
     elif sum_out is not None:
         raise ValueError("sum_out needs a residual")
     if mx8:
@@ -799,12 +811,12 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float = 1e-5,
             y = _empty_mx8(n, H, x, device)
         else:
             y = out
-            _need_mx8(y, "out", device, (n, H))
+            _need_mx8(y, "out", device, shape)
+        _run("moe_rms_norm", device, x.data_ptr(), r, w, w_dtype, n, H, dtype, eps, None, y, t)
     else:
-        y = _out_like(out, "out", x)
-    _run("moe_rms_norm", device, x.data_ptr(), None if residual is None else residual.data_ptr(),
-         w, w_dtype, n, H, DTYPE[x.dtype], eps, None if mx8 else y.data_ptr(),
-         y if mx8 else None, None if total is None else total.data_ptr())
+        y = torch.empty_like(x) if out is None else _out_like(out, "out", x)
+        _run("moe_rms_norm", device, x.data_ptr(), r, w, w_dtype, n, H, dtype, eps, y.data_ptr(),
+             None, t)
     return y if residual is None else (y, total)
 
 
@@ -832,8 +844,7 @@ def rms_norm_backward(d_y: torch.Tensor, x: torch.Tensor, weight: Optional[torch
         _need_on(d_sum, "d_sum", x.dtype, device, (n, H))
     w_dtype, w, d_weight, size = DTYPE[x.dtype], None, None, 0
     if weight is not None:
-        w = _need_vector(weight, "weight", (x.dtype, torch.float32), device, H)
-        w_dtype = DTYPE[weight.dtype]
+        w, w_dtype = _weight_vector(weight, x.dtype, device, H)
         d_weight = torch.empty_like(weight)
         size = rms_norm_backward_workspace_size(n, H)
     d_x = torch.empty_like(x)
