@@ -366,9 +366,9 @@ DensePlan dense_plan(int64_t M, int64_t N, int64_t K, int kind, bool mx);
 // blocks and partial: scratch of plan.blocks and plan.partial bytes.
 cudaError_t launch_dense(const DenseProduct &p, const DensePlan &plan, uint8_t *blocks,
                          float *partial, int32_t *status, cudaStream_t s);
-// A product of few 16-bit rows (any kind but EPI_GATED_MX), where dense_skinny
-// says so (dense_skinny.cu). No scratch.
-bool dense_skinny(int64_t n, int64_t out, int64_t in);
+// A product of few rows, where dense_skinny says so (dense_skinny.cu). No
+// scratch.
+bool dense_skinny(int64_t n, int64_t out, int64_t in, int kind, bool mx);
 cudaError_t launch_dense_skinny(const DenseProduct &p, cudaStream_t s);
 
 // Plans of two gradients that go in one launch.

@@ -54,7 +54,7 @@ moe_status check_workspace(const void *ws, size_t have, size_t need) {
 char *at(void *ws, size_t off) { return static_cast<char *>(ws) + off; }
 
 // --------------------------------------------------------------- products --
-// How a forward product runs: few 16-bit rows without a workspace, else by a
+// How a forward product runs: few rows without a workspace, else by a
 // plan, with the 8-bit scales in the tensor core's layout and the parts of a
 // split sum in the workspace.
 struct ForwardPlan {
@@ -64,7 +64,7 @@ struct ForwardPlan {
 };
 ForwardPlan forward_plan(int64_t n, int64_t out, int64_t in, int kind, bool mx) {
   ForwardPlan f{};
-  f.skinny = !mx && kind != EPI_GATED_MX && dense_skinny(n, out, in);
+  f.skinny = dense_skinny(n, out, in, kind, mx);
   if (f.skinny) return f;
   f.plan = dense_plan(n, out, in, kind, mx);
   f.bytes = align_up(f.plan.blocks, kAlign) + align_up(f.plan.partial, kAlign);
@@ -143,7 +143,7 @@ struct GradLayout {
 };
 GradLayout grad_layout(int64_t n, int64_t out, int64_t in, int kind, bool own_d, bool columns) {
   GradLayout g{};
-  g.skinny = dense_skinny(n, out, in);
+  g.skinny = dense_skinny(n, out, in, kind, false);
   if (own_d && !g.skinny) g.sums = dense_plan(n, out, in, kind, false);
   dense_plan_two(n, in, out, out, in, n, &g.d_x, &g.d_w);
   g.partial = own_d ? align_up((size_t)n * out * 2, kAlign) : 0;

@@ -14,6 +14,7 @@ def gen(seed):
 
 
 @pytest.mark.parametrize("n,R,C", [(1, 8, 32), (5, 33, 96), (8, 2880, 2880), (33, 200, 128),
+                                   (1, 2880, 2880), (9, 77, 1440), (16, 5761, 2880), (17, 96, 160),
                                    (64, 5761, 1408), (129, 193, 160), (257, 1000, 2880),
                                    (1000, 513, 512), (2047, 5760, 2880)])
 def test_linear(n, R, C):
@@ -35,7 +36,8 @@ def test_linear(n, R, C):
 
 @pytest.mark.parametrize("layout", ["packed", "interleaved"])
 @pytest.mark.parametrize("act", ["swiglu", "swiglu_oai"])
-@pytest.mark.parametrize("n,H,I", [(1, 32, 32), (7, 96, 40), (8, 2880, 2880), (40, 160, 64),
+@pytest.mark.parametrize("n,H,I", [(1, 32, 32), (7, 96, 40), (8, 2880, 2880), (16, 1440, 416),
+                                   (17, 64, 96), (40, 160, 64),
                                    (129, 512, 1408), (600, 288, 352), (2048, 2880, 96)])
 def test_gated_linear(n, H, I, act, layout):
     g = gen(n + I)
@@ -53,7 +55,7 @@ def test_gated_linear(n, H, I, act, layout):
 
 
 @pytest.mark.parametrize("layout", ["packed", "interleaved"])
-@pytest.mark.parametrize("n,H,I", [(1, 64, 32), (8, 2880, 2880), (33, 72, 96), (257, 512, 1408),
+@pytest.mark.parametrize("n,H,I", [(1, 64, 32), (8, 2880, 2880), (13, 264, 160), (33, 72, 96), (257, 512, 1408),
                                    (1500, 328, 160)])
 def test_gated_linear_writes_mx8(n, H, I, layout):
     """16-bit operands, the result in 8 bits."""
@@ -66,7 +68,8 @@ def test_gated_linear_writes_mx8(n, H, I, layout):
     check_mx8(q.codes, q.scales, h, slack)
 
 
-def test_every_scale_and_code():
+@pytest.mark.parametrize("n", [140, 5, 16])
+def test_every_scale_and_code(n):
     """Each row's own scales and each code at its place: x and w have one group
     that is not zero, with a scale of its own; all 254 finite codes occur."""
     C, R = 288, 256
@@ -76,7 +79,6 @@ def test_every_scale_and_code():
     for j in range(C // 32):
         wc[j::C // 32, 32 * j] = codes[j::C // 32]
     ws = (100 + torch.arange(R * C // 32, device="cuda") % 50).to(torch.uint8).view(R, C // 32)
-    n = 140
     xc = torch.full((n, C), 56, dtype=torch.uint8, device="cuda")   # 1.0
     xs = (110 + torch.arange(n * C // 32, device="cuda") % 37).to(torch.uint8).view(n, C // 32)
     wc, xc = wc.view(torch.float8_e4m3fn), xc.view(torch.float8_e4m3fn)
@@ -85,25 +87,27 @@ def test_every_scale_and_code():
     assert torch.equal(got.double(), want)            # one product each: exact in bf16
 
 
-def test_nan_reaches_its_rows_alone():
+@pytest.mark.parametrize("n", [200, 18, 16, 6])
+def test_nan_reaches_its_rows_alone(n):
     g = gen(1)
-    n, R, C = 200, 224, 192
+    R, C = 224, 192
     (xc, xs), (wc, ws) = mx8_rows(g, n, C), mx8_rows(g, R, C)
     want, _ = product(mx8_value(xc, xs), mx8_value(wc, ws))
-    xs[17, 3] = 255                                   # a scale that is NaN
+    xs[n - 2, 3] = 255                                   # a scale that is NaN
     wc.view(torch.uint8)[150, 100] = 127              # a code that is NaN
     got = moe.linear(moe.Mx8(xc, xs), moe.Mx8(wc, ws))
     bad = torch.zeros(n, R, dtype=torch.bool, device="cuda")
-    bad[17], bad[:, 150] = True, True
+    bad[n - 2], bad[:, 150] = True, True
     assert torch.equal(torch.isnan(got), bad)
     assert torch.allclose(got.double()[~bad], want[~bad], rtol=2.0 ** -7, atol=1e-3)
 
 
-def test_block_in_8_bits():
+@pytest.mark.parametrize("n", [300, 1, 11])
+def test_block_in_8_bits(n):
     """norm -> gated_linear -> linear, 8 bits between them, as a served block
     runs; each step against the formula on the rows that it was given."""
     g = gen(2)
-    n, H, I = 300, 320, 416
+    H, I = 320, 416
     x, res = randn(g, n, H), randn(g, n, H)
     w = (1 + 0.1 * randn(g, H, dtype=torch.float32)).to(torch.bfloat16)
     (c13, s13), (c2, s2) = mx8_rows(g, 2 * I, H, H ** -0.5), mx8_rows(g, H, I, I ** -0.5)

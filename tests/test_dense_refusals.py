@@ -40,13 +40,13 @@ CALLS = {
                                   eps=1e-5, d_x=P, d_weight=P, ws=P, bytes=PLENTY),
     "moe_linear": dict(x=P, w=P, bias=P, residual=P, n=100, R=64, C=2880, dtype=0, act=1, y=P,
                        ws=P, bytes=PLENTY, status=P),
-    "moe_linear_mx8": dict(x8=rows8(), w8=rows8(), bias=P, residual=P, n=4, R=64, C=64, dtype=0,
+    "moe_linear_mx8": dict(x8=rows8(), w8=rows8(), bias=P, residual=P, n=40, R=64, C=64, dtype=0,
                            act=0, y=P, ws=P, bytes=PLENTY, status=P),
     "moe_linear_backward": dict(d_y=P, x=P, w=P, bias=P, n=4, R=64, C=64, dtype=0, act=1, d_x=P,
                                 d_w=P, d_bias=P, ws=P, bytes=PLENTY, status=P),
     "moe_gated_linear": dict(x=P, w13=P, n=100, H=2880, I=64, params=params(), dtype=0, h=P,
                              h8=None, ws=P, bytes=PLENTY, status=P),
-    "moe_gated_linear_mx8": dict(x8=rows8(), w8=rows8(), n=4, H=64, I=64, params=params(),
+    "moe_gated_linear_mx8": dict(x8=rows8(), w8=rows8(), n=40, H=64, I=64, params=params(),
                                  dtype=0, h=None, h8=rows8(), ws=P, bytes=PLENTY, status=P),
     "moe_gated_linear_backward": dict(d_h=P, x=P, w13=P, n=4, H=64, I=64, params=params(),
                                       dtype=0, d_x=P, d_w13=P, ws=P, bytes=PLENTY, status=P),
@@ -134,9 +134,11 @@ def test_workspace_sizes(L):
     assert moe.linear_workspace_size(8, 2880, 2880) == 0          # few rows
     assert moe.linear_workspace_size(8192, 2880, 2880) == 0       # more tiles than SMs
     assert moe.linear_workspace_size(200, 256, 8192) > 0          # a split sum
-    assert moe.linear_workspace_size(8, 64, 64, True) > 0         # scales laid out
+    assert moe.linear_workspace_size(8, 64, 64, True) == 0
+    assert moe.linear_workspace_size(40, 64, 64, True) > 0        # scales laid out
     assert moe.gated_linear_workspace_size(8, 64, 64) == 0
-    assert moe.gated_linear_workspace_size(8, 64, 64, True, True) > 0
+    assert moe.gated_linear_workspace_size(8, 64, 64, True, True) == 0
+    assert moe.gated_linear_workspace_size(40, 64, 64, True, True) > 0
     assert moe.rms_norm_backward_workspace_size(8, 64) > 0
     assert moe.linear_backward_workspace_size(64, 64, 64) >= 0
     for bad in ((8, 64, 60), (-1, 64, 64), (8, 0, 64)):
