@@ -550,7 +550,8 @@ typedef enum {
  * `dtype` (MOE_BF16, MOE_FP16 or MOE_FP32; s = x without a residual): x, residual, y, sum
  * [n, H], any H. weight [H] of `dtype` or MOE_FP32, NULL = ones. sum: optional
  * output s (needs a residual). The result goes to exactly one of y and y_mx8
- * (H a multiple of 32). eps >= 0. */
+ * (H a multiple of 32). eps >= 0. The squares are summed in fp32: a row with
+ * values above about 1e19 comes out as zeros. */
 moe_status moe_rms_norm(const void *x, const void *residual, const void *weight,
                         int32_t weight_dtype, int64_t n, int32_t H, int32_t dtype, float eps,
                         void *y, const moe_mx8_rows *y_mx8, void *sum, moe_stream stream);

@@ -18,7 +18,7 @@
 //   warp 0      TMA producer (each CTA its own halves; bytes counted on the
 //               leader's barrier)
 //   warp 1      TMEM allocation; the leader's issues the MMAs
-//   warps 2..   epilogue, two or four per TMEM lane quarter, column chunks in turn
+//   warps 2..   epilogue, two to four per TMEM lane quarter, column chunks in turn
 // MXFP8 operands (moe_linear_mx8, moe_gated_linear_mx8) take the same kernel:
 // E4M3 codes with one power of two per 32 of them, which the tensor core
 // applies itself (kind::mxf8f6f4, block_scale), so nothing is converted and
@@ -47,8 +47,10 @@ constexpr int kMaxTn = 256;
 // epilogue has the latency of two column chunks; a group of 32 8-bit results
 // takes 64 columns and twice the registers, rows off 16 bytes 124 registers
 // (922 x 5281 x 280: 24.9 us with four, where they spill, 16.0 with three,
-// 16.9 with two).
-constexpr int epi_warps(int epi) { return epi == EPI_GATED_MX ? 8 : epi == EPI_COLUMNS ? 12 : 16; }
+// 16.9 with two), an activation's gradient 100 (three and four take the same time).
+constexpr int epi_warps(int epi) {
+  return epi == EPI_GATED_MX ? 8 : epi == EPI_COLUMNS || epi == EPI_DACT ? 12 : 16;
+}
 constexpr int gemm_threads(int epi) { return (2 + epi_warps(epi)) * 32; }
 constexpr int kRingBytes = 220 * 1024;
 constexpr int kMaxStages = 8;

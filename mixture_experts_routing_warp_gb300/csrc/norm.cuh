@@ -95,12 +95,6 @@ __device__ __forceinline__ void load_pack(const T *p, float (&f)[VEC]) {
   r.load(p);
   r.get(f);
 }
-template <typename T, int VEC>
-__device__ __forceinline__ void store_pack(T *p, const float (&f)[VEC]) {
-  Raw<T, VEC> r;
-  r.set(f);
-  r.store(p);
-}
 // VEC weights of WT (the rows' type or fp32); ones where there are none. Shifted
 // rows take them one by one, from L1.
 template <typename WT, int VEC, bool SHIFT = false>

@@ -125,6 +125,31 @@ def test_two_graphs_and_an_eager_call_at_a_time():
             assert same(want_b, out_b) and same(want_c, out_c) and same(want_b, eager), name
 
 
+def test_two_host_threads():
+    """Two threads call at once, on one stream and on two."""
+    import threading
+
+    b, c = Block(90, 256, 512, 1), Block(90, 256, 512, 2)
+    want = [{k: fn() for k, fn in x.calls().items()} for x in (b, c)]
+    torch.cuda.synchronize()
+    for streams in ([None, None], [torch.cuda.Stream(), torch.cuda.Stream()]):
+        bad = []
+
+        def work(i):
+            with torch.cuda.stream(streams[i]):
+                for _ in range(10):
+                    got = {k: fn() for k, fn in (b, c)[i].calls().items()}
+                    torch.cuda.current_stream().synchronize()
+                    bad.extend(k for k in got if not same(want[i][k], got[k]))
+
+        threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        assert not bad, bad
+
+
 def test_buffers_of_the_callers():
     b = Block(130, 512, 1024, 3)
     n, H = b.x.shape
