@@ -69,6 +69,25 @@ __device__ __forceinline__ float scale_of(uint32_t b) {
   return __uint_as_float(b == 0u ? 0x00400000u : b == 255u ? 0x7fc00000u : b << 23);
 }
 
+// The smaller and the larger of two scales, NaN where either is.
+__device__ __forceinline__ float lesser(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float greater(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// part s t + acc. A group's sum is 0 or 2^-18 to 2^22.6 and the scales are powers of two from 2^-127
+// to 2^127, so neither part s nor s t need be in fp32's range where part s t is. The
+// lesser scale goes first: that is exact (part is a multiple of 2^-18, and 2^-145 is
+// in fp32), and too large only where the result is.
+__device__ __forceinline__ float scaled(float part, float s, float t, float acc) {
+  return fmaf(part * lesser(s, t), greater(s, t), acc);
+}
+
 __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                             uint32_t a3, uint32_t b0, uint32_t b1, bool half) {
   if (half)
@@ -203,10 +222,10 @@ __device__ __forceinline__ void sum8(const SkinnyArgs &a, int mt, int slice, int
         mma_16x8x16(part, a0[0], a1[0], a0[1], a1[1], x0, x1, true);
         mma_16x8x16(part, a0[2], a1[2], a0[3], a1[3], x2, x3, true);
         const float t0 = sx[nb * 8 * wide + b + u], t1 = sx[(nb * 8 + 1) * wide + b + u];
-        acc[nb][0] = fmaf(part[0] * s0, t0, acc[nb][0]);
-        acc[nb][1] = fmaf(part[1] * s0, t1, acc[nb][1]);
-        acc[nb][2] = fmaf(part[2] * s1, t0, acc[nb][2]);
-        acc[nb][3] = fmaf(part[3] * s1, t1, acc[nb][3]);
+        acc[nb][0] = scaled(part[0], s0, t0, acc[nb][0]);
+        acc[nb][1] = scaled(part[1], s0, t1, acc[nb][1]);
+        acc[nb][2] = scaled(part[2], s1, t0, acc[nb][2]);
+        acc[nb][3] = scaled(part[3], s1, t1, acc[nb][3]);
       }
     }
   }
