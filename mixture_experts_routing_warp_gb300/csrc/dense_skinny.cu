@@ -190,8 +190,8 @@ __device__ __forceinline__ void sum8(const SkinnyArgs &a, int mt, int slice, int
   const float *sw0 = s_w + (mt * kRows + g) * wide + lo, *sw1 = sw0 + 8 * wide;
   const float *sx = s_x + 2 * t * wide + lo;
   const int count = hi - lo;
-  for (int b = 0; b < count; b += U) {
-    uint2 q0[U], q1[U], xq[U][NB];
+  uint2 q0[U], q1[U], xq[U][NB];
+  auto fetch = [&](int b) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const bool in = b + u < count;
@@ -203,7 +203,11 @@ __device__ __forceinline__ void sum8(const SkinnyArgs &a, int mt, int slice, int
         if (in) xq[u][nb] = __ldg(reinterpret_cast<const uint2 *>(x[nb] + (b + u) * 32));
       }
     }
-    if (b == 0) __syncthreads();  // the scales, with the first codes on their way
+  };
+  fetch(0);
+  __syncthreads();  // the scales, with the first codes on their way
+  for (int b = 0; b < count; b += U) {
+    if (b > 0) fetch(b);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (b + u >= count) break;
@@ -229,7 +233,6 @@ __device__ __forceinline__ void sum8(const SkinnyArgs &a, int mt, int slice, int
       }
     }
   }
-  if (count == 0) __syncthreads();
 }
 
 // NB blocks of 8 tokens; CTAS per SM that registers are left for.
