@@ -646,9 +646,10 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
         if constexpr (EPI == EPI_COLUMNS) fetch_columns(p.e, row0, c0 + part * W, column_add);
         else fetch_rows<EPI>(p.e, row0, c0 + part * W, add);
       }
-      if (!wait_bounded(tfull_bar(acc), (uint32_t)(local >> 1) & 1u, s_abort, args.status,
-                        args.timeout_ns))
-        break;
+      const bool ok = wait_bounded(tfull_bar(acc), (uint32_t)(local >> 1) & 1u, s_abort,
+                                   args.status, args.timeout_ns);
+      // all lanes or none: the loads from TMEM and the exchanges below take the whole warp
+      if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * acc_cols(MX));
       const bool partial = EPI == EPI_PARTIAL || (GRAD && p.partial);
