@@ -26,7 +26,8 @@
  * the dense blocks beside the experts, with gradients (moe_rms_norm,
  * moe_linear, moe_gated_linear, their _backward and _mx8 forms),
  * the workspace calls (moe_workspace_size, moe_workspace_init,
- * moe_workspace_regions), moe_read_status and moe_selftest_wait_timeout.
+ * moe_workspace_regions), moe_read_status, moe_selftest_wait_timeout and
+ * moe_selftest_linear_timeout.
  *
  * Sources (page title, section):
  *  [R1] "Reuse topk SparseMatrix routing metadata in GPT-OSS MoE forward"
@@ -691,6 +692,16 @@ moe_status moe_read_status(void *workspace, size_t workspace_bytes, int32_t rese
  * a fault or a hang. Read the result with moe_read_status. */
 moe_status moe_selftest_wait_timeout(void *workspace, size_t workspace_bytes, uint64_t timeout_ns,
                                      moe_stream stream);
+
+/* DIAGNOSTIC -- moe_linear (without bias, activation or residual) whose steps
+ * wait for bytes that nobody sends: every wait of the product's roles gives up
+ * after `timeout_ns` (1 .. 1e9), MOE_ERR_TIMEOUT goes to `status` (required), and
+ * the kernel frees what it holds and returns. y is left undefined. Sizes that
+ * take the tensor tiles (more than 32 rows); workspace as moe_linear's. */
+moe_status moe_selftest_linear_timeout(const void *x, const void *w, int64_t n, int32_t R,
+                                       int32_t C, int32_t dtype, void *y, void *workspace,
+                                       size_t workspace_bytes, uint64_t timeout_ns,
+                                       int32_t *status, moe_stream stream);
 
 #ifdef __cplusplus
 }

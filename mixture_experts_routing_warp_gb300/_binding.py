@@ -127,6 +127,8 @@ SIGNATURES = {
                                          _SZ, _P, _P]),
     "moe_read_status": (_I32, [_P, _SZ, _I32, _P]),
     "moe_selftest_wait_timeout": (_I32, [_P, _SZ, _U64, _P]),
+    "moe_selftest_linear_timeout": (_I32, [_P, _P, _I64, _I32, _I32, _I32, _P, _P, _SZ, _U64, _P,
+                                           _P]),
 }
 
 

@@ -360,6 +360,7 @@ struct DenseProduct {
   int64_t M, N, K;
   int kind;       // DenseKind, EPI_PARTIAL excepted
   DenseEpi epi;
+  uint64_t starve_ns;  // non-zero: every wait for operands runs out after so long (self-test)
 };
 
 DensePlan dense_plan(int64_t M, int64_t N, int64_t K, int kind, bool mx);

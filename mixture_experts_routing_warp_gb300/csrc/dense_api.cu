@@ -336,6 +336,25 @@ moe_status moe_linear_mx8(const moe_mx8_rows *x, const moe_mx8_rows *w, const vo
                     y, workspace, workspace_bytes, status, stream);
 }
 
+moe_status moe_selftest_linear_timeout(const void *x, const void *w, int64_t n, int32_t R,
+                                       int32_t C, int32_t dtype, void *y, void *workspace,
+                                       size_t workspace_bytes, uint64_t timeout_ns,
+                                       int32_t *status, moe_stream stream) {
+  const moe_status st = check_product(n, R, C, dtype, false);
+  if (st != MOE_OK) return st;
+  if (timeout_ns == 0 || timeout_ns > kWaitTimeoutNs) return MOE_ERR_INVALID_ARG;
+  if (!x || !w || !y || !status || n == 0 || dense_skinny(n, R, C, EPI_LINEAR, false))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 2) || !aligned(status, 4))
+    return MOE_ERR_MISALIGNED;
+  DenseProduct p = forward_product(x, w, n, R, C, EPI_LINEAR);
+  p.epi.half = dtype == MOE_FP16;
+  p.epi.out = y;
+  p.epi.vec = R % 8 == 0 && aligned(y, 16);
+  p.starve_ns = timeout_ns;
+  return run_forward(p, workspace, workspace_bytes, status, stream);
+}
+
 size_t moe_linear_backward_workspace_size(int64_t n, int32_t R, int32_t C, int32_t act) {
   if (check_product(n, R, C, MOE_BF16, false) != MOE_OK || R % 8 != 0 || !act_ok(act)) return 0;
   return grad_layout(n, R, C, EPI_DACT, act != MOE_LINEAR_NONE, true).total;

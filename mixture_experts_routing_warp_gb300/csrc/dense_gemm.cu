@@ -127,6 +127,10 @@ __device__ __forceinline__ void copy_scales_pair(uint32_t tmem, uint32_t saddr) 
                : "memory");
 }
 
+__device__ __forceinline__ void st_shared_cluster(uint32_t cluster_addr, int v) {
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+
 __device__ __forceinline__ void umma_mx8_pair(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc,
                                               uint32_t sa, uint32_t sb, uint32_t accumulate) {
   asm volatile(
@@ -550,17 +554,21 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
         }
       }
     }
-    // a pair's copies complete on the leader's barriers: the leader drains
-    // (the peer stays resident until the final cluster barrier)
-    if (!ok && leader) {
-      for (uint32_t i = 0; i < issued; ++i) {
-        int s = stage - 1 - (int)i;
-        uint32_t ph = phase;
-        if (s < 0) {
-          s += stages;
-          ph ^= 1u;
+    // A pair's copies are counted on the leader's barriers. Where a wait gave up,
+    // here or in the MMA warp after the last copy was issued, nobody else waits for
+    // those in flight. drain_bar says that the MMA warp is done, whichever way.
+    if (leader) {
+      wait_drain(drain_bar, 0, (kMaxStages + 2) * args.timeout_ns);
+      if (*s_abort) {
+        for (uint32_t i = 0; i < issued; ++i) {
+          int s = stage - 1 - (int)i;
+          uint32_t ph = phase;
+          if (s < 0) {
+            s += stages;
+            ph ^= 1u;
+          }
+          wait_drain(full_bar(s), ph, args.timeout_ns / 10);
         }
-        wait_drain(full_bar(s), ph, 100000000ull);
       }
     }
   } else if (warp == 1) {
@@ -695,8 +703,20 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
     }
   }
 
+  // a CTA that gave up tells its peer, which still has to reach the barrier
+  if (lane == 0 && *s_abort)
+    st_shared_cluster(map_to_rank(smem_u32((const void *)s_abort), rank ^ 1u), 1);
+  __syncwarp();
   tc_fence_before();
   cluster_sync();  // the leader's MMAs into the peer's TMEM are complete
+  if (*s_abort) {
+    // Nothing more is issued. Copies of the peer that the leader's barriers no
+    // longer expected have a millisecond to land before either CTA leaves.
+    const long long until = wait_deadline(1000000ull);
+    while (clock64() < until) __nanosleep(1000);
+    __syncwarp();
+    cluster_sync();
+  }
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
@@ -1098,6 +1118,11 @@ cudaError_t launch_dense(const DenseProduct &p, const DensePlan &plan, uint8_t *
   GemmArgs a{};
   set_problem(a.p[0], p, plan, false, mx, partial);
   set_ring(a, a.p[0].b_bytes, mx, status);
+  if (p.starve_ns) {  // each step waits for bytes that nobody sends
+    a.timeout_ns = p.starve_ns;
+    a.p[0].b_bytes += 16;
+    a.p[0].b_bytes_last += 16;
+  }
   a.pairs = p.b.pairs;
   const GemmProblem &g = a.p[0];
   auto map_b = [&](CUtensorMap *t, int cols) {
