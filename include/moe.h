@@ -26,8 +26,8 @@
  * the dense blocks beside the experts, with gradients (moe_rms_norm,
  * moe_linear, moe_gated_linear, their _backward and _mx8 forms),
  * the workspace calls (moe_workspace_size, moe_workspace_init,
- * moe_workspace_regions), moe_read_status, moe_selftest_wait_timeout and
- * moe_selftest_linear_timeout.
+ * moe_workspace_regions), moe_read_status, moe_read_dense_status,
+ * moe_selftest_wait_timeout and moe_selftest_linear_timeout.
  *
  * Sources (page title, section):
  *  [R1] "Reuse topk SparseMatrix routing metadata in GPT-OSS MoE forward"
@@ -49,8 +49,8 @@
  *  - Pointers named d_* / device buffers are CUDA device pointers on the
  *    current device. The caller allocates and owns every buffer, including
  *    the workspace; the library never allocates, frees, synchronises or
- *    copies device-to-host (moe_read_status is the one documented
- *    exception and is for debugging only).
+ *    copies device-to-host (moe_read_status and moe_read_dense_status are the
+ *    documented exceptions and are for debugging only).
  *  - `stream` is a cudaStream_t (NULL = the legacy default stream). All
  *    work is enqueued on it; outputs are valid in stream order.
  *  - Arguments are validated on the host before any launch; a rejected call
@@ -532,9 +532,10 @@ moe_status moe_forward_q4(const void *x, const float *logits, const moe_q4_matri
  * workspace: scratch of the size that the call's _workspace_size gives (0:
  * none, NULL is fine), 256-byte aligned; it needs no preparation and keeps
  * nothing between calls, but calls that may overlap need one each.
- * status: optional device int32, 0 before its first use (NULL = not
- * reported): a bounded wait that gives up records MOE_ERR_TIMEOUT there and
- * leaves the call's outputs undefined. */
+ * status: optional device int32, 0 before its first use: a bounded wait that
+ * gives up records MOE_ERR_TIMEOUT there and leaves the call's outputs
+ * undefined. NULL: a word that the library keeps per device, read by
+ * moe_read_dense_status. */
 typedef struct {
   uint8_t *codes;   /* device, 16-byte aligned */
   uint8_t *scales;  /* device */
@@ -684,6 +685,11 @@ moe_status moe_ffn_plan(int64_t n, int32_t E, int32_t k, int32_t H, int32_t I,
 moe_status moe_read_status(void *workspace, size_t workspace_bytes, int32_t reset,
                            moe_stream stream);
 
+/* DEBUG ONLY -- the same for the dense blocks' calls without a status word of the
+ * caller's: synchronises `stream` and returns what their waits recorded on the
+ * current device since the last reset (MOE_OK if nothing). */
+moe_status moe_read_dense_status(int32_t reset, moe_stream stream);
+
 /* DIAGNOSTIC -- launches one thread that waits, through the library's
  * bounded device-side wait, on a control word that nothing ever sets. After
  * `timeout_ns` (1 .. 1e9) the wait gives up, records MOE_ERR_TIMEOUT in the
@@ -695,8 +701,8 @@ moe_status moe_selftest_wait_timeout(void *workspace, size_t workspace_bytes, ui
 
 /* DIAGNOSTIC -- moe_linear (without bias, activation or residual) whose steps
  * wait for bytes that nobody sends: every wait of the product's roles gives up
- * after `timeout_ns` (1 .. 1e9), MOE_ERR_TIMEOUT goes to `status` (required), and
- * the kernel frees what it holds and returns. y is left undefined. Sizes that
+ * after `timeout_ns` (1 .. 1e9), MOE_ERR_TIMEOUT goes to `status` as moe_linear's would,
+ * and the kernel frees what it holds and returns. y is left undefined. Sizes that
  * take the tensor tiles (more than 32 rows); workspace as moe_linear's. */
 moe_status moe_selftest_linear_timeout(const void *x, const void *w, int64_t n, int32_t R,
                                        int32_t C, int32_t dtype, void *y, void *workspace,

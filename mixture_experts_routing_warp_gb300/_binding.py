@@ -126,6 +126,7 @@ SIGNATURES = {
     "moe_gated_linear_backward": (_I32, [_P, _P, _P, _I64, _I32, _I32, _PP, _I32, _P, _P, _P,
                                          _SZ, _P, _P]),
     "moe_read_status": (_I32, [_P, _SZ, _I32, _P]),
+    "moe_read_dense_status": (_I32, [_I32, _P]),
     "moe_selftest_wait_timeout": (_I32, [_P, _SZ, _U64, _P]),
     "moe_selftest_linear_timeout": (_I32, [_P, _P, _I64, _I32, _I32, _I32, _P, _P, _SZ, _U64, _P,
                                            _P]),
@@ -1072,8 +1073,14 @@ def ffn_plan(n: int, E: int, k: int, H: int, I: int, params: MoeParams) -> dict:
             "pair_w2": bool(plan[3]), "decode": bool(plan[4]), "fused": bool(plan[5])}
 
 
-def read_status(ws: torch.Tensor, reset: bool = False) -> int:
-    """DEBUG: synchronises and returns the device status word (0 = OK)."""
+def read_status(ws: Optional[torch.Tensor] = None, reset: bool = False) -> int:
+    """DEBUG: synchronises and returns the device status word (0 = OK) of a
+    workspace or, without one, of the current device: the one where linear,
+    gated_linear and their gradients record a wait that gave up when they were
+    given no `status`."""
+    if ws is None:
+        stream = torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return int(lib().moe_read_dense_status(int(reset), stream))
     return int(lib().moe_read_status(_ptr(ws), ws.numel(), int(reset), _stream(ws.device)))
 
 

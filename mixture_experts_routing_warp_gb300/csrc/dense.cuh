@@ -364,9 +364,11 @@ struct DenseProduct {
 };
 
 DensePlan dense_plan(int64_t M, int64_t N, int64_t K, int kind, bool mx);
-// blocks and partial: scratch of plan.blocks and plan.partial bytes.
+// blocks and partial: scratch of plan.blocks and plan.partial bytes. status null:
+// the current device's own word, which read_wait_status copies to the host.
 cudaError_t launch_dense(const DenseProduct &p, const DensePlan &plan, uint8_t *blocks,
                          float *partial, int32_t *status, cudaStream_t s);
+cudaError_t read_wait_status(int32_t *out, bool reset, cudaStream_t s);
 // A product of few rows, where dense_skinny says so (dense_skinny.cu). No
 // scratch.
 bool dense_skinny(int64_t n, int64_t out, int64_t in, int kind, bool mx);

@@ -336,6 +336,12 @@ moe_status moe_linear_mx8(const moe_mx8_rows *x, const moe_mx8_rows *w, const vo
                     y, workspace, workspace_bytes, status, stream);
 }
 
+moe_status moe_read_dense_status(int32_t reset, moe_stream stream) {
+  int32_t word = 0;
+  if (read_wait_status(&word, reset != 0, (cudaStream_t)stream) != cudaSuccess) return MOE_ERR_CUDA;
+  return (moe_status)word;
+}
+
 moe_status moe_selftest_linear_timeout(const void *x, const void *w, int64_t n, int32_t R,
                                        int32_t C, int32_t dtype, void *y, void *workspace,
                                        size_t workspace_bytes, uint64_t timeout_ns,
@@ -343,7 +349,7 @@ moe_status moe_selftest_linear_timeout(const void *x, const void *w, int64_t n, 
   const moe_status st = check_product(n, R, C, dtype, false);
   if (st != MOE_OK) return st;
   if (timeout_ns == 0 || timeout_ns > kWaitTimeoutNs) return MOE_ERR_INVALID_ARG;
-  if (!x || !w || !y || !status || n == 0 || dense_skinny(n, R, C, EPI_LINEAR, false))
+  if (!x || !w || !y || n == 0 || dense_skinny(n, R, C, EPI_LINEAR, false))
     return MOE_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 2) || !aligned(status, 4))
     return MOE_ERR_MISALIGNED;

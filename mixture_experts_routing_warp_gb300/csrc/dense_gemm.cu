@@ -1014,12 +1014,32 @@ void set_problem(GemmProblem &g, const DenseProduct &p, const DensePlan &plan, b
   }
 }
 
-void set_ring(GemmArgs &a, int b_bytes, bool mx, int32_t *status) {
+// Where calls without a status word of the caller's record a wait that gave up.
+__device__ uint32_t g_wait_status;
+
+cudaError_t wait_status_word(uint32_t **out) {
+  static PerDeviceOnce once;
+  static std::atomic<uint32_t *> word[PerDeviceOnce::kMaxDevices] = {};
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err == cudaSuccess)
+    err = once.run([&] {
+      void *p = nullptr;
+      const cudaError_t e = cudaGetSymbolAddress(&p, g_wait_status);
+      if (e == cudaSuccess) word[dev].store(static_cast<uint32_t *>(p), std::memory_order_relaxed);
+      return e;
+    });
+  if (err == cudaSuccess) *out = word[dev].load(std::memory_order_relaxed);
+  return err;
+}
+
+cudaError_t set_ring(GemmArgs &a, int b_bytes, bool mx, int32_t *status) {
   a.stage_bytes = kABytes + b_bytes;
   const int most = mx ? kMxStages : kMaxStages;
   a.stages = kRingBytes / a.stage_bytes < most ? kRingBytes / a.stage_bytes : most;
   a.status = reinterpret_cast<uint32_t *>(status);
   a.timeout_ns = kWaitTimeoutNs;
+  return status ? cudaSuccess : wait_status_word(&a.status);
 }
 
 }  // namespace
@@ -1117,7 +1137,8 @@ cudaError_t launch_dense(const DenseProduct &p, const DensePlan &plan, uint8_t *
   const bool mx = p.a.scales != nullptr;
   GemmArgs a{};
   set_problem(a.p[0], p, plan, false, mx, partial);
-  set_ring(a, a.p[0].b_bytes, mx, status);
+  cudaError_t err = set_ring(a, a.p[0].b_bytes, mx, status);
+  if (err != cudaSuccess) return err;
   if (p.starve_ns) {  // each step waits for bytes that nobody sends
     a.timeout_ns = p.starve_ns;
     a.p[0].b_bytes += 16;
@@ -1150,19 +1171,26 @@ cudaError_t launch_dense(const DenseProduct &p, const DensePlan &plan, uint8_t *
     if (grid > cap) grid = cap;
     const int G = (int)(p.K / 32);
     const uintptr_t bits = (uintptr_t)p.a.scales | (uintptr_t)p.b.scales | (uintptr_t)G;
-    const cudaError_t err =
-        launch_dependent(bits % 4 == 0   ? mx8_layout_kernel<4>
-                         : bits % 2 == 0 ? mx8_layout_kernel<2>
-                                         : mx8_layout_kernel<1>,
-                         dim3((unsigned)grid), dim3(256), 0, s, la, lb, G, g.num_kb);
+    err = launch_dependent(bits % 4 == 0   ? mx8_layout_kernel<4>
+                           : bits % 2 == 0 ? mx8_layout_kernel<2>
+                                           : mx8_layout_kernel<1>,
+                           dim3((unsigned)grid), dim3(256), 0, s, la, lb, G, g.num_kb);
     if (err != cudaSuccess) return err;
   }
   if (!ok) return cudaErrorInvalidValue;
   const int kind = plan.splits > 1                         ? (int)EPI_PARTIAL
                    : p.kind == EPI_LINEAR && !p.epi.vec ? (int)EPI_COLUMNS
                                                         : p.kind;
-  const cudaError_t err = mx ? launch_kind<true>(kind, maps, a, s) : launch_kind<false>(kind, maps, a, s);
+  err = mx ? launch_kind<true>(kind, maps, a, s) : launch_kind<false>(kind, maps, a, s);
   return err != cudaSuccess || plan.splits == 1 ? err : join_parts(p, plan, partial, s);
+}
+
+cudaError_t read_wait_status(int32_t *out, bool reset, cudaStream_t s) {
+  uint32_t *word = nullptr;
+  cudaError_t err = wait_status_word(&word);
+  if (err == cudaSuccess) err = cudaMemcpyAsync(out, word, 4, cudaMemcpyDeviceToHost, s);
+  if (err == cudaSuccess && reset) err = cudaMemsetAsync(word, 0, 4, s);
+  return err != cudaSuccess ? err : cudaStreamSynchronize(s);
 }
 
 cudaError_t launch_dense_gradients(const DenseProduct *const *p, const DensePlan *const *plan,
@@ -1183,9 +1211,10 @@ cudaError_t launch_dense_gradients(const DenseProduct *const *p, const DensePlan
       return cudaErrorInvalidValue;
   }
   for (int i = 2 * count; i < kMaps; ++i) maps.m[i] = maps.m[0];
-  set_ring(a, most, false, status);
+  cudaError_t err = set_ring(a, most, false, status);
+  if (err != cudaSuccess) return err;
   a.join = {column_part, column_out, column_rows, columns, half};
-  cudaError_t err = launch_gemm<true, EPI_GRAD, false>(maps, a, s);
+  err = launch_gemm<true, EPI_GRAD, false>(maps, a, s);
   for (int i = 0; i < count && err == cudaSuccess; ++i)
     if (plan[i]->splits > 1) err = join_parts(*p[i], *plan[i], partial[i], s);
   return err;

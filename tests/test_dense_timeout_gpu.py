@@ -1,5 +1,8 @@
 """A wait of the dense products' roles that runs out: the product gives up, says so in its
 status word and leaves the device as usable as before."""
+import os
+import subprocess
+import sys
 import time
 
 import pytest
@@ -9,6 +12,7 @@ import mixture_experts_routing_warp_gb300 as moe
 from mixture_experts_routing_warp_gb300 import build as cuda_build
 
 MS = 1_000_000
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 TIMEOUT = 5                    # MOE_ERR_TIMEOUT
 
 
@@ -26,7 +30,7 @@ def test_refusals():
     cuda_build.build()
     P = 1 << 20
     good = dict(x=P, w=P, y=P, ws=P, status=P, ns=MS, n=100, R=64, C=2880)
-    for spoil in ({"x": None}, {"w": None}, {"y": None}, {"status": None}, {"ns": 0},
+    for spoil in ({"x": None}, {"w": None}, {"y": None}, {"ns": 0},
                   {"ns": 10 ** 9 + 1}, {"n": 0}, {"n": 16}, {"R": 1 << 20}, {"C": 60},
                   {"dtype": 2}):
         assert starve(**dict(good, **spoil)) == 1, spoil
@@ -59,3 +63,53 @@ def test_a_wait_that_runs_out(n, R, C):
         st.zero_()
         assert torch.equal(moe.linear(x, w, status=st), want)   # right behind it
         assert st.item() == 0
+
+
+@pytest.mark.gpu
+def test_a_call_without_a_status_word_is_not_silent():
+    """What a call without a status word records is found in the device's own, by every kind
+    of call; one with a word of its own leaves that alone."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x, w = (torch.randn(300, 256, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    y, st = torch.empty(300, 300, dtype=torch.bfloat16, device="cuda"), \
+        torch.zeros(1, dtype=torch.int32, device="cuda")
+    size = moe.linear_workspace_size(300, 300, 256)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda") if size else None
+    assert moe.read_status() == 0
+    assert starve(x, w, y, ws, None, 5 * MS) == 0
+    assert moe.read_status() == TIMEOUT
+    moe.linear(x, w)
+    assert moe.read_status(reset=True) == TIMEOUT     # kept until it is reset
+    assert moe.read_status() == 0
+    assert starve(x, w, y, ws, st, 5 * MS) == 0
+    assert moe.read_status() == 0 and st.item() == TIMEOUT
+    # captured, on a stream of its own
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        assert starve(x, w, y, ws, None, 5 * MS) == 0
+    assert moe.read_status() == 0
+    graph.replay()
+    assert moe.read_status(reset=True) == TIMEOUT
+    assert torch.equal(moe.linear(x, w), moe.linear(x, w, status=st.zero_()))
+    assert moe.read_status() == 0 and st.item() == 0
+
+
+FIRST = """
+import torch, mixture_experts_routing_warp_gb300 as moe
+x = torch.ones(64, 256, dtype=torch.bfloat16, device="cuda")
+out = torch.empty(64, 64, dtype=torch.bfloat16, device="cuda")
+ws = torch.empty(max(1, moe.linear_workspace_size(64, 64, 256)), dtype=torch.uint8, device="cuda")
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    moe.linear(x, x, out=out, ws=ws)
+graph.replay()
+torch.cuda.synchronize()
+assert (out == 256).all() and moe.read_status() == 0
+"""
+
+
+@pytest.mark.gpu
+def test_the_first_call_of_a_process_may_be_a_captured_one():
+    r = subprocess.run([sys.executable, "-c", FIRST], cwd=ROOT, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
