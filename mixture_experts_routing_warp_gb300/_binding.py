@@ -707,10 +707,11 @@ def forward_q4(x: torch.Tensor, logits: torch.Tensor, w13: Q4Weight, w2: Q4Weigh
 
 class Mx8:
     """MXFP8 rows: codes float8_e4m3fn [rows, C] and scales uint8 [rows, C/32]
-    (E8M0), C a multiple of 32. The tensors are used where they lie; the
-    handle keeps them alive."""
+    (E8M0), C a multiple of 32. The tensors are used where they lie at each
+    call; the handle keeps them alive and is theirs for good: other tensors
+    take another handle."""
 
-    __slots__ = ("codes", "scales", "device", "shape", "_as_parameter_")
+    __slots__ = ("_codes", "_scales", "_rows", "device", "shape")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
         self.device = codes.get_device() if isinstance(codes, torch.Tensor) else -1
@@ -720,8 +721,27 @@ class Mx8:
                              f"{tuple(codes.shape)}")
         self.shape = codes.shape
         _need_on(scales, "scales", torch.uint8, self.device, (self.shape[0], self.shape[1] // 32))
-        self.codes, self.scales = codes, scales
-        self._as_parameter_ = ctypes.byref(Mx8Rows(codes.data_ptr(), scales.data_ptr()))
+        self._codes, self._scales, self._rows = codes, scales, Mx8Rows()
+
+    @property
+    def codes(self) -> torch.Tensor:
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        return self._scales
+
+    def _argument(self):
+        """The library's argument, with the tensors' addresses as they are now (a
+        tensor can be given other memory, or another shape, behind the handle)."""
+        c, s, shape = self._codes, self._scales, self.shape
+        if not (c.shape == shape and s.shape == (shape[0], shape[1] // 32)
+                and c.is_contiguous() and s.is_contiguous()
+                and c.get_device() == s.get_device() == self.device):
+            raise ValueError("codes or scales are no longer as they were when the handle was made")
+        rows = self._rows
+        rows.codes, rows.scales = c.data_ptr(), s.data_ptr()
+        return ctypes.byref(rows)
 
 
 def _empty_mx8(rows: int, cols: int, like: torch.Tensor, device: int) -> Mx8:
@@ -729,10 +749,10 @@ def _empty_mx8(rows: int, cols: int, like: torch.Tensor, device: int) -> Mx8:
         raise ValueError(f"8-bit rows need a multiple of 32 columns, got {cols}")
     m = Mx8.__new__(Mx8)
     on = like.device
-    m.codes = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=on)
-    m.scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=on)
-    m.device, m.shape = device, m.codes.shape
-    m._as_parameter_ = ctypes.byref(Mx8Rows(m.codes.data_ptr(), m.scales.data_ptr()))
+    m._codes = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=on)
+    m._scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=on)
+    m._rows = Mx8Rows(m._codes.data_ptr(), m._scales.data_ptr())
+    m.device, m.shape = device, m._codes.shape
     return m
 
 
@@ -812,10 +832,12 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float = 1e-5,
     if mx8:
         if out is None:
             y = _empty_mx8(n, H, x, device)
+            y8 = ctypes.byref(y._rows)
         else:
             y = out
             _need_mx8(y, "out", device, shape)
-        _run("moe_rms_norm", device, x.data_ptr(), r, w, w_dtype, n, H, dtype, eps, None, y, t)
+            y8 = y._argument()
+        _run("moe_rms_norm", device, x.data_ptr(), r, w, w_dtype, n, H, dtype, eps, None, y8, t)
     else:
         y = torch.empty_like(x) if out is None else _out_like(out, "out", x)
         _run("moe_rms_norm", device, x.data_ptr(), r, w, w_dtype, n, H, dtype, eps, y.data_ptr(),
@@ -932,7 +954,7 @@ def linear(x, w, bias: Optional[torch.Tensor] = None, act: str = "none",
     act_id = _need_act(act)
     device, n, C, R, dtype = _product_operands(x, w, "w", dtype)
     if type(x) is Mx8:
-        name, like, xp, wp = "moe_linear_mx8", x.codes, x, w
+        name, like, xp, wp = "moe_linear_mx8", x.codes, x._argument(), w._argument()
     else:
         name, like, xp, wp = "moe_linear", x, x.data_ptr(), w.data_ptr()
     b = None if bias is None else _need_vector(bias, "bias", (dtype,), device, R)
@@ -988,15 +1010,17 @@ def gated_linear(x, w13, params: MoeParams, out=None, mx8: bool = False,
         raise ValueError(f"w13 must have an even number of rows, got {rows}")
     I = rows // 2
     if type(x) is Mx8:
-        name, like, xp, wp = "moe_gated_linear_mx8", x.codes, x, w13
+        name, like, xp, wp = "moe_gated_linear_mx8", x.codes, x._argument(), w13._argument()
     else:
         name, like, xp, wp = "moe_gated_linear", x, x.data_ptr(), w13.data_ptr()
     if mx8:
         if out is None:
             out = _empty_mx8(n, I, like, device)
+            h8 = ctypes.byref(out._rows)
         else:
             _need_mx8(out, "out", device, (n, I))
-        hp, h8 = None, out
+            h8 = out._argument()
+        hp = None
     else:
         if out is None:
             out = torch.empty((n, I), dtype=dtype, device=like.device)
