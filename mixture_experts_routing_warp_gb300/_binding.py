@@ -566,7 +566,8 @@ class Q4Weight:
     codes per byte, the even column low) or [E, R, C/2], scales uint8
     [..., R, C/32] ("mxfp4": E8M0) or [..., R, C/16] ("nvfp4": E4M3, times
     matrix_scale fp32 [E] or [1]). The tensors are used where they lie; the
-    handle keeps them alive."""
+    handle keeps them alive and is theirs for good: other tensors take another
+    handle."""
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, fmt: str,
                  matrix_scale: Optional[torch.Tensor] = None):
@@ -584,10 +585,15 @@ class Q4Weight:
                  (*codes.shape[:-1], self.cols // Q4_GROUP[fmt]))
         if matrix_scale is not None:
             _need_on(matrix_scale, "matrix_scale", torch.float32, self.device, (self.count,))
-        self.codes, self.scales, self.matrix_scale, self.fmt = codes, scales, matrix_scale, fmt
+        self._codes, self._scales, self._matrix_scale, self._fmt = codes, scales, matrix_scale, fmt
         self._as_parameter_ = ctypes.byref(Q4Matrix(
             codes.data_ptr(), scales.data_ptr(),
             None if matrix_scale is None else matrix_scale.data_ptr(), Q4_FORMAT[fmt]))
+
+    codes = property(lambda self: self._codes)
+    scales = property(lambda self: self._scales)
+    matrix_scale = property(lambda self: self._matrix_scale)
+    fmt = property(lambda self: self._fmt)
 
 
 def _need_q4(w: Q4Weight, name: str, device: int) -> None:
