@@ -23,6 +23,8 @@
 // Before the wait for the preceding kernel the CTA asks L2 for its weights:
 // they come from HBM while that kernel ends, and L2 is coherent with whatever
 // it still writes.
+#include <type_traits>
+
 #include "dense.cuh"
 
 namespace moe {
@@ -80,12 +82,17 @@ __device__ __forceinline__ float greater(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-// part s t + acc. A group's sum is 0 or 2^-18 to 2^22.6 and the scales are powers of two from 2^-127
-// to 2^127, so neither part s nor s t need be in fp32's range where part s t is. The
-// lesser scale goes first: that is exact (part is a multiple of 2^-18, and 2^-145 is
-// in fp32), and too large only where the result is.
+// part s t + acc for a group's sum, 0 or 2^-18 to 2^22.6, and two scales, powers of two from
+// 2^-127 to 2^127. s t first is right wherever it is in fp32's range, as it is for bytes from
+// kNearLo to kNearHi: then nothing is rounded before acc is added. Else (WIDE) the lesser
+// scale goes first: that is exact (part is a multiple of 2^-18, and 2^-145 is in fp32),
+// and too large only where the result is. Four instructions more per group and
+// token pair: 16 rows, 2880 x 2880 9.2 us for 8.7.
+constexpr uint32_t kNearLo = 53, kNearHi = 190;  // 2^-74 and 2^63: products from 2^-148 to 2^126
+template <bool WIDE>
 __device__ __forceinline__ float scaled(float part, float s, float t, float acc) {
-  return fmaf(part * lesser(s, t), greater(s, t), acc);
+  if constexpr (WIDE) return fmaf(part * lesser(s, t), greater(s, t), acc);
+  else return fmaf(part, s * t, acc);
 }
 
 __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -165,13 +172,14 @@ __device__ __forceinline__ void sum16(const SkinnyArgs &a, int mt, int slice, in
 }
 
 // The same of MXFP8 operands. s_w, s_x: the scales of the CTA's weight rows and
-// of the tokens, a row of `wide` each. Rows and tokens that do not exist are
-// read as the last one; their sums go nowhere.
-template <int EPI, int NB>
+// of the tokens, a row of `wide` each; far: this thread saw one outside [kNearLo,
+// kNearHi]. A weight row that does not exist is read as row 0, a token as the last one;
+// their sums go nowhere. U groups of 32 k in flight: four, and two of 9 to 16 rows at four CTAs per
+// SM, whose registers hold no more (8192 x 2880, 9 rows: 10.1 us for 12.3 with spills).
+template <int EPI, int NB, int U>
 __device__ __forceinline__ void sum8(const SkinnyArgs &a, int mt, int slice, int lane,
-                                     const float *s_w, const float *s_x, int wide,
+                                     const float *s_w, const float *s_x, int wide, bool far,
                                      float (&acc)[NB][4]) {
-  constexpr int U = 4;  // groups of 32 k in flight
   const int g = lane >> 2, t = lane & 3, G = a.K / 32;
   bool live;
   int64_t r0 = weight_row<EPI>(a, mt, g, live);
@@ -204,35 +212,39 @@ __device__ __forceinline__ void sum8(const SkinnyArgs &a, int mt, int slice, int
       }
     }
   };
-  fetch(0);
-  __syncthreads();  // the scales, with the first codes on their way
-  for (int b = 0; b < count; b += U) {
-    if (b > 0) fetch(b);
+  auto sum = [&](auto is_far) {
+    for (int b = 0; b < count; b += U) {
+      if (b > 0) fetch(b);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (b + u >= count) break;
-      uint32_t a0[4], a1[4];
-      codes_to_half(q0[u].x, a0[0], a0[1]);
-      codes_to_half(q0[u].y, a0[2], a0[3]);
-      codes_to_half(q1[u].x, a1[0], a1[1]);
-      codes_to_half(q1[u].y, a1[2], a1[3]);
-      const float s0 = sw0[b + u], s1 = sw1[b + u];
+      for (int u = 0; u < U; ++u) {
+        if (b + u >= count) break;
+        uint32_t a0[4], a1[4];
+        codes_to_half(q0[u].x, a0[0], a0[1]);
+        codes_to_half(q0[u].y, a0[2], a0[3]);
+        codes_to_half(q1[u].x, a1[0], a1[1]);
+        codes_to_half(q1[u].y, a1[2], a1[3]);
+        const float s0 = sw0[b + u], s1 = sw1[b + u];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        uint32_t x0, x1, x2, x3;
-        codes_to_half(xq[u][nb].x, x0, x1);
-        codes_to_half(xq[u][nb].y, x2, x3);
-        float part[4] = {0.f, 0.f, 0.f, 0.f};
-        mma_16x8x16(part, a0[0], a1[0], a0[1], a1[1], x0, x1, true);
-        mma_16x8x16(part, a0[2], a1[2], a0[3], a1[3], x2, x3, true);
-        const float t0 = sx[nb * 8 * wide + b + u], t1 = sx[(nb * 8 + 1) * wide + b + u];
-        acc[nb][0] = scaled(part[0], s0, t0, acc[nb][0]);
-        acc[nb][1] = scaled(part[1], s0, t1, acc[nb][1]);
-        acc[nb][2] = scaled(part[2], s1, t0, acc[nb][2]);
-        acc[nb][3] = scaled(part[3], s1, t1, acc[nb][3]);
+        for (int nb = 0; nb < NB; ++nb) {
+          uint32_t x0, x1, x2, x3;
+          codes_to_half(xq[u][nb].x, x0, x1);
+          codes_to_half(xq[u][nb].y, x2, x3);
+          float part[4] = {0.f, 0.f, 0.f, 0.f};
+          mma_16x8x16(part, a0[0], a1[0], a0[1], a1[1], x0, x1, true);
+          mma_16x8x16(part, a0[2], a1[2], a0[3], a1[3], x2, x3, true);
+          const float t0 = sx[nb * 8 * wide + b + u], t1 = sx[(nb * 8 + 1) * wide + b + u];
+          acc[nb][0] = scaled<decltype(is_far)::value>(part[0], s0, t0, acc[nb][0]);
+          acc[nb][1] = scaled<decltype(is_far)::value>(part[1], s0, t1, acc[nb][1]);
+          acc[nb][2] = scaled<decltype(is_far)::value>(part[2], s1, t0, acc[nb][2]);
+          acc[nb][3] = scaled<decltype(is_far)::value>(part[3], s1, t1, acc[nb][3]);
+        }
       }
     }
-  }
+  };
+  fetch(0);
+  // the CTA's scales, with the first codes on their way
+  if (__syncthreads_or(far)) sum(std::true_type{});
+  else sum(std::false_type{});
 }
 
 // NB blocks of 8 tokens; CTAS per SM that registers are left for.
@@ -266,15 +278,21 @@ __global__ void __launch_bounds__(skinny_threads(EPI), CTAS)
   if constexpr (IN == IN_MX8) {
     extern __shared__ float s_scale[];  // [rows of the CTA and tokens][G | 1]
     const int G = a.K / 32, wide = G | 1;
+    bool far = false;
     for (int r = warp; r < MT * kRows + NB * 8; r += MT * KS) {
       const int tok = r - MT * kRows;
       bool live;
       const int64_t row = weight_row<EPI>(a, r / kRows, r % kRows, live);
       const uint8_t *src = tok < 0 ? a.w_scales + row * G : a.x_scales + (int64_t)tok * G;
       if (tok >= 0) live = tok < a.n;
-      for (int i = lane; i < G; i += 32) s_scale[r * wide + i] = live ? scale_of(__ldg(src + i)) : 0.f;
+      for (int i = lane; i < G; i += 32) {
+        const uint32_t byte = live ? __ldg(src + i) : kNearLo;
+        far |= byte < kNearLo || byte > kNearHi;
+        s_scale[r * wide + i] = live ? scale_of(byte) : 0.f;
+      }
     }
-    sum8<EPI, NB>(a, warp / KS, warp % KS, lane, s_scale, s_scale + MT * kRows * wide, wide, acc);
+    sum8<EPI, NB, NB == 2 && CTAS == 4 ? 2 : 4>(a, warp / KS, warp % KS, lane, s_scale, s_scale + MT * kRows * wide, wide, far,
+                  acc);
   } else sum16<EPI, IN == IN_FP16, NB>(a, warp / KS, warp % KS, lane, acc);
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb)

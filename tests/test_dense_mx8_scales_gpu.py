@@ -111,3 +111,22 @@ def test_a_scale_that_is_nan_beside_any_other(n):
     bad = torch.zeros(n, R, dtype=torch.bool, device="cuda")
     bad[n - 1], bad[:, 77] = True, True
     assert torch.equal(torch.isnan(got), bad)
+
+
+@pytest.mark.parametrize("n", ROWS)
+@pytest.mark.parametrize("lo,hi", [(53, 190), (53, 191), (52, 190)])
+def test_scales_around_the_border_of_the_two_orders(n, lo, hi):
+    """Few rows take a shorter way where no scale lies outside bytes 53 to 190: all pairs within
+    that range, and with the next byte at either end."""
+    C = 96
+    ends = torch.tensor([lo, hi, 127, 64], dtype=torch.uint8, device="cuda")
+    xb = ends[torch.arange(n, device="cuda") % 4]
+    wb = torch.arange(lo, hi + 1, device="cuda").to(torch.uint8)
+    for code in (ONE, TINY, TOP):
+        x = torch.zeros(n, C, dtype=torch.uint8, device="cuda")
+        w = torch.zeros(len(wb), C, dtype=torch.uint8, device="cuda")
+        x[:, 40], w[:, 40] = code, code
+        xs, ws = xb[:, None].expand(-1, 3).contiguous(), wb[:, None].expand(-1, 3).contiguous()
+        want = mx8_value(x.view(torch.float8_e4m3fn), xs) @ \
+            mx8_value(w.view(torch.float8_e4m3fn), ws).t()
+        assert torch.equal(moe.linear(rows8(x, xs), rows8(w, ws)), as_bf16(want)), code
