@@ -553,7 +553,8 @@ typedef enum {
  * [n, H], any H. weight [H] of `dtype` or MOE_FP32, NULL = ones. sum: optional
  * output s (needs a residual). The result goes to exactly one of y and y_mx8
  * (H a multiple of 32). eps >= 0. The squares are summed in fp32: a row with
- * values above about 1e19 comes out as zeros. */
+ * values above about 1e19 comes out as zeros; with eps = 0 one whose values are all below
+ * about 1e-19 is inaccurate, and below 1e-23 infinite. */
 moe_status moe_rms_norm(const void *x, const void *residual, const void *weight,
                         int32_t weight_dtype, int64_t n, int32_t H, int32_t dtype, float eps,
                         void *y, const moe_mx8_rows *y_mx8, void *sum, moe_stream stream);
@@ -589,7 +590,8 @@ moe_status moe_linear_mx8(const moe_mx8_rows *x, const moe_mx8_rows *w, const vo
  * NULL where it is not wanted; R a multiple of 8. With an activation its
  * argument is computed again, and d = d_y act'(x w^T + bias) is rounded to
  * `dtype` (as any 16-bit gradient between two layers) before
- *   d_x = d w [n, C],   d_w = d^T x [R, C],   d_bias = sum_t d [R]. */
+ *   d_x = d w [n, C],   d_w = d^T x [R, C],   d_bias = sum_t d [R],
+ * the last from d before that rounding, unless the sums behind it come in parts. */
 size_t moe_linear_backward_workspace_size(int64_t n, int32_t R, int32_t C, int32_t act);
 moe_status moe_linear_backward(const void *d_y, const void *x, const void *w, const void *bias,
                                int64_t n, int32_t R, int32_t C, int32_t dtype, int32_t act,

@@ -14,7 +14,8 @@ namespace moe {
 // What is done with the sums a[row, col] of a product.
 enum DenseKind {
   EPI_LINEAR = 0,    // out = act(a + bias) + add
-  EPI_DACT = 1,      // out = add * act'(a + bias): add is the gradient of act's result
+  EPI_DACT = 1,      // out = add * act'(a + bias): add is the gradient of act's result. 16 bits,
+                     // since the gradients' products take 16-bit operands; as EPI_DGATED
   EPI_GATED = 2,     // a holds (gate, up) pairs: out = h
   EPI_GATED_MX = 3,  // the same, h as E4M3 codes with a scale per 32
   EPI_DGATED = 4,    // (gate, up) pairs and add = d_h: out = (d_gate, d_up) in w13's row order

@@ -45,9 +45,9 @@ constexpr int kABytes = kRowsCta * kStepBytes;   // 16 KB
 constexpr int kMaxTn = 256;
 // Epilogue warps, two to four per TMEM lane quarter: with four a tile's
 // epilogue has the latency of two column chunks; a group of 32 8-bit results
-// takes 64 columns and twice the registers, rows off 16 bytes 124 registers
+// takes 64 columns and twice the registers, rows off 16 bytes 128 registers
 // (922 x 5281 x 280: 24.9 us with four, where they spill, 16.0 with three,
-// 16.9 with two), an activation's gradient 100 (three and four take the same time).
+// 16.9 with two), an activation's gradient 115 (with four, 52 bytes of spills).
 constexpr int epi_warps(int epi) {
   return epi == EPI_GATED_MX ? 8 : epi == EPI_COLUMNS || epi == EPI_DACT ? 12 : 16;
 }
@@ -960,10 +960,13 @@ cudaError_t join_parts(const DenseProduct &p, const DensePlan &plan, const float
 }
 
 // Estimated SM cycles of a K step of a tile of tn columns on a CTA pair: 2 per
-// column (256 x tn x 64 products at 8192 per cycle and SM; MXFP8 twice the
+// column (256 x tn x 64 products at 4096 per cycle and SM; MXFP8 twice the
 // products at twice the rate) and no less than its operands' way into shared
-// memory, which 74 bytes per cycle and SM fit over tiles of 64 to 256 columns
-// (2048 x 2880 x 2880: 36, 26, 22 and 30 us at 64, 128, 160 and 256 columns).
+// memory. The constants choose between tile widths and do not foretell times: 74
+// bytes per cycle and SM rank the widths of small products as they measured (2048 x
+// 2880 x 2880: 36, 26, 22 and 30 us at 64, 128, 160 and 256 columns), while large ones on
+// all SMs take in 52 to 54 (567 cycles per step of 224 columns, 8192 x 2880 x 2880 in bf16;
+// 620 in MXFP8, 2047 x 5760 x 2880; 582 of 192 columns, MXFP8, 8192 x 5760 x 2880).
 double step_cycles(int tn, bool mx) {
   const double mma = 2.08 * tn, load = (16384.0 + (mx ? kScaleBytes : 0) + 64.0 * tn) / 74.0;
   return mma > load ? mma : load;

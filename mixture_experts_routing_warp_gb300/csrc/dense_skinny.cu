@@ -12,13 +12,15 @@
 // the same 8 k of its token, so the products pair up although the slots are
 // not in order. tcgen05 has no use here: its tiles would wait for the same
 // bytes, and need their sums split over K to reach all SMs, with a second
-// launch (2880 x 2880, one row: 11.2 us that way, 4.2 here).
+// launch (2880 x 2880, one row: 11.2 us that way, 4.2 here). From HBM, over inputs that
+// together exceed twice the L2, one row takes 5.5 us and 2880 x 5760 gated 7.3 (their bytes alone
+// 2.5 and 4.9); the other figures here are of weights in L2.
 //
 // MXFP8: a lane loads the 8 codes of its k's in a group of 32, as fp16 (exact);
 // the two MMAs of a group start from zero, and their sums enter the total
 // times both scales, which the CTA has laid out as floats in shared memory (with
 // the bytes fetched and converted group by group 155 instructions for 84, and
-// 2880 x 2880 8.7 us for 6.2).
+// 2880 x 2880 8.7 us for 6.0).
 //
 // Before the wait for the preceding kernel the CTA asks L2 for its weights:
 // they come from HBM while that kernel ends, and L2 is coherent with whatever
@@ -429,8 +431,8 @@ cudaError_t launch_in(const SkinnyArgs &a, cudaStream_t s) {
 // twice the weights' bytes (from L2). 2880 x 2880: 32 rows 7.9 us for 10.1 on the
 // tensor tiles, 2880 x 5760 gated 10.3 for 11.6; 8192 x 8192: 16 rows 26.5 for
 // 28.1, 32 rows 47 for 29. MXFP8 is bound by issue (84 instructions for 512
-// codes): 2880 x 2880: 1 / 8 / 16 rows 6.2 / 6.7 / 8.7 us for 14 / 12 / 13.5 on the
-// tensor tiles; 8192 x 8192: 22 / 26 / 36 for 28 / 24.5 / 23.
+// codes): 2880 x 2880: 1 / 8 / 16 rows 6.0 / 6.5 / 8.7 us for 14 / 12.7 / 13 on the
+// tensor tiles; 8192 x 8192: 20.8 / 23.9 / 32.3 for 28.9 / 24.6 / 22.6.
 bool dense_skinny(int64_t n, int64_t out, int64_t in, int kind, bool mx) {
   if (mx) return in <= 32 * kMaxGroups && (n <= 8 || (n <= 16 && out * in <= (1 << 25)));
   if (kind == EPI_GATED_MX) return n <= 16;

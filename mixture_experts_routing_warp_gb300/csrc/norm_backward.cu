@@ -7,7 +7,9 @@
 // adds those rows in order. Two vectors per thread and two blocks of 384 per
 // SM: 8192 x 2880 with d_sum 41 us (the HBM copy rate: 28), V = 1 53, V = 3 44; rows fetched
 // one ahead 57 - 68 us (the registers cost more warps than the wait).
-// Bound by issue: 63 % of the slots at 5.9 warps per scheduler.
+// Neither limit is reached, 60 % of the issue slots and 56 % of HBM: a block's loads wait until
+// its previous rows are done, at 5.9 warps per scheduler. Spills: 16 bytes at V = 2 (40 with fp32
+// weights, 64 - 72 where rows are shifted), 128 - 168 at V = 4 (16-bit rows of 12289 elements and more).
 #include "norm.cuh"
 
 namespace moe {

@@ -33,8 +33,8 @@ cudaError_t launch_ffn_q4(const void *x, const moe_routing_meta &m, const moe_q4
 // moe_params checked and resolved (moe_api.cu).
 moe_status resolve_params(const moe_params *p, ActParams &out, int *gating);
 
-// The norm in front of a layer and column sums (norm.cu). codes null: y, else
-// codes and scales. Scratch sizes in bytes.
+// The norm in front of a layer (norm.cu), its gradients and column sums
+// (norm_backward.cu). codes null: y, else codes and scales. Scratch sizes in bytes.
 cudaError_t launch_rms_norm(const void *x, const void *residual, const void *weight, int w_dtype,
                             int64_t n, int H, int dtype, float eps, void *y, void *sum,
                             uint8_t *codes, uint8_t *scales, cudaStream_t s);
